@@ -672,6 +672,74 @@ bt_status bt_binary_conv2d_dscale_init(const void *x, bt_dtype x_dtype,
                                        void *workspace, size_t workspace_bytes,
                                        bt_stream stream);
 
+/* ------------------------------------------------------------------------
+ * Distillation from a teacher's top logits: the loss a binarized model (or
+ * the adapters beside it) is trained with when the float teacher's largest
+ * logits of every token were stored. The pages have no counterpart.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * bt_distill_topk -- the loss of every row (token), without its gradient. With
+ * a = z / temperature for the row's logits z, and q_k the teacher's
+ * probability of slot k:
+ *   lse  = log sum_v exp a_v            r = log sum over the v outside the slots
+ *   loss = sum_k q_k (log q_k - a_k + lse)  [+ q_r (log q_r - r + lse)]
+ *   teacher_lse NULL:  q = softmax(top / temperature) over the row's slots;
+ *   teacher_lse given: q_k = exp(top_k / temperature - teacher_lse), the
+ *                      teacher's own log sum of exp(t / temperature) over its
+ *                      whole vocabulary, and q_r = max(0, 1 - sum q) is one
+ *                      more outcome (the bracketed term; it counts where q_r > 0
+ *                      and the student has a logit above -inf outside the slots).
+ *   logits      device [T, V] in dtype (F32, BF16, F16), rows ld >= V elements
+ *               apart, any element alignment.
+ *   ids, top    device [T, S] dense: the slots' vocabulary entries (int32 or
+ *               int64: ids_bytes 4 or 8) and the teacher's logits (top_dtype
+ *               F32, BF16, F16). A slot whose id lies outside [0, V) (-1, say)
+ *               or whose teacher logit is -inf is empty. The ids of a row must
+ *               differ from one another.
+ *   teacher_lse device [T] or NULL.
+ *   loss        device [T] out. 0 for a row without a slot (a padding token),
+ *               whose logits are not used, and for a row with nothing left:
+ *               logits of -inf, or of at most -1.7e38 (a mask's lowest value),
+ *               only; r likewise. +inf where q_k > 0 and the student's logit
+ *               is -inf. A NaN among a row's logits makes its loss NaN.
+ *   stats       device [T, 2] out, or NULL: (lse, r), what
+ *               bt_distill_topk_backward needs; zeros for a row without a slot.
+ * The sums are fp32, in an order that depends on the sizes only: equal calls
+ * give equal results. temperature finite and > 0. S <= 1024; V <= 393216 (F32)
+ * or 786432 (16-bit types), T <= 2^24: BT_ERR_UNSUPPORTED beyond. T = 0 does
+ * nothing. Errors: INVALID_ARG, ALIGNMENT (a pointer not aligned to its
+ * element), UNSUPPORTED, CUDA.
+ */
+bt_status bt_distill_topk(const void *logits, bt_dtype dtype, int64_t T, int64_t V, int64_t ld, const void *ids,
+                          int ids_bytes, const void *top, bt_dtype top_dtype, int64_t S, const float *teacher_lse,
+                          float temperature, float *loss, float *stats, bt_stream stream);
+
+/*
+ * bt_distill_topk_backward -- grad[t, v] = grad_loss[t] * d loss[t] / d z[t, v]:
+ *   (1 / temperature) (exp(a_v - lse) - q_v)                 v in a slot
+ *   (1 / temperature) exp(a_v - lse)                         else, teacher_lse NULL
+ *   (1 / temperature) (exp(r - lse) - q_r) exp(a_v - r)      else, teacher_lse given
+ * for the arguments of the forward and its stats; grad_loss device [T]. grad
+ * [T, V] in the logits' dtype, rows ldg >= V elements apart, each value rounded
+ * once; it may be the logits themselves (ldg = ld). Rows without a slot and
+ * rows with nothing left get zeros.
+ */
+bt_status bt_distill_topk_backward(const float *grad_loss, const void *logits, bt_dtype dtype, int64_t T, int64_t V,
+                                   int64_t ld, const void *ids, int ids_bytes, const void *top, bt_dtype top_dtype,
+                                   int64_t S, const float *stats, const float *teacher_lse, float temperature,
+                                   void *grad, int64_t ldg, bt_stream stream);
+
+/*
+ * bt_distill_topk_step -- both at once, for a caller that knows the upstream
+ * gradient (a mean's 1 / tokens, a loss scale) beforehand: every logit is read
+ * once and its gradient written once. stats may be NULL.
+ */
+bt_status bt_distill_topk_step(const float *grad_loss, const void *logits, bt_dtype dtype, int64_t T, int64_t V,
+                               int64_t ld, const void *ids, int ids_bytes, const void *top, bt_dtype top_dtype,
+                               int64_t S, const float *teacher_lse, float temperature, float *loss, float *stats,
+                               void *grad, int64_t ldg, bt_stream stream);
+
 /*
  * bt_device_status -- synchronizes `stream`, then reads and clears the
  * device error word of the current device: BT_ERR_TIMEOUT if a kernel's

@@ -25,7 +25,7 @@ __all__ = [
     "bt_binary_conv2d", "bt_plan", "bt_device_status", "conv2d_out_size", "bt_binary_linear_noalloc",
     "bt_binary_linear_noalloc_max_bytes", "bt_pack_im2col", "bt_conv2d_single_pass", "bt_tune_linear",
     "bt_tune_reset", "bt_tune_conv2d", "bt_conv2d_plan_info", "bt_set_wait_timeout", "bt_binary_linear_dscale_init",
-    "bt_binary_conv2d_dscale_init",
+    "bt_binary_conv2d_dscale_init", "bt_distill_topk", "bt_distill_topk_backward", "bt_distill_topk_step",
 ]
 
 BT_OK, BT_ERR_INVALID_ARG, BT_ERR_UNSUPPORTED, BT_ERR_ALIGNMENT = 0, -1, -2, -3
@@ -90,6 +90,11 @@ _c_conv_dsi = _sig("bt_binary_conv2d_dscale_init", _i, [_p, _i, _p, _i, _i64, _i
 _c_w8_ws = _sig("bt_w8a8_conv2d_workspace", _sz, [_i64, _i64, _i64, _i64, _i64, _i, _i, _i, _i])
 _c_w8 = _sig("bt_w8a8_conv2d", _i, [_p, _i, _p, _i, _i64, _i64, _i64, _i64, _i64, _i, _i, _i, _i, _i, _p, _i, _p,
                                     _sz, _p])
+_c_distill = _sig("bt_distill_topk", _i, [_p, _i, _i64, _i64, _i64, _p, _i, _p, _i, _i64, _p, _f, _p, _p, _p])
+_c_distill_bwd = _sig("bt_distill_topk_backward", _i, [_p, _p, _i, _i64, _i64, _i64, _p, _i, _p, _i, _i64, _p, _p, _f,
+                                                      _p, _i64, _p])
+_c_distill_step = _sig("bt_distill_topk_step", _i, [_p, _p, _i, _i64, _i64, _i64, _p, _i, _p, _i, _i64, _p, _f, _p,
+                                                   _p, _p, _i64, _p])
 _c_plan = _sig("bt_plan", _i, [_i, _i64, _i64, _i64, ctypes.POINTER(_i), ctypes.POINTER(_i)])
 
 
@@ -125,7 +130,8 @@ EXPORTED = ["bt_version", "bt_status_string", "bt_packed_row_bytes", "bt_pack_si
             "bt_binary_linear_backward", "bt_binary_conv2d_backward_workspace", "bt_conv2d_backward_implicit",
             "bt_binary_conv2d_backward",
             "bt_scale_init", "bt_binary_linear_dscale", "bt_binary_conv2d_dscale", "bt_w8a8_conv2d_workspace",
-            "bt_w8a8_conv2d", "bt_set_wait_timeout", "bt_binary_linear_dscale_init", "bt_binary_conv2d_dscale_init"]
+            "bt_w8a8_conv2d", "bt_set_wait_timeout", "bt_binary_linear_dscale_init", "bt_binary_conv2d_dscale_init",
+            "bt_distill_topk", "bt_distill_topk_backward", "bt_distill_topk_step"]
 
 
 class BtError(RuntimeError):
@@ -512,6 +518,113 @@ def bt_scale_init(x: torch.Tensor, factor: float = 2.0, scale_dtype=None, out: t
     st = _DT[x.dtype if scale_dtype is None else scale_dtype]
     _check(_c_scale_init(_ptr(x), _DT[x.dtype], x.numel(), factor, st, _ptr(out), _stream(stream)))
     return out
+
+
+_ID_BYTES = {torch.int32: 4, torch.int64: 8}
+
+
+def _on_gpu(**tensors) -> None:
+    for name, t in tensors.items():
+        if t is not None and not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+
+
+def _empty(shape, dtype, device, stream):
+    """A tensor of the caching allocator that belongs to the stream the call runs on."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _dense(t, name: str, shape: tuple, dtype) -> None:
+    if t.shape != shape or t.dtype != dtype or not t.is_cuda:
+        raise ValueError(f"{name} must be a {dtype} CUDA tensor of shape {list(shape)}")
+    _contig(t, name)
+
+
+def _distill_args(logits, ids, top, teacher_lse):
+    _on_gpu(logits=logits, ids=ids, top=top, teacher_lse=teacher_lse)
+    if logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise ValueError("logits must be [T, V] with elements of a row next to each other")
+    T, V = logits.shape
+    if ids.dim() != 2 or ids.shape[0] != T or top.shape != ids.shape:
+        raise ValueError("ids and top must both be [T, S]")
+    if ids.dtype not in _ID_BYTES:
+        raise ValueError("ids must be int32 or int64")
+    _contig(ids, "ids")
+    _contig(top, "top")
+    if teacher_lse is not None:
+        _dense(teacher_lse, "teacher_lse", (T,), torch.float32)
+    return T, V, (logits.stride(0) if T > 1 else max(V, logits.stride(0)))
+
+
+def _distill_grad(logits, grad, T, V, stream):
+    if grad is None:
+        grad = _empty((T, V), logits.dtype, logits.device, stream)
+    elif not grad.is_cuda or grad.shape != logits.shape or grad.dtype != logits.dtype or (V > 1 and grad.stride(1) != 1):
+        raise ValueError("grad must be a CUDA tensor of the logits' shape and dtype, with elements of a row next to each other")
+    return grad, (grad.stride(0) if T > 1 else max(V, grad.stride(0)))
+
+
+def bt_distill_topk(logits: torch.Tensor, ids: torch.Tensor, top: torch.Tensor, teacher_lse: torch.Tensor | None = None,
+                    temperature: float = 1.0, loss: torch.Tensor | None = None, stats: torch.Tensor | None = None,
+                    stream=None) -> tuple[torch.Tensor, torch.Tensor]:
+    """Distillation loss of every row of logits [T, V] against a teacher's top
+    logits (top [T, S] at the vocabulary entries ids [T, S], -1 for an empty
+    slot): (loss [T], stats [T, 2]), both float. teacher_lse [T], the
+    teacher's log-sum-exp of its logits / temperature, counts the teacher's
+    remaining probability as one more outcome; without it the teacher is
+    normalized over its slots."""
+    T, V, ld = _distill_args(logits, ids, top, teacher_lse)
+    if loss is None:
+        loss = _empty((T,), torch.float32, logits.device, stream)
+    else:
+        _dense(loss, "loss", (T,), torch.float32)
+    if stats is None:
+        stats = _empty((T, 2), torch.float32, logits.device, stream)
+    else:
+        _dense(stats, "stats", (T, 2), torch.float32)
+    _check(_c_distill(_ptr(logits), _DT[logits.dtype], T, V, ld, _ptr(ids), _ID_BYTES[ids.dtype], _ptr(top),
+                      _DT[top.dtype], ids.shape[1], _ptr(teacher_lse), temperature, _ptr(loss), _ptr(stats),
+                      _stream(stream)))
+    return loss, stats
+
+
+def bt_distill_topk_backward(grad_loss: torch.Tensor, logits: torch.Tensor, ids: torch.Tensor, top: torch.Tensor,
+                             stats: torch.Tensor, teacher_lse: torch.Tensor | None = None, temperature: float = 1.0,
+                             grad: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Gradient [T, V] (the logits' dtype) of bt_distill_topk's loss for
+    grad_loss [T] and the forward's stats. grad may be the logits."""
+    T, V, ld = _distill_args(logits, ids, top, teacher_lse)
+    _dense(grad_loss, "grad_loss", (T,), torch.float32)
+    _dense(stats, "stats", (T, 2), torch.float32)
+    grad, ldg = _distill_grad(logits, grad, T, V, stream)
+    _check(_c_distill_bwd(_ptr(grad_loss), _ptr(logits), _DT[logits.dtype], T, V, ld, _ptr(ids), _ID_BYTES[ids.dtype],
+                          _ptr(top), _DT[top.dtype], ids.shape[1], _ptr(stats), _ptr(teacher_lse), temperature,
+                          _ptr(grad), ldg, _stream(stream)))
+    return grad
+
+
+def bt_distill_topk_step(grad_loss: torch.Tensor, logits: torch.Tensor, ids: torch.Tensor, top: torch.Tensor,
+                         teacher_lse: torch.Tensor | None = None, temperature: float = 1.0,
+                         loss: torch.Tensor | None = None, grad: torch.Tensor | None = None,
+                         stats: torch.Tensor | None = None, stream=None) -> tuple[torch.Tensor, torch.Tensor]:
+    """Loss [T] and gradient [T, V] in one read of the logits, for an upstream
+    gradient grad_loss [T] known beforehand. grad may be the logits."""
+    T, V, ld = _distill_args(logits, ids, top, teacher_lse)
+    _dense(grad_loss, "grad_loss", (T,), torch.float32)
+    if loss is None:
+        loss = _empty((T,), torch.float32, logits.device, stream)
+    else:
+        _dense(loss, "loss", (T,), torch.float32)
+    if stats is not None:
+        _dense(stats, "stats", (T, 2), torch.float32)
+    grad, ldg = _distill_grad(logits, grad, T, V, stream)
+    _check(_c_distill_step(_ptr(grad_loss), _ptr(logits), _DT[logits.dtype], T, V, ld, _ptr(ids),
+                           _ID_BYTES[ids.dtype], _ptr(top), _DT[top.dtype], ids.shape[1], _ptr(teacher_lse),
+                           temperature, _ptr(loss), _ptr(stats), _ptr(grad), ldg, _stream(stream)))
+    return loss, grad
 
 
 def bt_binary_linear_noalloc_max_bytes() -> int:
