@@ -673,6 +673,105 @@ bt_status bt_binary_conv2d_dscale_init(const void *x, bt_dtype x_dtype,
                                        bt_stream stream);
 
 /* ------------------------------------------------------------------------
+ * Low-rank adapters of many requests beside one shared projection: the 1-bit
+ * weights of a projection are frozen and shared, every request (or tenant, or
+ * task) brings two small 16-bit matrices. The pages have no counterpart.
+ *
+ *   out_t = cast(base_t + scale[a] * B_a (A_a x_t)),   a = the adapter of token t
+ *
+ * with A [L, R, K] and B [L, N, R] for L adapters of rank R (an adapter of a
+ * smaller rank has rows of A and columns of B of zeros), scale [L] fp32, base
+ * the projection's own result (bt_binary_linear's, say). Tokens come in any
+ * order; a token may have no adapter.
+ * ------------------------------------------------------------------------ */
+
+/* What bt_adapter_plan says of a batch; passed back with the plan. */
+typedef struct {
+    int64_t tokens, adapters;  /* T, L */
+    int32_t used;              /* adapters that have tokens */
+    int32_t most_tokens;       /* tokens of the one that has most */
+    int32_t without;           /* tokens without an adapter */
+    int32_t tiles;             /* tiles of up to 128 tokens of one adapter; */
+    int32_t large_tiles;       /*   the first of them, of adapters with more than 32 tokens */
+    int32_t small_tiles;       /* tiles of up to 16 tokens, of the other adapters */
+    int32_t parts, slots;      /* parts of a gradient's tokens; those that are summed afterwards */
+} bt_adapter_plan_info;
+
+/* Bytes of a plan for T tokens and L adapters; 0 for sizes out of range
+ * (T > 2^24, L > 65536). */
+size_t bt_adapter_plan_bytes(int64_t T, int64_t L);
+
+/*
+ * bt_adapter_plan -- sorts the tokens of a batch by adapter, on the host:
+ * adapter[t] (host memory) in [0, L), or -1 for a token without one. plan is
+ * host memory of bt_adapter_plan_bytes(T, L) bytes, which the caller copies
+ * to the device as it is; the copy and *info then go to the calls below, for
+ * every projection that the batch goes through. Host only: no CUDA call.
+ * Errors: INVALID_ARG (null pointers, T < 0, L < 1, an adapter out of range),
+ * ALIGNMENT (plan not 4-byte aligned), WORKSPACE (plan too small, or no host
+ * memory for L counts), UNSUPPORTED (T > 2^24, L > 65536).
+ */
+bt_status bt_adapter_plan(const int32_t *adapter, int64_t T, int64_t L, void *plan, size_t plan_bytes,
+                          bt_adapter_plan_info *info);
+
+/* Workspace bytes of bt_adapter_linear (0 when u is given, or for sizes out of range). */
+size_t bt_adapter_linear_workspace(int64_t T, int64_t R, int have_u);
+
+/*
+ * bt_adapter_linear -- the formula above for x [T, K].
+ *   x, A, B    device, BF16 or F16 (the same type).
+ *   scale      device fp32 [L].
+ *   plan, info the device copy of a plan for T tokens and L adapters, 16-byte
+ *              aligned, and what came with it (host).
+ *   base       device [T, N] of base_dtype (F32 or x's type), or NULL for 0.
+ *   out        device [T, N] of out_dtype (F32 or x's type); it may be base
+ *              (of the same dtype). A token without an adapter gets cast(base).
+ *   u          device fp32 [T, R] out, or NULL: A_a x_t, what the backward
+ *              needs; 0 for a token without an adapter.
+ *   ldx, ldb, ldo  elements from one row to the next, >= K, N, N.
+ * A_a x is summed in fp32 and enters the second product as the sum of two
+ * 16-bit values, so that 16 bits of it or more count; base + scale * sum is
+ * rounded once. Any sizes and element alignments are served; rows that start
+ * at multiples of 16 bytes (and R a multiple of 8) are faster. 1 <= R <= 128;
+ * T, K, N < 2^24. T = 0 or N = 0 does nothing. workspace:
+ * bt_adapter_linear_workspace(T, R, u != NULL) bytes, 256-byte aligned.
+ * Equal calls give equal results.
+ * Errors: INVALID_ARG, ALIGNMENT, WORKSPACE, UNSUPPORTED, CUDA.
+ */
+bt_status bt_adapter_linear(const void *x, bt_dtype x_dtype, int64_t ldx, const void *A, const void *B,
+                            const float *scale, const void *plan, const bt_adapter_plan_info *info, int64_t T,
+                            int64_t K, int64_t N, int64_t R, const void *base, bt_dtype base_dtype, int64_t ldb,
+                            void *out, bt_dtype out_dtype, int64_t ldo, float *u, void *workspace,
+                            size_t workspace_bytes, bt_stream stream);
+
+/* Workspace bytes of bt_adapter_linear_backward (0 for sizes out of range). */
+size_t bt_adapter_linear_backward_workspace(int64_t T, int64_t K, int64_t N, int64_t R,
+                                            const bt_adapter_plan_info *info);
+
+/*
+ * bt_adapter_linear_backward -- the gradients for the upstream gradient g of out:
+ *   dU_t     = scale[a] * B_a^T g_t
+ *   grad_x_t = cast(grad_base_t + A_a^T dU_t)    (cast(grad_base_t) without an adapter)
+ *   grad_A_a = sum over a's tokens of dU_t x_t^T,
+ *   grad_B_a = scale[a] * sum over a's tokens of g_t u_t^T, both 0 for an adapter without tokens.
+ *   x          device [T, K] BF16, the forward's input; g device [T, N] BF16.
+ *   u          device fp32 [T, R], what the forward kept.
+ *   grad_base  device [T, K] BF16 (the shared projection's own input gradient)
+ *              or NULL for 0; grad_x device [T, K] BF16 out, may be grad_base.
+ *   grad_A     device fp32 [L, R, K] out; grad_B device fp32 [L, N, R] out,
+ *              both overwritten.
+ *   ldx, ldg, ldgb, ldgx  elements from one row to the next.
+ * Sums are fp32; dU and u enter the products as the sum of two BF16 values.
+ * Tokens of an adapter are summed in a fixed order: equal calls give equal
+ * results. Limits, workspace rules and errors as bt_adapter_linear.
+ */
+bt_status bt_adapter_linear_backward(const void *x, int64_t ldx, const void *g, int64_t ldg, const float *u,
+                                     const void *A, const void *B, const float *scale, const void *plan,
+                                     const bt_adapter_plan_info *info, int64_t T, int64_t K, int64_t N, int64_t R,
+                                     const void *grad_base, int64_t ldgb, void *grad_x, int64_t ldgx, float *grad_A,
+                                     float *grad_B, void *workspace, size_t workspace_bytes, bt_stream stream);
+
+/* ------------------------------------------------------------------------
  * Distillation from a teacher's top logits: the loss a binarized model (or
  * the adapters beside it) is trained with when the float teacher's largest
  * logits of every token were stored. The pages have no counterpart.

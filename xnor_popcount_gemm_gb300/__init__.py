@@ -26,6 +26,8 @@ __all__ = [
     "bt_binary_linear_noalloc_max_bytes", "bt_pack_im2col", "bt_conv2d_single_pass", "bt_tune_linear",
     "bt_tune_reset", "bt_tune_conv2d", "bt_conv2d_plan_info", "bt_set_wait_timeout", "bt_binary_linear_dscale_init",
     "bt_binary_conv2d_dscale_init", "bt_distill_topk", "bt_distill_topk_backward", "bt_distill_topk_step",
+    "AdapterPlan", "bt_adapter_plan", "bt_adapter_plan_bytes", "bt_adapter_linear", "bt_adapter_linear_workspace",
+    "bt_adapter_linear_backward", "bt_adapter_linear_backward_workspace",
 ]
 
 BT_OK, BT_ERR_INVALID_ARG, BT_ERR_UNSUPPORTED, BT_ERR_ALIGNMENT = 0, -1, -2, -3
@@ -95,6 +97,23 @@ _c_distill_bwd = _sig("bt_distill_topk_backward", _i, [_p, _p, _i, _i64, _i64, _
                                                       _p, _i64, _p])
 _c_distill_step = _sig("bt_distill_topk_step", _i, [_p, _p, _i, _i64, _i64, _i64, _p, _i, _p, _i, _i64, _p, _f, _p,
                                                    _p, _p, _i64, _p])
+
+
+class AdapterPlanInfo(ctypes.Structure):
+    """bt_adapter_plan_info: what bt_adapter_plan says of a batch."""
+    _fields_ = [("tokens", _i64), ("adapters", _i64)] + [(n, ctypes.c_int32) for n in (
+        "used", "most_tokens", "without", "tiles", "large_tiles", "small_tiles", "parts", "slots")]
+
+
+_pinfo = ctypes.POINTER(AdapterPlanInfo)
+_c_aplan_bytes = _sig("bt_adapter_plan_bytes", _sz, [_i64, _i64])
+_c_aplan = _sig("bt_adapter_plan", _i, [_p, _i64, _i64, _p, _sz, _pinfo])
+_c_alin_ws = _sig("bt_adapter_linear_workspace", _sz, [_i64, _i64, _i])
+_c_alin = _sig("bt_adapter_linear", _i, [_p, _i, _i64, _p, _p, _p, _p, _pinfo, _i64, _i64, _i64, _i64, _p, _i, _i64,
+                                         _p, _i, _i64, _p, _p, _sz, _p])
+_c_abwd_ws = _sig("bt_adapter_linear_backward_workspace", _sz, [_i64, _i64, _i64, _i64, _pinfo])
+_c_abwd = _sig("bt_adapter_linear_backward", _i, [_p, _i64, _p, _i64, _p, _p, _p, _p, _p, _pinfo, _i64, _i64, _i64,
+                                                 _i64, _p, _i64, _p, _i64, _p, _p, _p, _sz, _p])
 _c_plan = _sig("bt_plan", _i, [_i, _i64, _i64, _i64, ctypes.POINTER(_i), ctypes.POINTER(_i)])
 
 
@@ -131,7 +150,9 @@ EXPORTED = ["bt_version", "bt_status_string", "bt_packed_row_bytes", "bt_pack_si
             "bt_binary_conv2d_backward",
             "bt_scale_init", "bt_binary_linear_dscale", "bt_binary_conv2d_dscale", "bt_w8a8_conv2d_workspace",
             "bt_w8a8_conv2d", "bt_set_wait_timeout", "bt_binary_linear_dscale_init", "bt_binary_conv2d_dscale_init",
-            "bt_distill_topk", "bt_distill_topk_backward", "bt_distill_topk_step"]
+            "bt_distill_topk", "bt_distill_topk_backward", "bt_distill_topk_step", "bt_adapter_plan_bytes",
+            "bt_adapter_plan", "bt_adapter_linear_workspace", "bt_adapter_linear",
+            "bt_adapter_linear_backward_workspace", "bt_adapter_linear_backward"]
 
 
 class BtError(RuntimeError):
@@ -625,6 +646,138 @@ def bt_distill_topk_step(grad_loss: torch.Tensor, logits: torch.Tensor, ids: tor
                            _ID_BYTES[ids.dtype], _ptr(top), _DT[top.dtype], ids.shape[1], _ptr(teacher_lse),
                            temperature, _ptr(loss), _ptr(stats), _ptr(grad), ldg, _stream(stream)))
     return loss, grad
+
+
+class AdapterPlan:
+    """The adapters of a batch's tokens, sorted for bt_adapter_linear and its
+    backward: `buffer` on the device, `info` on the host. One plan serves every
+    projection the batch goes through."""
+
+    def __init__(self, buffer: torch.Tensor, info: AdapterPlanInfo):
+        self.buffer, self.info = buffer, info
+        self._ref = ctypes.byref(info)
+
+    def __repr__(self) -> str:
+        return "AdapterPlan(%s)" % ", ".join(f"{f}={getattr(self.info, f)}" for f, _ in AdapterPlanInfo._fields_)
+
+
+def bt_adapter_plan_bytes(T: int, L: int) -> int:
+    return int(_c_aplan_bytes(T, L))
+
+
+def bt_adapter_plan(adapter_ids, num_adapters: int, device="cuda", stream=None) -> AdapterPlan:
+    """Plan of a batch from the adapter of every token (a sequence of ints or
+    a CPU tensor; -1 for a token without one), copied to the device on the
+    stream."""
+    ids = torch.as_tensor(adapter_ids) if len(adapter_ids) else torch.empty(0, dtype=torch.int32)
+    if ids.dim() != 1 or ids.is_cuda or ids.is_floating_point() or ids.dtype == torch.bool:
+        raise ValueError("adapter_ids must be a 1-D sequence or CPU tensor of integers")
+    if ids.dtype != torch.int32:
+        if ids.numel() and (int(ids.min()) < -1 or int(ids.max()) >= num_adapters):
+            raise BtError(BT_ERR_INVALID_ARG)
+        ids = ids.to(torch.int32)
+    ids = ids.contiguous()
+    T = ids.numel()
+    host = torch.empty(max(bt_adapter_plan_bytes(T, num_adapters) // 4, 1), dtype=torch.int32,
+                       pin_memory=torch.device(device).type == "cuda")
+    info = AdapterPlanInfo()
+    _check(_c_aplan(_ptr(ids), T, num_adapters, _ptr(host), host.numel() * 4, ctypes.byref(info)))
+    if stream is None:
+        return AdapterPlan(host.to(device, non_blocking=True), info)
+    with torch.cuda.stream(stream):
+        return AdapterPlan(host.to(device, non_blocking=True), info)
+
+
+def _rows(t: torch.Tensor, name: str, shape: tuple, dtypes) -> int:
+    """Elements from one row of a 2-D operand to the next."""
+    if t.shape != shape or t.dtype not in dtypes or not t.is_cuda or (shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be a CUDA tensor of shape {list(shape)} and type {' or '.join(map(str, dtypes))}, "
+                         "with elements of a row next to each other")
+    return t.stride(0) if shape[0] > 1 else max(shape[1], t.stride(0))
+
+
+def _adapter_args(x, a, b, scale, plan):
+    if x.dim() != 2 or a.dim() != 3 or b.dim() != 3:
+        raise ValueError("x must be [T, K], a [L, R, K] and b [L, N, R]")
+    T, K = x.shape
+    L, R, N = a.shape[0], a.shape[1], b.shape[1]
+    _dense(a, "a", (L, R, K), x.dtype)
+    _dense(b, "b", (L, N, R), x.dtype)
+    _dense(scale, "scale", (L,), torch.float32)
+    if not isinstance(plan, AdapterPlan) or plan.info.tokens != T or plan.info.adapters != L:
+        raise ValueError("plan must be bt_adapter_plan of these tokens and adapters")
+    _on_gpu(plan=plan.buffer)
+    return T, K, N, R
+
+
+def bt_adapter_linear_workspace(T: int, R: int, have_u: bool = False) -> int:
+    return int(_c_alin_ws(T, R, 1 if have_u else 0))
+
+
+def bt_adapter_linear(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, scale: torch.Tensor, plan: AdapterPlan,
+                      base: torch.Tensor | None = None, out_dtype=None, u: torch.Tensor | None = None,
+                      out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                      stream=None) -> torch.Tensor:
+    """base [T, N] plus scale[i] * b[i] (a[i] x_t) for the adapter i of every
+    token of x [T, K] (bf16 or f16), a [L, R, K], b [L, N, R]: out [T, N] in
+    out_dtype (base's type, else x's). out may be base. u [T, R] (float), if
+    given, receives a[i] x_t for the backward."""
+    T, K, N, R = _adapter_args(x, a, b, scale, plan)
+    ldx = _rows(x, "x", (T, K), (torch.bfloat16, torch.float16))
+    both = (x.dtype, torch.float32)
+    ldb = 0 if base is None else _rows(base, "base", (T, N), both)
+    if out is None:
+        out = _empty((T, N), out_dtype if out_dtype is not None else x.dtype if base is None else base.dtype, x.device,
+                     stream)
+    ldo = _rows(out, "out", (T, N), both if out_dtype is None else (out_dtype,))
+    need = 0
+    if u is not None:
+        _dense(u, "u", (T, R), torch.float32)
+    else:
+        need = bt_adapter_linear_workspace(T, R)
+        if need and (workspace is None or workspace.numel() < need):
+            workspace = _empty((need,), torch.uint8, x.device, stream)
+    _check(_c_alin(_ptr(x), _DT[x.dtype], ldx, _ptr(a), _ptr(b), _ptr(scale), _ptr(plan.buffer), plan._ref, T, K, N, R,
+                   _ptr(base), BT_F32 if base is None else _DT[base.dtype], ldb, _ptr(out), _DT[out.dtype], ldo,
+                   _ptr(u), _ptr(workspace), need, _stream(stream)))
+    return out
+
+
+def bt_adapter_linear_backward_workspace(T: int, K: int, N: int, R: int, plan: AdapterPlan) -> int:
+    return int(_c_abwd_ws(T, K, N, R, plan._ref))
+
+
+def bt_adapter_linear_backward(x: torch.Tensor, g: torch.Tensor, u: torch.Tensor, a: torch.Tensor, b: torch.Tensor,
+                               scale: torch.Tensor, plan: AdapterPlan, grad_base: torch.Tensor | None = None,
+                               grad_x: torch.Tensor | None = None, grad_a: torch.Tensor | None = None,
+                               grad_b: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None):
+    """Gradients of bt_adapter_linear for g [T, N] (bf16, the gradient of its
+    result), its input x and its u: (grad_x [T, K] bf16, grad_a [L, R, K],
+    grad_b [L, N, R], both float). grad_base [T, K], the projection's own
+    input gradient, is added to grad_x, which may be grad_base itself."""
+    T, K, N, R = _adapter_args(x, a, b, scale, plan)
+    bf16 = (torch.bfloat16,)
+    ldx, ldg = _rows(x, "x", (T, K), bf16), _rows(g, "g", (T, N), bf16)
+    _dense(u, "u", (T, R), torch.float32)
+    ldgb = 0 if grad_base is None else _rows(grad_base, "grad_base", (T, K), bf16)
+    if grad_x is None:
+        grad_x = _empty((T, K), torch.bfloat16, x.device, stream)
+    ldgx = _rows(grad_x, "grad_x", (T, K), bf16)
+    if grad_a is None:
+        grad_a = _empty(a.shape, torch.float32, x.device, stream)
+    else:
+        _dense(grad_a, "grad_a", tuple(a.shape), torch.float32)
+    if grad_b is None:
+        grad_b = _empty(b.shape, torch.float32, x.device, stream)
+    else:
+        _dense(grad_b, "grad_b", tuple(b.shape), torch.float32)
+    need = bt_adapter_linear_backward_workspace(T, K, N, R, plan)
+    if need and (workspace is None or workspace.numel() < need):
+        workspace = _empty((need,), torch.uint8, x.device, stream)
+    _check(_c_abwd(_ptr(x), ldx, _ptr(g), ldg, _ptr(u), _ptr(a), _ptr(b), _ptr(scale), _ptr(plan.buffer), plan._ref, T,
+                   K, N, R, _ptr(grad_base), ldgb, _ptr(grad_x), ldgx, _ptr(grad_a), _ptr(grad_b), _ptr(workspace), need,
+                   _stream(stream)))
+    return grad_x, grad_a, grad_b
 
 
 def bt_binary_linear_noalloc_max_bytes() -> int:

@@ -1,0 +1,114 @@
+// The plan of a batch's adapters, built on the host: which token uses which
+// adapter is known to the scheduler that put the batch together, so the sorting
+// costs no launch and no synchronisation, and every projection of every layer
+// shares one plan. Checks that the kernels rely on (every adapter index in
+// range, every row once) are made here.
+#include <cstdlib>
+#include <cstring>
+#include <memory>
+
+#include "adapter_plan.h"
+
+namespace bt {
+
+// Words of the plan: rows [T], the tiles, the small tiles, the gradient's parts.
+AdapterPlanLayout adapter_plan_layout(int64_t T, int64_t L) {
+    AdapterPlanLayout p;
+    const int64_t tiles = T < T / kAdapterTile + L + 1 ? T : T / kAdapterTile + L + 1;
+    const int64_t small = T < T / kAdapterSmall + L + 1 ? T : T / kAdapterSmall + L + 1;
+    p.rows = 0;
+    p.tiles = (T + 3) / 4 * 4;
+    p.small = p.tiles + 4 * tiles;
+    p.parts = p.small + 4 * small;
+    p.words = p.parts + 4 * (2 * kAdapterParts + L + 1);
+    return p;
+}
+
+}  // namespace bt
+
+using namespace bt;
+
+extern "C" {
+
+size_t bt_adapter_plan_bytes(int64_t T, int64_t L) {
+    if (T < 0 || T > kAdapterMaxTokens || L < 1 || L > kAdapterMaxAdapters) return 0;
+    return static_cast<size_t>(adapter_plan_layout(T, L).words) * 4;
+}
+
+bt_status bt_adapter_plan(const int32_t *adapter, int64_t T, int64_t L, void *plan, size_t plan_bytes,
+                          bt_adapter_plan_info *info) {
+    if (info == nullptr || T < 0 || L < 1) return BT_ERR_INVALID_ARG;
+    if (T > kAdapterMaxTokens || L > kAdapterMaxAdapters) return BT_ERR_UNSUPPORTED;
+    if (plan == nullptr || (T > 0 && adapter == nullptr)) return BT_ERR_INVALID_ARG;
+    if (!aligned(plan, 4)) return BT_ERR_ALIGNMENT;
+    const AdapterPlanLayout lay = adapter_plan_layout(T, L);
+    if (plan_bytes < static_cast<size_t>(lay.words) * 4) return BT_ERR_WORKSPACE;
+    for (int64_t t = 0; t < T; ++t)
+        if (adapter[t] < -1 || adapter[t] >= L) return BT_ERR_INVALID_ARG;
+    int32_t *w = static_cast<int32_t *>(plan);
+    memset(w, 0, static_cast<size_t>(lay.words) * 4);
+
+    // Stable counting sort by adapter, tokens without one last. last[a]: the end of adapter a's rows.
+    std::unique_ptr<int32_t, void (*)(void *)> counts(static_cast<int32_t *>(calloc(static_cast<size_t>(L) + 1, 4)), free);
+    int32_t *last = counts.get();
+    if (last == nullptr) return BT_ERR_WORKSPACE;
+    for (int64_t t = 0; t < T; ++t) ++last[adapter[t] < 0 ? L : adapter[t]];
+    int32_t off = 0;
+    for (int64_t a = 0; a <= L; ++a) {
+        const int32_t n = last[a];
+        last[a] = off;
+        off += n;
+    }
+    for (int64_t t = 0; t < T; ++t) w[lay.rows + last[adapter[t] < 0 ? L : adapter[t]]++] = static_cast<int32_t>(t);
+
+    bt_adapter_plan_info r = {};
+    r.tokens = T;
+    r.adapters = L;
+    AdapterTile *tiles = reinterpret_cast<AdapterTile *>(w + lay.tiles);
+    AdapterTile *small = reinterpret_cast<AdapterTile *>(w + lay.small);
+    auto even = [](AdapterTile *out, int32_t a, int32_t first, int32_t n, int32_t most) {
+        const int32_t k = (n + most - 1) / most;
+        for (int32_t i = 0; i < k; ++i) {
+            const int32_t b = static_cast<int32_t>(static_cast<int64_t>(n) * i / k);
+            const int32_t e = static_cast<int32_t>(static_cast<int64_t>(n) * (i + 1) / k);
+            out[i] = AdapterTile{a, first + b, e - b, 0};
+        }
+        return k;
+    };
+    // Adapters with many tokens first: the forward takes those tiles alone, the backward all.
+    for (int pass = 0; pass < 2; ++pass) {
+        for (int64_t a = 0; a < L; ++a) {
+            const int32_t first = a == 0 ? 0 : last[a - 1], n = last[a] - first;
+            if (n == 0 || (n > kAdapterSmallMost) != (pass == 0)) continue;
+            r.tiles += even(tiles + r.tiles, static_cast<int32_t>(a), first, n, kAdapterTile);
+            if (pass == 1) r.small_tiles += even(small + r.small_tiles, static_cast<int32_t>(a), first, n, kAdapterSmall);
+            if (n > r.most_tokens) r.most_tokens = n;
+            ++r.used;
+        }
+        if (pass == 0) r.large_tiles = r.tiles;
+    }
+    r.without = static_cast<int32_t>(T) - last[L - 1];
+
+    // The gradients' parts: at most a quarter of the tokens each (whole 64s, at
+    // least 256), every adapter once at least, so that one without tokens gets its
+    // zeros. A split adapter's parts have a slot each for their sums.
+    int32_t len = static_cast<int32_t>((T + kAdapterParts - 1) / kAdapterParts);
+    len = len < 256 ? 256 : (len + 63) / 64 * 64;
+    AdapterTile *parts = reinterpret_cast<AdapterTile *>(w + lay.parts);
+    for (int pass = 0; pass < 2; ++pass) {                 // the split adapters first
+        for (int64_t a = 0; a < L; ++a) {
+            const int32_t first = a == 0 ? 0 : last[a - 1], n = last[a] - first;
+            if ((n > len) != (pass == 0)) continue;
+            if (pass == 1) {
+                parts[r.parts++] = AdapterTile{static_cast<int32_t>(a), first, n, -1};
+            } else {
+                const int32_t k = even(parts + r.parts, static_cast<int32_t>(a), first, n, len);
+                for (int32_t i = 0; i < k; ++i) parts[r.parts++].slot = r.slots++;
+            }
+        }
+    }
+    *info = r;
+    return BT_OK;
+}
+
+}  // extern "C"

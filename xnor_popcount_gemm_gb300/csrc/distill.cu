@@ -40,7 +40,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 // octave, where a row's sum has its weight (measured on GB300 against exp2 in
 // double: -4.86e-8 over [-16, 0], -2.2e-8 over [-1, 0]). Single errors average
 // out in the sum, the mean does not and is taken out of it.
-constexpr double kEx2Mean = 1.0 + 5.0e-8;
+constexpr float kEx2Mean = 5.0e-8f;
 
 __device__ __forceinline__ float ex2(float v) {
     float r;
@@ -62,14 +62,22 @@ __device__ __forceinline__ void ms_add(MaxSum &a, float v, float c) {
     }
     a.s += ex2((v - a.m) * c);
 }
-// The sum of n of them, which lie `stride` floats apart in shared memory. In
-// double: these few additions would else make most of the sum's error.
-__device__ __forceinline__ MaxSum ms_sum(const float *p, int n, int stride, float c, bool last) {
+// The sum of n of them, which lie `stride` floats apart in shared memory,
+// with what each addition rounds off carried along (Knuth's two-sum): these
+// few additions would else make most of the sum's error. `mean`: take
+// ex2.approx's mean error out.
+__device__ __forceinline__ MaxSum ms_sum(const float *p, int n, int stride, float c, bool mean) {
     float m = p[0];
     for (int i = 1; i < n; ++i) m = fmaxf(m, p[i * stride]);
-    double s = 0.0;
-    for (int i = 0; i < n; ++i) s += static_cast<double>(p[i * stride + 1] * ex2((p[i * stride] - m) * c));
-    return MaxSum{m, static_cast<float>(last ? s * kEx2Mean : s)};
+    float s = 0.0f, lost = 0.0f;
+    for (int i = 0; i < n; ++i) {
+        const float v = p[i * stride + 1] * ex2((p[i * stride] - m) * c);
+        const float t = __fadd_rn(s, v), b = __fsub_rn(t, s);
+        lost += __fadd_rn(__fsub_rn(s, __fsub_rn(t, b)), __fsub_rn(v, b));
+        s = t;
+    }
+    if (mean) lost += s * kEx2Mean;
+    return MaxSum{m, s + lost};
 }
 __device__ __forceinline__ MaxSum ms_join(const MaxSum &a, const MaxSum &b, float c) {
     const float m = fmaxf(a.m, b.m);
