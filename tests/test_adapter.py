@@ -52,6 +52,7 @@ def test_plan_covers_every_token_once(T, L, none, skew):
     covered(tiles, TILE, [a for a in range(L) if count[a]])
     covered(tiles[:info.large_tiles], TILE, [a for a in range(L) if count[a] > SMALL_MOST])
     covered(small, SMALL, [a for a in range(L) if 0 < count[a] <= SMALL_MOST])
+    assert info.small_most == max([n for _, _, n, _ in small], default=0)
     # every adapter has its parts, one after the other; those of split ones come first and have the slots in order
     length = max(256, (-(-T // PARTS) + 63) // 64 * 64)
     assert sorted({a for a, *_ in parts}) == list(range(L))
@@ -133,12 +134,16 @@ def test_forward_refusals():
     for bad in (dict(R=129), dict(K=1 << 24, ldx=1 << 24), dict(N=1 << 24, ldo=1 << 24), dict(ldx=1 << 37)):
         assert _fwd(**bad) == bt.BT_ERR_UNSUPPORTED, bad
     for bad in (dict(x=257), dict(A=513), dict(B=1025), dict(s=2050), dict(plan=4100), dict(out=8193), dict(u=2),
-                dict(ot=bt.BT_F32, out=8194), dict(base=258, ldb=32, bt_=bt.BT_F32), dict(ws=16384 + 16)):
+                dict(ot=bt.BT_F32, out=8194), dict(base=258, ldb=32, bt_=bt.BT_F32)):
         assert _fwd(**bad) == bt.BT_ERR_ALIGNMENT, bad
-    assert _fwd(ws=None) == _fwd(wsb=127) == bt.BT_ERR_WORKSPACE
+    large = dict(T=40, info=_info(T=40))
+    assert _fwd(**large, ws=None) == _fwd(**large, wsb=40 * 32 - 1) == bt.BT_ERR_WORKSPACE
+    assert _fwd(**large, ws=16384 + 16) == bt.BT_ERR_ALIGNMENT
     assert _fwd(T=0, info=_info(T=0), x=None) == _fwd(N=0, out=None) == bt.BT_OK
-    assert bt.bt_adapter_linear_workspace(4, 8) == 256
-    assert bt.bt_adapter_linear_workspace(4, 8, True) == bt.bt_adapter_linear_workspace(4, 129) == 0
+    few, many = (bt.bt_adapter_plan([0] * n, 2, device="cpu") for n in (4, 40))
+    assert bt.bt_adapter_linear_workspace(40, 8, many) == 1280
+    assert bt.bt_adapter_linear_workspace(40, 8, many, True) == bt.bt_adapter_linear_workspace(40, 129, many) == 0
+    assert bt.bt_adapter_linear_workspace(4, 8, few) == 0
 
 
 def test_backward_refusals():

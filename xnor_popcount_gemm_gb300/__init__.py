@@ -102,13 +102,13 @@ _c_distill_step = _sig("bt_distill_topk_step", _i, [_p, _p, _i, _i64, _i64, _i64
 class AdapterPlanInfo(ctypes.Structure):
     """bt_adapter_plan_info: what bt_adapter_plan says of a batch."""
     _fields_ = [("tokens", _i64), ("adapters", _i64)] + [(n, ctypes.c_int32) for n in (
-        "used", "most_tokens", "without", "tiles", "large_tiles", "small_tiles", "parts", "slots")]
+        "used", "most_tokens", "without", "tiles", "large_tiles", "small_tiles", "small_most", "parts", "slots")]
 
 
 _pinfo = ctypes.POINTER(AdapterPlanInfo)
 _c_aplan_bytes = _sig("bt_adapter_plan_bytes", _sz, [_i64, _i64])
 _c_aplan = _sig("bt_adapter_plan", _i, [_p, _i64, _i64, _p, _sz, _pinfo])
-_c_alin_ws = _sig("bt_adapter_linear_workspace", _sz, [_i64, _i64, _i])
+_c_alin_ws = _sig("bt_adapter_linear_workspace", _sz, [_i64, _i64, _pinfo, _i])
 _c_alin = _sig("bt_adapter_linear", _i, [_p, _i, _i64, _p, _p, _p, _p, _pinfo, _i64, _i64, _i64, _i64, _p, _i, _i64,
                                          _p, _i, _i64, _p, _p, _sz, _p])
 _c_abwd_ws = _sig("bt_adapter_linear_backward_workspace", _sz, [_i64, _i64, _i64, _i64, _pinfo])
@@ -550,6 +550,11 @@ def _on_gpu(**tensors) -> None:
             raise ValueError(f"{name} must be a CUDA tensor")
 
 
+def _on_stream(stream, device) -> int:
+    """The raw stream of a call: the one given, or the device's current one."""
+    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
+
+
 def _empty(shape, dtype, device, stream):
     """A tensor of the caching allocator that belongs to the stream the call runs on."""
     if stream is None:
@@ -608,7 +613,7 @@ def bt_distill_topk(logits: torch.Tensor, ids: torch.Tensor, top: torch.Tensor, 
         _dense(stats, "stats", (T, 2), torch.float32)
     _check(_c_distill(_ptr(logits), _DT[logits.dtype], T, V, ld, _ptr(ids), _ID_BYTES[ids.dtype], _ptr(top),
                       _DT[top.dtype], ids.shape[1], _ptr(teacher_lse), temperature, _ptr(loss), _ptr(stats),
-                      _stream(stream)))
+                      _on_stream(stream, logits.device)))
     return loss, stats
 
 
@@ -623,7 +628,7 @@ def bt_distill_topk_backward(grad_loss: torch.Tensor, logits: torch.Tensor, ids:
     grad, ldg = _distill_grad(logits, grad, T, V, stream)
     _check(_c_distill_bwd(_ptr(grad_loss), _ptr(logits), _DT[logits.dtype], T, V, ld, _ptr(ids), _ID_BYTES[ids.dtype],
                           _ptr(top), _DT[top.dtype], ids.shape[1], _ptr(stats), _ptr(teacher_lse), temperature,
-                          _ptr(grad), ldg, _stream(stream)))
+                          _ptr(grad), ldg, _on_stream(stream, logits.device)))
     return grad
 
 
@@ -644,7 +649,7 @@ def bt_distill_topk_step(grad_loss: torch.Tensor, logits: torch.Tensor, ids: tor
     grad, ldg = _distill_grad(logits, grad, T, V, stream)
     _check(_c_distill_step(_ptr(grad_loss), _ptr(logits), _DT[logits.dtype], T, V, ld, _ptr(ids),
                            _ID_BYTES[ids.dtype], _ptr(top), _DT[top.dtype], ids.shape[1], _ptr(teacher_lse),
-                           temperature, _ptr(loss), _ptr(stats), _ptr(grad), ldg, _stream(stream)))
+                           temperature, _ptr(loss), _ptr(stats), _ptr(grad), ldg, _on_stream(stream, logits.device)))
     return loss, grad
 
 
@@ -710,8 +715,8 @@ def _adapter_args(x, a, b, scale, plan):
     return T, K, N, R
 
 
-def bt_adapter_linear_workspace(T: int, R: int, have_u: bool = False) -> int:
-    return int(_c_alin_ws(T, R, 1 if have_u else 0))
+def bt_adapter_linear_workspace(T: int, R: int, plan: AdapterPlan, have_u: bool = False) -> int:
+    return int(_c_alin_ws(T, R, plan._ref, 1 if have_u else 0))
 
 
 def bt_adapter_linear(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, scale: torch.Tensor, plan: AdapterPlan,
@@ -734,12 +739,12 @@ def bt_adapter_linear(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, scale: 
     if u is not None:
         _dense(u, "u", (T, R), torch.float32)
     else:
-        need = bt_adapter_linear_workspace(T, R)
+        need = _c_alin_ws(T, R, plan._ref, 0)
         if need and (workspace is None or workspace.numel() < need):
             workspace = _empty((need,), torch.uint8, x.device, stream)
     _check(_c_alin(_ptr(x), _DT[x.dtype], ldx, _ptr(a), _ptr(b), _ptr(scale), _ptr(plan.buffer), plan._ref, T, K, N, R,
                    _ptr(base), BT_F32 if base is None else _DT[base.dtype], ldb, _ptr(out), _DT[out.dtype], ldo,
-                   _ptr(u), _ptr(workspace), need, _stream(stream)))
+                   _ptr(u), _ptr(workspace), need, _on_stream(stream, x.device)))
     return out
 
 
@@ -776,7 +781,7 @@ def bt_adapter_linear_backward(x: torch.Tensor, g: torch.Tensor, u: torch.Tensor
         workspace = _empty((need,), torch.uint8, x.device, stream)
     _check(_c_abwd(_ptr(x), ldx, _ptr(g), ldg, _ptr(u), _ptr(a), _ptr(b), _ptr(scale), _ptr(plan.buffer), plan._ref, T,
                    K, N, R, _ptr(grad_base), ldgb, _ptr(grad_x), ldgx, _ptr(grad_a), _ptr(grad_b), _ptr(workspace), need,
-                   _stream(stream)))
+                   _on_stream(stream, x.device)))
     return grad_x, grad_a, grad_b
 
 

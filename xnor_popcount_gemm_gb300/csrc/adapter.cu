@@ -681,6 +681,229 @@ __global__ void __launch_bounds__(kThreads) sum_kernel(const SumArgs a) {
 }
 
 // ---------------------------------------------------------------------------
+// Few tokens of many adapters (decoding): the whole adapter in one kernel. A
+// cluster of 1 to 8 CTAs takes up to 16 tokens of one adapter. Each CTA reduces
+// a piece of the long axis, the pieces are exchanged through distributed shared
+// memory, and each CTA writes a range of the columns. Weights go from memory
+// straight to the registers of the matrix instructions, 16 bytes a lane: the
+// reduction index may be permuted as long as both operands agree, so lane t of
+// a quad takes elements 8t .. 8t + 7 of 32 as its share of two instructions.
+// The first of B's rows are fetched before anything waits for the sums: a
+// token costs about one trip to memory and one exchange.
+//
+// The rank (A's rows) and the columns (B's rows) are the 16 rows of the
+// instruction, tokens its 8 columns.
+// ---------------------------------------------------------------------------
+struct SmallArgs {
+    Plan plan;
+    const uint16_t *x, *A, *B;
+    int64_t ldx;
+    int K, N, R;
+    int vec_k, vec_r;          // rows of x and A, rows of B start at 16-byte multiples (B: R a multiple of 8)
+    const float *scale;
+    const void *base;
+    int base_f32;
+    int64_t ldb;
+    void *out;
+    int64_t ldo;
+    float *u;                  // NULL: not wanted
+    int cluster;
+};
+
+// Elements k .. k + 7 of a row of n, zeros beyond; VEC: k + 8 <= n or k >= n, and 16-byte aligned.
+__device__ __forceinline__ uint4 row8(const uint16_t *p, int k, int n, bool vec) {
+    if (vec) return k < n ? __ldg(reinterpret_cast<const uint4 *>(p + k)) : make_uint4(0u, 0u, 0u, 0u);
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t lo = k + 2 * i < n ? __ldg(p + k + 2 * i) : 0u, hi = k + 2 * i + 1 < n ? __ldg(p + k + 2 * i + 1) : 0u;
+        w[i] = lo | (hi << 16);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// RB: blocks of 16 ranks; NB: blocks of 8 tokens.
+template <typename T, int RB, int NB, bool OF32>
+__global__ void __launch_bounds__(kThreads, RB <= 4 ? 2 : 1) small_kernel(const SmallArgs a) {
+    constexpr int RP = 16 * RB, TOK = 8 * NB, UP = RP + 4;
+    constexpr int RK = (RB + 1) / 2;                        // 32-rank pieces of B's rows
+    constexpr int PRE = RK == 1 ? 4 : RK == 2 ? 2 : 1;      // B's row blocks fetched ahead
+    extern __shared__ __align__(128) uint8_t smem[];
+    float(*part)[TOK][UP] = reinterpret_cast<float(*)[TOK][UP]>(smem);                                 // [warp]
+    float(*slot)[TOK][RP] = reinterpret_cast<float(*)[TOK][RP]>(smem + 8 * TOK * UP * sizeof(float));  // [rank]
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+    const int c = a.cluster;
+    const int rank = c > 1 ? static_cast<int>(tc::cluster_ctarank()) : 0;
+    pdl_launch_dependents();
+    pdl_wait();
+    const AdapterTile tile = a.plan.tiles[blockIdx.x / c];
+    const uint16_t *A = a.A + static_cast<int64_t>(tile.adapter) * a.R * a.K;
+    const uint16_t *B = a.B + static_cast<int64_t>(tile.adapter) * a.R * a.N;
+    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+
+    // columns of this CTA, in blocks of 16; this warp's are b0 + warp, b0 + warp + 8, ...
+    const int blocks = (a.N + 15) / 16;
+    const int b0 = static_cast<int>(static_cast<int64_t>(blocks) * rank / c);
+    const int b1 = static_cast<int>(static_cast<int64_t>(blocks) * (rank + 1) / c);
+    auto load_b = [&](int b, uint4 (&w)[RK][2]) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int n = 16 * b + 8 * h + g;
+            const uint16_t *p = B + static_cast<int64_t>(n) * a.R;
+#pragma unroll
+            for (int q = 0; q < RK; ++q) w[q][h] = b < b1 && n < a.N ? row8(p, 32 * q + 8 * t, a.R, a.vec_r) : zero;
+        }
+    };
+
+    float acc[RB][NB][4];
+#pragma unroll
+    for (int m = 0; m < RB; ++m)
+#pragma unroll
+        for (int j = 0; j < NB; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[m][j][e] = 0.0f;
+    const uint16_t *xr[NB];
+    bool live[NB];
+#pragma unroll
+    for (int j = 0; j < NB; ++j) {
+        live[j] = 8 * j + g < tile.n;
+        xr[j] = a.x + static_cast<int64_t>(a.plan.rows[tile.first + (live[j] ? 8 * j + g : 0)]) * a.ldx;
+    }
+    uint4 wb[PRE][RK][2];
+#pragma unroll
+    for (int i = 0; i < PRE; ++i) load_b(b0 + warp + 8 * i, wb[i]);
+    // this warp's steps of 32 elements
+    const int steps = (a.K + 31) / 32, who = rank * 8 + warp, all = c * 8;
+#pragma unroll 2
+    for (int s = who; s < steps; s += all) {
+        const int k = 32 * s + 8 * t;
+        uint4 xv[NB];
+#pragma unroll
+        for (int j = 0; j < NB; ++j) xv[j] = live[j] ? row8(xr[j], k, a.K, a.vec_k) : zero;
+#pragma unroll
+        for (int m = 0; m < RB; ++m) {
+            const int r0 = 16 * m + g, r1 = r0 + 8;
+            const uint4 w0 = r0 < a.R ? row8(A + static_cast<int64_t>(r0) * a.K, k, a.K, a.vec_k) : zero;
+            const uint4 w1 = r1 < a.R ? row8(A + static_cast<int64_t>(r1) * a.K, k, a.K, a.vec_k) : zero;
+            const uint32_t f0[4] = {w0.x, w1.x, w0.y, w1.y}, f1[4] = {w0.z, w1.z, w0.w, w1.w};
+#pragma unroll
+            for (int j = 0; j < NB; ++j) {
+                mma<T>(acc[m][j], f0, xv[j].x, xv[j].y);
+                mma<T>(acc[m][j], f1, xv[j].z, xv[j].w);
+            }
+        }
+    }
+#pragma unroll
+    for (int m = 0; m < RB; ++m)
+#pragma unroll
+        for (int j = 0; j < NB; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                part[warp][8 * j + 2 * t + (e & 1)][16 * m + g + (e >> 1) * 8] = acc[m][j][e];
+    __syncthreads();
+    if (c > 1) tc::cluster_sync();                          // every CTA of the cluster has started
+    for (int i = tid; i < TOK * RP; i += kThreads) {
+        const int tok = i / RP, r = i % RP;
+        float v = 0.0f;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) v += part[w][tok][r];
+        const uint32_t at = smem_u32(&slot[rank][tok][r]);
+        if (c == 1) {
+            slot[0][tok][r] = v;
+        } else {
+            for (int q = 0; q < c; ++q)
+                asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(tc::mapa(at, q)), "f"(v) : "memory");
+        }
+    }
+    if (c > 1) tc::cluster_sync();
+    else __syncthreads();
+    // u of this tile's tokens, whole, in part[0]
+    float(*u)[UP] = part[0];
+    for (int i = tid; i < TOK * RP; i += kThreads) {
+        const int tok = i / RP, r = i % RP;
+        float v = 0.0f;
+        for (int q = 0; q < c; ++q) v += slot[q][tok][r];
+        u[tok][r] = v;
+        if (a.u != nullptr && rank == 0 && tok < tile.n && r < a.R)
+            a.u[static_cast<int64_t>(a.plan.rows[tile.first + tok]) * a.R + r] = v;
+    }
+    __syncthreads();
+    // its fragments: lane t of a quad holds ranks 32q + 8t .. + 7 of token g
+    const float s = a.scale[tile.adapter];
+    uint32_t uh[RK][NB][4], ul[RK][NB][4];
+    float mul[NB];
+#pragma unroll
+    for (int j = 0; j < NB; ++j) {
+        float v[RK][8], amax = 0.0f;
+#pragma unroll
+        for (int q = 0; q < RK; ++q)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int r = 32 * q + 8 * t + e;
+                v[q][e] = r < RP ? u[8 * j + g][r] : 0.0f;
+                amax = fmaxf(amax, fabsf(v[q][e]));
+            }
+        amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
+        amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
+        const float p = row_power<T>(amax);
+        mul[j] = s / p;
+#pragma unroll
+        for (int q = 0; q < RK; ++q)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) split2<T>(v[q][2 * e] * p, v[q][2 * e + 1] * p, uh[q][j][e], ul[q][j][e]);
+    }
+    // a result's tokens are 2t and 2t + 1: their rows and multipliers
+    int64_t row[NB][2];
+    bool there[NB][2];
+    float m2[NB][2];
+#pragma unroll
+    for (int j = 0; j < NB; ++j)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int tok = 8 * j + 2 * t + e;
+            there[j][e] = tok < tile.n;
+            row[j][e] = a.plan.rows[tile.first + (there[j][e] ? tok : 0)];
+            m2[j][e] = __shfl_sync(0xFFFFFFFFu, mul[j], (2 * t + e) * 4);
+        }
+    for (int first = b0 + warp; first < b1; first += 8 * PRE) {
+#pragma unroll
+        for (int i = 0; i < PRE; ++i) {
+            const int b = first + 8 * i;
+            if (b >= b1) break;
+            float d[NB][4];
+#pragma unroll
+            for (int j = 0; j < NB; ++j) {
+                d[j][0] = d[j][1] = d[j][2] = d[j][3] = 0.0f;
+#pragma unroll
+                for (int q = 0; q < RK; ++q) {
+                    const uint4 w0 = wb[i][q][0], w1 = wb[i][q][1];
+                    const uint32_t f0[4] = {w0.x, w1.x, w0.y, w1.y}, f1[4] = {w0.z, w1.z, w0.w, w1.w};
+                    mma<T>(d[j], f0, uh[q][j][0], uh[q][j][1]);
+                    mma<T>(d[j], f1, uh[q][j][2], uh[q][j][3]);
+                    mma<T>(d[j], f0, ul[q][j][0], ul[q][j][1]);
+                    mma<T>(d[j], f1, ul[q][j][2], ul[q][j][3]);
+                }
+            }
+            load_b(b + 8 * PRE, wb[i]);
+#pragma unroll
+            for (int j = 0; j < NB; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int n = 16 * b + g + (e >> 1) * 8;
+                    if (!there[j][e & 1] || n >= a.N) continue;
+                    float v = 0.0f;
+                    if (a.base != nullptr)
+                        v = a.base_f32 ? static_cast<const float *>(a.base)[row[j][e & 1] * a.ldb + n]
+                                       : Elem<T>::to_f32(static_cast<const T *>(a.base)[row[j][e & 1] * a.ldb + n]);
+                    v = __fmaf_rn(d[j][e], m2[j][e & 1], v);
+                    if constexpr (OF32) static_cast<float *>(a.out)[row[j][e & 1] * a.ldo + n] = v;
+                    else static_cast<T *>(a.out)[row[j][e & 1] * a.ldo + n] = to16<T>(v);
+                }
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
 // Launches
 // ---------------------------------------------------------------------------
 // The largest of 16, 8, 4, 2 bytes that p and every multiple of `bytes` share.
@@ -691,6 +914,24 @@ int align_of(const void *p, int64_t bytes) {
 template <typename K> cudaError_t allow_smem(K kern, int bytes, std::once_flag &once, cudaError_t &err) {
     std::call_once(once, [&] { err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes); });
     return err;
+}
+
+// `grid` CTAs in clusters of c, programmatic dependent launch allowed.
+template <typename K, typename Args>
+cudaError_t launch_cluster(K kern, int grid, int c, int smem, cudaStream_t s, const Args &a) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    attr[0] = pdl_attribute();
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(c);
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kern, a);
 }
 
 template <typename T, int RP, bool WT> cudaError_t launch_shrink_rp(ShrinkArgs a, int tiles, cudaStream_t s) {
@@ -704,19 +945,7 @@ template <typename T, int RP, bool WT> cudaError_t launch_shrink_rp(ShrinkArgs a
     // pieces of at least four stages until the CTAs fill the machine twice
     while (c < 8 && tiles * c < 2 * device_sm_count() && steps >= 8 * c) c *= 2;
     a.cluster = c;
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[2];
-    attr[0] = pdl_attribute();
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = static_cast<unsigned>(c);
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cfg.gridDim = dim3(static_cast<unsigned>(tiles * c));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, kern, static_cast<const ShrinkArgs>(a));
+    return launch_cluster(kern, tiles * c, c, smem, s, static_cast<const ShrinkArgs>(a));
 }
 template <typename T, bool WT> cudaError_t launch_shrink(const ShrinkArgs &a, int tiles, cudaStream_t s) {
     if (tiles == 0) return cudaSuccess;
@@ -755,6 +984,30 @@ cudaError_t launch_grad(GradArgs a, int parts, cudaStream_t s) {
     return launch_grad_rp<128>(a, parts, s);
 }
 
+template <typename T, int RB, int NB, bool OF32> cudaError_t launch_small_rn(SmallArgs a, int tiles, cudaStream_t s) {
+    int c = 1;
+    // the widest cluster with two CTAs an SM, or up to 8 where the tiles do not fill the machine once
+    while (c < 8 && tiles * c * 2 <= 2 * device_sm_count()) c *= 2;
+    a.cluster = c;
+    auto kern = small_kernel<T, RB, NB, OF32>;
+    constexpr int smem = 8 * 8 * NB * (32 * RB + 4) * static_cast<int>(sizeof(float));
+    static std::once_flag once;
+    static cudaError_t err = cudaSuccess;
+    if (allow_smem(kern, smem, once, err) != cudaSuccess) return err;
+    return launch_cluster(kern, tiles * c, c, smem, s, static_cast<const SmallArgs>(a));
+}
+template <typename T, int NB, bool OF32> cudaError_t launch_small_n(const SmallArgs &a, int tiles, cudaStream_t s) {
+    if (a.R <= 16) return launch_small_rn<T, 1, NB, OF32>(a, tiles, s);
+    if (a.R <= 32) return launch_small_rn<T, 2, NB, OF32>(a, tiles, s);
+    if (a.R <= 64) return launch_small_rn<T, 4, NB, OF32>(a, tiles, s);
+    return launch_small_rn<T, 8, NB, OF32>(a, tiles, s);
+}
+// most: tokens of the largest tile
+template <typename T, bool OF32> cudaError_t launch_small(const SmallArgs &a, int tiles, int most, cudaStream_t s) {
+    if (tiles == 0) return cudaSuccess;
+    return most <= 8 ? launch_small_n<T, 1, OF32>(a, tiles, s) : launch_small_n<T, 2, OF32>(a, tiles, s);
+}
+
 template <typename T, bool OF32> cudaError_t launch_pass(const PassArgs &a, cudaStream_t s) {
     if (a.n == 0 || (a.out == nullptr && a.u == nullptr)) return cudaSuccess;
     const unsigned y = static_cast<unsigned>(a.N < 4 * kThreads ? 1 : a.N < 16 * kThreads ? 2 : 4);
@@ -766,7 +1019,7 @@ constexpr int64_t kMaxSide = int64_t(1) << 24;
 bool plan_fits(const bt_adapter_plan_info &p, int64_t T) {
     return p.tokens == T && p.adapters >= 1 && p.adapters <= kAdapterMaxAdapters && p.without >= 0 && p.without <= T &&
            p.tiles >= 0 && p.tiles <= T && p.large_tiles >= 0 && p.large_tiles <= p.tiles && p.small_tiles >= 0 &&
-           p.small_tiles <= T && p.parts >= 1 && p.parts <= 2 * kAdapterParts + p.adapters + 1 && p.slots >= 0 &&
+           p.small_tiles <= T && p.small_most >= 0 && p.small_most <= kAdapterSmall && p.parts >= 1 && p.parts <= 2 * kAdapterParts + p.adapters + 1 && p.slots >= 0 &&
            p.slots <= 2 * kAdapterParts;
 }
 bt_status sizes_fit(int64_t T, int64_t K, int64_t N, int64_t R) {
@@ -793,12 +1046,27 @@ struct Forward {
 template <typename T, bool OF32> cudaError_t forward(const Forward &f, cudaStream_t s) {
     const AdapterPlanLayout lay = adapter_plan_layout(f.T, f.info->adapters);
     const Plan plan{f.plan + lay.rows, reinterpret_cast<const AdapterTile *>(f.plan + lay.tiles)};
+    cudaError_t e;
+    if (f.info->small_tiles > 0) {
+        SmallArgs sm = {};
+        sm.plan = Plan{plan.rows, reinterpret_cast<const AdapterTile *>(f.plan + lay.small)};
+        sm.x = f.x; sm.A = f.A; sm.B = f.B; sm.ldx = f.ldx;
+        sm.K = f.K; sm.N = f.N; sm.R = f.R;
+        sm.vec_k = f.K % 8 == 0 && align_of(f.x, f.ldx * 2) == 16 && align_of(f.A, 16) == 16;
+        sm.vec_r = f.R % 8 == 0 && align_of(f.B, 16) == 16;
+        sm.scale = f.scale;
+        sm.base = f.base; sm.base_f32 = f.base_f32; sm.ldb = f.ldb;
+        sm.out = f.out; sm.ldo = f.ldo;
+        sm.u = f.want_u ? f.u : nullptr;
+        e = launch_small<T, OF32>(sm, f.info->small_tiles, f.info->small_most, s);
+        if (e != cudaSuccess) return e;
+    }
     ShrinkArgs sh = {};
     sh.plan = plan;
     sh.x = f.x; sh.ldx = f.ldx; sh.ax = align_of(f.x, f.ldx * 2);
     sh.w = f.A; sh.aw = align_of(f.A, int64_t(f.K) * 2);
     sh.C = f.K; sh.R = f.R; sh.u = f.u;
-    cudaError_t e = launch_shrink<T, false>(sh, f.info->tiles, s);
+    e = launch_shrink<T, false>(sh, f.info->large_tiles, s);
     if (e != cudaSuccess) return e;
     ExpandArgs ex = {};
     ex.plan = plan;
@@ -808,7 +1076,7 @@ template <typename T, bool OF32> cudaError_t forward(const Forward &f, cudaStrea
     ex.out = f.out; ex.ldo = f.ldo;
     ex.wide = align_of(f.out, f.ldo * (OF32 ? 4 : 2)) == 16 &&
               (f.base == nullptr || align_of(f.base, f.ldb * (f.base_f32 ? 4 : 2)) == 16) && f.N % 8 == 0;
-    e = launch_expand<T, false, OF32>(ex, f.info->tiles, s);
+    e = launch_expand<T, false, OF32>(ex, f.info->large_tiles, s);
     if (e != cudaSuccess) return e;
     PassArgs pa = {};
     pa.n = f.info->without;
@@ -827,8 +1095,8 @@ using namespace bt;
 
 extern "C" {
 
-size_t bt_adapter_linear_workspace(int64_t T, int64_t R, int have_u) {
-    if (have_u || sizes_fit(T, 1, 0, R) != BT_OK) return 0;
+size_t bt_adapter_linear_workspace(int64_t T, int64_t R, const bt_adapter_plan_info *info, int have_u) {
+    if (have_u || sizes_fit(T, 1, 0, R) != BT_OK || info == nullptr || info->large_tiles == 0) return 0;
     return round_up256(static_cast<size_t>(T * R) * 4);
 }
 
@@ -852,7 +1120,7 @@ bt_status bt_adapter_linear(const void *x, bt_dtype x_dtype, int64_t ldx, const 
     if (!aligned(x, 2) || !aligned(A, 2) || !aligned(B, 2) || !aligned(scale, 4) || !aligned(plan, 16) || !aligned(u, 4) ||
         !aligned(out, dtype_bytes(out_dtype)) || (base != nullptr && !aligned(base, dtype_bytes(base_dtype))))
         return BT_ERR_ALIGNMENT;
-    const size_t need = bt_adapter_linear_workspace(T, R, u != nullptr);
+    const size_t need = bt_adapter_linear_workspace(T, R, info, u != nullptr);
     if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return BT_ERR_WORKSPACE;
     if (need > 0 && !aligned(workspace, 256)) return BT_ERR_ALIGNMENT;
     Forward f = {};

@@ -81,7 +81,12 @@ bt_status bt_adapter_plan(const int32_t *adapter, int64_t T, int64_t L, void *pl
             const int32_t first = a == 0 ? 0 : last[a - 1], n = last[a] - first;
             if (n == 0 || (n > kAdapterSmallMost) != (pass == 0)) continue;
             r.tiles += even(tiles + r.tiles, static_cast<int32_t>(a), first, n, kAdapterTile);
-            if (pass == 1) r.small_tiles += even(small + r.small_tiles, static_cast<int32_t>(a), first, n, kAdapterSmall);
+            if (pass == 1) {
+                const int32_t k = even(small + r.small_tiles, static_cast<int32_t>(a), first, n, kAdapterSmall);
+                for (int32_t i = 0; i < k; ++i)
+                    if (small[r.small_tiles + i].n > r.small_most) r.small_most = small[r.small_tiles + i].n;
+                r.small_tiles += k;
+            }
             if (n > r.most_tokens) r.most_tokens = n;
             ++r.used;
         }
