@@ -728,7 +728,7 @@ size_t bt_adapter_linear_workspace(int64_t T, int64_t R, const bt_adapter_plan_i
  *   base       device [T, N] of base_dtype (F32 or x's type), or NULL for 0.
  *   out        device [T, N] of out_dtype (F32 or x's type); it may be base
  *              (of the same dtype). A token without an adapter gets cast(base).
- *   u          device fp32 [T, R] out, or NULL: A_a x_t, what the backward
+ *   u          device fp32 [T, R] out, 16-byte aligned, or NULL: A_a x_t, what the backward
  *              needs; 0 for a token without an adapter.
  *   ldx, ldb, ldo  elements from one row to the next, >= K, N, N.
  * A_a x is summed in fp32 and enters the second product as the sum of two
@@ -757,10 +757,10 @@ size_t bt_adapter_linear_backward_workspace(int64_t T, int64_t K, int64_t N, int
  *   grad_A_a = sum over a's tokens of dU_t x_t^T,
  *   grad_B_a = scale[a] * sum over a's tokens of g_t u_t^T, both 0 for an adapter without tokens.
  *   x          device [T, K] BF16, the forward's input; g device [T, N] BF16.
- *   u          device fp32 [T, R], what the forward kept.
+ *   u          device fp32 [T, R], 16-byte aligned, what the forward kept.
  *   grad_base  device [T, K] BF16 (the shared projection's own input gradient)
  *              or NULL for 0; grad_x device [T, K] BF16 out, may be grad_base.
- *   grad_A     device fp32 [L, R, K] out; grad_B device fp32 [L, N, R] out,
+ *   grad_A     device fp32 [L, R, K] out; grad_B device fp32 [L, N, R] out, 16-byte aligned,
  *              both overwritten.
  *   ldx, ldg, ldgb, ldgx  elements from one row to the next.
  * Sums are fp32; dU and u enter the products as the sum of two BF16 values.

@@ -1,0 +1,248 @@
+// Declarations and device helpers shared by the adapters' kernels (see adapter.cu).
+#pragma once
+
+#include <mutex>
+#include <type_traits>
+
+#include "adapter_plan.h"
+#include "bt_device.cuh"
+#include "tc_ptx.cuh"
+
+namespace bt {
+namespace adapter {
+
+constexpr int kThreads = 256;
+constexpr int kStep = 64;                  // long-axis elements of a stage
+constexpr int kXPitch = kStep + 8;         // shared rows of 64 elements: 8 more spread ldmatrix over all banks
+
+// ---------------------------------------------------------------------------
+// Matrix instructions: D (16 x 8, fp32) += A (16 x 16) B (16 x 8).
+// ---------------------------------------------------------------------------
+template <typename T>
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    if constexpr (std::is_same<T, __half>::value) {
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    } else {
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    }
+}
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+
+// ---------------------------------------------------------------------------
+// 16-bit values
+// ---------------------------------------------------------------------------
+template <typename T> __device__ __forceinline__ T to16(float v);
+template <> __device__ __forceinline__ __nv_bfloat16 to16<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+template <> __device__ __forceinline__ __half to16<__half>(float v) { return __float2half_rn(v); }
+template <typename T> __device__ __forceinline__ uint32_t bits16(T v) { return *reinterpret_cast<const uint16_t *>(&v); }
+template <typename T> __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    return bits16(to16<T>(lo)) | (bits16(to16<T>(hi)) << 16);
+}
+template <typename T> __device__ __forceinline__ float2 unpack2(uint32_t w) {
+    if constexpr (std::is_same<T, __half>::value) return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+    else return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+// v as the sum of two 16-bit values, pairwise: hi and lo words of (v0, v1).
+// Infinities keep a zero low part.
+template <typename T> __device__ __forceinline__ void split2(float v0, float v1, uint32_t &hi, uint32_t &lo) {
+    hi = pack2<T>(v0, v1);
+    const float2 h = unpack2<T>(hi);
+    lo = pack2<T>(isinf(h.x) ? 0.0f : v0 - h.x, isinf(h.y) ? 0.0f : v1 - h.y);
+}
+// Half precision reaches 65504 and ends at 2^-24: rows of u are brought to a
+// largest value of about 2^14 by a power of two first (taken out again in fp32).
+template <typename T> __device__ __forceinline__ float row_power(float amax) {
+    if constexpr (std::is_same<T, __half>::value) {
+        if (!(amax > 0.0f) || isinf(amax)) return 1.0f;
+        int e = 14 - ilogbf(amax);
+        e = e > 100 ? 100 : e < -100 ? -100 : e;
+        return exp2f(static_cast<float>(e));
+    }
+    return 1.0f;
+}
+
+// ---------------------------------------------------------------------------
+// Eight consecutive elements of a global row to shared memory (16 bytes, 16-byte
+// aligned), `valid` of them there (<= 0: none), the rest zeros. AL: bytes that
+// every row of the operand starts at a multiple of.
+// ---------------------------------------------------------------------------
+template <int B> __device__ __forceinline__ void cp_async_small(uint32_t dst, const void *src, int bytes) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;\n" ::"r"(dst), "l"(src), "n"(B), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ int clamp_to(int v, int hi) { return v < 0 ? 0 : v > hi ? hi : v; }
+__device__ __forceinline__ void copy8(uint16_t *dst, const uint16_t *src, int valid, int al) {
+    if (al == 16) {
+        cp_async_16(dst, src, clamp_to(valid, 8) * 2);
+    } else if (al >= 4) {
+        const uint32_t d = smem_u32(dst);
+        if (al == 8) {
+            cp_async_small<8>(d, src, clamp_to(valid, 4) * 2);
+            cp_async_small<8>(d + 8, valid > 4 ? src + 4 : src, clamp_to(valid - 4, 4) * 2);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                cp_async_small<4>(d + 4 * i, valid > 2 * i ? src + 2 * i : src, clamp_to(valid - 2 * i, 2) * 2);
+        }
+    } else {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t lo = 2 * i < valid ? __ldg(src + 2 * i) : 0u, hi = 2 * i + 1 < valid ? __ldg(src + 2 * i + 1) : 0u;
+            w[i] = lo | (hi << 16);
+        }
+        *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
+// The rows in the plan's order, and the tiles (or parts) a launch walks.
+struct Plan {
+    const int32_t *rows;
+    const AdapterTile *tiles;
+};
+
+// U[t, :] = s sum_c X[t, c] W[c, :] over tiles of 128 rows. WT = false: W is
+// [R, C] (A, for u), true: [C, R] (B, for dU).
+struct ShrinkArgs {
+    Plan plan;
+    const uint16_t *x;
+    int64_t ldx;
+    int ax, aw;                // alignment of the rows of X and W, bytes
+    const uint16_t *w;         // [L, R, C] or [L, C, R]
+    int C, R;
+    const float *scale;        // NULL: 1
+    float *u;                  // [T, R]
+    int cluster;
+    unsigned int *err;
+    unsigned long long limit_ns;
+};
+cudaError_t launch_shrink(bt_dtype t, bool wt, const ShrinkArgs &a, int tiles, cudaStream_t s);
+
+
+// OUT[t, c] = cast(BASE[t, c] + s sum_r U[t, r] W[r, c]) over tiles of 128 rows.
+// WT = false: W is [C, R] (B, for out), true: [R, C] (A, for dX; bf16 only).
+struct ExpandArgs {
+    Plan plan;
+    const float *u;            // [T, R]
+    const uint16_t *w;         // [L, C, R] or [L, R, C]
+    int aw;
+    int C, R;
+    const float *scale;        // NULL: 1
+    const void *base;          // NULL: 0
+    int base_f32;
+    int64_t ldb;
+    void *out;
+    int64_t ldo;
+    int wide;                  // rows of base and out start at 16-byte multiples
+    int splits;                // column ranges per tile
+};
+cudaError_t launch_expand(bt_dtype t, bool wt, bool out_f32, const ExpandArgs &a, int tiles, cudaStream_t s);
+
+
+// Tokens without an adapter: out = cast(base), u = 0.
+struct PassArgs {
+    const int32_t *rows;
+    int n, N, R;
+    const void *base;
+    int base_f32;
+    int64_t ldb;
+    void *out;                 // NULL: the rows are in place already
+    int64_t ldo;
+    float *u;
+};
+cudaError_t launch_pass(bt_dtype t, bool out_f32, const PassArgs &a, cudaStream_t s);
+
+
+// G[r, c] = s sum_t U[t, r] X[t, c] over every part of the adapters' tokens, for
+// two products in one launch: dA = dU^T x as [R, K], dB = s u^T g as [N, R].
+struct GradProduct {
+    const float *u;            // [T, R]
+    const uint16_t *x;         // [T, C]
+    int64_t ldx;
+    int ax;                    // alignment of the rows of X, bytes
+    int C;
+    int rc;                    // 1: G is [R, C], 0: [C, R]
+    const float *scale;        // NULL: 1
+    float *grad;               // [L, R * C]
+    float *slots;              // the parts' sums: slot i at i * slot_stride
+    int slices;                // column ranges
+};
+struct GradArgs {
+    Plan plan;                 // tiles: the parts
+    GradProduct p[2];
+    int R;
+    int64_t slot_stride;
+    unsigned int *err;
+    unsigned long long limit_ns;
+};
+cudaError_t launch_grad(const GradArgs &a, int parts, cudaStream_t s);
+
+// Adds the parts' sums of every adapter that has several.
+struct SumArgs {
+    const AdapterTile *parts;
+    int n;                     // parts with a slot
+    const float *slots;
+    int64_t slot_stride;
+    int64_t len_a, len_b;      // R * K, R * N: the two gradients lie one after the other in a slot
+    int64_t off_b;             // where the second begins in a slot
+    float *grad_a, *grad_b;
+};
+cudaError_t launch_sum(const SumArgs &a, cudaStream_t s);
+
+// Tiles of up to 16 tokens: the whole adapter in one kernel.
+
+struct SmallArgs {
+    Plan plan;
+    const uint16_t *x, *A, *B;
+    int64_t ldx;
+    int K, N, R;
+    int ax, aa, ab;            // alignment of the rows of x, A and B, bytes
+    int wide;                  // rows of base and out start at 16-byte multiples, N a multiple of 8
+    const float *scale;
+    const void *base;
+    int base_f32;
+    int64_t ldb;
+    void *out;
+    int64_t ldo;
+    float *u;                  // NULL: not wanted
+    int cluster;
+};
+// most: tokens of the fullest tile
+cudaError_t launch_small(bt_dtype t, bool out_f32, const SmallArgs &a, int tiles, int most, cudaStream_t s);
+
+template <typename K> cudaError_t allow_smem(K kern, int bytes, std::once_flag &once, cudaError_t &err) {
+    std::call_once(once, [&] { err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes); });
+    return err;
+}
+
+
+// `grid` CTAs in clusters of c, programmatic dependent launch allowed.
+template <typename K, typename Args>
+cudaError_t launch_cluster(K kern, int grid, int c, int smem, cudaStream_t s, const Args &a) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    attr[0] = pdl_attribute();
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(c);
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kern, a);
+}
+
+}  // namespace adapter
+}  // namespace bt

@@ -342,5 +342,18 @@ __device__ __forceinline__ uint64_t sw128_kmajor_desc(uint32_t saddr) {
     return d;
 }
 
+// The same for an MN-major operand: a row of 128 bytes holds 64 consecutive
+// rows (or columns) of the operand for one k, 8 k's make 1024 bytes; the next
+// 64 rows of the operand lie `atom` bytes further. 16 k's are 2048 bytes.
+__device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t saddr, uint32_t atom) {
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);       // start address
+    d |= static_cast<uint64_t>(atom >> 4) << 16;                // leading byte offset
+    d |= static_cast<uint64_t>(1024u >> 4) << 32;               // stride byte offset
+    d |= static_cast<uint64_t>(1u) << 46;                       // descriptor version
+    d |= static_cast<uint64_t>(2u) << 61;                       // 128-byte swizzle
+    return d;
+}
+
 }  // namespace tc
 }  // namespace bt
