@@ -801,14 +801,14 @@ bt_status bt_adapter_linear_backward(const void *x, int64_t ldx, const void *g, 
  *   teacher_lse device [T] or NULL.
  *   loss        device [T] out. 0 for a row without a slot (a padding token),
  *               whose logits are not used, and for a row with nothing left:
- *               logits of -inf, or of at most -1.7e38 (a mask's lowest value),
- *               only; r likewise. +inf where q_k > 0 and the student's logit
+ *               logits of -inf, or below -1e30 (a mask's lowest value), only; r
+ *               likewise. +inf where q_k > 0 and the student's logit
  *               is -inf. A NaN among a row's logits makes its loss NaN.
  *   stats       device [T, 2] out, or NULL: (lse, r), what
  *               bt_distill_topk_backward needs; zeros for a row without a slot.
  * The sums are fp32, in an order that depends on the sizes only: equal calls
- * give equal results. temperature finite and > 0. S <= 1024; V <= 393216 (F32)
- * or 786432 (16-bit types), T <= 2^24: BT_ERR_UNSUPPORTED beyond. T = 0 does
+ * give equal results. temperature finite and > 0. S <= 1024;
+ * V <= 2^28, T <= 2^24: BT_ERR_UNSUPPORTED beyond. T = 0 does
  * nothing. Errors: INVALID_ARG, ALIGNMENT (a pointer not aligned to its
  * element), UNSUPPORTED, CUDA.
  */

@@ -33,8 +33,7 @@ def test_refusals(call):
                 dict(tau=0.0), dict(tau=-1.0), dict(tau=float("nan")), dict(tau=float("inf")), dict(tau=1e-45),
                 dict(z=None), dict(ids=None), dict(top=None)):
         assert call(**bad) == bt.BT_ERR_INVALID_ARG, bad
-    for bad in (dict(S=1025), dict(V=786433, ld=786433, ldg=786433), dict(dt=bt.BT_F32, V=393217, ld=393217, ldg=393217),
-                dict(T=(1 << 24) + 1)):
+    for bad in (dict(S=1025), dict(V=(1 << 28) + 1, ld=1 << 29, ldg=1 << 29), dict(ld=1 << 37), dict(T=(1 << 24) + 1)):
         if call is _loss:
             bad.pop("ldg", None)
         assert call(**bad) == bt.BT_ERR_UNSUPPORTED, bad
