@@ -715,9 +715,9 @@ size_t bt_adapter_plan_bytes(int64_t T, int64_t L);
 bt_status bt_adapter_plan(const int32_t *adapter, int64_t T, int64_t L, void *plan, size_t plan_bytes,
                           bt_adapter_plan_info *info);
 
-/* Workspace bytes of bt_adapter_linear (0 when u is given, when no adapter has
- * more than 32 tokens, or for sizes out of range). */
-size_t bt_adapter_linear_workspace(int64_t T, int64_t R, const bt_adapter_plan_info *info, int have_u);
+/* Workspace bytes of bt_adapter_linear (0 when no adapter has more than 32
+ * tokens, or for sizes out of range). */
+size_t bt_adapter_linear_workspace(int64_t T, int64_t R, const bt_adapter_plan_info *info);
 
 /*
  * bt_adapter_linear -- the formula above for x [T, K].
@@ -736,7 +736,7 @@ size_t bt_adapter_linear_workspace(int64_t T, int64_t R, const bt_adapter_plan_i
  * rounded once. Any sizes and element alignments are served; rows that start
  * at multiples of 16 bytes (and R a multiple of 8) are faster. 1 <= R <= 128;
  * T, K, N < 2^24. T = 0 or N = 0 does nothing. workspace:
- * bt_adapter_linear_workspace(T, R, info, u != NULL) bytes, 256-byte aligned.
+ * bt_adapter_linear_workspace(T, R, info) bytes, 256-byte aligned.
  * Equal calls give equal results.
  * Errors: INVALID_ARG, ALIGNMENT, WORKSPACE, UNSUPPORTED, CUDA.
  */

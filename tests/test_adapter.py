@@ -137,12 +137,12 @@ def test_forward_refusals():
                 dict(ot=bt.BT_F32, out=8194), dict(base=258, ldb=32, bt_=bt.BT_F32)):
         assert _fwd(**bad) == bt.BT_ERR_ALIGNMENT, bad
     large = dict(T=40, info=_info(T=40))
-    assert _fwd(**large, ws=None) == _fwd(**large, wsb=40 * 32 - 1) == bt.BT_ERR_WORKSPACE
+    assert _fwd(**large, ws=None) == _fwd(**large, wsb=2 * 1280 + 256 - 1) == bt.BT_ERR_WORKSPACE
     assert _fwd(**large, ws=16384 + 16) == bt.BT_ERR_ALIGNMENT
     assert _fwd(T=0, info=_info(T=0), x=None) == _fwd(N=0, out=None) == bt.BT_OK
     few, many = (bt.bt_adapter_plan([0] * n, 2, device="cpu") for n in (4, 40))
-    assert bt.bt_adapter_linear_workspace(40, 8, many) == 1280
-    assert bt.bt_adapter_linear_workspace(40, 8, many, True) == bt.bt_adapter_linear_workspace(40, 129, many) == 0
+    assert bt.bt_adapter_linear_workspace(40, 8, many) == 2 * 1280 + 256         # two 16-bit values of 16 ranks, a power
+    assert bt.bt_adapter_linear_workspace(40, 129, many) == 0
     assert bt.bt_adapter_linear_workspace(4, 8, few) == 0
 
 

@@ -108,7 +108,7 @@ class AdapterPlanInfo(ctypes.Structure):
 _pinfo = ctypes.POINTER(AdapterPlanInfo)
 _c_aplan_bytes = _sig("bt_adapter_plan_bytes", _sz, [_i64, _i64])
 _c_aplan = _sig("bt_adapter_plan", _i, [_p, _i64, _i64, _p, _sz, _pinfo])
-_c_alin_ws = _sig("bt_adapter_linear_workspace", _sz, [_i64, _i64, _pinfo, _i])
+_c_alin_ws = _sig("bt_adapter_linear_workspace", _sz, [_i64, _i64, _pinfo])
 _c_alin = _sig("bt_adapter_linear", _i, [_p, _i, _i64, _p, _p, _p, _p, _pinfo, _i64, _i64, _i64, _i64, _p, _i, _i64,
                                          _p, _i, _i64, _p, _p, _sz, _p])
 _c_abwd_ws = _sig("bt_adapter_linear_backward_workspace", _sz, [_i64, _i64, _i64, _i64, _pinfo])
@@ -715,8 +715,8 @@ def _adapter_args(x, a, b, scale, plan):
     return T, K, N, R
 
 
-def bt_adapter_linear_workspace(T: int, R: int, plan: AdapterPlan, have_u: bool = False) -> int:
-    return int(_c_alin_ws(T, R, plan._ref, 1 if have_u else 0))
+def bt_adapter_linear_workspace(T: int, R: int, plan: AdapterPlan) -> int:
+    return int(_c_alin_ws(T, R, plan._ref))
 
 
 def bt_adapter_linear(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, scale: torch.Tensor, plan: AdapterPlan,
@@ -735,13 +735,11 @@ def bt_adapter_linear(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, scale: 
         out = _empty((T, N), out_dtype if out_dtype is not None else x.dtype if base is None else base.dtype, x.device,
                      stream)
     ldo = _rows(out, "out", (T, N), both if out_dtype is None else (out_dtype,))
-    need = 0
     if u is not None:
         _dense(u, "u", (T, R), torch.float32)
-    else:
-        need = _c_alin_ws(T, R, plan._ref, 0)
-        if need and (workspace is None or workspace.numel() < need):
-            workspace = _empty((need,), torch.uint8, x.device, stream)
+    need = _c_alin_ws(T, R, plan._ref)
+    if need and (workspace is None or workspace.numel() < need):
+        workspace = _empty((need,), torch.uint8, x.device, stream)
     _check(_c_alin(_ptr(x), _DT[x.dtype], ldx, _ptr(a), _ptr(b), _ptr(scale), _ptr(plan.buffer), plan._ref, T, K, N, R,
                    _ptr(base), BT_F32 if base is None else _DT[base.dtype], ldb, _ptr(out), _DT[out.dtype], ldo,
                    _ptr(u), _ptr(workspace), need, _on_stream(stream, x.device)))

@@ -46,6 +46,15 @@ bt_status sizes_fit(int64_t T, int64_t K, int64_t N, int64_t R) {
     return BT_OK;
 }
 
+// u as two 16-bit values a rank, in a workspace: the bytes of both, and where they lie.
+size_t split_bytes(int64_t T, int R) { return 2 * round_up256(static_cast<size_t>(T) * padded_rank(R) * 2); }
+SplitRows split_rows(void *p, int64_t T, int R, bool unpower) {
+    const size_t one = split_bytes(T, R) / 2;
+    uint8_t *b = static_cast<uint8_t *>(p);
+    return SplitRows{reinterpret_cast<uint16_t *>(b), reinterpret_cast<uint16_t *>(b + one),
+                     unpower ? reinterpret_cast<float *>(b + 2 * one) : nullptr};
+}
+
 struct Forward {
     const uint16_t *x, *A, *B;
     int64_t ldx, ldb, ldo;
@@ -57,8 +66,9 @@ struct Forward {
     const void *base;
     int base_f32;
     void *out;
-    float *u;
-    bool want_u, out_f32;
+    float *u;                  // NULL: not wanted
+    void *workspace;
+    bool out_f32;
     bt_dtype type;
     unsigned int *err;
 };
@@ -83,7 +93,7 @@ cudaError_t forward(const Forward &f, cudaStream_t s) {
         sm.scale = f.scale;
         sm.base = f.base; sm.base_f32 = f.base_f32; sm.ldb = f.ldb;
         sm.out = f.out; sm.ldo = f.ldo;
-        sm.u = f.want_u ? f.u : nullptr;
+        sm.u = f.u;
         e = launch_small(t, of32, sm, f.info->small_tiles, f.info->small_most, s);
         if (e != cudaSuccess) return e;
     }
@@ -92,16 +102,18 @@ cudaError_t forward(const Forward &f, cudaStream_t s) {
     sh.x = f.x; sh.ldx = f.ldx; sh.ax = align_of(f.x, f.ldx * 2);
     sh.w = f.A; sh.aw = align_of(f.A, int64_t(f.K) * 2);
     sh.C = f.K; sh.R = f.R; sh.u = f.u;
+    sh.out = split_rows(f.workspace, f.T, f.R, t == BT_F16);
     sh.err = f.err; sh.limit_ns = wait_limit_ns();
     e = launch_shrink(t, false, sh, f.info->large_tiles, s);
     if (e != cudaSuccess) return e;
     ExpandArgs ex = {};
     ex.plan = plan;
-    ex.u = f.u; ex.w = f.B; ex.aw = align_of(f.B, int64_t(f.R) * 2);
+    ex.u = sh.out; ex.w = f.B; ex.aw = align_of(f.B, int64_t(f.R) * 2);
     ex.C = f.N; ex.R = f.R; ex.scale = f.scale;
     ex.base = f.base; ex.base_f32 = f.base_f32; ex.ldb = f.ldb;
     ex.out = f.out; ex.ldo = f.ldo;
     ex.wide = wide;
+    ex.err = f.err; ex.limit_ns = wait_limit_ns();
     e = launch_expand(t, false, of32, ex, f.info->large_tiles, s);
     if (e != cudaSuccess) return e;
     PassArgs pa = {};
@@ -110,7 +122,7 @@ cudaError_t forward(const Forward &f, cudaStream_t s) {
     pa.N = f.N; pa.R = f.R;
     pa.base = f.base; pa.base_f32 = f.base_f32; pa.ldb = f.ldb;
     pa.out = f.out == f.base ? nullptr : f.out; pa.ldo = f.ldo;
-    pa.u = f.want_u ? f.u : nullptr;
+    pa.u = f.u;
     return launch_pass(t, of32, pa, s);
 }
 
@@ -122,9 +134,9 @@ using namespace bt::adapter;
 
 extern "C" {
 
-size_t bt_adapter_linear_workspace(int64_t T, int64_t R, const bt_adapter_plan_info *info, int have_u) {
-    if (have_u || sizes_fit(T, 1, 0, R) != BT_OK || info == nullptr || info->large_tiles == 0) return 0;
-    return round_up256(static_cast<size_t>(T * R) * 4);
+size_t bt_adapter_linear_workspace(int64_t T, int64_t R, const bt_adapter_plan_info *info) {
+    if (sizes_fit(T, 1, 0, R) != BT_OK || info == nullptr || info->large_tiles == 0) return 0;
+    return split_bytes(T, static_cast<int>(R)) + round_up256(static_cast<size_t>(T) * 4);
 }
 
 bt_status bt_adapter_linear(const void *x, bt_dtype x_dtype, int64_t ldx, const void *A, const void *B,
@@ -147,7 +159,7 @@ bt_status bt_adapter_linear(const void *x, bt_dtype x_dtype, int64_t ldx, const 
     if (!aligned(x, 2) || !aligned(A, 2) || !aligned(B, 2) || !aligned(scale, 4) || !aligned(plan, 16) || !aligned(u, 16) ||
         !aligned(out, dtype_bytes(out_dtype)) || (base != nullptr && !aligned(base, dtype_bytes(base_dtype))))
         return BT_ERR_ALIGNMENT;
-    const size_t need = bt_adapter_linear_workspace(T, R, info, u != nullptr);
+    const size_t need = bt_adapter_linear_workspace(T, R, info);
     if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return BT_ERR_WORKSPACE;
     if (need > 0 && !aligned(workspace, 256)) return BT_ERR_ALIGNMENT;
     Forward f = {};
@@ -161,8 +173,8 @@ bt_status bt_adapter_linear(const void *x, bt_dtype x_dtype, int64_t ldx, const 
     f.T = T; f.K = static_cast<int>(K); f.N = static_cast<int>(N); f.R = static_cast<int>(R);
     f.base = base; f.base_f32 = base_dtype == BT_F32;
     f.out = out;
-    f.want_u = u != nullptr;
-    f.u = u != nullptr ? u : static_cast<float *>(workspace);
+    f.u = u;
+    f.workspace = workspace;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     f.out_f32 = out_dtype == BT_F32;
     f.type = x_dtype;
@@ -176,7 +188,7 @@ size_t bt_adapter_linear_backward_workspace(int64_t T, int64_t K, int64_t N, int
                                             const bt_adapter_plan_info *info) {
     if (sizes_fit(T, K, N, R) != BT_OK || info == nullptr || !plan_fits(*info, T)) return 0;
     const size_t slot = round_up256(static_cast<size_t>(R * K) * 4) + round_up256(static_cast<size_t>(R * N) * 4);
-    return round_up256(static_cast<size_t>(T * R) * 4) + static_cast<size_t>(info->slots) * slot;
+    return 2 * split_bytes(T, static_cast<int>(R)) + static_cast<size_t>(info->slots) * slot;
 }
 
 bt_status bt_adapter_linear_backward(const void *x, int64_t ldx, const void *g, int64_t ldg, const float *u,
@@ -218,8 +230,10 @@ bt_status bt_adapter_linear_backward(const void *x, int64_t ldx, const void *g, 
     const AdapterPlanLayout lay = adapter_plan_layout(T, info->adapters);
     const Plan tiles{pw + lay.rows, reinterpret_cast<const AdapterTile *>(pw + lay.tiles)};
     const Plan parts{pw + lay.rows, reinterpret_cast<const AdapterTile *>(pw + lay.parts)};
-    float *du = static_cast<float *>(workspace);
-    float *slots = du + round_up256(static_cast<size_t>(T * R) * 4) / 4;
+    const size_t split = split_bytes(T, static_cast<int>(R));
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    const SplitRows du = split_rows(ws, T, static_cast<int>(R), false), us = split_rows(ws + split, T, static_cast<int>(R), false);
+    float *slots = reinterpret_cast<float *>(ws + 2 * split);
     const int64_t off_b = static_cast<int64_t>(round_up256(static_cast<size_t>(R * K) * 4) / 4);
     const int64_t stride = off_b + static_cast<int64_t>(round_up256(static_cast<size_t>(R * N) * 4) / 4);
     const int ax = align_of(x, ldx * 2), ag = align_of(g, ldg * 2);
@@ -229,7 +243,8 @@ bt_status bt_adapter_linear_backward(const void *x, int64_t ldx, const void *g, 
     sh.x = gp; sh.ldx = ldg; sh.ax = ag;
     sh.w = Bp; sh.aw = align_of(B, R * 2);
     sh.C = static_cast<int>(N); sh.R = static_cast<int>(R);
-    sh.scale = scale; sh.u = du;
+    sh.scale = scale; sh.out = du;
+    sh.given = u; sh.given_out = us;
     sh.err = err; sh.limit_ns = wait_limit_ns();
     cudaError_t e = launch_shrink(BT_BF16, true, sh, info->tiles, s);
     if (e != cudaSuccess) return BT_ERR_CUDA;
@@ -239,7 +254,7 @@ bt_status bt_adapter_linear_backward(const void *x, int64_t ldx, const void *g, 
     gr.R = static_cast<int>(R);
     gr.slot_stride = stride;
     gr.err = err; gr.limit_ns = wait_limit_ns();
-    gr.p[0].u = u; gr.p[0].x = gp; gr.p[0].ldx = ldg; gr.p[0].ax = ag;
+    gr.p[0].u = us; gr.p[0].x = gp; gr.p[0].ldx = ldg; gr.p[0].ax = ag;
     gr.p[0].C = static_cast<int>(N); gr.p[0].rc = 0;
     gr.p[0].scale = scale; gr.p[0].grad = grad_B; gr.p[0].slots = slots + off_b;
     gr.p[1].u = du; gr.p[1].x = xp; gr.p[1].ldx = ldx; gr.p[1].ax = ax;
@@ -250,7 +265,8 @@ bt_status bt_adapter_linear_backward(const void *x, int64_t ldx, const void *g, 
 
     ExpandArgs ex = {};
     ex.plan = tiles;
-    ex.u = du; ex.w = Ap; ex.aw = align_of(A, K * 2);
+    ex.u = du; ex.w = Ap;
+    ex.err = err; ex.limit_ns = wait_limit_ns(); ex.aw = align_of(A, K * 2);
     ex.C = static_cast<int>(K); ex.R = static_cast<int>(R);
     ex.base = grad_base; ex.ldb = ldgb;
     ex.out = grad_x; ex.ldo = ldgx;

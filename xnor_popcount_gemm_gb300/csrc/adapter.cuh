@@ -13,7 +13,6 @@ namespace adapter {
 
 constexpr int kThreads = 256;
 constexpr int kStep = 64;                  // long-axis elements of a stage
-constexpr int kXPitch = kStep + 8;         // shared rows of 64 elements: 8 more spread ldmatrix over all banks
 
 // ---------------------------------------------------------------------------
 // Matrix instructions: D (16 x 8, fp32) += A (16 x 16) B (16 x 8).
@@ -29,14 +28,6 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
                      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
     }
-}
-__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
-}
-__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
 }
 
 // ---------------------------------------------------------------------------
@@ -74,15 +65,30 @@ template <typename T> __device__ __forceinline__ float row_power(float amax) {
 
 // ---------------------------------------------------------------------------
 // Eight consecutive elements of a global row to shared memory (16 bytes, 16-byte
-// aligned), `valid` of them there (<= 0: none), the rest zeros. AL: bytes that
-// every row of the operand starts at a multiple of.
+// aligned), `valid` of them there (<= 0: none), the rest zeros. al: bytes that
+// every row of the operand starts at a multiple of; V16: 16.
 // ---------------------------------------------------------------------------
 template <int B> __device__ __forceinline__ void cp_async_small(uint32_t dst, const void *src, int bytes) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;\n" ::"r"(dst), "l"(src), "n"(B), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ int clamp_to(int v, int hi) { return v < 0 ? 0 : v > hi ? hi : v; }
-__device__ __forceinline__ void copy8(uint16_t *dst, const uint16_t *src, int valid, int al) {
-    if (al == 16) {
+// The words of eight elements at any element address, from the aligned words that hold a valid one.
+__device__ __forceinline__ uint4 load8(const uint16_t *src, int valid) {
+    const int odd = static_cast<int>(reinterpret_cast<uintptr_t>(src) & 2) >> 1;
+    const uint32_t *p = reinterpret_cast<const uint32_t *>(src - odd);
+    uint32_t w[5], r[4];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) w[i] = 2 * i - odd < valid && (i < 4 || odd) ? __ldg(p + i) : 0u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        r[i] = odd ? __funnelshift_r(w[i], w[i + 1], 16) : w[i];
+        const int left = valid - 2 * i;
+        r[i] = left >= 2 ? r[i] : left == 1 ? r[i] & 0xFFFFu : 0u;
+    }
+    return make_uint4(r[0], r[1], r[2], r[3]);
+}
+template <bool V16> __device__ __forceinline__ void copy8(void *dst, const uint16_t *src, int valid, int al) {
+    if (V16 || al == 16) {
         cp_async_16(dst, src, clamp_to(valid, 8) * 2);
     } else if (al >= 4) {
         const uint32_t d = smem_u32(dst);
@@ -95,13 +101,21 @@ __device__ __forceinline__ void copy8(uint16_t *dst, const uint16_t *src, int va
                 cp_async_small<4>(d + 4 * i, valid > 2 * i ? src + 2 * i : src, clamp_to(valid - 2 * i, 2) * 2);
         }
     } else {
-        uint32_t w[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t lo = 2 * i < valid ? __ldg(src + 2 * i) : 0u, hi = 2 * i + 1 < valid ? __ldg(src + 2 * i + 1) : 0u;
-            w[i] = lo | (hi << 16);
-        }
-        *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+        *reinterpret_cast<uint4 *>(dst) = valid > 0 ? load8(src, valid) : make_uint4(0u, 0u, 0u, 0u);
+    }
+}
+
+// The 128-byte swizzle: chunk j (16 bytes) of row r of a tile of 128-byte rows.
+__device__ __forceinline__ uint32_t sw128(int row, int chunk) { return static_cast<uint32_t>(row * 128 + ((chunk ^ (row & 7)) << 4)); }
+constexpr int kAtom = 8192;                // 64 rows of 128 bytes
+
+// A wait for copies or products in flight: if it gives up (which it records),
+// it still lets them land before memory is given back.
+__device__ __forceinline__ void wait_landed(uint64_t &bar, uint32_t parity, uint32_t *abort_flag, unsigned int *err,
+                                            unsigned long long limit_ns) {
+    if (!tc::wait_fast(smem_u32(&bar), parity, abort_flag, err, limit_ns)) {
+        uint32_t drain = 0;
+        tc::wait_bounded(smem_u32(&bar), parity, &drain, err);
     }
 }
 
@@ -110,6 +124,15 @@ struct Plan {
     const int32_t *rows;
     const AdapterTile *tiles;
 };
+
+// u and dU between the products: rows in the plan's order, padded to RP = 16,
+// 32, 64 or 128 ranks, as the sum of two 16-bit values; in half precision times
+// a power of two of the row's own, whose inverse is in unpower.
+struct SplitRows {
+    uint16_t *hi, *lo;         // [T, RP]
+    float *unpower;            // [T], NULL: 1
+};
+inline int padded_rank(int R) { return R <= 16 ? 16 : R <= 32 ? 32 : R <= 64 ? 64 : 128; }
 
 // U[t, :] = s sum_c X[t, c] W[c, :] over tiles of 128 rows. WT = false: W is
 // [R, C] (A, for u), true: [C, R] (B, for dU).
@@ -121,21 +144,23 @@ struct ShrinkArgs {
     const uint16_t *w;         // [L, R, C] or [L, C, R]
     int C, R;
     const float *scale;        // NULL: 1
-    float *u;                  // [T, R]
+    float *u;                  // [T, R] by token; NULL: not wanted
+    SplitRows out;
+    const float *given;        // (WT) [T, R] by token, to be split as well; into given_out
+    SplitRows given_out;
     int cluster;
     unsigned int *err;
     unsigned long long limit_ns;
 };
 cudaError_t launch_shrink(bt_dtype t, bool wt, const ShrinkArgs &a, int tiles, cudaStream_t s);
 
-
 // OUT[t, c] = cast(BASE[t, c] + s sum_r U[t, r] W[r, c]) over tiles of 128 rows.
 // WT = false: W is [C, R] (B, for out), true: [R, C] (A, for dX; bf16 only).
 struct ExpandArgs {
     Plan plan;
-    const float *u;            // [T, R]
+    SplitRows u;
     const uint16_t *w;         // [L, C, R] or [L, R, C]
-    int aw;
+    int aw;                    // alignment of its rows, bytes
     int C, R;
     const float *scale;        // NULL: 1
     const void *base;          // NULL: 0
@@ -143,11 +168,12 @@ struct ExpandArgs {
     int64_t ldb;
     void *out;
     int64_t ldo;
-    int wide;                  // rows of base and out start at 16-byte multiples
+    int wide;                  // rows of base and out start at 16-byte multiples, C a multiple of 8
     int splits;                // column ranges per tile
+    unsigned int *err;
+    unsigned long long limit_ns;
 };
 cudaError_t launch_expand(bt_dtype t, bool wt, bool out_f32, const ExpandArgs &a, int tiles, cudaStream_t s);
-
 
 // Tokens without an adapter: out = cast(base), u = 0.
 struct PassArgs {
@@ -166,7 +192,7 @@ cudaError_t launch_pass(bt_dtype t, bool out_f32, const PassArgs &a, cudaStream_
 // G[r, c] = s sum_t U[t, r] X[t, c] over every part of the adapters' tokens, for
 // two products in one launch: dA = dU^T x as [R, K], dB = s u^T g as [N, R].
 struct GradProduct {
-    const float *u;            // [T, R]
+    SplitRows u;
     const uint16_t *x;         // [T, C]
     int64_t ldx;
     int ax;                    // alignment of the rows of X, bytes
@@ -228,7 +254,7 @@ template <typename K> cudaError_t allow_smem(K kern, int bytes, std::once_flag &
 
 // `grid` CTAs in clusters of c, programmatic dependent launch allowed.
 template <typename K, typename Args>
-cudaError_t launch_cluster(K kern, int grid, int c, int smem, cudaStream_t s, const Args &a) {
+cudaError_t launch_cluster(K kern, int grid, int c, int threads, int smem, cudaStream_t s, const Args &a) {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
     attr[0] = pdl_attribute();
@@ -236,7 +262,7 @@ cudaError_t launch_cluster(K kern, int grid, int c, int smem, cudaStream_t s, co
     attr[1].val.clusterDim.x = static_cast<unsigned>(c);
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.gridDim = dim3(static_cast<unsigned>(grid));
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
     cfg.dynamicSmemBytes = static_cast<size_t>(smem);
     cfg.stream = s;
     cfg.attrs = attr;

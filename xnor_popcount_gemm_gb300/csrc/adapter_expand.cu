@@ -5,16 +5,25 @@ namespace bt {
 namespace adapter {
 namespace {
 
-// A warp keeps its 16 rows of U in registers, as two 16-bit values each, and
-// walks a range of columns, 64 at a time: W's next 64 columns and base's next
-// values arrive while these are multiplied.
-// Bound: base and out. WIDE: their rows start at 16-byte multiples; the results
-// of a quad's four lanes are turned so that a lane loads and stores 16
-// bytes. Otherwise a warp's 16 x 64 results pass through shared memory and
-// every lane walks a column, so that a row's elements still travel together.
-template <int RP, bool WT> constexpr int kWElems = WT ? RP * kXPitch : kStep * (RP + 8);
-constexpr int kTurnPitch = kStep + 4;      // floats of a row of a warp's results
-template <int RP, bool WT, bool WIDE> constexpr int kSmem = 4 * kWElems<RP, WT> + (WIDE ? 0 : kThreads / 32 * 16 * kTurnPitch * 4);
+// A CTA keeps its tile's 128 rows of U in shared memory, as two 16-bit values
+// each, and walks a range of columns, 128 at a time: D (128 rows x 128 columns,
+// fp32, tensor memory, two of them) = U_hi W + U_lo W. While one D is added to
+// base and written, the next is worked out, and the columns of W after that and
+// base's next values arrive.
+// Bound: base and out. D is read in the layout in which a quad's four lanes hold
+// 8 columns of a row. WIDE (rows of base and out start at 16-byte multiples):
+// a quad's words are turned so that a lane loads and stores 16 bytes. Otherwise a
+// warp's 16 x 64 results pass through shared memory and every lane walks a
+// column, so that a row's elements still travel together.
+// (The same with warp-level matrix instructions and U in registers: 8192 x 4096,
+// rank 64, 53 us.)
+constexpr int kTile = 128;                 // columns
+template <int RP> constexpr int kParts = RP <= 64 ? 1 : 2;                  // of 64 ranks
+template <int RP> constexpr int kUBytes = kParts<RP> * 2 * kAtom;           // one of hi, lo: 128 rows of 128 bytes
+template <int RP, bool WT> constexpr int kWBytes = WT ? 2 * RP * 128 : kParts<RP> * 2 * kAtom;
+constexpr int kTurnPitch = 64 + 4;         // floats of a row of a warp's results
+template <int RP, bool WT, bool WIDE> constexpr int kSmem =
+    2 * kUBytes<RP> + 2 * kWBytes<RP, WT> + (WIDE ? 0 : kThreads / 32 * 16 * kTurnPitch * 4) + 1024;
 
 // 4 x 4 transpose of words across a quad: lane t gives word j to lane j's word t.
 __device__ __forceinline__ void quad_transpose(uint32_t (&w)[4], int t) {
@@ -29,241 +38,279 @@ __device__ __forceinline__ void quad_transpose(uint32_t (&w)[4], int t) {
     if (t & 2) { w[0] = p; w[1] = q; } else { w[2] = p; w[3] = q; }
 }
 
-template <typename T, int RP, bool WT, bool OF32, bool WIDE>
+// 64 consecutive fp32 columns of 16 lanes (rows): lane 4g + t gets, of every 8
+// columns, 2t and 2t + 1 of row g (words 0, 1) and of row g + 8 (words 2, 3).
+__device__ __forceinline__ void tmem_ld_16x64(uint32_t addr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(addr));
+}
+
+// FAST: WIDE, and W's rows start at 16-byte multiples.
+template <typename T, int RP, bool WT, bool OF32, bool FAST>
 __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) expand_kernel(const ExpandArgs a) {
-    extern __shared__ __align__(128) uint8_t smem[];
-    uint16_t *wbuf = reinterpret_cast<uint16_t *>(smem);
+    extern __shared__ uint8_t dyn[];
+    __shared__ alignas(8) uint64_t ready[2];
+    __shared__ uint32_t tmem_slot, abort_flag;
+    uint8_t *us = dyn + ((1024u - (smem_u32(dyn) & 1023u)) & 1023u), *wbuf = us + 2 * kUBytes<RP>;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-    float *turn = reinterpret_cast<float *>(smem + 4 * kWElems<RP, WT>) + warp * 16 * kTurnPitch;
-    pdl_launch_dependents();
-    pdl_wait();
+    float *turn = reinterpret_cast<float *>(wbuf + 2 * kWBytes<RP, WT>) + warp * 16 * kTurnPitch;
+    pdl_wait();                                             // before tensor memory is taken, see shrink_kernel
     const AdapterTile tile = a.plan.tiles[blockIdx.x / a.splits];
     const int part = blockIdx.x % a.splits;
-    const int total = (a.C + kStep - 1) / kStep;
+    const int total = (a.C + kTile - 1) / kTile;
     const int s0 = static_cast<int>(static_cast<int64_t>(total) * part / a.splits);
     const int s1 = static_cast<int>(static_cast<int64_t>(total) * (part + 1) / a.splits);
     const uint16_t *w = a.w + static_cast<int64_t>(tile.adapter) * a.R * a.C;
-    auto load = [&](int s) {
-        uint16_t *ws = wbuf + (s & 1) * kWElems<RP, WT>;
-        const int c0 = s * kStep;
+    auto load_w = [&](int s) {
+        uint8_t *ws = wbuf + (s & 1) * kWBytes<RP, WT>;
+        const int c0 = s * kTile;
         if constexpr (!WT) {
-            for (int i = tid; i < kStep * (RP / 8); i += kThreads) {
-                const int k = i / (RP / 8), r = (i % (RP / 8)) * 8, valid = c0 + k < a.C ? a.R - r : 0;
-                copy8(ws + k * (RP + 8) + r, valid > 0 ? w + static_cast<int64_t>(c0 + k) * a.R + r : a.w, valid, a.aw);
+            // 128 columns' rows of RP ranks, 64 to an atom
+#pragma unroll
+            for (int i = 0; i < kTile * (RP / 8) / kThreads; ++i) {
+                const int at = tid + kThreads * i, k = at / (RP / 8), j = at % (RP / 8), valid = c0 + k < a.C ? a.R - 8 * j : 0;
+                copy8<FAST>(ws + (j >> 3) * 2 * kAtom + sw128(k, j & 7), valid > 0 ? w + static_cast<int64_t>(c0 + k) * a.R + 8 * j : a.w,
+                            valid, a.aw);
             }
         } else {
-            for (int i = tid; i < RP * 8; i += kThreads) {
-                const int r = i >> 3, k = (i & 7) * 8, valid = r < a.R ? a.C - c0 - k : 0;
-                copy8(ws + r * kXPitch + k, valid > 0 ? w + static_cast<int64_t>(r) * a.C + c0 + k : a.w, valid, a.aw);
+            // RP rows of 128 columns, 64 to an atom
+#pragma unroll
+            for (int i = 0; i < RP * 16 / kThreads; ++i) {
+                const int at = tid + kThreads * i, r = at >> 4, j = at & 15, valid = r < a.R ? a.C - c0 - 8 * j : 0;
+                copy8<FAST>(ws + (j >> 3) * RP * 128 + sw128(r, j & 7), valid > 0 ? w + static_cast<int64_t>(r) * a.C + c0 + 8 * j : a.w,
+                            valid, a.aw);
             }
         }
     };
-    load(s0);
-    cp_async_commit();
-    const int m0 = warp * 16;
-    int row[2];
-    bool live[2];
+    // U: 128 rows of RP ranks, hi and lo
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const int m = m0 + 8 * h + g;
-        live[h] = m < tile.n;
-        row[h] = a.plan.rows[tile.first + (live[h] ? m : 0)];
+    for (int i = 0; i < 2 * 128 * (RP / 8) / kThreads; ++i) {
+        const int at = tid + kThreads * i, half = at / (128 * (RP / 8)), k = at % (128 * (RP / 8));
+        const int m = k / (RP / 8), j = k % (RP / 8);
+        const uint16_t *u = half ? a.u.lo : a.u.hi;
+        cp_async_16(us + half * kUBytes<RP> + (j >> 3) * 2 * kAtom + sw128(m, j & 7),
+                    m < tile.n ? u + static_cast<int64_t>(tile.first + m) * RP + 8 * j : u, m < tile.n ? 16 : 0);
     }
-    // Base's values of a step. WIDE: 16-bit base as lane t's columns 8t.. of each 32 (one vector per half and row
-    // half); else column `lane` and `lane + 32` of the warp's 16 rows, two 16-bit values a word.
+    load_w(s0);
+    cp_async_commit();
+    if (s0 + 1 < s1) load_w(s0 + 1);
+    cp_async_commit();
+    if (warp == 0) {
+        tc::tmem_alloc(smem_u32(&tmem_slot), 2 * kTile);
+        tc::tmem_relinquish();
+        if (lane == 0) {
+            abort_flag = 0;
+            tc::mbar_init(smem_u32(&ready[0]), 1);
+            tc::mbar_init(smem_u32(&ready[1]), 1);
+            tc::fence_mbar_init();
+        }
+    }
+    // this warp's rows, 32 (warp % 4) .. + 31, in two halves of 16; its 64 columns of a tile
+    const int m0 = (warp & 3) * 32, cw = (warp >> 2) * 64;
+    const float s = a.scale != nullptr ? a.scale[tile.adapter] : 1.0f;
+    int row[2][2];
+    bool live[2][2];
+    float mul[2][2];
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int m = m0 + 16 * b + 8 * h + g, at = tile.first + (m < tile.n ? m : 0);
+            live[b][h] = m < tile.n;
+            row[b][h] = a.plan.rows[at];
+            mul[b][h] = a.u.unpower != nullptr ? s * a.u.unpower[at] : s;
+        }
+    // Base's values of a step. FAST: 16-bit base as lane t's columns 8t.. of each 32; else column `lane` and
+    // `lane + 32` of the warp's rows, two 16-bit values a word.
     const bool b16 = a.base != nullptr && !a.base_f32;
-    uint4 bw[2][2];
-    uint32_t bn[16];
-    const int mrow = __shfl_sync(0xFFFFFFFFu, row[0], (lane & 7) * 4), mrow8 = __shfl_sync(0xFFFFFFFFu, row[1], (lane & 7) * 4);
-    const int lane_row = (lane & 8) ? mrow8 : mrow;         // lane m: row m of the 16
-    const int rows_here = tile.n - m0;
-    auto load_base = [&](int s) {
-        if constexpr (WIDE) {
+    uint4 bw[2][2][2];
+    uint32_t bn[2][16];
+    int lane_row[2];
+    float lane_mul[2];
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {                           // lane m: row m of the 16
+        const int r0 = __shfl_sync(0xFFFFFFFFu, row[b][0], (lane & 7) * 4), r8 = __shfl_sync(0xFFFFFFFFu, row[b][1], (lane & 7) * 4);
+        const float f0 = __shfl_sync(0xFFFFFFFFu, mul[b][0], (lane & 7) * 4), f8 = __shfl_sync(0xFFFFFFFFu, mul[b][1], (lane & 7) * 4);
+        lane_row[b] = (lane & 8) ? r8 : r0;
+        lane_mul[b] = (lane & 8) ? f8 : f0;
+    }
+    auto load_base = [&](int st, int b) {
+        const int c0 = st * kTile + cw;
+        if constexpr (FAST) {
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
-                    const int cj = s * kStep + 32 * q + 8 * t;
-                    bw[h][q] = make_uint4(0u, 0u, 0u, 0u);
-                    if (b16 && live[h] && s < s1 && cj < a.C)
-                        bw[h][q] = ld_stream_v4(static_cast<const uint16_t *>(a.base) + static_cast<int64_t>(row[h]) * a.ldb + cj);
+                    const int cj = c0 + 32 * q + 8 * t;
+                    bw[b][h][q] = make_uint4(0u, 0u, 0u, 0u);
+                    if (b16 && live[b][h] && st < s1 && cj < a.C)
+                        bw[b][h][q] = ld_stream_v4(static_cast<const uint16_t *>(a.base) + static_cast<int64_t>(row[b][h]) * a.ldb + cj);
                 }
         } else if (b16) {
 #pragma unroll
             for (int m = 0; m < 16; ++m) {
-                const uint16_t *b = static_cast<const uint16_t *>(a.base) +
-                                    static_cast<int64_t>(__shfl_sync(0xFFFFFFFFu, lane_row, m)) * a.ldb + s * kStep + lane;
-                const bool ok = m < rows_here && s < s1;
-                const uint32_t lo = ok && s * kStep + lane < a.C ? b[0] : 0u;
-                const uint32_t hi = ok && s * kStep + lane + 32 < a.C ? b[32] : 0u;
-                bn[m] = lo | (hi << 16);
+                const uint16_t *p = static_cast<const uint16_t *>(a.base) +
+                                    static_cast<int64_t>(__shfl_sync(0xFFFFFFFFu, lane_row[b], m)) * a.ldb + c0 + lane;
+                const bool ok = m0 + 16 * b + m < tile.n && st < s1;
+                const uint32_t lo = ok && c0 + lane < a.C ? p[0] : 0u;
+                const uint32_t hi = ok && c0 + lane + 32 < a.C ? p[32] : 0u;
+                bn[b][m] = lo | (hi << 16);
             }
         }
     };
-    load_base(s0);
-    // U's fragments: rows g and g + 8 of the warp's 16
-    float mul[2];
-    uint32_t uh[RP / 16][4], ul[RP / 16][4];
-    const float s = a.scale != nullptr ? a.scale[tile.adapter] : 1.0f;
+    load_base(s0, 0);
+    load_base(s0, 1);
+    // fp32 sums, W MN-major where it is [R, C], N = M = 128
+    constexpr uint32_t kFmt = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
+    constexpr uint32_t kIdesc = (1u << 4) | (kFmt << 7) | (kFmt << 10) | ((WT ? 1u : 0u) << 16) |
+                                ((static_cast<uint32_t>(kTile) >> 3) << 17) | ((128u >> 4) << 24);
+    auto multiply = [&](int st, uint32_t tmem) {            // one thread
+        tc::fence_after_sync();
+        const uint32_t u0 = smem_u32(us), w0 = smem_u32(wbuf + (st & 1) * kWBytes<RP, WT>);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const float *u = a.u + static_cast<int64_t>(row[h]) * a.R;
-        float v[RP / 16][4], amax = 0.0f;
-        if ((a.R & 1) == 0) {
+        for (int half = 0; half < 2; ++half)
 #pragma unroll
-            for (int k = 0; k < RP / 16; ++k)
+            for (int k = 0; k < RP / 16; ++k) {             // 16 ranks
+                const uint64_t da = tc::sw128_kmajor_desc(u0 + half * kUBytes<RP> + (k >> 2) * 2 * kAtom + 32 * (k & 3));
+                const uint64_t db = WT ? tc::sw128_mnmajor_desc(w0 + 2048 * k, RP * 128)
+                                       : tc::sw128_kmajor_desc(w0 + (k >> 2) * 2 * kAtom + 32 * (k & 3));
+                tc::mma_f16(tmem + (st & 1) * kTile, da, db, kIdesc, (half | k) != 0);
+            }
+        tc::mma_commit(smem_u32(&ready[st & 1]));
+    };
+    cp_async_wait<1>();
+    tc::fence_proxy_async_smem();
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    pdl_launch_dependents();
+    const uint32_t tmem = tmem_slot;
+    if (tid == 0) multiply(s0, tmem);
+    for (int st = s0; st < s1; ++st) {
+        // the next columns' product, into the other D, which every warp has read
+        cp_async_wait<0>();
+        tc::fence_proxy_async_smem();
+        tc::fence_before_sync();
+        __syncthreads();
+        if (tid == 0 && st + 1 < s1) multiply(st + 1, tmem);
+        wait_landed(ready[st & 1], static_cast<uint32_t>((st - s0) >> 1) & 1u, &abort_flag, a.err, a.limit_ns);
+        tc::fence_after_sync();
+        if (st + 2 < s1) load_w(st + 2);                    // over the columns just multiplied
+        cp_async_commit();
+        const int c0 = st * kTile + cw;
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int r = 16 * k + 2 * t + 8 * e;
-                    const float2 f = live[h] && r < a.R ? *reinterpret_cast<const float2 *>(u + r) : make_float2(0.0f, 0.0f);
-                    v[k][2 * e] = f.x;
-                    v[k][2 * e + 1] = f.y;
+        for (int b = 0; b < 2; ++b) {
+            uint32_t acc[32];
+            tmem_ld_16x64(tmem + (static_cast<uint32_t>(m0 + 16 * b) << 16) + (st & 1) * kTile + cw, acc);
+            tc::tmem_ld_wait();
+            if constexpr (FAST) {
+                // C a multiple of 8: whole vectors
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int64_t bo = static_cast<int64_t>(row[b][h]) * a.ldb, oo = static_cast<int64_t>(row[b][h]) * a.ldo;
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {           // 32 columns: blocks 4q .. 4q + 3
+                        float2 v[4];                        // base, then base + s * sum in one rounding each
+                        const int cq = c0 + 32 * q;
+                        if (a.base_f32) {
+                            const float *p = static_cast<const float *>(a.base) + bo;
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                const int cj = cq + 8 * j + 2 * t;
+                                v[j] = a.base != nullptr && live[b][h] && cj < a.C ? *reinterpret_cast<const float2 *>(p + cj)
+                                                                                   : make_float2(0.0f, 0.0f);
+                            }
+                        } else {
+                            uint32_t xw[4] = {bw[b][h][q].x, bw[b][h][q].y, bw[b][h][q].z, bw[b][h][q].w};
+                            quad_transpose(xw, t);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) v[j] = unpack2<T>(xw[j]);
+                        }
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            v[j] = make_float2(__fmaf_rn(__uint_as_float(acc[4 * (4 * q + j) + 2 * h]), mul[b][h], v[j].x),
+                                               __fmaf_rn(__uint_as_float(acc[4 * (4 * q + j) + 2 * h + 1]), mul[b][h], v[j].y));
+                        if constexpr (OF32) {
+                            float *o = static_cast<float *>(a.out) + oo;
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                const int cj = cq + 8 * j + 2 * t;
+                                if (live[b][h] && cj < a.C) *reinterpret_cast<float2 *>(o + cj) = v[j];
+                            }
+                        } else {
+                            uint32_t ow[4];
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) ow[j] = pack2<T>(v[j].x, v[j].y);
+                            quad_transpose(ow, t);
+                            const int cj = cq + 8 * t;
+                            if (live[b][h] && cj < a.C)
+                                *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + oo + cj) =
+                                    make_uint4(ow[0], ow[1], ow[2], ow[3]);
+                        }
+                    }
                 }
-        } else {
+            } else {
 #pragma unroll
-            for (int k = 0; k < RP / 16; ++k)
+                for (int h = 0; h < 2; ++h)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int r = 16 * k + 2 * t + (e & 1) + (e >> 1) * 8;
-                    v[k][e] = live[h] && r < a.R ? u[r] : 0.0f;
+                    for (int j = 0; j < 8; ++j)
+                        *reinterpret_cast<uint2 *>(turn + (8 * h + g) * kTurnPitch + 8 * j + 2 * t) =
+                            make_uint2(acc[4 * j + 2 * h], acc[4 * j + 2 * h + 1]);
+                __syncwarp();
+#pragma unroll
+                for (int m = 0; m < 16; ++m) {
+                    const int64_t r = __shfl_sync(0xFFFFFFFFu, lane_row[b], m);
+                    const float ms = __shfl_sync(0xFFFFFFFFu, lane_mul[b], m);
+                    if (m0 + 16 * b + m >= tile.n) continue;
+                    const float2 f = unpack2<T>(b16 ? bn[b][m] : 0u);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int cj = c0 + lane + 32 * e;
+                        if (cj >= a.C) continue;
+                        float v = e ? f.y : f.x;
+                        if (a.base_f32 && a.base != nullptr) v = static_cast<const float *>(a.base)[r * a.ldb + cj];
+                        v = __fmaf_rn(turn[m * kTurnPitch + lane + 32 * e], ms, v);
+                        if constexpr (OF32) static_cast<float *>(a.out)[r * a.ldo + cj] = v;
+                        else static_cast<T *>(a.out)[r * a.ldo + cj] = to16<T>(v);
+                    }
                 }
-        }
-#pragma unroll
-        for (int k = 0; k < RP / 16; ++k)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) amax = fmaxf(amax, fabsf(v[k][e]));
-        amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
-        amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
-        const float p = row_power<T>(amax);
-        mul[h] = s / p;
-#pragma unroll
-        for (int k = 0; k < RP / 16; ++k) {
-            split2<T>(v[k][0] * p, v[k][1] * p, uh[k][h], ul[k][h]);
-            split2<T>(v[k][2] * p, v[k][3] * p, uh[k][2 + h], ul[k][2 + h]);
+                __syncwarp();
+            }
+            load_base(st + 1, b);
         }
     }
-    const float mq = __shfl_sync(0xFFFFFFFFu, mul[0], (lane & 7) * 4), mq8 = __shfl_sync(0xFFFFFFFFu, mul[1], (lane & 7) * 4);
-    const float lane_mul = (lane & 8) ? mq8 : mq;
-    for (int st = s0; st < s1; ++st) {
-        cp_async_wait<0>();
-        __syncthreads();
-        if (st + 1 < s1) load(st + 1);
-        cp_async_commit();
-        const uint16_t *ws = wbuf + (st & 1) * kWElems<RP, WT>;
-        float acc[8][4];
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[j][e] = 0.0f;
-#pragma unroll
-        for (int k = 0; k < RP / 16; ++k)
-#pragma unroll
-            for (int j = 0; j < 8; j += 2) {
-                uint32_t bf[4];
-                if constexpr (!WT)
-                    ldsm4(bf, smem_u32(ws + (8 * j + (lane >> 4) * 8 + (lane & 7)) * (RP + 8) + 16 * k + ((lane >> 3) & 1) * 8));
-                else
-                    ldsm4t(bf, smem_u32(ws + (16 * k + (lane & 15)) * kXPitch + 8 * j + (lane >> 4) * 8));
-                mma<T>(acc[j], uh[k], bf[0], bf[1]);
-                mma<T>(acc[j + 1], uh[k], bf[2], bf[3]);
-                mma<T>(acc[j], ul[k], bf[0], bf[1]);
-                mma<T>(acc[j + 1], ul[k], bf[2], bf[3]);
-            }
-        const int c0 = st * kStep;
-        if constexpr (WIDE) {
-            // C a multiple of 8: whole vectors
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int64_t bo = static_cast<int64_t>(row[h]) * a.ldb, oo = static_cast<int64_t>(row[h]) * a.ldo;
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {               // 32 columns: blocks 4q .. 4q + 3
-                    float2 v[4];                            // base, then base + s * sum in one rounding each
-                    const int cq = c0 + 32 * q;
-                    if (a.base_f32) {
-                        const float *b = static_cast<const float *>(a.base) + bo;
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const int cj = cq + 8 * j + 2 * t;
-                            v[j] = a.base != nullptr && live[h] && cj < a.C ? *reinterpret_cast<const float2 *>(b + cj)
-                                                                            : make_float2(0.0f, 0.0f);
-                        }
-                    } else {
-                        uint32_t xw[4] = {bw[h][q].x, bw[h][q].y, bw[h][q].z, bw[h][q].w};
-                        quad_transpose(xw, t);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) v[j] = unpack2<T>(xw[j]);
-                    }
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        v[j] = make_float2(__fmaf_rn(acc[4 * q + j][2 * h], mul[h], v[j].x),
-                                           __fmaf_rn(acc[4 * q + j][2 * h + 1], mul[h], v[j].y));
-                    if constexpr (OF32) {
-                        float *o = static_cast<float *>(a.out) + oo;
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const int cj = cq + 8 * j + 2 * t;
-                            if (live[h] && cj < a.C) *reinterpret_cast<float2 *>(o + cj) = v[j];
-                        }
-                    } else {
-                        uint32_t ow[4];
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) ow[j] = pack2<T>(v[j].x, v[j].y);
-                        quad_transpose(ow, t);
-                        const int cj = cq + 8 * t;
-                        if (live[h] && cj < a.C)
-                            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + oo + cj) =
-                                make_uint4(ow[0], ow[1], ow[2], ow[3]);
-                    }
-                }
-            }
-            load_base(st + 1);
-        } else {
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    *reinterpret_cast<float2 *>(turn + (8 * h + g) * kTurnPitch + 8 * j + 2 * t) =
-                        make_float2(acc[j][2 * h], acc[j][2 * h + 1]);
-            __syncwarp();
-#pragma unroll
-            for (int m = 0; m < 16; ++m) {
-                const int64_t r = __shfl_sync(0xFFFFFFFFu, lane_row, m);
-                const float ms = __shfl_sync(0xFFFFFFFFu, lane_mul, m);
-                if (m >= rows_here) continue;
-                const float2 f = unpack2<T>(b16 ? bn[m] : 0u);
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int cj = c0 + lane + 32 * e;
-                    if (cj >= a.C) continue;
-                    float v = e ? f.y : f.x;
-                    if (a.base_f32 && a.base != nullptr) v = static_cast<const float *>(a.base)[r * a.ldb + cj];
-                    v = __fmaf_rn(turn[m * kTurnPitch + lane + 32 * e], ms, v);
-                    if constexpr (OF32) static_cast<float *>(a.out)[r * a.ldo + cj] = v;
-                    else static_cast<T *>(a.out)[r * a.ldo + cj] = to16<T>(v);
-                }
-            }
-            __syncwarp();
-            load_base(st + 1);
-        }
+    cp_async_wait<0>();
+    tc::fence_before_sync();
+    __syncthreads();
+    if (warp == 0) {
+        tc::fence_after_sync();
+        tc::tmem_dealloc(tmem, 2 * kTile);
     }
 }
 
-template <typename T, int RP, bool WT, bool OF32, bool WIDE> cudaError_t launch_rp(const ExpandArgs &a, int tiles, cudaStream_t s) {
-    auto kern = expand_kernel<T, RP, WT, OF32, WIDE>;
-    constexpr int smem = kSmem<RP, WT, WIDE>;
+template <typename T, int RP, bool WT, bool OF32, bool FAST> cudaError_t launch_rp(const ExpandArgs &a, int tiles, cudaStream_t s) {
+    auto kern = expand_kernel<T, RP, WT, OF32, FAST>;
+    constexpr int smem = kSmem<RP, WT, FAST>;
     static std::once_flag once;
     static cudaError_t err = cudaSuccess;
     if (allow_smem(kern, smem, once, err) != cudaSuccess) return err;
     return launch_pdl_smem(kern, dim3(static_cast<unsigned>(tiles * a.splits)), dim3(kThreads), smem, s, a);
 }
-template <typename T, bool WT, bool OF32, bool WIDE> cudaError_t launch_r(const ExpandArgs &a, int tiles, cudaStream_t s) {
-    if (a.R <= 16) return launch_rp<T, 16, WT, OF32, WIDE>(a, tiles, s);
-    if (a.R <= 32) return launch_rp<T, 32, WT, OF32, WIDE>(a, tiles, s);
-    if (a.R <= 64) return launch_rp<T, 64, WT, OF32, WIDE>(a, tiles, s);
-    return launch_rp<T, 128, WT, OF32, WIDE>(a, tiles, s);
+template <typename T, bool WT, bool OF32, bool FAST> cudaError_t launch_r(const ExpandArgs &a, int tiles, cudaStream_t s) {
+    if (a.R <= 16) return launch_rp<T, 16, WT, OF32, FAST>(a, tiles, s);
+    if (a.R <= 32) return launch_rp<T, 32, WT, OF32, FAST>(a, tiles, s);
+    if (a.R <= 64) return launch_rp<T, 64, WT, OF32, FAST>(a, tiles, s);
+    return launch_rp<T, 128, WT, OF32, FAST>(a, tiles, s);
 }
 template <typename T, bool WT, bool OF32> cudaError_t launch_t(const ExpandArgs &a, int tiles, cudaStream_t s) {
-    return a.wide ? launch_r<T, WT, OF32, true>(a, tiles, s) : launch_r<T, WT, OF32, false>(a, tiles, s);
+    return a.wide && a.aw == 16 ? launch_r<T, WT, OF32, true>(a, tiles, s) : launch_r<T, WT, OF32, false>(a, tiles, s);
 }
 
 template <typename T, bool OF32> __global__ void __launch_bounds__(kThreads) pass_kernel(const PassArgs a) {
@@ -293,7 +340,7 @@ template <typename T> cudaError_t launch_pass_t(bool out_f32, const PassArgs &a,
 cudaError_t launch_expand(bt_dtype t, bool wt, bool out_f32, const ExpandArgs &args, int tiles, cudaStream_t s) {
     if (tiles == 0) return cudaSuccess;
     ExpandArgs a = args;
-    const int steps = (a.C + kStep - 1) / kStep;
+    const int steps = (a.C + kTile - 1) / kTile;
     // two CTAs an SM, and twice that many so that the last ones end close together
     int splits = (4 * device_sm_count() + tiles - 1) / tiles;
     if (splits > steps) splits = steps;

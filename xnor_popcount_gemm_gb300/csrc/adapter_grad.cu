@@ -8,37 +8,44 @@ namespace {
 // A CTA takes 128 columns of x (or g) and a part of one adapter's tokens, 64 at
 // a time: D (128 columns x rank, fp32, tensor memory) += X^T (U_hi + U_lo). Both
 // operands lie as they arrive, a token a row, and go to the tensor cores
-// MN-major: nothing is transposed. U is fp32 in memory and is split into its
-// two 16-bit values on the way to shared memory, a stage ahead. A part that is
-// its adapter's only one writes the gradient; the others write their sums to
-// the workspace, which sum_kernel adds up in order. Both products run in one
-// launch, so that neither leaves the machine half empty at its end.
+// MN-major: nothing is transposed. Eight warps gather, a ninth issues the
+// products. A part that is its adapter's only one writes the gradient; the
+// others write their sums to the workspace, which sum_kernel adds up in order.
+// Both products run in one launch, so that neither leaves the machine half
+// empty at its end.
 using T = __nv_bfloat16;
 constexpr int kCols = 128, kTok = 64;
-constexpr int kAtom = 8192;                                 // 64 tokens' rows of 128 bytes
-constexpr int kXBytes = 2 * kAtom;                          // 128 columns
-constexpr int kStages = 4;
+constexpr int kWarps = 9;
+constexpr int kXBytes = 2 * kAtom;                          // 64 tokens x 128 columns
 template <int RP> constexpr int kUPart = (RP <= 64 ? 1 : 2) * kAtom;       // one of hi, lo
-template <int RP> constexpr int kSmem = kStages * kXBytes + 2 * 2 * kUPart<RP> + 1024;
+template <int RP> constexpr int kStageBytes = kXBytes + 2 * kUPart<RP>;
+template <int RP> constexpr int kStages = RP <= 64 ? 3 : 4;
+template <int RP> constexpr int kSmem = kStages<RP> * kStageBytes<RP> + 1024;
 
-__device__ __forceinline__ uint32_t sw128(int row, int chunk) { return static_cast<uint32_t>(row * 128 + ((chunk ^ (row & 7)) << 4)); }
-
-template <int RP>
-__global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) grad_kernel(const GradArgs a) {
+template <int RP, bool V16>
+__global__ void __launch_bounds__(32 * kWarps, RP <= 64 ? 2 : 1) grad_kernel(const GradArgs a) {
     extern __shared__ uint8_t dyn[];
-    __shared__ alignas(8) uint64_t bars[kStages];
+    constexpr int S = kStages<RP>, kTmem = RP < 32 ? 32 : RP;
+    __shared__ alignas(8) uint64_t full[S], empty[S], done;
     __shared__ uint32_t tmem_slot, abort_flag;
-    constexpr int kTmem = RP < 32 ? 32 : RP;
     uint8_t *smem = dyn + ((1024u - (smem_u32(dyn) & 1023u)) & 1023u);
-    uint8_t *ubase = smem + kStages * kXBytes;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int both = a.p[0].slices + a.p[1].slices;
+    const int sl = static_cast<int>(blockIdx.x % both);
+    const GradProduct &p = a.p[sl < a.p[0].slices ? 0 : 1];
+    const int c0 = (sl < a.p[0].slices ? sl : sl - a.p[0].slices) * kCols;
     pdl_wait();                                             // before tensor memory is taken, see shrink_kernel
-    if (warp == 0) {
+    const AdapterTile part = a.plan.tiles[blockIdx.x / both];
+    if (warp == kWarps - 1) {
         tc::tmem_alloc(smem_u32(&tmem_slot), kTmem);
         tc::tmem_relinquish();
         if (lane == 0) {
             abort_flag = 0;
-            for (int i = 0; i < kStages; ++i) tc::mbar_init(smem_u32(&bars[i]), 1);
+            for (int i = 0; i < S; ++i) {
+                tc::mbar_init(smem_u32(&full[i]), kWarps - 1);
+                tc::mbar_init(smem_u32(&empty[i]), 1);
+            }
+            tc::mbar_init(smem_u32(&done), 1);
             tc::fence_mbar_init();
         }
     }
@@ -47,163 +54,110 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) grad_kernel(const 
     tc::fence_after_sync();
     pdl_launch_dependents();
     const uint32_t tmem = tmem_slot;
-
-    const int both = a.p[0].slices + a.p[1].slices;
-    const AdapterTile part = a.plan.tiles[blockIdx.x / both];
-    const int sl = static_cast<int>(blockIdx.x % both);
-    const GradProduct &p = a.p[sl < a.p[0].slices ? 0 : 1];
-    const int c0 = (sl < a.p[0].slices ? sl : sl - a.p[0].slices) * kCols;
-    const int32_t *rows = a.plan.rows + part.first;
     const int n = (part.n + kTok - 1) / kTok;
-    // this thread's chunks of X: column chunk tid % 16 of tokens tid / 16 + 16 i
-    const int cj = tid & 15, ct = tid >> 4;
-    int xrow[4];
-    auto fetch_rows = [&](int s) {
+    if (warp < kWarps - 1) {
+        const int32_t *rows = a.plan.rows + part.first;
+        // this thread's chunks of X: column chunk tid % 16 of tokens tid / 16 + 16 i
+        const int cj = tid & 15, ct = tid >> 4;
+        int xrow[4];
+        auto fetch_rows = [&](int s) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int at = s * kTok + ct + 16 * i;
-            xrow[i] = at < part.n ? rows[at] : -1;
-        }
-    };
-    auto load_x = [&](int s) {
-        uint8_t *xs = smem + (s % kStages) * kXBytes + (cj >> 3) * kAtom;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int valid = xrow[i] >= 0 ? p.C - c0 - 8 * cj : 0;
-            copy8(reinterpret_cast<uint16_t *>(xs + sw128(ct + 16 * i, cj & 7)),
-                  valid > 0 ? p.x + static_cast<int64_t>(xrow[i]) * p.ldx + c0 + 8 * cj : p.x, valid, p.ax);
-        }
-    };
-    // U: thread (token tid / 4, a quarter of the ranks), pairs of ranks
-    constexpr int UV = RP / 8;
-    const int utok = tid >> 2, ur = (tid & 3) * 2;
-    float2 uv[UV];
-    int urow;
-    auto fetch_urow = [&](int s) {
-        const int at = s * kTok + utok;
-        urow = at < part.n ? rows[at] : -1;
-    };
-    auto load_u = [&]() {
-        const float *u = p.u + static_cast<int64_t>(urow < 0 ? 0 : urow) * a.R;
-        if ((a.R & 1) == 0) {
-#pragma unroll
-            for (int i = 0; i < UV; ++i) {
-                const int r = ur + 8 * i;
-                uv[i] = urow >= 0 && r < a.R ? *reinterpret_cast<const float2 *>(u + r) : make_float2(0.0f, 0.0f);
+            for (int i = 0; i < 4; ++i) {
+                const int at = s * kTok + ct + 16 * i;
+                xrow[i] = at < part.n ? rows[at] : -1;
             }
-        } else {
+        };
+        const int left = p.C - c0 - 8 * cj;
+        const uint16_t *x = p.x + c0 + 8 * cj;
+        fetch_rows(0);
+        for (int s = 0; s < n + S - 1; ++s) {
+            if (s < n) {
+                if (s >= S) wait_landed(empty[s % S], static_cast<uint32_t>(s / S - 1) & 1u, &abort_flag, a.err, a.limit_ns);
+                uint8_t *xs = smem + (s % S) * kStageBytes<RP>, *us = xs + kXBytes;
 #pragma unroll
-            for (int i = 0; i < UV; ++i) {
-                const int r = ur + 8 * i;
-                uv[i].x = urow >= 0 && r < a.R ? u[r] : 0.0f;
-                uv[i].y = urow >= 0 && r + 1 < a.R ? u[r + 1] : 0.0f;
+                for (int i = 0; i < 4; ++i) {
+                    const int valid = xrow[i] >= 0 ? left : 0;
+                    copy8<V16>(xs + (cj >> 3) * kAtom + sw128(ct + 16 * i, cj & 7),
+                               valid > 0 ? x + static_cast<int64_t>(xrow[i]) * p.ldx : p.x, valid, p.ax);
+                }
+                fetch_rows(s + 1);
+                // U: its two parts, RP / 8 chunks of 64 tokens
+#pragma unroll
+                for (int i = 0; i < 2 * kTok * (RP / 8) / 256; ++i) {
+                    const int at = tid + 256 * i, part2 = at / (kTok * (RP / 8)), k = at % (kTok * (RP / 8));
+                    const int tok = k / (RP / 8), j = k % (RP / 8), row = s * kTok + tok;
+                    const uint16_t *u = part2 ? p.u.lo : p.u.hi;
+                    cp_async_16(us + part2 * kUPart<RP> + (j >> 3) * kAtom + sw128(tok, j & 7),
+                                row < part.n ? u + static_cast<int64_t>(part.first + row) * RP + 8 * j : u, row < part.n ? 16 : 0);
+                }
+            }
+            cp_async_commit();
+            if (s >= S - 1) {                               // the stage asked for S - 1 turns ago has landed
+                cp_async_wait<S - 1>();
+                tc::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(smem_u32(&full[(s - (S - 1)) % S]));
             }
         }
-    };
-    auto store_u = [&](int s) {
-        uint8_t *hi = ubase + (s & 1) * 2 * kUPart<RP>, *lo = hi + kUPart<RP>;
-#pragma unroll
-        for (int i = 0; i < UV; ++i) {
-            uint32_t h, l;
-            split2<T>(uv[i].x, uv[i].y, h, l);
-            const uint32_t off = (i >> 3) * kAtom + sw128(utok, i & 7) + 2 * ur;
-            *reinterpret_cast<uint32_t *>(hi + off) = h;
-            *reinterpret_cast<uint32_t *>(lo + off) = l;
-        }
-    };
-    auto wait_mma = [&](int s) {
-        const uint32_t bar = smem_u32(&bars[s % kStages]), parity = static_cast<uint32_t>(s / kStages) & 1u;
-        if (!tc::wait_fast(bar, parity, &abort_flag, a.err, a.limit_ns)) {
-            uint32_t drain = 0;                             // recorded; the products in flight must still land
-            tc::wait_bounded(bar, parity, &drain, a.err);
-        }
-    };
-    // fp32 sums, bf16 operands, both MN-major, N = RP, M = 128
-    constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 15) | (1u << 16) |
-                                ((static_cast<uint32_t>(RP) >> 3) << 17) | ((128u >> 4) << 24);
-#pragma unroll
-    for (int s = 0; s < kStages - 1; ++s) {
-        if (s < n) {
-            fetch_rows(s);
-            load_x(s);
-        }
-        cp_async_commit();
-    }
-    if (n > 0) {
-        fetch_urow(0);
-        load_u();
-        store_u(0);
-        fetch_urow(1);
-        load_u();
-        fetch_urow(2);
-    }
-    fetch_rows(kStages - 1);
-    for (int s = 0; s < n; ++s) {
-        cp_async_wait<kStages - 2>();
-        tc::fence_proxy_async_smem();
-        __syncthreads();
-        if (tid == 0) {
+    } else if (lane == 0) {
+        // fp32 sums, bf16 operands, both MN-major, N = RP, M = 128
+        constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 15) | (1u << 16) |
+                                    ((static_cast<uint32_t>(RP) >> 3) << 17) | ((128u >> 4) << 24);
+        for (int s = 0; s < n; ++s) {
+            wait_landed(full[s % S], static_cast<uint32_t>(s / S) & 1u, &abort_flag, a.err, a.limit_ns);
             tc::fence_after_sync();
-            const uint32_t xs = smem_u32(smem + (s % kStages) * kXBytes);
-            const uint32_t hi = smem_u32(ubase + (s & 1) * 2 * kUPart<RP>), lo = hi + kUPart<RP>;
+            const uint32_t xs = smem_u32(smem + (s % S) * kStageBytes<RP>), hi = xs + kXBytes, lo = hi + kUPart<RP>;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {                   // 16 tokens: 16 rows of either operand
                 const uint64_t da = tc::sw128_mnmajor_desc(xs + 2048 * k, kAtom);
                 tc::mma_f16(tmem, da, tc::sw128_mnmajor_desc(hi + 2048 * k, kAtom), kIdesc, (s | k) != 0);
                 tc::mma_f16(tmem, da, tc::sw128_mnmajor_desc(lo + 2048 * k, kAtom), kIdesc, 1);
             }
-            tc::mma_commit(smem_u32(&bars[s % kStages]));
+            tc::mma_commit(smem_u32(&empty[s % S]));
         }
-        if (s > 0) wait_mma(s - 1);                         // X's slot and U's buffer are free again
-        if (s + kStages - 1 < n) {
-            load_x(s + kStages - 1);
-            fetch_rows(s + kStages);
-        }
-        cp_async_commit();
-        if (s + 1 < n) {
-            store_u(s + 1);
-            load_u();
-            fetch_urow(s + 3);
-        }
+        if (n > 0) tc::mma_commit(smem_u32(&done));
+        else tc::mbar_arrive(smem_u32(&done));
     }
-    cp_async_wait<0>();
-    if (n > 0) wait_mma(n - 1);
+    __syncwarp();
+    wait_landed(done, 0, &abort_flag, a.err, a.limit_ns);
     tc::fence_after_sync();
-    const float scale = p.scale != nullptr ? p.scale[part.adapter] : 1.0f;
-    float *out = part.slot >= 0 ? p.slots + part.slot * a.slot_stride : p.grad + static_cast<int64_t>(part.adapter) * a.R * p.C;
-    const int col = c0 + (warp & 3) * 32 + lane;            // the accumulator's lane
-    for (int r0 = (warp >> 2) * 32; r0 < RP; r0 += 64) {
-        uint32_t v[32];
-        if (n > 0) {
-            tc::tmem_ld32(tmem + (static_cast<uint32_t>(warp & 3) << 21) + r0, v);
-            tc::tmem_ld_wait();
-        } else {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = 0u;
-        }
-        if (col < p.C) {
-            if (p.rc) {
-#pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    if (r0 + i < a.R) out[static_cast<int64_t>(r0 + i) * p.C + col] = __uint_as_float(v[i]) * scale;
-            } else if ((a.R & 3) == 0) {
-                float *o = out + static_cast<int64_t>(col) * a.R + r0;
-#pragma unroll
-                for (int i = 0; i < 32; i += 4)
-                    if (r0 + i < a.R)
-                        *reinterpret_cast<float4 *>(o + i) =
-                            make_float4(__uint_as_float(v[i]) * scale, __uint_as_float(v[i + 1]) * scale,
-                                        __uint_as_float(v[i + 2]) * scale, __uint_as_float(v[i + 3]) * scale);
+    if (warp < kWarps - 1) {
+        const float scale = p.scale != nullptr ? p.scale[part.adapter] : 1.0f;
+        float *out = part.slot >= 0 ? p.slots + part.slot * a.slot_stride : p.grad + static_cast<int64_t>(part.adapter) * a.R * p.C;
+        const int col = c0 + (warp & 3) * 32 + lane;        // the accumulator's lane
+        for (int r0 = (warp >> 2) * 32; r0 < RP; r0 += 64) {
+            uint32_t v[32];
+            if (n > 0) {
+                tc::tmem_ld32(tmem + (static_cast<uint32_t>(warp & 3) << 21) + r0, v);
+                tc::tmem_ld_wait();
             } else {
 #pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    if (r0 + i < a.R) out[static_cast<int64_t>(col) * a.R + r0 + i] = __uint_as_float(v[i]) * scale;
+                for (int i = 0; i < 32; ++i) v[i] = 0u;
+            }
+            if (col < p.C) {
+                if (p.rc) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (r0 + i < a.R) out[static_cast<int64_t>(r0 + i) * p.C + col] = __uint_as_float(v[i]) * scale;
+                } else if ((a.R & 3) == 0) {
+                    float *o = out + static_cast<int64_t>(col) * a.R + r0;
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4)
+                        if (r0 + i < a.R)
+                            *reinterpret_cast<float4 *>(o + i) =
+                                make_float4(__uint_as_float(v[i]) * scale, __uint_as_float(v[i + 1]) * scale,
+                                            __uint_as_float(v[i + 2]) * scale, __uint_as_float(v[i + 3]) * scale);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (r0 + i < a.R) out[static_cast<int64_t>(col) * a.R + r0 + i] = __uint_as_float(v[i]) * scale;
+                }
             }
         }
     }
     tc::fence_before_sync();
     __syncthreads();
-    if (warp == 0) {
+    if (warp == kWarps - 1) {
         tc::fence_after_sync();
         tc::tmem_dealloc(tmem, kTmem);
     }
@@ -231,13 +185,16 @@ __global__ void __launch_bounds__(kThreads) sum_kernel(const SumArgs a) {
     }
 }
 
-template <int RP> cudaError_t launch_rp(const GradArgs &a, int parts, cudaStream_t s) {
-    auto kern = grad_kernel<RP>;
+template <int RP, bool V16> cudaError_t launch_v(const GradArgs &a, int parts, cudaStream_t s) {
+    auto kern = grad_kernel<RP, V16>;
     static std::once_flag once;
     static cudaError_t err = cudaSuccess;
     if (allow_smem(kern, kSmem<RP>, once, err) != cudaSuccess) return err;
-    return launch_pdl_smem(kern, dim3(static_cast<unsigned>(parts * (a.p[0].slices + a.p[1].slices))), dim3(kThreads),
+    return launch_pdl_smem(kern, dim3(static_cast<unsigned>(parts * (a.p[0].slices + a.p[1].slices))), dim3(32 * kWarps),
                            kSmem<RP>, s, a);
+}
+template <int RP> cudaError_t launch_rp(const GradArgs &a, int parts, cudaStream_t s) {
+    return a.p[0].ax == 16 && a.p[1].ax == 16 ? launch_v<RP, true>(a, parts, s) : launch_v<RP, false>(a, parts, s);
 }
 
 }  // namespace

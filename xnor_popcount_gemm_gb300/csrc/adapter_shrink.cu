@@ -7,16 +7,16 @@ namespace {
 
 // A cluster of 1 to 8 CTAs shares a tile of 128 rows, each reducing a piece of
 // the long axis on the 5th-generation tensor cores: M = 128 rows, N = the
-// rank, fp32 sums in tensor memory. The rows are gathered by 16-byte
-// asynchronous copies into the 128-byte swizzle (row r's chunk j lies at j ^ (r
-// mod 8)); W needs no transposing for either of its two layouts, the
-// descriptors take it K-major or MN-major. The pieces are added in a fixed order
-// through distributed shared memory: u leaves once, no partial sum touches memory.
+// rank, fp32 sums in tensor memory. Eight warps gather the rows by 16-byte
+// asynchronous copies into the 128-byte swizzle, a ninth issues the products;
+// stages are handed over by mbarriers, so that no warp waits for another's
+// copies. W needs no transposing for either of its two layouts, the descriptors
+// take it K-major or MN-major. The pieces are added in a fixed order through
+// distributed shared memory: u leaves once, no partial sum touches memory.
 //
-// Bound: the long rows, read once. With the warp-level instructions this
-// kernel spent as long in the tensor pipe as in reading the rows at rank 64
-// (8192 x 11008: 66 us, 2.7 TB/s).
-constexpr int kAtom = 8192;                                 // 64 rows of 128 bytes
+// Bound: the long rows, read once. (Warp-level matrix instructions kept the
+// tensor pipe as long as the rows' reading at rank 64.)
+constexpr int kWarps = 9;
 constexpr int kXBytes = 2 * kAtom;
 template <int RP, bool WT> constexpr int kWBytes = WT ? (RP <= 64 ? 1 : 2) * kAtom : RP * 128;
 template <int RP, bool WT> constexpr int kStageBytes = kXBytes + kWBytes<RP, WT>;
@@ -26,99 +26,120 @@ template <int RP, bool WT> constexpr int kSmem = kStages<RP, WT> * kStageBytes<R
 static_assert(kAdapterTile * kSumPitch<128> * 4 <= kStages<128, false> * kStageBytes<128, false>, "sums take the ring's place");
 static_assert(kAdapterTile * kSumPitch<128> * 4 <= kStages<128, true> * kStageBytes<128, true>, "sums take the ring's place");
 
-// The layout's element (row, chunk of 8) in units of bytes.
-__device__ __forceinline__ uint32_t sw128(int row, int chunk) { return static_cast<uint32_t>(row * 128 + ((chunk ^ (row & 7)) << 4)); }
+// A row's four values at ranks r .. r + 3 (the row's others lie in the RP / 4 lanes around), split.
+template <typename T, int RP>
+__device__ __forceinline__ void put_split(const SplitRows &o, int64_t at, int r, const float (&f)[4], bool ok) {
+    float p = 1.0f;
+    if constexpr (std::is_same<T, __half>::value) {
+        float amax = fmaxf(fmaxf(fabsf(f[0]), fabsf(f[1])), fmaxf(fabsf(f[2]), fabsf(f[3])));
+#pragma unroll
+        for (int d = 1; d < RP / 4; d *= 2) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, d));
+        p = row_power<T>(amax);
+        if (ok && r == 0) o.unpower[at] = 1.0f / p;
+    }
+    uint2 h, l;
+    split2<T>(f[0] * p, f[1] * p, h.x, l.x);
+    split2<T>(f[2] * p, f[3] * p, h.y, l.y);
+    if (ok) {
+        *reinterpret_cast<uint2 *>(o.hi + at * RP + r) = h;
+        *reinterpret_cast<uint2 *>(o.lo + at * RP + r) = l;
+    }
+}
 
-template <typename T, int RP, bool WT>
-__global__ void __launch_bounds__(kThreads, 2) shrink_kernel(const ShrinkArgs a) {
+template <typename T, int RP, bool WT, bool V16>
+__global__ void __launch_bounds__(32 * kWarps, 2) shrink_kernel(const ShrinkArgs a) {
     extern __shared__ uint8_t dyn[];
-    __shared__ alignas(8) uint64_t bars[8];
-    __shared__ uint32_t tmem_slot, abort_flag;
-    __shared__ int rows[kAdapterTile];
     constexpr int S = kStages<RP, WT>, kCols = RP < 32 ? 32 : RP;
     static_assert(S >= 3 && S <= 8, "stages");
+    __shared__ alignas(8) uint64_t full[S], empty[S], done;
+    __shared__ uint32_t tmem_slot, abort_flag;
+    __shared__ int rows[kAdapterTile];
     uint8_t *smem = dyn + ((1024u - (smem_u32(dyn) & 1023u)) & 1023u);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int c = a.cluster;
-    const uint32_t rank = c > 1 ? tc::cluster_ctarank() : 0u;
+    const int rank = c > 1 ? static_cast<int>(tc::cluster_ctarank()) : 0;
     // Tensor memory is taken after the previous grid has ended and before the
     // next one may start, so that no grid waits for columns of one that waits for it.
     pdl_wait();
-    if (warp == 0) {
+    const AdapterTile tile = a.plan.tiles[blockIdx.x / c];
+    if (tid < kAdapterTile) rows[tid] = a.plan.rows[tile.first + (tid < tile.n ? tid : 0)];
+    if (warp == kWarps - 1) {
         tc::tmem_alloc(smem_u32(&tmem_slot), kCols);
         tc::tmem_relinquish();
         if (lane == 0) {
             abort_flag = 0;
-            for (int i = 0; i < S; ++i) tc::mbar_init(smem_u32(&bars[i]), 1);
+            for (int i = 0; i < S; ++i) {
+                tc::mbar_init(smem_u32(&full[i]), kWarps - 1);
+                tc::mbar_init(smem_u32(&empty[i]), 1);
+            }
+            tc::mbar_init(smem_u32(&done), 1);
             tc::fence_mbar_init();
         }
     }
-    const AdapterTile tile = a.plan.tiles[blockIdx.x / c];
-    if (tid < kAdapterTile) rows[tid] = a.plan.rows[tile.first + (tid < tile.n ? tid : 0)];
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
     pdl_launch_dependents();
     const uint32_t tmem = tmem_slot;
 
-    const uint16_t *w = a.w + static_cast<int64_t>(tile.adapter) * a.R * a.C;
     const int total = (a.C + kStep - 1) / kStep;
     const int s0 = static_cast<int>(static_cast<int64_t>(total) * rank / c);
     const int n = static_cast<int>(static_cast<int64_t>(total) * (rank + 1) / c) - s0;
-    // this thread's chunks of a stage: column chunk tid % 8 of rows tid / 8 + 32 i
-    const int cc = (tid & 7) * 8;
-    const uint16_t *xr[4];
-    bool live[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = (tid >> 3) + 32 * i;
-        live[i] = r < tile.n;
-        xr[i] = a.x + static_cast<int64_t>(rows[r]) * a.ldx;
-    }
-    auto load = [&](int s) {
-        uint8_t *xs = smem + (s % S) * kStageBytes<RP, WT>, *ws = xs + kXBytes;
-        const int k0 = (s0 + s) * kStep;
+    if (warp < kWarps - 1) {
+        const uint16_t *w = a.w + static_cast<int64_t>(tile.adapter) * a.R * a.C;
+        // this thread's chunks of a stage: column chunk tid % 8 of rows tid / 8 + 32 i
+        const int cj = tid & 7, cr = tid >> 3;
+        const uint16_t *xr[4];
+        bool live[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int r = (tid >> 3) + 32 * i, valid = live[i] ? a.C - k0 - cc : 0;
-            copy8(reinterpret_cast<uint16_t *>(xs + sw128(r, tid & 7)), valid > 0 ? xr[i] + k0 + cc : a.x, valid, a.ax);
+            live[i] = cr + 32 * i < tile.n;
+            xr[i] = a.x + static_cast<int64_t>(rows[cr + 32 * i]) * a.ldx + 8 * cj;
         }
-        if constexpr (!WT) {
-            for (int i = tid; i < RP * 8; i += kThreads) {
-                const int r = i >> 3, j = i & 7, valid = r < a.R ? a.C - k0 - 8 * j : 0;
-                copy8(reinterpret_cast<uint16_t *>(ws + sw128(r, j)), valid > 0 ? w + static_cast<int64_t>(r) * a.C + k0 + 8 * j : a.w,
-                      valid, a.aw);
-            }
-        } else {
-            // rows of 64 ranks, 64 elements of the long axis to an atom
-            for (int i = tid; i < kStep * (RP / 8); i += kThreads) {
-                const int k = i / (RP / 8), j = i % (RP / 8), valid = k0 + k < a.C ? a.R - 8 * j : 0;
-                copy8(reinterpret_cast<uint16_t *>(ws + (j >> 3) * kAtom + sw128(k, j & 7)),
-                      valid > 0 ? w + static_cast<int64_t>(k0 + k) * a.R + 8 * j : a.w, valid, a.aw);
-            }
-        }
-    };
-    // fp32 sums, bf16 or f16 operands, B MN-major where W is [C, R], N = RP, M = 128
-    constexpr uint32_t kFmt = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
-    constexpr uint32_t kIdesc = (1u << 4) | (kFmt << 7) | (kFmt << 10) | ((WT ? 1u : 0u) << 16) |
-                                ((static_cast<uint32_t>(RP) >> 3) << 17) | ((128u >> 4) << 24);
-    auto wait_mma = [&](int s) {
-        const uint32_t bar = smem_u32(&bars[s % S]), parity = static_cast<uint32_t>(s / S) & 1u;
-        if (!tc::wait_fast(bar, parity, &abort_flag, a.err, a.limit_ns)) {
-            uint32_t drain = 0;                             // recorded; the products in flight must still land
-            tc::wait_bounded(bar, parity, &drain, a.err);
-        }
-    };
+        for (int s = 0; s < n + S - 1; ++s) {
+            if (s < n) {
+                if (s >= S) wait_landed(empty[s % S], static_cast<uint32_t>(s / S - 1) & 1u, &abort_flag, a.err, a.limit_ns);
+                uint8_t *xs = smem + (s % S) * kStageBytes<RP, WT>, *ws = xs + kXBytes;
+                const int k0 = (s0 + s) * kStep, left = a.C - k0;
 #pragma unroll
-    for (int s = 0; s < S - 1; ++s) {
-        if (s < n) load(s);
-        cp_async_commit();
-    }
-    for (int s = 0; s < n; ++s) {
-        cp_async_wait<S - 2>();
-        tc::fence_proxy_async_smem();
-        __syncthreads();
-        if (tid == 0) {
+                for (int i = 0; i < 4; ++i) {
+                    const int valid = live[i] ? left - 8 * cj : 0;
+                    copy8<V16>(xs + sw128(cr + 32 * i, cj), valid > 0 ? xr[i] + k0 : a.x, valid, a.ax);
+                }
+                if constexpr (!WT) {
+#pragma unroll
+                    for (int i = 0; i < (RP + 31) / 32; ++i) {
+                        const int r = cr + 32 * i, valid = r < a.R ? left - 8 * cj : 0;
+                        if (RP >= 32 || r < RP)
+                            copy8<V16>(ws + sw128(r, cj), valid > 0 ? w + static_cast<int64_t>(r) * a.C + k0 + 8 * cj : a.w, valid, a.aw);
+                    }
+                } else {
+                    // rows of 64 ranks, 64 elements of the long axis to an atom
+#pragma unroll
+                    for (int i = 0; i < (kStep * (RP / 8) + 255) / 256; ++i) {
+                        const int at = tid + 256 * i, k = at / (RP / 8), j = at % (RP / 8);
+                        const int valid = k < left ? a.R - 8 * j : 0;
+                        if (RP >= 32 || k < kStep)
+                            copy8<V16>(ws + (j >> 3) * kAtom + sw128(k, j & 7),
+                                       valid > 0 ? w + static_cast<int64_t>(k0 + k) * a.R + 8 * j : a.w, valid, a.aw);
+                    }
+                }
+            }
+            cp_async_commit();
+            if (s >= S - 1) {                               // the stage asked for S - 1 turns ago has landed
+                cp_async_wait<S - 1>();
+                tc::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(smem_u32(&full[(s - (S - 1)) % S]));
+            }
+        }
+    } else if (lane == 0) {
+        // fp32 sums, bf16 or f16 operands, B MN-major where W is [C, R], N = RP, M = 128
+        constexpr uint32_t kFmt = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
+        constexpr uint32_t kIdesc = (1u << 4) | (kFmt << 7) | (kFmt << 10) | ((WT ? 1u : 0u) << 16) |
+                                    ((static_cast<uint32_t>(RP) >> 3) << 17) | ((128u >> 4) << 24);
+        for (int s = 0; s < n; ++s) {
+            wait_landed(full[s % S], static_cast<uint32_t>(s / S) & 1u, &abort_flag, a.err, a.limit_ns);
             tc::fence_after_sync();
             const uint32_t xs = smem_u32(smem + (s % S) * kStageBytes<RP, WT>), ws = xs + kXBytes;
 #pragma unroll
@@ -127,65 +148,74 @@ __global__ void __launch_bounds__(kThreads, 2) shrink_kernel(const ShrinkArgs a)
                 const uint64_t db = WT ? tc::sw128_mnmajor_desc(ws + 2048 * k, kAtom) : tc::sw128_kmajor_desc(ws + 32 * k);
                 tc::mma_f16(tmem, da, db, kIdesc, (s | k) != 0);
             }
-            tc::mma_commit(smem_u32(&bars[s % S]));
+            tc::mma_commit(smem_u32(&empty[s % S]));
         }
-        if (s + S - 1 < n) {
-            if (s > 0) wait_mma(s - 1);                     // the slot's last products
-            load(s + S - 1);
-        }
-        cp_async_commit();
+        tc::mma_commit(smem_u32(&done));
     }
-    cp_async_wait<0>();
-    wait_mma(n - 1);
+    __syncwarp();
+    wait_landed(done, 0, &abort_flag, a.err, a.limit_ns);
     tc::fence_after_sync();
-    __syncthreads();
     // the sums, [row][r], where the ring was
     float *sums = reinterpret_cast<float *>(smem);
-    for (int col = (warp >> 2) * 32; col < RP; col += 64) {
-        uint32_t v[32];
-        tc::tmem_ld32(tmem + (static_cast<uint32_t>(warp & 3) << 21) + col, v);
-        tc::tmem_ld_wait();
-        float *p = sums + ((warp & 3) * 32 + lane) * kSumPitch<RP> + col;
+    if (warp < kWarps - 1) {
+        for (int col = (warp >> 2) * 32; col < RP; col += 64) {
+            uint32_t v[32];
+            tc::tmem_ld32(tmem + (static_cast<uint32_t>(warp & 3) << 21) + col, v);
+            tc::tmem_ld_wait();
+            float *p = sums + ((warp & 3) * 32 + lane) * kSumPitch<RP> + col;
 #pragma unroll
-        for (int i = 0; i < (RP < 32 ? RP : 32); i += 4)
-            *reinterpret_cast<uint4 *>(p + i) = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+            for (int i = 0; i < (RP < 32 ? RP : 32); i += 4)
+                *reinterpret_cast<uint4 *>(p + i) = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+        }
     }
     tc::fence_before_sync();
     if (c > 1) tc::cluster_sync();
     else __syncthreads();
-    if (warp == 0) {
+    if (warp == kWarps - 1) {
         tc::fence_after_sync();
         tc::tmem_dealloc(tmem, kCols);
-    }
-    const float mul = a.scale != nullptr ? a.scale[tile.adapter] : 1.0f;
-    const int r0 = kAdapterTile * static_cast<int>(rank) / c, r1 = kAdapterTile * (static_cast<int>(rank) + 1) / c;
-    for (int i = tid; i < (r1 - r0) * (RP / 4); i += kThreads) {
-        const int row = r0 + i / (RP / 4), r = (i % (RP / 4)) * 4;
-        if (row >= tile.n) break;
-        const float *at = sums + row * kSumPitch<RP> + r;
-        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (c == 1) {
-            v = *reinterpret_cast<const float4 *>(at);
-        } else {
+    } else {
+        const float mul = a.scale != nullptr ? a.scale[tile.adapter] : 1.0f;
+        const int r0 = kAdapterTile * rank / c, r1 = kAdapterTile * (rank + 1) / c;
+        // whole warps: 128 / 8 rows of RP / 4 lanes
+        for (int i = tid; i < (r1 - r0) * (RP / 4); i += 32 * (kWarps - 1)) {
+            const int row = r0 + i / (RP / 4), r = (i % (RP / 4)) * 4;
+            const bool ok = row < tile.n;
+            const float *at = sums + row * kSumPitch<RP> + r;
+            float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (c == 1) {
+                v = *reinterpret_cast<const float4 *>(at);
+            } else {
 #pragma unroll 4
-            for (int q = 0; q < c; ++q) {
-                float4 p;
-                asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                             : "=f"(p.x), "=f"(p.y), "=f"(p.z), "=f"(p.w) : "r"(tc::mapa(smem_u32(at), q)) : "memory");
-                v.x += p.x; v.y += p.y; v.z += p.z; v.w += p.w;
+                for (int q = 0; q < c; ++q) {
+                    float4 p;
+                    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                                 : "=f"(p.x), "=f"(p.y), "=f"(p.z), "=f"(p.w) : "r"(tc::mapa(smem_u32(at), q)) : "memory");
+                    v.x += p.x; v.y += p.y; v.z += p.z; v.w += p.w;
+                }
+            }
+            const float f[4] = {v.x * mul, v.y * mul, v.z * mul, v.w * mul};
+            if (a.u != nullptr && ok) {
+                float *u = a.u + static_cast<int64_t>(rows[row]) * a.R + r;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (r + e < a.R) u[e] = f[e];
+            }
+            put_split<T, RP>(a.out, tile.first + row, r, f, ok);
+            if constexpr (WT) {
+                const float *u = a.given + static_cast<int64_t>(rows[row]) * a.R + r;
+                float g[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) g[e] = ok && r + e < a.R ? u[e] : 0.0f;
+                put_split<T, RP>(a.given_out, tile.first + row, r, g, ok);
             }
         }
-        float *u = a.u + static_cast<int64_t>(rows[row]) * a.R + r;
-        const float f[4] = {v.x * mul, v.y * mul, v.z * mul, v.w * mul};
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (r + e < a.R) u[e] = f[e];
     }
     if (c > 1) tc::cluster_sync();                          // nobody leaves while its sums are read
 }
 
-template <typename T, int RP, bool WT> cudaError_t launch_rp(ShrinkArgs a, int tiles, cudaStream_t s) {
-    auto kern = shrink_kernel<T, RP, WT>;
+template <typename T, int RP, bool WT, bool V16> cudaError_t launch_v(ShrinkArgs a, int tiles, cudaStream_t s) {
+    auto kern = shrink_kernel<T, RP, WT, V16>;
     static std::once_flag once;
     static cudaError_t err = cudaSuccess;
     if (allow_smem(kern, kSmem<RP, WT>, once, err) != cudaSuccess) return err;
@@ -194,7 +224,10 @@ template <typename T, int RP, bool WT> cudaError_t launch_rp(ShrinkArgs a, int t
     // pieces of at least four stages until the CTAs fill the machine twice
     while (c < 8 && tiles * c < 2 * device_sm_count() && steps >= 8 * c) c *= 2;
     a.cluster = c;
-    return launch_cluster(kern, tiles * c, c, kSmem<RP, WT>, s, static_cast<const ShrinkArgs>(a));
+    return launch_cluster(kern, tiles * c, c, 32 * kWarps, kSmem<RP, WT>, s, static_cast<const ShrinkArgs>(a));
+}
+template <typename T, int RP, bool WT> cudaError_t launch_rp(const ShrinkArgs &a, int tiles, cudaStream_t s) {
+    return a.ax == 16 && a.aw == 16 ? launch_v<T, RP, WT, true>(a, tiles, s) : launch_v<T, RP, WT, false>(a, tiles, s);
 }
 template <typename T, bool WT> cudaError_t launch_t(const ShrinkArgs &a, int tiles, cudaStream_t s) {
     if (a.R <= 16) return launch_rp<T, 16, WT>(a, tiles, s);
