@@ -80,6 +80,16 @@ cudaError_t forward(const Forward &f, cudaStream_t s) {
     const Plan plan{f.plan + lay.rows, reinterpret_cast<const AdapterTile *>(f.plan + lay.tiles)};
     const bool wide = align_of(f.out, f.ldo * (of32 ? 4 : 2)) == 16 && f.N % 8 == 0 &&
                       (f.base == nullptr || align_of(f.base, f.ldb * (f.base_f32 ? 4 : 2)) == 16);
+    // tokens without an adapter go along with the first kernel that writes results
+    PassArgs pa = {};
+    pa.n = f.info->without;
+    pa.rows = plan.rows + (f.T - pa.n);
+    pa.N = f.N; pa.R = f.R;
+    pa.base = f.base; pa.base_f32 = f.base_f32; pa.ldb = f.ldb;
+    pa.out = f.out == f.base ? nullptr : f.out; pa.ldo = f.ldo;
+    pa.u = f.u;
+    if (pa.out == nullptr && pa.u == nullptr) pa.n = 0;
+    const bool pass_along = f.info->small_tiles > 0 || f.info->large_tiles > 0;
     cudaError_t e;
     if (f.info->small_tiles > 0) {
         SmallArgs sm = {};
@@ -94,6 +104,7 @@ cudaError_t forward(const Forward &f, cudaStream_t s) {
         sm.base = f.base; sm.base_f32 = f.base_f32; sm.ldb = f.ldb;
         sm.out = f.out; sm.ldo = f.ldo;
         sm.u = f.u;
+        sm.pass = pa;
         e = launch_small(t, of32, sm, f.info->small_tiles, f.info->small_most, s);
         if (e != cudaSuccess) return e;
     }
@@ -108,6 +119,7 @@ cudaError_t forward(const Forward &f, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     ExpandArgs ex = {};
     ex.plan = plan;
+    if (f.info->small_tiles == 0) ex.pass = pa;
     ex.u = sh.out; ex.w = f.B; ex.aw = align_of(f.B, int64_t(f.R) * 2);
     ex.C = f.N; ex.R = f.R; ex.scale = f.scale;
     ex.base = f.base; ex.base_f32 = f.base_f32; ex.ldb = f.ldb;
@@ -116,14 +128,7 @@ cudaError_t forward(const Forward &f, cudaStream_t s) {
     ex.err = f.err; ex.limit_ns = wait_limit_ns();
     e = launch_expand(t, false, of32, ex, f.info->large_tiles, s);
     if (e != cudaSuccess) return e;
-    PassArgs pa = {};
-    pa.n = f.info->without;
-    pa.rows = plan.rows + (f.T - pa.n);
-    pa.N = f.N; pa.R = f.R;
-    pa.base = f.base; pa.base_f32 = f.base_f32; pa.ldb = f.ldb;
-    pa.out = f.out == f.base ? nullptr : f.out; pa.ldo = f.ldo;
-    pa.u = f.u;
-    return launch_pass(t, of32, pa, s);
+    return pass_along ? cudaSuccess : launch_pass(t, of32, pa, s);
 }
 
 }  // namespace
@@ -263,7 +268,16 @@ bt_status bt_adapter_linear_backward(const void *x, int64_t ldx, const void *g, 
     e = launch_grad(gr, info->parts, s);
     if (e != cudaSuccess) return BT_ERR_CUDA;
 
+    PassArgs pa = {};
+    pa.n = info->without;
+    pa.rows = tiles.rows + (T - pa.n);
+    pa.N = static_cast<int>(K); pa.R = static_cast<int>(R);
+    pa.base = grad_base; pa.ldb = ldgb;
+    pa.out = grad_x == grad_base ? nullptr : grad_x; pa.ldo = ldgx;
+    if (pa.out == nullptr) pa.n = 0;
+    if (info->tiles == 0 && launch_pass(BT_BF16, false, pa, s) != cudaSuccess) return BT_ERR_CUDA;
     ExpandArgs ex = {};
+    ex.pass = pa;
     ex.plan = tiles;
     ex.u = du; ex.w = Ap;
     ex.err = err; ex.limit_ns = wait_limit_ns(); ex.aw = align_of(A, K * 2);
@@ -274,14 +288,6 @@ bt_status bt_adapter_linear_backward(const void *x, int64_t ldx, const void *g, 
     e = launch_expand(BT_BF16, true, false, ex, info->tiles, s);
     if (e != cudaSuccess) return BT_ERR_CUDA;
 
-    PassArgs pa = {};
-    pa.n = info->without;
-    pa.rows = tiles.rows + (T - pa.n);
-    pa.N = static_cast<int>(K); pa.R = static_cast<int>(R);
-    pa.base = grad_base; pa.ldb = ldgb;
-    pa.out = grad_x == grad_base ? nullptr : grad_x; pa.ldo = ldgx;
-    e = launch_pass(BT_BF16, false, pa, s);
-    if (e != cudaSuccess) return BT_ERR_CUDA;
 
     if (info->slots > 0) {
         SumArgs su = {};

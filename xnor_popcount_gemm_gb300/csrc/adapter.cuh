@@ -65,8 +65,7 @@ template <typename T> __device__ __forceinline__ float row_power(float amax) {
 
 // ---------------------------------------------------------------------------
 // Eight consecutive elements of a global row to shared memory (16 bytes, 16-byte
-// aligned), `valid` of them there (<= 0: none), the rest zeros. al: bytes that
-// every row of the operand starts at a multiple of; V16: 16.
+// aligned), `valid` of them there (<= 0: none), the rest zeros.
 // ---------------------------------------------------------------------------
 template <int B> __device__ __forceinline__ void cp_async_small(uint32_t dst, const void *src, int bytes) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;\n" ::"r"(dst), "l"(src), "n"(B), "r"(bytes) : "memory");
@@ -87,10 +86,15 @@ __device__ __forceinline__ uint4 load8(const uint16_t *src, int valid) {
     }
     return make_uint4(r[0], r[1], r[2], r[3]);
 }
-template <bool V16> __device__ __forceinline__ void copy8(void *dst, const uint16_t *src, int valid, int al) {
-    if (V16 || al == 16) {
+// How an operand's rows are fetched, by what they start at multiples of.
+constexpr int kRows16 = 0;                 // 16 bytes: asynchronous copies
+constexpr int kRows4 = 1;                  // 4 bytes: asynchronous copies of 4, 8 or 16
+constexpr int kRows2 = 2;                  // less: through registers
+inline int rows_mode(int al) { return al == 16 ? kRows16 : al >= 4 ? kRows4 : kRows2; }
+template <int MODE> __device__ __forceinline__ void copy8(void *dst, const uint16_t *src, int valid, int al) {
+    if (MODE == kRows16 || (MODE == kRows4 && al == 16)) {
         cp_async_16(dst, src, clamp_to(valid, 8) * 2);
-    } else if (al >= 4) {
+    } else if (MODE == kRows4) {
         const uint32_t d = smem_u32(dst);
         if (al == 8) {
             cp_async_small<8>(d, src, clamp_to(valid, 4) * 2);
@@ -124,6 +128,37 @@ struct Plan {
     const int32_t *rows;
     const AdapterTile *tiles;
 };
+
+// Tokens without an adapter: out = cast(base), u = 0.
+struct PassArgs {
+    const int32_t *rows;
+    int n, N, R;
+    const void *base;
+    int base_f32;
+    int64_t ldb;
+    void *out;                 // NULL: the rows are in place already
+    int64_t ldo;
+    float *u;
+};
+// Rows first, first + step, ... of them: CTAs of the kernels below that are left over take them along.
+template <typename T> __device__ void pass_rows(const PassArgs &a, bool out_f32, int first, int step) {
+    for (int i = first; i < a.n; i += step) {
+        const int64_t row = a.rows[i];
+        if (a.u != nullptr)
+            for (int r = threadIdx.x; r < a.R; r += blockDim.x) a.u[row * a.R + r] = 0.0f;
+        if (a.out == nullptr) continue;
+#pragma unroll 4
+        for (int c = threadIdx.x; c < a.N; c += blockDim.x) {
+            float v = 0.0f;
+            if (a.base != nullptr)
+                v = a.base_f32 ? static_cast<const float *>(a.base)[row * a.ldb + c]
+                               : Elem<T>::to_f32(static_cast<const T *>(a.base)[row * a.ldb + c]);
+            if (out_f32) static_cast<float *>(a.out)[row * a.ldo + c] = v;
+            else static_cast<T *>(a.out)[row * a.ldo + c] = to16<T>(v);
+        }
+    }
+}
+cudaError_t launch_pass(bt_dtype t, bool out_f32, const PassArgs &a, cudaStream_t s);
 
 // u and dU between the products: rows in the plan's order, padded to RP = 16,
 // 32, 64 or 128 ranks, as the sum of two 16-bit values; in half precision times
@@ -169,24 +204,13 @@ struct ExpandArgs {
     void *out;
     int64_t ldo;
     int wide;                  // rows of base and out start at 16-byte multiples, C a multiple of 8
-    int splits;                // column ranges per tile
+    int tiles, splits;         // column ranges per tile
+    PassArgs pass;             // rows that the CTAs after the tiles' take along (n = 0: none)
     unsigned int *err;
     unsigned long long limit_ns;
 };
 cudaError_t launch_expand(bt_dtype t, bool wt, bool out_f32, const ExpandArgs &a, int tiles, cudaStream_t s);
 
-// Tokens without an adapter: out = cast(base), u = 0.
-struct PassArgs {
-    const int32_t *rows;
-    int n, N, R;
-    const void *base;
-    int base_f32;
-    int64_t ldb;
-    void *out;                 // NULL: the rows are in place already
-    int64_t ldo;
-    float *u;
-};
-cudaError_t launch_pass(bt_dtype t, bool out_f32, const PassArgs &a, cudaStream_t s);
 
 
 // G[r, c] = s sum_t U[t, r] X[t, c] over every part of the adapters' tokens, for
@@ -241,7 +265,8 @@ struct SmallArgs {
     void *out;
     int64_t ldo;
     float *u;                  // NULL: not wanted
-    int cluster;
+    int tiles, cluster;
+    PassArgs pass;             // rows that the CTAs after the tiles' take along (n = 0: none)
 };
 // most: tokens of the fullest tile
 cudaError_t launch_small(bt_dtype t, bool out_f32, const SmallArgs &a, int tiles, int most, cudaStream_t s);

@@ -52,40 +52,50 @@ __device__ __forceinline__ void tmem_ld_16x64(uint32_t addr, uint32_t (&r)[32]) 
         : "r"(addr));
 }
 
-// FAST: WIDE, and W's rows start at 16-byte multiples.
-template <typename T, int RP, bool WT, bool OF32, bool FAST>
+// FAST: WIDE, and W's rows start at 16-byte multiples. BF32: base is fp32.
+template <typename T, int RP, bool WT, bool OF32, bool FAST, bool BF32>
 __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) expand_kernel(const ExpandArgs a) {
     extern __shared__ uint8_t dyn[];
     __shared__ alignas(8) uint64_t ready[2];
     __shared__ uint32_t tmem_slot, abort_flag;
+    __shared__ int64_t rows_s[FAST ? 1 : 128];
+    __shared__ float mul_s[FAST ? 1 : 128];
     uint8_t *us = dyn + ((1024u - (smem_u32(dyn) & 1023u)) & 1023u), *wbuf = us + 2 * kUBytes<RP>;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     float *turn = reinterpret_cast<float *>(wbuf + 2 * kWBytes<RP, WT>) + warp * 16 * kTurnPitch;
     pdl_wait();                                             // before tensor memory is taken, see shrink_kernel
+    if (static_cast<int>(blockIdx.x) >= a.tiles * a.splits) {
+        pdl_launch_dependents();
+        pass_rows<T>(a.pass, OF32, blockIdx.x - a.tiles * a.splits, gridDim.x - a.tiles * a.splits);
+        return;
+    }
     const AdapterTile tile = a.plan.tiles[blockIdx.x / a.splits];
     const int part = blockIdx.x % a.splits;
     const int total = (a.C + kTile - 1) / kTile;
     const int s0 = static_cast<int>(static_cast<int64_t>(total) * part / a.splits);
     const int s1 = static_cast<int>(static_cast<int64_t>(total) * (part + 1) / a.splits);
     const uint16_t *w = a.w + static_cast<int64_t>(tile.adapter) * a.R * a.C;
+    auto put = [&](uint8_t *dst, const uint16_t *src, int valid) {
+        if constexpr (FAST) copy8<kRows16>(dst, src, valid, 16);
+        else if (a.aw >= 4) copy8<kRows4>(dst, src, valid, a.aw);
+        else copy8<kRows2>(dst, src, valid, 2);
+    };
     auto load_w = [&](int s) {
-        uint8_t *ws = wbuf + (s & 1) * kWBytes<RP, WT>;
         const int c0 = s * kTile;
+        uint8_t *ws = wbuf + (s & 1) * kWBytes<RP, WT>;
         if constexpr (!WT) {
             // 128 columns' rows of RP ranks, 64 to an atom
 #pragma unroll
             for (int i = 0; i < kTile * (RP / 8) / kThreads; ++i) {
                 const int at = tid + kThreads * i, k = at / (RP / 8), j = at % (RP / 8), valid = c0 + k < a.C ? a.R - 8 * j : 0;
-                copy8<FAST>(ws + (j >> 3) * 2 * kAtom + sw128(k, j & 7), valid > 0 ? w + static_cast<int64_t>(c0 + k) * a.R + 8 * j : a.w,
-                            valid, a.aw);
+                put(ws + (j >> 3) * 2 * kAtom + sw128(k, j & 7), valid > 0 ? w + static_cast<int64_t>(c0 + k) * a.R + 8 * j : a.w, valid);
             }
         } else {
             // RP rows of 128 columns, 64 to an atom
 #pragma unroll
             for (int i = 0; i < RP * 16 / kThreads; ++i) {
                 const int at = tid + kThreads * i, r = at >> 4, j = at & 15, valid = r < a.R ? a.C - c0 - 8 * j : 0;
-                copy8<FAST>(ws + (j >> 3) * RP * 128 + sw128(r, j & 7), valid > 0 ? w + static_cast<int64_t>(r) * a.C + c0 + 8 * j : a.w,
-                            valid, a.aw);
+                put(ws + (j >> 3) * RP * 128 + sw128(r, j & 7), valid > 0 ? w + static_cast<int64_t>(r) * a.C + c0 + 8 * j : a.w, valid);
             }
         }
     };
@@ -127,20 +137,16 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) expand_kernel(cons
             row[b][h] = a.plan.rows[at];
             mul[b][h] = a.u.unpower != nullptr ? s * a.u.unpower[at] : s;
         }
-    // Base's values of a step. FAST: 16-bit base as lane t's columns 8t.. of each 32; else column `lane` and
-    // `lane + 32` of the warp's rows, two 16-bit values a word.
-    const bool b16 = a.base != nullptr && !a.base_f32;
-    uint4 bw[2][2][2];
-    uint32_t bn[2][16];
-    int lane_row[2];
-    float lane_mul[2];
-#pragma unroll
-    for (int b = 0; b < 2; ++b) {                           // lane m: row m of the 16
-        const int r0 = __shfl_sync(0xFFFFFFFFu, row[b][0], (lane & 7) * 4), r8 = __shfl_sync(0xFFFFFFFFu, row[b][1], (lane & 7) * 4);
-        const float f0 = __shfl_sync(0xFFFFFFFFu, mul[b][0], (lane & 7) * 4), f8 = __shfl_sync(0xFFFFFFFFu, mul[b][1], (lane & 7) * 4);
-        lane_row[b] = (lane & 8) ? r8 : r0;
-        lane_mul[b] = (lane & 8) ? f8 : f0;
+    if constexpr (!FAST) {
+        if (tid < 128) {
+            const int at = tile.first + (tid < tile.n ? tid : 0);
+            rows_s[tid] = a.plan.rows[at];
+            mul_s[tid] = a.u.unpower != nullptr ? s * a.u.unpower[at] : s;
+        }
     }
+    // (FAST) 16-bit base's values of a step, lane t's columns 8t.. of each 32
+    const bool b16 = a.base != nullptr && !BF32;
+    uint4 bw[2][2][2];
     auto load_base = [&](int st, int b) {
         const int c0 = st * kTile + cw;
         if constexpr (FAST) {
@@ -153,16 +159,6 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) expand_kernel(cons
                     if (b16 && live[b][h] && st < s1 && cj < a.C)
                         bw[b][h][q] = ld_stream_v4(static_cast<const uint16_t *>(a.base) + static_cast<int64_t>(row[b][h]) * a.ldb + cj);
                 }
-        } else if (b16) {
-#pragma unroll
-            for (int m = 0; m < 16; ++m) {
-                const uint16_t *p = static_cast<const uint16_t *>(a.base) +
-                                    static_cast<int64_t>(__shfl_sync(0xFFFFFFFFu, lane_row[b], m)) * a.ldb + c0 + lane;
-                const bool ok = m0 + 16 * b + m < tile.n && st < s1;
-                const uint32_t lo = ok && c0 + lane < a.C ? p[0] : 0u;
-                const uint32_t hi = ok && c0 + lane + 32 < a.C ? p[32] : 0u;
-                bn[b][m] = lo | (hi << 16);
-            }
         }
     };
     load_base(s0, 0);
@@ -219,7 +215,7 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) expand_kernel(cons
                     for (int q = 0; q < 2; ++q) {           // 32 columns: blocks 4q .. 4q + 3
                         float2 v[4];                        // base, then base + s * sum in one rounding each
                         const int cq = c0 + 32 * q;
-                        if (a.base_f32) {
+                        if constexpr (BF32) {
                             const float *p = static_cast<const float *>(a.base) + bo;
 #pragma unroll
                             for (int j = 0; j < 4; ++j) {
@@ -264,21 +260,33 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) expand_kernel(cons
                         *reinterpret_cast<uint2 *>(turn + (8 * h + g) * kTurnPitch + 8 * j + 2 * t) =
                             make_uint2(acc[4 * j + 2 * h], acc[4 * j + 2 * h + 1]);
                 __syncwarp();
+                // eight rows at a time: their base first, all on its way at once
+#pragma unroll 1
+                for (int m8 = 0; m8 < 16; m8 += 8) {
+                    float v[8][2];
 #pragma unroll
-                for (int m = 0; m < 16; ++m) {
-                    const int64_t r = __shfl_sync(0xFFFFFFFFu, lane_row[b], m);
-                    const float ms = __shfl_sync(0xFFFFFFFFu, lane_mul[b], m);
-                    if (m0 + 16 * b + m >= tile.n) continue;
-                    const float2 f = unpack2<T>(b16 ? bn[b][m] : 0u);
+                    for (int m = 0; m < 8; ++m) {
+                        const int at = m0 + 16 * b + m8 + m;
+                        const int64_t r = rows_s[at] * a.ldb + c0 + lane;
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int cj = c0 + lane + 32 * e;
-                        if (cj >= a.C) continue;
-                        float v = e ? f.y : f.x;
-                        if (a.base_f32 && a.base != nullptr) v = static_cast<const float *>(a.base)[r * a.ldb + cj];
-                        v = __fmaf_rn(turn[m * kTurnPitch + lane + 32 * e], ms, v);
-                        if constexpr (OF32) static_cast<float *>(a.out)[r * a.ldo + cj] = v;
-                        else static_cast<T *>(a.out)[r * a.ldo + cj] = to16<T>(v);
+                        for (int e = 0; e < 2; ++e) {
+                            const bool ok = a.base != nullptr && at < tile.n && c0 + lane + 32 * e < a.C;
+                            if constexpr (BF32) v[m][e] = ok ? static_cast<const float *>(a.base)[r + 32 * e] : 0.0f;
+                            else v[m][e] = ok ? Elem<T>::to_f32(static_cast<const T *>(a.base)[r + 32 * e]) : 0.0f;
+                        }
+                    }
+#pragma unroll
+                    for (int m = 0; m < 8; ++m) {
+                        const int at = m0 + 16 * b + m8 + m;
+                        const float ms = mul_s[at];
+                        const int64_t r = rows_s[at] * a.ldo + c0 + lane;
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            if (at >= tile.n || c0 + lane + 32 * e >= a.C) continue;
+                            const float f = __fmaf_rn(turn[(m8 + m) * kTurnPitch + lane + 32 * e], ms, v[m][e]);
+                            if constexpr (OF32) static_cast<float *>(a.out)[r + 32 * e] = f;
+                            else static_cast<T *>(a.out)[r + 32 * e] = to16<T>(f);
+                        }
                     }
                 }
                 __syncwarp();
@@ -295,44 +303,35 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) expand_kernel(cons
     }
 }
 
-template <typename T, int RP, bool WT, bool OF32, bool FAST> cudaError_t launch_rp(const ExpandArgs &a, int tiles, cudaStream_t s) {
-    auto kern = expand_kernel<T, RP, WT, OF32, FAST>;
+template <typename T, int RP, bool WT, bool OF32, bool FAST, bool BF32>
+cudaError_t launch_rp(const ExpandArgs &a, cudaStream_t s) {
+    auto kern = expand_kernel<T, RP, WT, OF32, FAST, BF32>;
     constexpr int smem = kSmem<RP, WT, FAST>;
     static std::once_flag once;
     static cudaError_t err = cudaSuccess;
     if (allow_smem(kern, smem, once, err) != cudaSuccess) return err;
-    return launch_pdl_smem(kern, dim3(static_cast<unsigned>(tiles * a.splits)), dim3(kThreads), smem, s, a);
+    const int pass = a.pass.n < 2 * device_sm_count() ? a.pass.n : 2 * device_sm_count();
+    return launch_pdl_smem(kern, dim3(static_cast<unsigned>(a.tiles * a.splits + pass)), dim3(kThreads), smem, s, a);
 }
-template <typename T, bool WT, bool OF32, bool FAST> cudaError_t launch_r(const ExpandArgs &a, int tiles, cudaStream_t s) {
-    if (a.R <= 16) return launch_rp<T, 16, WT, OF32, FAST>(a, tiles, s);
-    if (a.R <= 32) return launch_rp<T, 32, WT, OF32, FAST>(a, tiles, s);
-    if (a.R <= 64) return launch_rp<T, 64, WT, OF32, FAST>(a, tiles, s);
-    return launch_rp<T, 128, WT, OF32, FAST>(a, tiles, s);
+template <typename T, bool WT, bool OF32, bool FAST, bool BF32> cudaError_t launch_r(const ExpandArgs &a, cudaStream_t s) {
+    if (a.R <= 16) return launch_rp<T, 16, WT, OF32, FAST, BF32>(a, s);
+    if (a.R <= 32) return launch_rp<T, 32, WT, OF32, FAST, BF32>(a, s);
+    if (a.R <= 64) return launch_rp<T, 64, WT, OF32, FAST, BF32>(a, s);
+    return launch_rp<T, 128, WT, OF32, FAST, BF32>(a, s);
 }
-template <typename T, bool WT, bool OF32> cudaError_t launch_t(const ExpandArgs &a, int tiles, cudaStream_t s) {
-    return a.wide && a.aw == 16 ? launch_r<T, WT, OF32, true>(a, tiles, s) : launch_r<T, WT, OF32, false>(a, tiles, s);
+template <typename T, bool WT, bool OF32> cudaError_t launch_t(const ExpandArgs &a, cudaStream_t s) {
+    const bool fast = a.wide && a.aw == 16;
+    if constexpr (!WT) {                                    // (dX's base has its type)
+        if (a.base != nullptr && a.base_f32)
+            return fast ? launch_r<T, WT, OF32, true, true>(a, s) : launch_r<T, WT, OF32, false, true>(a, s);
+    }
+    return fast ? launch_r<T, WT, OF32, true, false>(a, s) : launch_r<T, WT, OF32, false, false>(a, s);
 }
 
-template <typename T, bool OF32> __global__ void __launch_bounds__(kThreads) pass_kernel(const PassArgs a) {
+template <typename T> __global__ void __launch_bounds__(kThreads) pass_kernel(const PassArgs a, int out_f32) {
     pdl_launch_dependents();
     pdl_wait();
-    const int64_t row = a.rows[blockIdx.x];
-    if (a.u != nullptr && blockIdx.y == 0)
-        for (int r = threadIdx.x; r < a.R; r += kThreads) a.u[row * a.R + r] = 0.0f;
-    if (a.out == nullptr) return;
-#pragma unroll 4
-    for (int c = blockIdx.y * kThreads + threadIdx.x; c < a.N; c += gridDim.y * kThreads) {
-        float v = 0.0f;
-        if (a.base != nullptr)
-            v = a.base_f32 ? static_cast<const float *>(a.base)[row * a.ldb + c]
-                           : Elem<T>::to_f32(static_cast<const T *>(a.base)[row * a.ldb + c]);
-        if constexpr (OF32) static_cast<float *>(a.out)[row * a.ldo + c] = v;
-        else static_cast<T *>(a.out)[row * a.ldo + c] = to16<T>(v);
-    }
-}
-template <typename T> cudaError_t launch_pass_t(bool out_f32, const PassArgs &a, dim3 grid, cudaStream_t s) {
-    return out_f32 ? launch_pdl(pass_kernel<T, true>, grid, dim3(kThreads), s, a)
-                   : launch_pdl(pass_kernel<T, false>, grid, dim3(kThreads), s, a);
+    pass_rows<T>(a, out_f32 != 0, blockIdx.x, gridDim.x);
 }
 
 }  // namespace
@@ -340,20 +339,32 @@ template <typename T> cudaError_t launch_pass_t(bool out_f32, const PassArgs &a,
 cudaError_t launch_expand(bt_dtype t, bool wt, bool out_f32, const ExpandArgs &args, int tiles, cudaStream_t s) {
     if (tiles == 0) return cudaSuccess;
     ExpandArgs a = args;
-    const int steps = (a.C + kTile - 1) / kTile;
-    // two CTAs an SM, and twice that many so that the last ones end close together
-    int splits = (4 * device_sm_count() + tiles - 1) / tiles;
-    if (splits > steps) splits = steps;
-    a.splits = splits < 1 ? 1 : splits;
-    if (wt) return launch_t<__nv_bfloat16, true, false>(a, tiles, s);
-    if (t == BT_F16) return out_f32 ? launch_t<__half, false, true>(a, tiles, s) : launch_t<__half, false, false>(a, tiles, s);
-    return out_f32 ? launch_t<__nv_bfloat16, false, true>(a, tiles, s) : launch_t<__nv_bfloat16, false, false>(a, tiles, s);
+    a.tiles = tiles;
+    // Column ranges a tile, as many as end soonest: in waves of two CTAs an SM, each of its 128-column steps and
+    // of what it costs to begin, about two steps' time.
+    const int steps = (a.C + kTile - 1) / kTile, slots = 2 * device_sm_count();
+    int64_t best = 0;
+    for (int waves = 1; waves <= 4; ++waves) {
+        int splits = static_cast<int>(static_cast<int64_t>(slots) * waves / tiles);
+        if (splits < 1) splits = 1;
+        if (splits > steps) splits = steps;
+        const int64_t real = (static_cast<int64_t>(tiles) * splits + slots - 1) / slots, cost = real * ((steps + splits - 1) / splits + 2);
+        if (waves == 1 || cost < best) {
+            best = cost;
+            a.splits = splits;
+        }
+    }
+    if (wt) return launch_t<__nv_bfloat16, true, false>(a, s);
+    if (t == BT_F16) return out_f32 ? launch_t<__half, false, true>(a, s) : launch_t<__half, false, false>(a, s);
+    return out_f32 ? launch_t<__nv_bfloat16, false, true>(a, s) : launch_t<__nv_bfloat16, false, false>(a, s);
 }
 
 cudaError_t launch_pass(bt_dtype t, bool out_f32, const PassArgs &a, cudaStream_t s) {
     if (a.n == 0 || (a.out == nullptr && a.u == nullptr)) return cudaSuccess;
-    const dim3 grid(static_cast<unsigned>(a.n), static_cast<unsigned>(a.N < 4 * kThreads ? 1 : a.N < 16 * kThreads ? 2 : 4));
-    return t == BT_F16 ? launch_pass_t<__half>(out_f32, a, grid, s) : launch_pass_t<__nv_bfloat16>(out_f32, a, grid, s);
+    const int slots = 8 * device_sm_count();
+    const dim3 grid(static_cast<unsigned>(a.n < slots ? a.n : slots));
+    return t == BT_F16 ? launch_pdl(pass_kernel<__half>, grid, dim3(kThreads), s, a, static_cast<int>(out_f32))
+                       : launch_pdl(pass_kernel<__nv_bfloat16>, grid, dim3(kThreads), s, a, static_cast<int>(out_f32));
 }
 
 }  // namespace adapter

@@ -19,11 +19,11 @@ constexpr int kWarps = 9;
 constexpr int kXBytes = 2 * kAtom;                          // 64 tokens x 128 columns
 template <int RP> constexpr int kUPart = (RP <= 64 ? 1 : 2) * kAtom;       // one of hi, lo
 template <int RP> constexpr int kStageBytes = kXBytes + 2 * kUPart<RP>;
-template <int RP> constexpr int kStages = RP <= 64 ? 3 : 4;
+template <int RP> constexpr int kStages = RP <= 64 ? 2 : 4;
 template <int RP> constexpr int kSmem = kStages<RP> * kStageBytes<RP> + 1024;
 
-template <int RP, bool V16>
-__global__ void __launch_bounds__(32 * kWarps, RP <= 64 ? 2 : 1) grad_kernel(const GradArgs a) {
+template <int RP, int MODE>
+__global__ void __launch_bounds__(32 * kWarps, RP <= 64 ? 3 : 1) grad_kernel(const GradArgs a) {
     extern __shared__ uint8_t dyn[];
     constexpr int S = kStages<RP>, kTmem = RP < 32 ? 32 : RP;
     __shared__ alignas(8) uint64_t full[S], empty[S], done;
@@ -69,18 +69,38 @@ __global__ void __launch_bounds__(32 * kWarps, RP <= 64 ? 2 : 1) grad_kernel(con
         };
         const int left = p.C - c0 - 8 * cj;
         const uint16_t *x = p.x + c0 + 8 * cj;
+        uint4 held[MODE == kRows2 ? 4 : 1];                 // (kRows2) the next stage, on its way
+        auto hold = [&]() {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                held[MODE == kRows2 ? i : 0] = xrow[i] >= 0 && left > 0 ? load8(x + static_cast<int64_t>(xrow[i]) * p.ldx, left)
+                                                                        : make_uint4(0u, 0u, 0u, 0u);
+        };
         fetch_rows(0);
+        if (MODE == kRows2) {
+            hold();
+            fetch_rows(1);
+        }
         for (int s = 0; s < n + S - 1; ++s) {
             if (s < n) {
                 if (s >= S) wait_landed(empty[s % S], static_cast<uint32_t>(s / S - 1) & 1u, &abort_flag, a.err, a.limit_ns);
                 uint8_t *xs = smem + (s % S) * kStageBytes<RP>, *us = xs + kXBytes;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int valid = xrow[i] >= 0 ? left : 0;
-                    copy8<V16>(xs + (cj >> 3) * kAtom + sw128(ct + 16 * i, cj & 7),
-                               valid > 0 ? x + static_cast<int64_t>(xrow[i]) * p.ldx : p.x, valid, p.ax);
+                    uint8_t *dst = xs + (cj >> 3) * kAtom + sw128(ct + 16 * i, cj & 7);
+                    if (MODE == kRows2) {
+                        *reinterpret_cast<uint4 *>(dst) = held[MODE == kRows2 ? i : 0];
+                    } else {
+                        const int valid = xrow[i] >= 0 ? left : 0;
+                        copy8<MODE>(dst, valid > 0 ? x + static_cast<int64_t>(xrow[i]) * p.ldx : p.x, valid, p.ax);
+                    }
                 }
-                fetch_rows(s + 1);
+                if (MODE == kRows2) {
+                    hold();
+                    fetch_rows(s + 2);
+                } else {
+                    fetch_rows(s + 1);
+                }
                 // U: its two parts, RP / 8 chunks of 64 tokens
 #pragma unroll
                 for (int i = 0; i < 2 * kTok * (RP / 8) / 256; ++i) {
@@ -185,8 +205,8 @@ __global__ void __launch_bounds__(kThreads) sum_kernel(const SumArgs a) {
     }
 }
 
-template <int RP, bool V16> cudaError_t launch_v(const GradArgs &a, int parts, cudaStream_t s) {
-    auto kern = grad_kernel<RP, V16>;
+template <int RP, int MODE> cudaError_t launch_m(const GradArgs &a, int parts, cudaStream_t s) {
+    auto kern = grad_kernel<RP, MODE>;
     static std::once_flag once;
     static cudaError_t err = cudaSuccess;
     if (allow_smem(kern, kSmem<RP>, once, err) != cudaSuccess) return err;
@@ -194,7 +214,11 @@ template <int RP, bool V16> cudaError_t launch_v(const GradArgs &a, int parts, c
                            kSmem<RP>, s, a);
 }
 template <int RP> cudaError_t launch_rp(const GradArgs &a, int parts, cudaStream_t s) {
-    return a.p[0].ax == 16 && a.p[1].ax == 16 ? launch_v<RP, true>(a, parts, s) : launch_v<RP, false>(a, parts, s);
+    switch (rows_mode(a.p[0].ax < a.p[1].ax ? a.p[0].ax : a.p[1].ax)) {
+        case kRows16: return launch_m<RP, kRows16>(a, parts, s);
+        case kRows4: return launch_m<RP, kRows4>(a, parts, s);
+        default: return launch_m<RP, kRows2>(a, parts, s);
+    }
 }
 
 }  // namespace

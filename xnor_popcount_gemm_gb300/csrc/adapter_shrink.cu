@@ -46,7 +46,8 @@ __device__ __forceinline__ void put_split(const SplitRows &o, int64_t at, int r,
     }
 }
 
-template <typename T, int RP, bool WT, bool V16>
+// MODE: how the rows of X and W are fetched.
+template <typename T, int RP, bool WT, int MODE>
 __global__ void __launch_bounds__(32 * kWarps, 2) shrink_kernel(const ShrinkArgs a) {
     extern __shared__ uint8_t dyn[];
     constexpr int S = kStages<RP, WT>, kCols = RP < 32 ? 32 : RP;
@@ -96,34 +97,54 @@ __global__ void __launch_bounds__(32 * kWarps, 2) shrink_kernel(const ShrinkArgs
             live[i] = cr + 32 * i < tile.n;
             xr[i] = a.x + static_cast<int64_t>(rows[cr + 32 * i]) * a.ldx + 8 * cj;
         }
+        // its chunk i of stage s: where it goes, where it comes from, how much of it there is
+        constexpr int kXChunks = 4, kWChunks = WT ? (kStep * (RP / 8) + 255) / 256 : (RP + 31) / 32;
+        auto chunk = [&](int s, int i, uint8_t *&dst, const uint16_t *&src, int &valid) {
+            uint8_t *xs = smem + (s % S) * kStageBytes<RP, WT>, *ws = xs + kXBytes;
+            const int k0 = (s0 + s) * kStep, left = a.C - k0;
+            if (i < kXChunks) {
+                valid = live[i] ? left - 8 * cj : 0;
+                dst = xs + sw128(cr + 32 * i, cj);
+                src = valid > 0 ? xr[i] + k0 : a.x;
+            } else if constexpr (!WT) {
+                const int r = cr + 32 * (i - kXChunks);
+                valid = r < a.R ? left - 8 * cj : 0;
+                dst = RP >= 32 || r < RP ? ws + sw128(r, cj) : nullptr;
+                src = valid > 0 ? w + static_cast<int64_t>(r) * a.C + k0 + 8 * cj : a.w;
+            } else {
+                // rows of 64 ranks, 64 elements of the long axis to an atom
+                const int at = tid + 256 * (i - kXChunks), k = at / (RP / 8), j = at % (RP / 8);
+                valid = k < left ? a.R - 8 * j : 0;
+                dst = RP >= 32 || k < kStep ? ws + (j >> 3) * kAtom + sw128(k, j & 7) : nullptr;
+                src = valid > 0 ? w + static_cast<int64_t>(k0 + k) * a.R + 8 * j : a.w;
+            }
+        };
+        uint4 held[MODE == kRows2 ? kXChunks + kWChunks : 1];    // (kRows2) the next stage, on its way
+        auto hold = [&](int s) {
+#pragma unroll
+            for (int i = 0; i < kXChunks + kWChunks; ++i) {
+                uint8_t *dst;
+                const uint16_t *src;
+                int valid;
+                chunk(s, i, dst, src, valid);
+                held[MODE == kRows2 ? i : 0] = valid > 0 ? load8(src, valid) : make_uint4(0u, 0u, 0u, 0u);
+            }
+        };
+        if (MODE == kRows2) hold(0);
         for (int s = 0; s < n + S - 1; ++s) {
             if (s < n) {
                 if (s >= S) wait_landed(empty[s % S], static_cast<uint32_t>(s / S - 1) & 1u, &abort_flag, a.err, a.limit_ns);
-                uint8_t *xs = smem + (s % S) * kStageBytes<RP, WT>, *ws = xs + kXBytes;
-                const int k0 = (s0 + s) * kStep, left = a.C - k0;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int valid = live[i] ? left - 8 * cj : 0;
-                    copy8<V16>(xs + sw128(cr + 32 * i, cj), valid > 0 ? xr[i] + k0 : a.x, valid, a.ax);
+                for (int i = 0; i < kXChunks + kWChunks; ++i) {
+                    uint8_t *dst;
+                    const uint16_t *src;
+                    int valid;
+                    chunk(s, i, dst, src, valid);
+                    if (i >= kXChunks && dst == nullptr) continue;
+                    if (MODE == kRows2) *reinterpret_cast<uint4 *>(dst) = held[MODE == kRows2 ? i : 0];
+                    else copy8<MODE>(dst, src, valid, i < kXChunks ? a.ax : a.aw);
                 }
-                if constexpr (!WT) {
-#pragma unroll
-                    for (int i = 0; i < (RP + 31) / 32; ++i) {
-                        const int r = cr + 32 * i, valid = r < a.R ? left - 8 * cj : 0;
-                        if (RP >= 32 || r < RP)
-                            copy8<V16>(ws + sw128(r, cj), valid > 0 ? w + static_cast<int64_t>(r) * a.C + k0 + 8 * cj : a.w, valid, a.aw);
-                    }
-                } else {
-                    // rows of 64 ranks, 64 elements of the long axis to an atom
-#pragma unroll
-                    for (int i = 0; i < (kStep * (RP / 8) + 255) / 256; ++i) {
-                        const int at = tid + 256 * i, k = at / (RP / 8), j = at % (RP / 8);
-                        const int valid = k < left ? a.R - 8 * j : 0;
-                        if (RP >= 32 || k < kStep)
-                            copy8<V16>(ws + (j >> 3) * kAtom + sw128(k, j & 7),
-                                       valid > 0 ? w + static_cast<int64_t>(k0 + k) * a.R + 8 * j : a.w, valid, a.aw);
-                    }
-                }
+                if (MODE == kRows2 && s + 1 < n) hold(s + 1);
             }
             cp_async_commit();
             if (s >= S - 1) {                               // the stage asked for S - 1 turns ago has landed
@@ -214,20 +235,32 @@ __global__ void __launch_bounds__(32 * kWarps, 2) shrink_kernel(const ShrinkArgs
     if (c > 1) tc::cluster_sync();                          // nobody leaves while its sums are read
 }
 
-template <typename T, int RP, bool WT, bool V16> cudaError_t launch_v(ShrinkArgs a, int tiles, cudaStream_t s) {
-    auto kern = shrink_kernel<T, RP, WT, V16>;
+template <typename T, int RP, bool WT, int MODE> cudaError_t launch_m(ShrinkArgs a, int tiles, cudaStream_t s) {
+    auto kern = shrink_kernel<T, RP, WT, MODE>;
     static std::once_flag once;
     static cudaError_t err = cudaSuccess;
     if (allow_smem(kern, kSmem<RP, WT>, once, err) != cudaSuccess) return err;
-    const int steps = (a.C + kStep - 1) / kStep;
-    int c = 1;
-    // pieces of at least four stages until the CTAs fill the machine twice
-    while (c < 8 && tiles * c < 2 * device_sm_count() && steps >= 8 * c) c *= 2;
-    a.cluster = c;
-    return launch_cluster(kern, tiles * c, c, 32 * kWarps, kSmem<RP, WT>, s, static_cast<const ShrinkArgs>(a));
+    // CTAs a tile, as many as end soonest: in waves of two CTAs an SM, each of its steps and of what it
+    // costs to begin, join and end, about six steps' time. (Half precision joins rows by whole warps:
+    // powers of two.)
+    const int steps = (a.C + kStep - 1) / kStep, slots = 2 * device_sm_count();
+    int64_t best = 0;
+    for (int c = 1; c <= 8; ++c) {
+        if (std::is_same<T, __half>::value && (c & (c - 1)) != 0) continue;
+        const int64_t waves = (static_cast<int64_t>(tiles) * c + slots - 1) / slots, cost = waves * ((steps + c - 1) / c + 6);
+        if (c == 1 || (cost < best && steps >= 2 * c)) {
+            best = cost;
+            a.cluster = c;
+        }
+    }
+    return launch_cluster(kern, tiles * a.cluster, a.cluster, 32 * kWarps, kSmem<RP, WT>, s, static_cast<const ShrinkArgs>(a));
 }
 template <typename T, int RP, bool WT> cudaError_t launch_rp(const ShrinkArgs &a, int tiles, cudaStream_t s) {
-    return a.ax == 16 && a.aw == 16 ? launch_v<T, RP, WT, true>(a, tiles, s) : launch_v<T, RP, WT, false>(a, tiles, s);
+    switch (rows_mode(a.ax < a.aw ? a.ax : a.aw)) {
+        case kRows16: return launch_m<T, RP, WT, kRows16>(a, tiles, s);
+        case kRows4: return launch_m<T, RP, WT, kRows4>(a, tiles, s);
+        default: return launch_m<T, RP, WT, kRows2>(a, tiles, s);
+    }
 }
 template <typename T, bool WT> cudaError_t launch_t(const ShrinkArgs &a, int tiles, cudaStream_t s) {
     if (a.R <= 16) return launch_rp<T, 16, WT>(a, tiles, s);

@@ -20,26 +20,16 @@ namespace {
 // 32 are its columns 2t, 2t + 1 in the unit's instruction j, so that a lane ends
 // up with 8 consecutive results of a token.
 
-// Elements k .. k + 7 of a row of n, zeros beyond. al: bytes the rows start at multiples of.
-__device__ __forceinline__ uint4 row8(const uint16_t *p, int k, int n, int al) {
-    uint32_t w[4] = {0u, 0u, 0u, 0u};
+// Elements k .. k + 7 of a row of n, zeros beyond. al: bytes the rows start at multiples of (FAST: 16).
+template <bool FAST> __device__ __forceinline__ uint4 row8(const uint16_t *p, int k, int n, int al) {
     if (k >= n) return make_uint4(0u, 0u, 0u, 0u);
+    if constexpr (FAST) return __ldg(reinterpret_cast<const uint4 *>(p + k));
     if (al == 16 && k + 8 <= n) return __ldg(reinterpret_cast<const uint4 *>(p + k));
     if (al >= 8 && k + 8 <= n) {
         const uint2 lo = __ldg(reinterpret_cast<const uint2 *>(p + k)), hi = __ldg(reinterpret_cast<const uint2 *>(p + k + 4));
         return make_uint4(lo.x, lo.y, hi.x, hi.y);
     }
-    if (al >= 4 && k + 8 <= n) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = __ldg(reinterpret_cast<const uint32_t *>(p + k) + i);
-        return make_uint4(w[0], w[1], w[2], w[3]);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t lo = k + 2 * i < n ? __ldg(p + k + 2 * i) : 0u, hi = k + 2 * i + 1 < n ? __ldg(p + k + 2 * i + 1) : 0u;
-        w[i] = lo | (hi << 16);
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
+    return load8(p + k, n - k);
 }
 
 // Eight consecutive values of base, as they lie there (fp32: two vectors).
@@ -47,8 +37,8 @@ struct Base8 {
     uint4 v[2];
 };
 
-// RB: blocks of 16 ranks; NB: blocks of 8 tokens.
-template <typename T, int RB, int NB>
+// RB: blocks of 16 ranks; NB: blocks of 8 tokens. FAST: every row starts at a 16-byte multiple and holds whole vectors.
+template <typename T, int RB, int NB, bool FAST>
 __global__ void __launch_bounds__(kThreads, RB * NB <= 4 ? 2 : 1) small_kernel(const SmallArgs a, int out_f32) {
     constexpr int RP = 16 * RB, TOK = 8 * NB, UP = RP + 4;
     constexpr int RK = (RB + 1) / 2;                        // 32-rank pieces of B's rows
@@ -61,6 +51,11 @@ __global__ void __launch_bounds__(kThreads, RB * NB <= 4 ? 2 : 1) small_kernel(c
     const int rank = c > 1 ? static_cast<int>(tc::cluster_ctarank()) : 0;
     pdl_launch_dependents();
     pdl_wait();
+    if (static_cast<int>(blockIdx.x) >= a.tiles * c) {      // whole clusters
+        pass_rows<T>(a.pass, out_f32 != 0, blockIdx.x - a.tiles * c, gridDim.x - a.tiles * c);
+        return;
+    }
+    if (c > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");   // this CTA has started
     const AdapterTile tile = a.plan.tiles[blockIdx.x / c];
     const uint16_t *A = a.A + static_cast<int64_t>(tile.adapter) * a.R * a.K;
     const uint16_t *B = a.B + static_cast<int64_t>(tile.adapter) * a.R * a.N;
@@ -83,7 +78,7 @@ __global__ void __launch_bounds__(kThreads, RB * NB <= 4 ? 2 : 1) small_kernel(c
             const int n = 32 * unit + 8 * (g >> 1) + 2 * j + (g & 1);
             const uint16_t *p = B + static_cast<int64_t>(n) * a.R;
 #pragma unroll
-            for (int q = 0; q < RK; ++q) w[j][q] = unit < n1 && n < a.N ? row8(p, 32 * q + 8 * t, a.R, a.ab) : zero;
+            for (int q = 0; q < RK; ++q) w[j][q] = unit < n1 && n < a.N ? row8<FAST>(p, 32 * q + 8 * t, a.R, a.ab) : zero;
         }
     };
     auto load_base = [&](int unit, Base8 (&b)[NB]) {
@@ -95,7 +90,7 @@ __global__ void __launch_bounds__(kThreads, RB * NB <= 4 ? 2 : 1) small_kernel(c
             const int64_t at = row[j] * a.ldb + n;
             if (a.base_f32) {
                 const float *p = static_cast<const float *>(a.base) + at;
-                if (a.wide) {
+                if (FAST || a.wide) {
                     b[j].v[0] = __ldcs(reinterpret_cast<const uint4 *>(p));
                     b[j].v[1] = __ldcs(reinterpret_cast<const uint4 *>(p) + 1);
                 } else {
@@ -107,7 +102,7 @@ __global__ void __launch_bounds__(kThreads, RB * NB <= 4 ? 2 : 1) small_kernel(c
                 }
             } else {
                 const uint16_t *p = static_cast<const uint16_t *>(a.base) + at;
-                if (a.wide) {
+                if (FAST || a.wide) {
                     b[j].v[0] = __ldcs(reinterpret_cast<const uint4 *>(p));
                 } else {
                     uint32_t f[4];
@@ -141,12 +136,12 @@ __global__ void __launch_bounds__(kThreads, RB * NB <= 4 ? 2 : 1) small_kernel(c
         const int k = 32 * s + 8 * t;
         uint4 xv[NB];
 #pragma unroll
-        for (int j = 0; j < NB; ++j) xv[j] = live[j] ? row8(a.x + row[j] * a.ldx, k, a.K, a.ax) : zero;
+        for (int j = 0; j < NB; ++j) xv[j] = live[j] ? row8<FAST>(a.x + row[j] * a.ldx, k, a.K, a.ax) : zero;
 #pragma unroll
         for (int m = 0; m < RB; ++m) {
             const int r0 = 16 * m + g, r1 = r0 + 8;
-            const uint4 w0 = r0 < a.R ? row8(A + static_cast<int64_t>(r0) * a.K, k, a.K, a.aa) : zero;
-            const uint4 w1 = r1 < a.R ? row8(A + static_cast<int64_t>(r1) * a.K, k, a.K, a.aa) : zero;
+            const uint4 w0 = r0 < a.R ? row8<FAST>(A + static_cast<int64_t>(r0) * a.K, k, a.K, a.aa) : zero;
+            const uint4 w1 = r1 < a.R ? row8<FAST>(A + static_cast<int64_t>(r1) * a.K, k, a.K, a.aa) : zero;
             const uint32_t f0[4] = {w0.x, w1.x, w0.y, w1.y}, f1[4] = {w0.z, w1.z, w0.w, w1.w};
 #pragma unroll
             for (int j = 0; j < NB; ++j) {
@@ -162,8 +157,8 @@ __global__ void __launch_bounds__(kThreads, RB * NB <= 4 ? 2 : 1) small_kernel(c
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 part[warp][8 * j + 2 * t + (e & 1)][16 * m + g + (e >> 1) * 8] = acc[m][j][e];
-    if (c > 1) tc::cluster_sync();                          // and every CTA of the cluster has started
-    else __syncthreads();
+    __syncthreads();
+    if (c > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");             // every CTA of the cluster has
     for (int i = tid; i < TOK * RP; i += kThreads) {
         const int tok = i / RP, r = i % RP;
         float v = 0.0f;
@@ -266,7 +261,7 @@ __global__ void __launch_bounds__(kThreads, RB * NB <= 4 ? 2 : 1) small_kernel(c
                 const int64_t at = row[j] * a.ldo + n;
                 if (out_f32) {
                     float *o = static_cast<float *>(a.out) + at;
-                    if (a.wide) {
+                    if (FAST || a.wide) {
                         *reinterpret_cast<float4 *>(o) = make_float4(f[j][0], f[j][1], f[j][2], f[j][3]);
                         *(reinterpret_cast<float4 *>(o) + 1) = make_float4(f[j][4], f[j][5], f[j][6], f[j][7]);
                     } else {
@@ -276,7 +271,7 @@ __global__ void __launch_bounds__(kThreads, RB * NB <= 4 ? 2 : 1) small_kernel(c
                     }
                 } else {
                     uint16_t *o = static_cast<uint16_t *>(a.out) + at;
-                    if (a.wide) {
+                    if (FAST || a.wide) {
                         *reinterpret_cast<uint4 *>(o) = make_uint4(pack2<T>(f[j][0], f[j][1]), pack2<T>(f[j][2], f[j][3]),
                                                                    pack2<T>(f[j][4], f[j][5]), pack2<T>(f[j][6], f[j][7]));
                     } else {
@@ -290,8 +285,8 @@ __global__ void __launch_bounds__(kThreads, RB * NB <= 4 ? 2 : 1) small_kernel(c
     }
 }
 
-template <typename T, int RB, int NB> cudaError_t launch_rn(SmallArgs a, bool out_f32, int tiles, cudaStream_t s) {
-    auto kern = small_kernel<T, RB, NB>;
+template <typename T, int RB, int NB, bool FAST> cudaError_t launch_f(SmallArgs a, bool out_f32, int tiles, cudaStream_t s) {
+    auto kern = small_kernel<T, RB, NB, FAST>;
     constexpr int smem = 8 * 8 * NB * (32 * RB + 4) * static_cast<int>(sizeof(float));
     static std::once_flag once;
     static cudaError_t err = cudaSuccess;
@@ -300,19 +295,25 @@ template <typename T, int RB, int NB> cudaError_t launch_rn(SmallArgs a, bool ou
     // the widest cluster with which two CTAs an SM hold all tiles
     while (c < 8 && tiles * c <= device_sm_count()) c *= 2;
     a.cluster = c;
+    a.tiles = tiles;
+    const int pass = a.pass.n < device_sm_count() ? a.pass.n : device_sm_count();
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
     attr[0] = pdl_attribute();
     attr[1].id = cudaLaunchAttributeClusterDimension;
     attr[1].val.clusterDim.x = static_cast<unsigned>(c);
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cfg.gridDim = dim3(static_cast<unsigned>(tiles * c));
+    cfg.gridDim = dim3(static_cast<unsigned>((tiles + (pass + c - 1) / c) * c));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, kern, static_cast<const SmallArgs>(a), static_cast<int>(out_f32));
+}
+template <typename T, int RB, int NB> cudaError_t launch_rn(const SmallArgs &a, bool out_f32, int tiles, cudaStream_t s) {
+    const bool fast = a.ax == 16 && a.aa == 16 && a.ab == 16 && a.wide;
+    return fast ? launch_f<T, RB, NB, true>(a, out_f32, tiles, s) : launch_f<T, RB, NB, false>(a, out_f32, tiles, s);
 }
 template <typename T, int NB> cudaError_t launch_n(const SmallArgs &a, bool out_f32, int tiles, cudaStream_t s) {
     if (a.R <= 16) return launch_rn<T, 1, NB>(a, out_f32, tiles, s);
