@@ -140,21 +140,34 @@ struct PassArgs {
     int64_t ldo;
     float *u;
 };
-// Rows first, first + step, ... of them: CTAs of the kernels below that are left over take them along.
+// Pieces first, first + step, ... of them (8 columns a thread of 256): CTAs of the kernels below that are left
+// over take them along.
+constexpr int kPassCols = 2048;
+inline int64_t pass_pieces(const PassArgs &a) { return static_cast<int64_t>(a.n) * ((a.N + kPassCols - 1) / kPassCols); }
 template <typename T> __device__ void pass_rows(const PassArgs &a, bool out_f32, int first, int step) {
-    for (int i = first; i < a.n; i += step) {
-        const int64_t row = a.rows[i];
-        if (a.u != nullptr)
-            for (int r = threadIdx.x; r < a.R; r += blockDim.x) a.u[row * a.R + r] = 0.0f;
+    const int per = (a.N + kPassCols - 1) / kPassCols;
+    if (threadIdx.x >= 256) return;
+    for (int64_t i = first; i < static_cast<int64_t>(a.n) * per; i += step) {
+        const int64_t row = a.rows[i / per];
+        const int c0 = static_cast<int>(i % per) * kPassCols;
+        if (a.u != nullptr && c0 == 0)
+            for (int r = threadIdx.x; r < a.R; r += 256) a.u[row * a.R + r] = 0.0f;
         if (a.out == nullptr) continue;
-#pragma unroll 4
-        for (int c = threadIdx.x; c < a.N; c += blockDim.x) {
-            float v = 0.0f;
-            if (a.base != nullptr)
-                v = a.base_f32 ? static_cast<const float *>(a.base)[row * a.ldb + c]
-                               : Elem<T>::to_f32(static_cast<const T *>(a.base)[row * a.ldb + c]);
-            if (out_f32) static_cast<float *>(a.out)[row * a.ldo + c] = v;
-            else static_cast<T *>(a.out)[row * a.ldo + c] = to16<T>(v);
+        float v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {                       // neighbours take neighbours: any alignment travels together
+            const int c = c0 + static_cast<int>(threadIdx.x) + 256 * k;
+            v[k] = 0.0f;
+            if (a.base != nullptr && c < a.N)
+                v[k] = a.base_f32 ? static_cast<const float *>(a.base)[row * a.ldb + c]
+                                  : Elem<T>::to_f32(static_cast<const T *>(a.base)[row * a.ldb + c]);
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int c = c0 + static_cast<int>(threadIdx.x) + 256 * k;
+            if (c >= a.N) continue;
+            if (out_f32) static_cast<float *>(a.out)[row * a.ldo + c] = v[k];
+            else static_cast<T *>(a.out)[row * a.ldo + c] = to16<T>(v[k]);
         }
     }
 }

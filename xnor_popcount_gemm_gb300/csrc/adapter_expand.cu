@@ -310,7 +310,8 @@ cudaError_t launch_rp(const ExpandArgs &a, cudaStream_t s) {
     static std::once_flag once;
     static cudaError_t err = cudaSuccess;
     if (allow_smem(kern, smem, once, err) != cudaSuccess) return err;
-    const int pass = a.pass.n < 2 * device_sm_count() ? a.pass.n : 2 * device_sm_count();
+    const int64_t pieces = pass_pieces(a.pass);
+    const int pass = static_cast<int>(pieces < 2 * device_sm_count() ? pieces : 2 * device_sm_count());
     return launch_pdl_smem(kern, dim3(static_cast<unsigned>(a.tiles * a.splits + pass)), dim3(kThreads), smem, s, a);
 }
 template <typename T, bool WT, bool OF32, bool FAST, bool BF32> cudaError_t launch_r(const ExpandArgs &a, cudaStream_t s) {
@@ -361,8 +362,8 @@ cudaError_t launch_expand(bt_dtype t, bool wt, bool out_f32, const ExpandArgs &a
 
 cudaError_t launch_pass(bt_dtype t, bool out_f32, const PassArgs &a, cudaStream_t s) {
     if (a.n == 0 || (a.out == nullptr && a.u == nullptr)) return cudaSuccess;
-    const int slots = 8 * device_sm_count();
-    const dim3 grid(static_cast<unsigned>(a.n < slots ? a.n : slots));
+    const int64_t pieces = pass_pieces(a), slots = 8 * device_sm_count();
+    const dim3 grid(static_cast<unsigned>(pieces < slots ? pieces : slots));
     return t == BT_F16 ? launch_pdl(pass_kernel<__half>, grid, dim3(kThreads), s, a, static_cast<int>(out_f32))
                        : launch_pdl(pass_kernel<__nv_bfloat16>, grid, dim3(kThreads), s, a, static_cast<int>(out_f32));
 }

@@ -21,6 +21,9 @@ constexpr int kXBytes = 2 * kAtom;
 template <int RP, bool WT> constexpr int kWBytes = WT ? (RP <= 64 ? 1 : 2) * kAtom : RP * 128;
 template <int RP, bool WT> constexpr int kStageBytes = kXBytes + kWBytes<RP, WT>;
 template <int RP, bool WT> constexpr int kStages = 100 * 1024 / kStageBytes<RP, WT>;
+// A stage is handed over once the one kLag turns later has been asked for, two fewer than there are, so that asking
+// never waits for the products of the stage just handed over.
+template <int RP, bool WT> constexpr int kLag = kStages<RP, WT> - 2;
 template <int RP> constexpr int kSumPitch = RP + 4;
 template <int RP, bool WT> constexpr int kSmem = kStages<RP, WT> * kStageBytes<RP, WT> + 1024;
 static_assert(kAdapterTile * kSumPitch<128> * 4 <= kStages<128, false> * kStageBytes<128, false>, "sums take the ring's place");
@@ -50,7 +53,7 @@ __device__ __forceinline__ void put_split(const SplitRows &o, int64_t at, int r,
 template <typename T, int RP, bool WT, int MODE>
 __global__ void __launch_bounds__(32 * kWarps, 2) shrink_kernel(const ShrinkArgs a) {
     extern __shared__ uint8_t dyn[];
-    constexpr int S = kStages<RP, WT>, kCols = RP < 32 ? 32 : RP;
+    constexpr int S = kStages<RP, WT>, D = kLag<RP, WT>, kCols = RP < 32 ? 32 : RP;
     static_assert(S >= 3 && S <= 8, "stages");
     __shared__ alignas(8) uint64_t full[S], empty[S], done;
     __shared__ uint32_t tmem_slot, abort_flag;
@@ -131,7 +134,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) shrink_kernel(const ShrinkArgs
             }
         };
         if (MODE == kRows2) hold(0);
-        for (int s = 0; s < n + S - 1; ++s) {
+        for (int s = 0; s < n + D; ++s) {
             if (s < n) {
                 if (s >= S) wait_landed(empty[s % S], static_cast<uint32_t>(s / S - 1) & 1u, &abort_flag, a.err, a.limit_ns);
 #pragma unroll
@@ -147,11 +150,11 @@ __global__ void __launch_bounds__(32 * kWarps, 2) shrink_kernel(const ShrinkArgs
                 if (MODE == kRows2 && s + 1 < n) hold(s + 1);
             }
             cp_async_commit();
-            if (s >= S - 1) {                               // the stage asked for S - 1 turns ago has landed
-                cp_async_wait<S - 1>();
+            if (s >= D) {                                   // the stage asked for D turns ago has landed
+                cp_async_wait<D>();
                 tc::fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) tc::mbar_arrive(smem_u32(&full[(s - (S - 1)) % S]));
+                if (lane == 0) tc::mbar_arrive(smem_u32(&full[(s - D) % S]));
             }
         }
     } else if (lane == 0) {

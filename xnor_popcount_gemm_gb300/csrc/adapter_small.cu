@@ -296,7 +296,8 @@ template <typename T, int RB, int NB, bool FAST> cudaError_t launch_f(SmallArgs 
     while (c < 8 && tiles * c <= device_sm_count()) c *= 2;
     a.cluster = c;
     a.tiles = tiles;
-    const int pass = a.pass.n < device_sm_count() ? a.pass.n : device_sm_count();
+    const int64_t pieces = pass_pieces(a.pass);
+    const int pass = static_cast<int>(pieces < 2 * device_sm_count() ? pieces : 2 * device_sm_count());
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
     attr[0] = pdl_attribute();
