@@ -717,7 +717,7 @@ bt_status bt_adapter_plan(const int32_t *adapter, int64_t T, int64_t L, void *pl
 
 /* Workspace bytes of bt_adapter_linear (0 when no adapter has more than 32
  * tokens, or for sizes out of range). */
-size_t bt_adapter_linear_workspace(int64_t T, int64_t R, const bt_adapter_plan_info *info);
+size_t bt_adapter_linear_workspace(int64_t T, int64_t K, int64_t R, const bt_adapter_plan_info *info);
 
 /*
  * bt_adapter_linear -- the formula above for x [T, K].
@@ -736,7 +736,7 @@ size_t bt_adapter_linear_workspace(int64_t T, int64_t R, const bt_adapter_plan_i
  * rounded once. Any sizes and element alignments are served; rows that start
  * at multiples of 16 bytes (and R a multiple of 8) are faster. 1 <= R <= 128;
  * T, K, N < 2^24. T = 0 or N = 0 does nothing. workspace:
- * bt_adapter_linear_workspace(T, R, info) bytes, 256-byte aligned.
+ * bt_adapter_linear_workspace(T, K, R, info) bytes, 256-byte aligned.
  * Equal calls give equal results.
  * Errors: INVALID_ARG, ALIGNMENT, WORKSPACE, UNSUPPORTED, CUDA.
  */

@@ -9,7 +9,7 @@ import torch
 
 import xnor_popcount_gemm_gb300 as bt
 
-TILE, SMALL, SMALL_MOST, PARTS = 128, 16, 32, 4
+TILE, SMALL, SMALL_MOST, PARTS = 128, 16, 32, 8
 
 
 def _plan(ids, L):
@@ -129,7 +129,7 @@ def test_forward_refusals():
                 dict(A=None), dict(B=None), dict(s=None), dict(plan=None), dict(out=None),
                 dict(base=8192, ldb=32, bt_=bt.BT_F32), dict(base=8192, ldb=40, bt_=bt.BT_BF16, ldo=32),
                 dict(info=_info(tiles=5)), dict(info=_info(tiles=-1)), dict(info=_info(without=5)),
-                dict(info=_info(slots=9)), dict(info=_info(parts=0))):
+                dict(info=_info(slots=17)), dict(info=_info(parts=0))):
         assert _fwd(**bad) == bt.BT_ERR_INVALID_ARG, bad
     for bad in (dict(R=129), dict(K=1 << 24, ldx=1 << 24), dict(N=1 << 24, ldo=1 << 24), dict(ldx=1 << 37)):
         assert _fwd(**bad) == bt.BT_ERR_UNSUPPORTED, bad
@@ -141,9 +141,11 @@ def test_forward_refusals():
     assert _fwd(**large, ws=16384 + 16) == bt.BT_ERR_ALIGNMENT
     assert _fwd(T=0, info=_info(T=0), x=None) == _fwd(N=0, out=None) == bt.BT_OK
     few, many = (bt.bt_adapter_plan([0] * n, 2, device="cpu") for n in (4, 40))
-    assert bt.bt_adapter_linear_workspace(40, 8, many) == 2 * 1280 + 256         # two 16-bit values of 16 ranks, a power
-    assert bt.bt_adapter_linear_workspace(40, 129, many) == 0
-    assert bt.bt_adapter_linear_workspace(4, 8, few) == 0
+    assert bt.bt_adapter_linear_workspace(40, 64, 8, many) == 2 * 1280 + 256         # two 16-bit values of 16 ranks, a power
+    # a width that is no multiple of 4: room for the rows of x and A at 16-byte multiples
+    assert bt.bt_adapter_linear_workspace(40, 66, 8, many) == 2 * 1280 + 256 + 5888 + 2304
+    assert bt.bt_adapter_linear_workspace(40, 64, 129, many) == 0
+    assert bt.bt_adapter_linear_workspace(4, 64, 8, few) == 0
 
 
 def test_backward_refusals():

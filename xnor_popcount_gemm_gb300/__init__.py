@@ -108,7 +108,7 @@ class AdapterPlanInfo(ctypes.Structure):
 _pinfo = ctypes.POINTER(AdapterPlanInfo)
 _c_aplan_bytes = _sig("bt_adapter_plan_bytes", _sz, [_i64, _i64])
 _c_aplan = _sig("bt_adapter_plan", _i, [_p, _i64, _i64, _p, _sz, _pinfo])
-_c_alin_ws = _sig("bt_adapter_linear_workspace", _sz, [_i64, _i64, _pinfo])
+_c_alin_ws = _sig("bt_adapter_linear_workspace", _sz, [_i64, _i64, _i64, _pinfo])
 _c_alin = _sig("bt_adapter_linear", _i, [_p, _i, _i64, _p, _p, _p, _p, _pinfo, _i64, _i64, _i64, _i64, _p, _i, _i64,
                                          _p, _i, _i64, _p, _p, _sz, _p])
 _c_abwd_ws = _sig("bt_adapter_linear_backward_workspace", _sz, [_i64, _i64, _i64, _i64, _pinfo])
@@ -660,6 +660,7 @@ class AdapterPlan:
 
     def __init__(self, buffer: torch.Tensor, info: AdapterPlanInfo):
         self.buffer, self.info = buffer, info
+        self.tokens, self.adapters = info.tokens, info.adapters
         self._ref = ctypes.byref(info)
 
     def __repr__(self) -> str:
@@ -693,30 +694,43 @@ def bt_adapter_plan(adapter_ids, num_adapters: int, device="cuda", stream=None) 
         return AdapterPlan(host.to(device, non_blocking=True), info)
 
 
-def _rows(t: torch.Tensor, name: str, shape: tuple, dtypes) -> int:
-    """Elements from one row of a 2-D operand to the next."""
-    if t.shape != shape or t.dtype not in dtypes or not t.is_cuda or (shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"{name} must be a CUDA tensor of shape {list(shape)} and type {' or '.join(map(str, dtypes))}, "
-                         "with elements of a row next to each other")
-    return t.stride(0) if shape[0] > 1 else max(shape[1], t.stride(0))
+_F32, _BF16, _F16 = (torch.float32,), (torch.bfloat16,), (torch.float16,)
+_HALVES = {torch.bfloat16: _BF16 + _F32, torch.float16: _F16 + _F32}
+
+
+def _rows(t: torch.Tensor, name: str, T: int, C: int, dtypes) -> int:
+    """Elements from one row of a [T, C] operand to the next."""
+    if t.shape != (T, C) or t.dtype not in dtypes or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor of shape {[T, C]} and type {' or '.join(map(str, dtypes))}")
+    ld, one = t.stride()
+    if one != 1 and C > 1:
+        raise ValueError(f"{name} must have the elements of a row next to each other")
+    return ld if T > 1 else max(C, ld)
 
 
 def _adapter_args(x, a, b, scale, plan):
     if x.dim() != 2 or a.dim() != 3 or b.dim() != 3:
         raise ValueError("x must be [T, K], a [L, R, K] and b [L, N, R]")
     T, K = x.shape
-    L, R, N = a.shape[0], a.shape[1], b.shape[1]
-    _dense(a, "a", (L, R, K), x.dtype)
-    _dense(b, "b", (L, N, R), x.dtype)
+    L, R, _ = a.shape
+    N = b.shape[1]
+    dt = x.dtype
+    if dt not in _HALVES:
+        raise ValueError("x must be bfloat16 or float16")
+    if a.shape != (L, R, K) or b.shape != (L, N, R) or a.dtype != dt or b.dtype != dt or not (a.is_cuda and b.is_cuda):
+        raise ValueError("a [L, R, K] and b [L, N, R] must be CUDA tensors of x's type that agree with x and with each other")
+    if not (a.is_contiguous() and b.is_contiguous()):
+        raise ValueError("a and b must be contiguous")
+    if scale.shape != (L,):
+        raise ValueError("scale must be [L]")
     _dense(scale, "scale", (L,), torch.float32)
-    if not isinstance(plan, AdapterPlan) or plan.info.tokens != T or plan.info.adapters != L:
-        raise ValueError("plan must be bt_adapter_plan of these tokens and adapters")
-    _on_gpu(plan=plan.buffer)
+    if type(plan) is not AdapterPlan or plan.tokens != T or plan.adapters != L or not plan.buffer.is_cuda:
+        raise ValueError("plan must be bt_adapter_plan of these tokens and adapters, on the device")
     return T, K, N, R
 
 
-def bt_adapter_linear_workspace(T: int, R: int, plan: AdapterPlan) -> int:
-    return int(_c_alin_ws(T, R, plan._ref))
+def bt_adapter_linear_workspace(T: int, K: int, R: int, plan: AdapterPlan) -> int:
+    return int(_c_alin_ws(T, K, R, plan._ref))
 
 
 def bt_adapter_linear(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, scale: torch.Tensor, plan: AdapterPlan,
@@ -728,21 +742,25 @@ def bt_adapter_linear(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, scale: 
     out_dtype (base's type, else x's). out may be base. u [T, R] (float), if
     given, receives a[i] x_t for the backward."""
     T, K, N, R = _adapter_args(x, a, b, scale, plan)
-    ldx = _rows(x, "x", (T, K), (torch.bfloat16, torch.float16))
-    both = (x.dtype, torch.float32)
-    ldb = 0 if base is None else _rows(base, "base", (T, N), both)
+    dt = x.dtype
+    ldx = _rows(x, "x", T, K, (dt,))
+    if base is None:
+        pbase, base_type, ldb = None, BT_F32, 0
+    else:
+        ldb = _rows(base, "base", T, N, _HALVES[dt])
+        pbase, base_type = base.data_ptr(), _DT[base.dtype]
     if out is None:
-        out = _empty((T, N), out_dtype if out_dtype is not None else x.dtype if base is None else base.dtype, x.device,
-                     stream)
-    ldo = _rows(out, "out", (T, N), both if out_dtype is None else (out_dtype,))
+        out = _empty((T, N), out_dtype if out_dtype is not None else dt if base is None else base.dtype, x.device, stream)
+    ldo = _rows(out, "out", T, N, _HALVES[dt] if out_dtype is None else (out_dtype,))
     if u is not None:
         _dense(u, "u", (T, R), torch.float32)
-    need = _c_alin_ws(T, R, plan._ref)
+    need = _c_alin_ws(T, K, R, plan._ref)
     if need and (workspace is None or workspace.numel() < need):
         workspace = _empty((need,), torch.uint8, x.device, stream)
-    _check(_c_alin(_ptr(x), _DT[x.dtype], ldx, _ptr(a), _ptr(b), _ptr(scale), _ptr(plan.buffer), plan._ref, T, K, N, R,
-                   _ptr(base), BT_F32 if base is None else _DT[base.dtype], ldb, _ptr(out), _DT[out.dtype], ldo,
-                   _ptr(u), _ptr(workspace), need, _on_stream(stream, x.device)))
+    _check(_c_alin(x.data_ptr(), _DT[dt], ldx, a.data_ptr(), b.data_ptr(), scale.data_ptr(), plan.buffer.data_ptr(),
+                   plan._ref, T, K, N, R, pbase, base_type, ldb, out.data_ptr(), _DT[out.dtype], ldo,
+                   None if u is None else u.data_ptr(), None if workspace is None else workspace.data_ptr(), need,
+                   _on_stream(stream, x.device)))
     return out
 
 
@@ -759,13 +777,12 @@ def bt_adapter_linear_backward(x: torch.Tensor, g: torch.Tensor, u: torch.Tensor
     grad_b [L, N, R], both float). grad_base [T, K], the projection's own
     input gradient, is added to grad_x, which may be grad_base itself."""
     T, K, N, R = _adapter_args(x, a, b, scale, plan)
-    bf16 = (torch.bfloat16,)
-    ldx, ldg = _rows(x, "x", (T, K), bf16), _rows(g, "g", (T, N), bf16)
+    ldx, ldg = _rows(x, "x", T, K, _BF16), _rows(g, "g", T, N, _BF16)
     _dense(u, "u", (T, R), torch.float32)
-    ldgb = 0 if grad_base is None else _rows(grad_base, "grad_base", (T, K), bf16)
+    ldgb = 0 if grad_base is None else _rows(grad_base, "grad_base", T, K, _BF16)
     if grad_x is None:
         grad_x = _empty((T, K), torch.bfloat16, x.device, stream)
-    ldgx = _rows(grad_x, "grad_x", (T, K), bf16)
+    ldgx = _rows(grad_x, "grad_x", T, K, _BF16)
     if grad_a is None:
         grad_a = _empty(a.shape, torch.float32, x.device, stream)
     else:

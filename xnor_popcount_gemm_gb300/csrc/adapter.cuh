@@ -182,6 +182,20 @@ struct SplitRows {
 };
 inline int padded_rank(int R) { return R <= 16 ? 16 : R <= 32 ? 32 : R <= 64 ? 64 : 128; }
 
+// Rows of an odd width, copied to rows that start at 16-byte multiples: `rows` of them, or, with parts, the R rows
+// of every adapter that has tokens.
+struct AlignArgs {
+    const uint16_t *src;
+    int64_t lds;
+    uint16_t *dst;
+    int64_t ldd;
+    int C;
+    int64_t rows;
+    const AdapterTile *parts;
+    int R, nparts;
+};
+cudaError_t launch_align(const AlignArgs &a, cudaStream_t s);
+
 // U[t, :] = s sum_c X[t, c] W[c, :] over tiles of 128 rows. WT = false: W is
 // [R, C] (A, for u), true: [C, R] (B, for dU).
 struct ShrinkArgs {
@@ -189,13 +203,16 @@ struct ShrinkArgs {
     const uint16_t *x;
     int64_t ldx;
     int ax, aw;                // alignment of the rows of X and W, bytes
-    const uint16_t *w;         // [L, R, C] or [L, C, R]
+    const uint16_t *w;         // [L, R, ldw] or [L, C, R]
+    int64_t ldw;               // (WT = false)
     int C, R;
     const float *scale;        // NULL: 1
     float *u;                  // [T, R] by token; NULL: not wanted
     SplitRows out;
     const float *given;        // (WT) [T, R] by token, to be split as well; into given_out
     SplitRows given_out;
+    unsigned int *zero;        // words to be zeroed for the kernels that follow
+    int zeros;
     int cluster;
     unsigned int *err;
     unsigned long long limit_ns;
@@ -207,7 +224,8 @@ cudaError_t launch_shrink(bt_dtype t, bool wt, const ShrinkArgs &a, int tiles, c
 struct ExpandArgs {
     Plan plan;
     SplitRows u;
-    const uint16_t *w;         // [L, C, R] or [L, R, C]
+    const uint16_t *w;         // [L, C, R] or [L, R, ldw]
+    int64_t ldw;               // (WT = true)
     int aw;                    // alignment of its rows, bytes
     int C, R;
     const float *scale;        // NULL: 1
@@ -245,22 +263,13 @@ struct GradArgs {
     GradProduct p[2];
     int R;
     int64_t slot_stride;
+    unsigned int *arrived;     // zeros: parts of a split adapter's column range that are done
+    int parts;
+    bool alone;                // no kernel of this call comes before
     unsigned int *err;
     unsigned long long limit_ns;
 };
 cudaError_t launch_grad(const GradArgs &a, int parts, cudaStream_t s);
-
-// Adds the parts' sums of every adapter that has several.
-struct SumArgs {
-    const AdapterTile *parts;
-    int n;                     // parts with a slot
-    const float *slots;
-    int64_t slot_stride;
-    int64_t len_a, len_b;      // R * K, R * N: the two gradients lie one after the other in a slot
-    int64_t off_b;             // where the second begins in a slot
-    float *grad_a, *grad_b;
-};
-cudaError_t launch_sum(const SumArgs &a, cudaStream_t s);
 
 // Tiles of up to 16 tokens: the whole adapter in one kernel.
 

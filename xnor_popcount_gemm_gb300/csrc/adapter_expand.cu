@@ -63,8 +63,10 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) expand_kernel(cons
     uint8_t *us = dyn + ((1024u - (smem_u32(dyn) & 1023u)) & 1023u), *wbuf = us + 2 * kUBytes<RP>;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     float *turn = reinterpret_cast<float *>(wbuf + 2 * kWBytes<RP, WT>) + warp * 16 * kTurnPitch;
-    pdl_wait();                                             // before tensor memory is taken, see shrink_kernel
+    // The plan, W and base were there before this call's first kernel began, which waited for all before it: only
+    // U, which that kernel writes, has to be waited for.
     if (static_cast<int>(blockIdx.x) >= a.tiles * a.splits) {
+        pdl_wait();
         pdl_launch_dependents();
         pass_rows<T>(a.pass, OF32, blockIdx.x - a.tiles * a.splits, gridDim.x - a.tiles * a.splits);
         return;
@@ -74,7 +76,7 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) expand_kernel(cons
     const int total = (a.C + kTile - 1) / kTile;
     const int s0 = static_cast<int>(static_cast<int64_t>(total) * part / a.splits);
     const int s1 = static_cast<int>(static_cast<int64_t>(total) * (part + 1) / a.splits);
-    const uint16_t *w = a.w + static_cast<int64_t>(tile.adapter) * a.R * a.C;
+    const uint16_t *w = a.w + static_cast<int64_t>(tile.adapter) * a.R * (WT ? a.ldw : a.C);
     auto put = [&](uint8_t *dst, const uint16_t *src, int valid) {
         if constexpr (FAST) copy8<kRows16>(dst, src, valid, 16);
         else if (a.aw >= 4) copy8<kRows4>(dst, src, valid, a.aw);
@@ -95,39 +97,16 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) expand_kernel(cons
 #pragma unroll
             for (int i = 0; i < RP * 16 / kThreads; ++i) {
                 const int at = tid + kThreads * i, r = at >> 4, j = at & 15, valid = r < a.R ? a.C - c0 - 8 * j : 0;
-                put(ws + (j >> 3) * RP * 128 + sw128(r, j & 7), valid > 0 ? w + static_cast<int64_t>(r) * a.C + c0 + 8 * j : a.w, valid);
+                put(ws + (j >> 3) * RP * 128 + sw128(r, j & 7), valid > 0 ? w + static_cast<int64_t>(r) * a.ldw + c0 + 8 * j : a.w, valid);
             }
         }
     };
-    // U: 128 rows of RP ranks, hi and lo
-#pragma unroll
-    for (int i = 0; i < 2 * 128 * (RP / 8) / kThreads; ++i) {
-        const int at = tid + kThreads * i, half = at / (128 * (RP / 8)), k = at % (128 * (RP / 8));
-        const int m = k / (RP / 8), j = k % (RP / 8);
-        const uint16_t *u = half ? a.u.lo : a.u.hi;
-        cp_async_16(us + half * kUBytes<RP> + (j >> 3) * 2 * kAtom + sw128(m, j & 7),
-                    m < tile.n ? u + static_cast<int64_t>(tile.first + m) * RP + 8 * j : u, m < tile.n ? 16 : 0);
-    }
     load_w(s0);
-    cp_async_commit();
-    if (s0 + 1 < s1) load_w(s0 + 1);
-    cp_async_commit();
-    if (warp == 0) {
-        tc::tmem_alloc(smem_u32(&tmem_slot), 2 * kTile);
-        tc::tmem_relinquish();
-        if (lane == 0) {
-            abort_flag = 0;
-            tc::mbar_init(smem_u32(&ready[0]), 1);
-            tc::mbar_init(smem_u32(&ready[1]), 1);
-            tc::fence_mbar_init();
-        }
-    }
     // this warp's rows, 32 (warp % 4) .. + 31, in two halves of 16; its 64 columns of a tile
     const int m0 = (warp & 3) * 32, cw = (warp >> 2) * 64;
     const float s = a.scale != nullptr ? a.scale[tile.adapter] : 1.0f;
     int row[2][2];
     bool live[2][2];
-    float mul[2][2];
 #pragma unroll
     for (int b = 0; b < 2; ++b)
 #pragma unroll
@@ -135,13 +114,11 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) expand_kernel(cons
             const int m = m0 + 16 * b + 8 * h + g, at = tile.first + (m < tile.n ? m : 0);
             live[b][h] = m < tile.n;
             row[b][h] = a.plan.rows[at];
-            mul[b][h] = a.u.unpower != nullptr ? s * a.u.unpower[at] : s;
         }
     if constexpr (!FAST) {
         if (tid < 128) {
             const int at = tile.first + (tid < tile.n ? tid : 0);
             rows_s[tid] = a.plan.rows[at];
-            mul_s[tid] = a.u.unpower != nullptr ? s * a.u.unpower[at] : s;
         }
     }
     // (FAST) 16-bit base's values of a step, lane t's columns 8t.. of each 32
@@ -163,6 +140,40 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) expand_kernel(cons
     };
     load_base(s0, 0);
     load_base(s0, 1);
+    pdl_wait();                                             // before tensor memory is taken, see shrink_kernel
+    // U: 128 rows of RP ranks, hi and lo
+#pragma unroll
+    for (int i = 0; i < 2 * 128 * (RP / 8) / kThreads; ++i) {
+        const int at = tid + kThreads * i, half = at / (128 * (RP / 8)), k = at % (128 * (RP / 8));
+        const int m = k / (RP / 8), j = k % (RP / 8);
+        const uint16_t *u = half ? a.u.lo : a.u.hi;
+        cp_async_16(us + half * kUBytes<RP> + (j >> 3) * 2 * kAtom + sw128(m, j & 7),
+                    m < tile.n ? u + static_cast<int64_t>(tile.first + m) * RP + 8 * j : u, m < tile.n ? 16 : 0);
+    }
+    cp_async_commit();
+    if (s0 + 1 < s1) load_w(s0 + 1);
+    cp_async_commit();
+    float mul[2][2];
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int m = m0 + 16 * b + 8 * h + g;
+            mul[b][h] = a.u.unpower != nullptr ? s * a.u.unpower[tile.first + (m < tile.n ? m : 0)] : s;
+        }
+    if constexpr (!FAST) {
+        if (tid < 128) mul_s[tid] = a.u.unpower != nullptr ? s * a.u.unpower[tile.first + (tid < tile.n ? tid : 0)] : s;
+    }
+    if (warp == 0) {
+        tc::tmem_alloc(smem_u32(&tmem_slot), 2 * kTile);
+        tc::tmem_relinquish();
+        if (lane == 0) {
+            abort_flag = 0;
+            tc::mbar_init(smem_u32(&ready[0]), 1);
+            tc::mbar_init(smem_u32(&ready[1]), 1);
+            tc::fence_mbar_init();
+        }
+    }
     // fp32 sums, W MN-major where it is [R, C], N = M = 128
     constexpr uint32_t kFmt = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
     constexpr uint32_t kIdesc = (1u << 4) | (kFmt << 7) | (kFmt << 10) | ((WT ? 1u : 0u) << 16) |

@@ -1,4 +1,4 @@
-// The adapters' gradients (dA = dU^T x, dB = s u^T g) and the sum of their parts: see adapter.cu.
+// The adapters' gradients (dA = dU^T x, dB = s u^T g): see adapter.cu.
 #include "adapter.cuh"
 
 namespace bt {
@@ -11,21 +11,23 @@ namespace {
 // they arrive, a token a row, and go to the tensor cores MN-major: nothing is
 // transposed. Eight warps gather, a ninth issues the
 // products. A part that is its adapter's only one writes the gradient; the
-// others write their sums to the workspace, which sum_kernel adds up in order.
-// Both products run in one launch, so that neither leaves the machine half
-// empty at its end.
+// others write their sums to the workspace, and whichever ends last adds them up
+// in the parts' order: the result does not depend on which that is. Both
+// products run in one launch, so that neither leaves the machine half empty at
+// its end. x and g are asked for before the previous kernel, which works out
+// dU, has ended.
 using T = __nv_bfloat16;
 constexpr int kCols = 128, kTok = 64;
 constexpr int kWarps = 9;
 constexpr int kXBytes = 2 * kAtom;                          // 64 tokens x 128 columns
 template <int RP> constexpr int kUBytes = (RP <= 32 ? 1 : RP / 32) * kAtom;   // hi and lo side by side, 64 ranks an atom
 template <int RP> constexpr int kStageBytes = kXBytes + kUBytes<RP>;
-template <int RP> constexpr int kStages = RP <= 32 ? 4 : RP == 64 ? 3 : 4;
+template <int RP> constexpr int kStages = RP <= 64 ? 3 : 4;
 template <int RP> constexpr int kLag = kStages<RP> - 2;     // see adapter_shrink.cu
 template <int RP> constexpr int kSmem = kStages<RP> * kStageBytes<RP> + 1024;
 
 template <int RP, int MODE>
-__global__ void __launch_bounds__(32 * kWarps, RP <= 64 ? 2 : 1) grad_kernel(const GradArgs a) {
+__global__ void __launch_bounds__(32 * kWarps, RP <= 32 ? 3 : RP <= 64 ? 2 : 1) grad_kernel(const GradArgs a) {
     extern __shared__ uint8_t dyn[];
     constexpr int S = kStages<RP>, D = kLag<RP>, kTmem = 2 * RP;
     __shared__ alignas(8) uint64_t full[S], empty[S], done;
@@ -36,9 +38,13 @@ __global__ void __launch_bounds__(32 * kWarps, RP <= 64 ? 2 : 1) grad_kernel(con
     const int sl = static_cast<int>(blockIdx.x % both);
     const GradProduct &p = a.p[sl < a.p[0].slices ? 0 : 1];
     const int c0 = (sl < a.p[0].slices ? sl : sl - a.p[0].slices) * kCols;
-    pdl_wait();                                             // before tensor memory is taken, see shrink_kernel
+    // The plan, x and g were there before this call's first kernel began, which waited for all before it: only
+    // what that kernel writes has to be waited for.
+    if (a.alone) pdl_wait();
     const AdapterTile part = a.plan.tiles[blockIdx.x / both];
+    const int n = (part.n + kTok - 1) / kTok;
     if (warp == kWarps - 1) {
+        pdl_wait();                                         // before tensor memory is taken, see shrink_kernel
         tc::tmem_alloc(smem_u32(&tmem_slot), kTmem);
         tc::tmem_relinquish();
         if (lane == 0) {
@@ -51,12 +57,6 @@ __global__ void __launch_bounds__(32 * kWarps, RP <= 64 ? 2 : 1) grad_kernel(con
             tc::fence_mbar_init();
         }
     }
-    tc::fence_before_sync();
-    __syncthreads();
-    tc::fence_after_sync();
-    pdl_launch_dependents();
-    const uint32_t tmem = tmem_slot;
-    const int n = (part.n + kTok - 1) / kTok;
     if (warp < kWarps - 1) {
         const int32_t *rows = a.plan.rows + part.first;
         // this thread's chunks of X: column chunk tid % 16 of tokens tid / 16 + 16 i
@@ -78,31 +78,42 @@ __global__ void __launch_bounds__(32 * kWarps, RP <= 64 ? 2 : 1) grad_kernel(con
                 held[MODE == kRows2 ? i : 0] = xrow[i] >= 0 && left > 0 ? load8(x + static_cast<int64_t>(xrow[i]) * p.ldx, left)
                                                                         : make_uint4(0u, 0u, 0u, 0u);
         };
+        auto load_x = [&](int s) {
+            uint8_t *xs = smem + (s % S) * kStageBytes<RP>;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint8_t *dst = xs + (cj >> 3) * kAtom + sw128(ct + 16 * i, cj & 7);
+                if (MODE == kRows2) {
+                    *reinterpret_cast<uint4 *>(dst) = held[MODE == kRows2 ? i : 0];
+                } else {
+                    const int valid = xrow[i] >= 0 ? left : 0;
+                    copy8<MODE>(dst, valid > 0 ? x + static_cast<int64_t>(xrow[i]) * p.ldx : p.x, valid, p.ax);
+                }
+            }
+            if (MODE == kRows2) {
+                hold();
+                fetch_rows(s + 2);
+            } else {
+                fetch_rows(s + 1);
+            }
+        };
         fetch_rows(0);
         if (MODE == kRows2) {
             hold();
             fetch_rows(1);
         }
+        const int early = n < S ? n : S;                    // every stage once
+        for (int s = 0; s < early; ++s) load_x(s);
+        pdl_wait();
+        __syncthreads();                                    // the barriers and the tensor memory are there
+        pdl_launch_dependents();
         for (int s = 0; s < n + D; ++s) {
             if (s < n) {
-                if (s >= S) wait_landed(empty[s % S], static_cast<uint32_t>(s / S - 1) & 1u, &abort_flag, a.err, a.limit_ns);
-                uint8_t *xs = smem + (s % S) * kStageBytes<RP>, *us = xs + kXBytes;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    uint8_t *dst = xs + (cj >> 3) * kAtom + sw128(ct + 16 * i, cj & 7);
-                    if (MODE == kRows2) {
-                        *reinterpret_cast<uint4 *>(dst) = held[MODE == kRows2 ? i : 0];
-                    } else {
-                        const int valid = xrow[i] >= 0 ? left : 0;
-                        copy8<MODE>(dst, valid > 0 ? x + static_cast<int64_t>(xrow[i]) * p.ldx : p.x, valid, p.ax);
-                    }
+                if (s >= S) {
+                    wait_landed(empty[s % S], static_cast<uint32_t>(s / S - 1) & 1u, &abort_flag, a.err, a.limit_ns);
+                    load_x(s);
                 }
-                if (MODE == kRows2) {
-                    hold();
-                    fetch_rows(s + 2);
-                } else {
-                    fetch_rows(s + 1);
-                }
+                uint8_t *us = smem + (s % S) * kStageBytes<RP> + kXBytes;
                 // U: its two parts, RP / 8 chunks of 64 tokens
 #pragma unroll
                 for (int i = 0; i < 2 * kTok * (RP / 8) / 256; ++i) {
@@ -122,7 +133,13 @@ __global__ void __launch_bounds__(32 * kWarps, RP <= 64 ? 2 : 1) grad_kernel(con
                 if (lane == 0) tc::mbar_arrive(smem_u32(&full[(s - D) % S]));
             }
         }
-    } else if (lane == 0) {
+    } else {
+        tc::fence_before_sync();
+        __syncthreads();
+    }
+    tc::fence_after_sync();
+    const uint32_t tmem = tmem_slot;
+    if (warp == kWarps - 1 && lane == 0) {
         // fp32 sums, bf16 operands, both MN-major, N = 2 RP, M = 128
         constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 15) | (1u << 16) |
                                     ((static_cast<uint32_t>(2 * RP) >> 3) << 17) | ((128u >> 4) << 24);
@@ -142,9 +159,10 @@ __global__ void __launch_bounds__(32 * kWarps, RP <= 64 ? 2 : 1) grad_kernel(con
     __syncwarp();
     wait_landed(done, 0, &abort_flag, a.err, a.limit_ns);
     tc::fence_after_sync();
+    float *const grad = p.grad + static_cast<int64_t>(part.adapter) * a.R * p.C;
     if (warp < kWarps - 1) {
         const float scale = p.scale != nullptr ? p.scale[part.adapter] : 1.0f;
-        float *out = part.slot >= 0 ? p.slots + part.slot * a.slot_stride : p.grad + static_cast<int64_t>(part.adapter) * a.R * p.C;
+        float *out = part.slot >= 0 ? p.slots + part.slot * a.slot_stride : grad;
         const int col = c0 + (warp & 3) * 32 + lane;        // the accumulator's lane
         for (int r0 = (warp >> 2) * 32; r0 < RP; r0 += 64) {
             float v[32];
@@ -186,43 +204,58 @@ __global__ void __launch_bounds__(32 * kWarps, RP <= 64 ? 2 : 1) grad_kernel(con
         }
     }
     tc::fence_before_sync();
+    if (part.slot >= 0) __threadfence();                    // this part's sums, before it is counted
     __syncthreads();
     if (warp == kWarps - 1) {
         tc::fence_after_sync();
         tc::tmem_dealloc(tmem, kTmem);
     }
-}
-
-// Split adapters' parts come first in the plan; block y takes part y if an
-// adapter begins there.
-__global__ void __launch_bounds__(kThreads) sum_kernel(const SumArgs a) {
-    pdl_launch_dependents();
-    pdl_wait();
-    const int p = blockIdx.y;
-    const AdapterTile first = a.parts[p];
-    if (p > 0 && a.parts[p - 1].adapter == first.adapter) return;
-    int k = 1;
-    while (p + k < a.n && a.parts[p + k].adapter == first.adapter) ++k;
-    const float *s = a.slots + first.slot * a.slot_stride;
-    const int64_t i = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) * 4;
-    // both gradients are laid out in whole 16-byte vectors, but for their last values
-    const bool of_a = i < a.off_b;
-    const int64_t j = of_a ? i : i - a.off_b, len = of_a ? a.len_a : a.len_b;
-    if (j >= len) return;
-    float4 v = *reinterpret_cast<const float4 *>(s + i);
-#pragma unroll 4
-    for (int q = 1; q < k; ++q) {
-        const float4 w = *reinterpret_cast<const float4 *>(s + q * a.slot_stride + i);
-        v.x += w.x; v.y += w.y; v.z += w.z; v.w += w.w;
-    }
-    float *o = (of_a ? a.grad_a + first.adapter * a.len_a : a.grad_b + first.adapter * a.len_b) + j;
-    if ((len & 3) == 0) {
-        *reinterpret_cast<float4 *>(o) = v;
-    } else {
-        const float f[4] = {v.x, v.y, v.z, v.w};
+    if (part.slot < 0) return;
+    // Of a split adapter: its parts lie next to each other in the plan.
+    const int here = static_cast<int>(blockIdx.x) / both;
+    int first = here, end = here + 1;
+    while (first > 0 && a.plan.tiles[first - 1].adapter == part.adapter) --first;
+    while (end < a.parts && a.plan.tiles[end].adapter == part.adapter) ++end;
+    __shared__ unsigned int before;
+    if (tid == 0) before = atomicAdd(a.arrived + static_cast<int64_t>(first) * both + sl, 1u);
+    __syncthreads();
+    if (before != static_cast<unsigned int>(end - first - 1)) return;
+    __threadfence();
+    const int cols = min(kCols, p.C - c0), parts = end - first;
+    const float *from = p.slots + (part.slot - (here - first)) * a.slot_stride;
+    // four values at a time, four parts' on their way at once: of [R, C] 128 columns of every rank, of [C, R] one stretch
+    const int64_t base = p.rc ? c0 : static_cast<int64_t>(c0) * a.R, pitch = p.rc ? p.C : 0;
+    const int len = p.rc ? cols : cols * a.R, per = (len + 3) / 4, rows_n = p.rc ? a.R : 1;
+    const bool whole = ((base | pitch | len | (static_cast<int64_t>(a.R) * p.C)) & 3) == 0;
+    for (int i = tid; i < rows_n * per; i += 32 * kWarps) {
+        const int r = i / per, k = (i - r * per) * 4;
+        const int64_t at = base + r * pitch + k;
+        float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int q0 = 0; q0 < parts; q0 += 4) {
+            float w[4][4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (j + e < len) o[e] = f[e];
+            for (int q = 0; q < 4; ++q) {
+                const float *f = from + (q0 + q) * a.slot_stride + at;
+                if (whole) {
+                    const float4 t = q0 + q < parts ? __ldcg(reinterpret_cast<const float4 *>(f)) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    w[q][0] = t.x; w[q][1] = t.y; w[q][2] = t.z; w[q][3] = t.w;
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) w[q][e] = q0 + q < parts && k + e < len ? __ldcg(f + e) : 0.0f;
+                }
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] += w[q][e];
+        }
+        if (whole) {
+            *reinterpret_cast<float4 *>(grad + at) = make_float4(v[0], v[1], v[2], v[3]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (k + e < len) grad[at + e] = v[e];
+        }
     }
 }
 
@@ -247,16 +280,11 @@ template <int RP> cudaError_t launch_rp(const GradArgs &a, int parts, cudaStream
 cudaError_t launch_grad(const GradArgs &args, int parts, cudaStream_t s) {
     GradArgs a = args;
     for (GradProduct &p : a.p) p.slices = (p.C + kCols - 1) / kCols;
+    a.parts = parts;
     if (a.R <= 16) return launch_rp<16>(a, parts, s);
     if (a.R <= 32) return launch_rp<32>(a, parts, s);
     if (a.R <= 64) return launch_rp<64>(a, parts, s);
     return launch_rp<128>(a, parts, s);
-}
-
-cudaError_t launch_sum(const SumArgs &a, cudaStream_t s) {
-    const int64_t blocks = (a.off_b + a.len_b + 4 * kThreads - 1) / (4 * kThreads);
-    return launch_pdl(sum_kernel, dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(a.n)),
-                      dim3(kThreads), s, a);
 }
 
 }  // namespace adapter

@@ -3,6 +3,7 @@
 // costs no launch and no synchronisation, and every projection of every layer
 // shares one plan. Checks that the kernels rely on (every adapter index in
 // range, every row once) are made here.
+#include <algorithm>
 #include <cstdlib>
 #include <cstring>
 #include <memory>
@@ -49,7 +50,7 @@ bt_status bt_adapter_plan(const int32_t *adapter, int64_t T, int64_t L, void *pl
     memset(w, 0, static_cast<size_t>(lay.words) * 4);
 
     // Stable counting sort by adapter, tokens without one last. last[a]: the end of adapter a's rows.
-    std::unique_ptr<int32_t, void (*)(void *)> counts(static_cast<int32_t *>(calloc(static_cast<size_t>(L) + 1, 4)), free);
+    std::unique_ptr<int32_t, void (*)(void *)> counts(static_cast<int32_t *>(calloc(2 * static_cast<size_t>(L) + 1, 4)), free);
     int32_t *last = counts.get();
     if (last == nullptr) return BT_ERR_WORKSPACE;
     for (int64_t t = 0; t < T; ++t) ++last[adapter[t] < 0 ? L : adapter[t]];
@@ -94,22 +95,24 @@ bt_status bt_adapter_plan(const int32_t *adapter, int64_t T, int64_t L, void *pl
     }
     r.without = static_cast<int32_t>(T) - last[L - 1];
 
-    // The gradients' parts: at most a quarter of the tokens each (whole 64s, at
+    // The gradients' parts: at most an eighth of the tokens each (whole 64s, at
     // least 256), every adapter once at least, so that one without tokens gets its
-    // zeros. A split adapter's parts have a slot each for their sums.
+    // zeros. A split adapter's parts have a slot each for their sums. Adapters with
+    // many tokens first: their parts begin first, and what ends last is short.
     int32_t len = static_cast<int32_t>((T + kAdapterParts - 1) / kAdapterParts);
     len = len < 256 ? 256 : (len + 63) / 64 * 64;
+    int32_t *order = last + L + 1;
+    auto count = [&](int32_t a) { return last[a] - (a == 0 ? 0 : last[a - 1]); };
+    for (int64_t a = 0; a < L; ++a) order[a] = static_cast<int32_t>(a);
+    std::sort(order, order + L, [&](int32_t a, int32_t b) { return count(a) != count(b) ? count(a) > count(b) : a < b; });
     AdapterTile *parts = reinterpret_cast<AdapterTile *>(w + lay.parts);
-    for (int pass = 0; pass < 2; ++pass) {                 // the split adapters first
-        for (int64_t a = 0; a < L; ++a) {
-            const int32_t first = a == 0 ? 0 : last[a - 1], n = last[a] - first;
-            if ((n > len) != (pass == 0)) continue;
-            if (pass == 1) {
-                parts[r.parts++] = AdapterTile{static_cast<int32_t>(a), first, n, -1};
-            } else {
-                const int32_t k = even(parts + r.parts, static_cast<int32_t>(a), first, n, len);
-                for (int32_t i = 0; i < k; ++i) parts[r.parts++].slot = r.slots++;
-            }
+    for (int64_t i = 0; i < L; ++i) {
+        const int32_t a = order[i], n = count(a), first = last[a] - n;
+        if (n <= len) {
+            parts[r.parts++] = AdapterTile{a, first, n, -1};
+        } else {
+            const int32_t k = even(parts + r.parts, a, first, n, len);
+            for (int32_t q = 0; q < k; ++q) parts[r.parts++].slot = r.slots++;
         }
     }
     *info = r;

@@ -86,11 +86,13 @@ __global__ void __launch_bounds__(32 * kWarps, 2) shrink_kernel(const ShrinkArgs
     pdl_launch_dependents();
     const uint32_t tmem = tmem_slot;
 
+    if (blockIdx.x == 0)
+        for (int i = tid; i < a.zeros; i += 32 * kWarps) a.zero[i] = 0;
     const int total = (a.C + kStep - 1) / kStep;
     const int s0 = static_cast<int>(static_cast<int64_t>(total) * rank / c);
     const int n = static_cast<int>(static_cast<int64_t>(total) * (rank + 1) / c) - s0;
     if (warp < kWarps - 1) {
-        const uint16_t *w = a.w + static_cast<int64_t>(tile.adapter) * a.R * a.C;
+        const uint16_t *w = a.w + static_cast<int64_t>(tile.adapter) * a.R * (WT ? a.C : a.ldw);
         // this thread's chunks of a stage: column chunk tid % 8 of rows tid / 8 + 32 i
         const int cj = tid & 7, cr = tid >> 3;
         const uint16_t *xr[4];
@@ -113,7 +115,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) shrink_kernel(const ShrinkArgs
                 const int r = cr + 32 * (i - kXChunks);
                 valid = r < a.R ? left - 8 * cj : 0;
                 dst = RP >= 32 || r < RP ? ws + sw128(r, cj) : nullptr;
-                src = valid > 0 ? w + static_cast<int64_t>(r) * a.C + k0 + 8 * cj : a.w;
+                src = valid > 0 ? w + static_cast<int64_t>(r) * a.ldw + k0 + 8 * cj : a.w;
             } else {
                 // rows of 64 ranks, 64 elements of the long axis to an atom
                 const int at = tid + 256 * (i - kXChunks), k = at / (RP / 8), j = at % (RP / 8);
@@ -238,6 +240,26 @@ __global__ void __launch_bounds__(32 * kWarps, 2) shrink_kernel(const ShrinkArgs
     if (c > 1) tc::cluster_sync();                          // nobody leaves while its sums are read
 }
 
+__global__ void __launch_bounds__(kThreads) align_kernel(const AlignArgs a) {
+    pdl_wait();
+    pdl_launch_dependents();
+    const int chunks = (a.C + 7) / 8;
+    int64_t first = 0, rows = a.rows;
+    if (a.parts != nullptr) {
+        const AdapterTile part = a.parts[blockIdx.y];
+        if (part.n == 0 || (blockIdx.y > 0 && a.parts[blockIdx.y - 1].adapter == part.adapter)) return;
+        first = static_cast<int64_t>(part.adapter) * a.R;
+        rows = a.R;
+    }
+    const int64_t total = rows * chunks, step = static_cast<int64_t>(gridDim.x) * kThreads;
+#pragma unroll 4
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < total; i += step) {
+        const int64_t row = first + i / chunks;
+        const int j = static_cast<int>(i % chunks) * 8;
+        *reinterpret_cast<uint4 *>(a.dst + row * a.ldd + j) = load8(a.src + row * a.lds + j, a.C - j);
+    }
+}
+
 template <typename T, int RP, bool WT, int MODE> cudaError_t launch_m(ShrinkArgs a, int tiles, cudaStream_t s) {
     auto kern = shrink_kernel<T, RP, WT, MODE>;
     static std::once_flag once;
@@ -273,6 +295,14 @@ template <typename T, bool WT> cudaError_t launch_t(const ShrinkArgs &a, int til
 }
 
 }  // namespace
+
+cudaError_t launch_align(const AlignArgs &a, cudaStream_t s) {
+    const int64_t total = (a.parts != nullptr ? a.R : a.rows) * ((a.C + 7) / 8);
+    if (total == 0) return cudaSuccess;
+    const int64_t blocks = (total + 4 * kThreads - 1) / (4 * kThreads), most = 8 * device_sm_count();
+    return launch_pdl(align_kernel, dim3(static_cast<unsigned>(blocks < most ? blocks : most), static_cast<unsigned>(a.parts != nullptr ? a.nparts : 1)),
+                      dim3(kThreads), s, a);
+}
 
 cudaError_t launch_shrink(bt_dtype t, bool wt, const ShrinkArgs &a, int tiles, cudaStream_t s) {
     if (tiles == 0) return cudaSuccess;
