@@ -24,12 +24,14 @@ template <int RP> constexpr int kUBytes = (RP <= 32 ? 1 : RP / 32) * kAtom;   //
 template <int RP> constexpr int kStageBytes = kXBytes + kUBytes<RP>;
 template <int RP> constexpr int kStages = RP <= 64 ? 3 : 4;
 template <int RP> constexpr int kLag = kStages<RP> - 2;     // see adapter_shrink.cu
+// Sums of their own for the 16-token steps of a stage, see adapter_shrink.cu.
+template <int RP> constexpr int kSums = RP <= 16 ? 4 : RP <= 64 ? 2 : 1;
 template <int RP> constexpr int kSmem = kStages<RP> * kStageBytes<RP> + 1024;
 
 template <int RP, int MODE>
 __global__ void __launch_bounds__(32 * kWarps, RP <= 32 ? 3 : RP <= 64 ? 2 : 1) grad_kernel(const GradArgs a) {
     extern __shared__ uint8_t dyn[];
-    constexpr int S = kStages<RP>, D = kLag<RP>, kTmem = 2 * RP;
+    constexpr int S = kStages<RP>, D = kLag<RP>, kTmem = kSums<RP> * 2 * RP;
     __shared__ alignas(8) uint64_t full[S], empty[S], done;
     __shared__ uint32_t tmem_slot, abort_flag;
     uint8_t *smem = dyn + ((1024u - (smem_u32(dyn) & 1023u)) & 1023u);
@@ -149,8 +151,8 @@ __global__ void __launch_bounds__(32 * kWarps, RP <= 32 ? 3 : RP <= 64 ? 2 : 1) 
             const uint32_t xs = smem_u32(smem + (s % S) * kStageBytes<RP>), us = xs + kXBytes;
 #pragma unroll
             for (int k = 0; k < 4; ++k)                     // 16 tokens: 16 rows of either operand
-                tc::mma_f16(tmem, tc::sw128_mnmajor_desc(xs + 2048 * k, kAtom), tc::sw128_mnmajor_desc(us + 2048 * k, kAtom), kIdesc,
-                            (s | k) != 0);
+                tc::mma_f16(tmem + (k % kSums<RP>) * 2 * RP, tc::sw128_mnmajor_desc(xs + 2048 * k, kAtom),
+                            tc::sw128_mnmajor_desc(us + 2048 * k, kAtom), kIdesc, s != 0 || k >= kSums<RP>);
             tc::mma_commit(smem_u32(&empty[s % S]));
         }
         if (n > 0) tc::mma_commit(smem_u32(&done));
@@ -169,19 +171,32 @@ __global__ void __launch_bounds__(32 * kWarps, RP <= 32 ? 3 : RP <= 64 ? 2 : 1) 
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = 0.0f;
             if (n > 0) {
-                uint32_t h[32];
-                tc::tmem_ld32(tmem + (static_cast<uint32_t>(warp & 3) << 21) + r0, h);
-                tc::tmem_ld_wait();
-                if constexpr (RP == 16) {                   // both halves at once
+                float small[RP == 16 ? 16 : 32];
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) v[i] = (__uint_as_float(h[i]) + __uint_as_float(h[16 + i])) * scale;
-                } else {
-                    uint32_t l[32];
-                    tc::tmem_ld32(tmem + (static_cast<uint32_t>(warp & 3) << 21) + RP + r0, l);
+                for (int q = 0; q < kSums<RP>; ++q) {
+                    uint32_t h[32];
+                    const uint32_t at = tmem + (static_cast<uint32_t>(warp & 3) << 21) + q * 2 * RP + r0;
+                    tc::tmem_ld32(at, h);
                     tc::tmem_ld_wait();
+                    if constexpr (RP == 16) {               // both halves at once
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] = (__uint_as_float(h[i]) + __uint_as_float(l[i])) * scale;
+                        for (int i = 0; i < 16; ++i) {
+                            v[i] += __uint_as_float(h[i]);
+                            small[i] = q == 0 ? __uint_as_float(h[16 + i]) : small[i] + __uint_as_float(h[16 + i]);
+                        }
+                    } else {
+                        uint32_t l[32];
+                        tc::tmem_ld32(at + RP, l);
+                        tc::tmem_ld_wait();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            v[i] += __uint_as_float(h[i]);
+                            small[i] = q == 0 ? __uint_as_float(l[i]) : small[i] + __uint_as_float(l[i]);
+                        }
+                    }
                 }
+#pragma unroll
+                for (int i = 0; i < (RP == 16 ? 16 : 32); ++i) v[i] = (v[i] + small[i]) * scale;
             }
             if (col < p.C) {
                 if (p.rc) {

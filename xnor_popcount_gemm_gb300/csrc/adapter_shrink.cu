@@ -24,6 +24,9 @@ template <int RP, bool WT> constexpr int kStages = 100 * 1024 / kStageBytes<RP, 
 // A stage is handed over once the one kLag turns later has been asked for, two fewer than there are, so that asking
 // never waits for the products of the stage just handed over.
 template <int RP, bool WT> constexpr int kLag = kStages<RP, WT> - 2;
+// The tensor cores' fp32 sums drop what does not fit instead of rounding it. The 16-element steps of a stage go to
+// sums of their own, which are added in fp32 at the end: shorter sums drop less, and not all to one side.
+template <int RP> constexpr int kSums = RP <= 64 ? 4 : 2;
 template <int RP> constexpr int kSumPitch = RP + 4;
 template <int RP, bool WT> constexpr int kSmem = kStages<RP, WT> * kStageBytes<RP, WT> + 1024;
 static_assert(kAdapterTile * kSumPitch<128> * 4 <= kStages<128, false> * kStageBytes<128, false>, "sums take the ring's place");
@@ -53,7 +56,7 @@ __device__ __forceinline__ void put_split(const SplitRows &o, int64_t at, int r,
 template <typename T, int RP, bool WT, int MODE>
 __global__ void __launch_bounds__(32 * kWarps, 2) shrink_kernel(const ShrinkArgs a) {
     extern __shared__ uint8_t dyn[];
-    constexpr int S = kStages<RP, WT>, D = kLag<RP, WT>, kCols = RP < 32 ? 32 : RP;
+    constexpr int S = kStages<RP, WT>, D = kLag<RP, WT>, kCols = kSums<RP> * RP;
     static_assert(S >= 3 && S <= 8, "stages");
     __shared__ alignas(8) uint64_t full[S], empty[S], done;
     __shared__ uint32_t tmem_slot, abort_flag;
@@ -172,7 +175,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) shrink_kernel(const ShrinkArgs
             for (int k = 0; k < 4; ++k) {                   // 16 elements: 32 bytes along a row, or 16 rows
                 const uint64_t da = tc::sw128_kmajor_desc(xs + 32 * k);
                 const uint64_t db = WT ? tc::sw128_mnmajor_desc(ws + 2048 * k, kAtom) : tc::sw128_kmajor_desc(ws + 32 * k);
-                tc::mma_f16(tmem, da, db, kIdesc, (s | k) != 0);
+                tc::mma_f16(tmem + (k % kSums<RP>) * RP, da, db, kIdesc, s != 0 || k >= kSums<RP>);
             }
             tc::mma_commit(smem_u32(&empty[s % S]));
         }
@@ -184,14 +187,31 @@ __global__ void __launch_bounds__(32 * kWarps, 2) shrink_kernel(const ShrinkArgs
     // the sums, [row][r], where the ring was
     float *sums = reinterpret_cast<float *>(smem);
     if (warp < kWarps - 1) {
-        for (int col = (warp >> 2) * 32; col < RP; col += 64) {
-            uint32_t v[32];
-            tc::tmem_ld32(tmem + (static_cast<uint32_t>(warp & 3) << 21) + col, v);
-            tc::tmem_ld_wait();
+        constexpr int kWide = RP < 32 ? RP : 32;            // columns at a time
+        for (int col = (warp >> 2) * kWide; col < RP; col += 2 * kWide) {
+            float v[kWide];
+#pragma unroll
+            for (int q = 0; q < kSums<RP>; ++q) {
+                // (rank 16: the 32 columns read are this sum and the next)
+                uint32_t w[32];
+                if (RP >= 32 || (q & 1) == 0) {
+                    tc::tmem_ld32(tmem + (static_cast<uint32_t>(warp & 3) << 21) + q * RP + col, w);
+                    tc::tmem_ld_wait();
+                }
+                if constexpr (RP >= 32) {
+#pragma unroll
+                    for (int i = 0; i < kWide; ++i) v[i] = q == 0 ? __uint_as_float(w[i]) : v[i] + __uint_as_float(w[i]);
+                } else if ((q & 1) == 0) {
+#pragma unroll
+                    for (int i = 0; i < kWide; ++i) {
+                        const float two = __uint_as_float(w[i]) + __uint_as_float(w[16 + i]);
+                        v[i] = q == 0 ? two : v[i] + two;
+                    }
+                }
+            }
             float *p = sums + ((warp & 3) * 32 + lane) * kSumPitch<RP> + col;
 #pragma unroll
-            for (int i = 0; i < (RP < 32 ? RP : 32); i += 4)
-                *reinterpret_cast<uint4 *>(p + i) = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+            for (int i = 0; i < kWide; i += 4) *reinterpret_cast<float4 *>(p + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
         }
     }
     tc::fence_before_sync();
