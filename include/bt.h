@@ -763,7 +763,8 @@ size_t bt_adapter_linear_backward_workspace(int64_t T, int64_t K, int64_t N, int
  *   grad_A     device fp32 [L, R, K] out; grad_B device fp32 [L, N, R] out, 16-byte aligned,
  *              both overwritten.
  *   ldx, ldg, ldgb, ldgx  elements from one row to the next.
- * Sums are fp32; dU and u enter the products as the sum of two BF16 values.
+ * Sums are fp32; dU and u enter the products as the sum of two (for grad_x)
+ * or three (for grad_A and grad_B) BF16 values.
  * Tokens of an adapter are summed in a fixed order: equal calls give equal
  * results. Limits, workspace rules and errors as bt_adapter_linear.
  */

@@ -12,8 +12,9 @@
 //   adapter_grad.cu     dA, dB: reduce the tokens
 //   adapter_small.cu    the whole forward for a few tokens of each adapter
 // The 16-bit operands go to the matrix instructions as they are; u and dU, fp32
-// sums, go as the sum of two 16-bit values (16 bits or more of mantissa), so
-// that the only rounding to 16 bits is the result's own.
+// sums, go as the sum of two 16-bit values (16 bits or more of mantissa; three
+// for the fp32 gradients), so that the only rounding to 16 bits is the result's
+// own.
 //
 // Tokens of an adapter are gathered through the plan's row list: a tile's rows
 // lie anywhere in the batch.
@@ -46,13 +47,13 @@ bt_status sizes_fit(int64_t T, int64_t K, int64_t N, int64_t R) {
     return BT_OK;
 }
 
-// u as two 16-bit values a rank, in a workspace: the bytes of both, and where they lie.
-size_t split_bytes(int64_t T, int R) { return 2 * round_up256(static_cast<size_t>(T) * padded_rank(R) * 2); }
-SplitRows split_rows(void *p, int64_t T, int R, bool unpower) {
-    const size_t one = split_bytes(T, R) / 2;
+// u as two or three 16-bit values a rank, in a workspace: the bytes of one, and where they lie.
+size_t split_bytes(int64_t T, int64_t R) { return round_up256(static_cast<size_t>(T) * padded_rank(static_cast<int>(R)) * 2); }
+SplitRows split_rows(void *p, int64_t T, int R, bool rest, bool unpower) {
+    const size_t one = split_bytes(T, R);
     uint8_t *b = static_cast<uint8_t *>(p);
     return SplitRows{reinterpret_cast<uint16_t *>(b), reinterpret_cast<uint16_t *>(b + one),
-                     unpower ? reinterpret_cast<float *>(b + 2 * one) : nullptr};
+                     rest ? reinterpret_cast<uint16_t *>(b + 2 * one) : nullptr, unpower ? reinterpret_cast<float *>(b + 2 * one) : nullptr};
 }
 
 // Rows whose width is odd in this sense are copied to rows that start at 16-byte multiples first: what fetches them
@@ -132,7 +133,7 @@ cudaError_t forward(const Forward &f, cudaStream_t s) {
     sh.x = f.x; sh.ldx = f.ldx;
     sh.w = f.A; sh.ldw = f.K;
     if (odd_width(f.K)) {
-        uint8_t *ws = static_cast<uint8_t *>(f.workspace) + split_bytes(f.T, f.R) + round_up256(static_cast<size_t>(f.T) * 4);
+        uint8_t *ws = static_cast<uint8_t *>(f.workspace) + 2 * split_bytes(f.T, f.R) + round_up256(static_cast<size_t>(f.T) * 4);
         uint16_t *xa = reinterpret_cast<uint16_t *>(ws), *Aa = reinterpret_cast<uint16_t *>(ws + aligned_bytes(f.T, f.K));
         e = align_rows(f.x, f.ldx, f.T, f.K, xa, s);
         if (e == cudaSuccess)
@@ -144,7 +145,7 @@ cudaError_t forward(const Forward &f, cudaStream_t s) {
     sh.ax = align_of(sh.x, sh.ldx * 2);
     sh.aw = align_of(sh.w, sh.ldw * 2);
     sh.C = f.K; sh.R = f.R; sh.u = f.u;
-    sh.out = split_rows(f.workspace, f.T, f.R, t == BT_F16);
+    sh.out = split_rows(f.workspace, f.T, f.R, false, t == BT_F16);
     sh.err = f.err; sh.limit_ns = wait_limit_ns();
     e = launch_shrink(t, false, sh, f.info->large_tiles, s);
     if (e != cudaSuccess) return e;
@@ -170,7 +171,7 @@ extern "C" {
 
 size_t bt_adapter_linear_workspace(int64_t T, int64_t K, int64_t R, const bt_adapter_plan_info *info) {
     if (sizes_fit(T, K, 0, R) != BT_OK || info == nullptr || info->large_tiles == 0) return 0;
-    size_t n = split_bytes(T, static_cast<int>(R)) + round_up256(static_cast<size_t>(T) * 4);
+    size_t n = 2 * split_bytes(T, R) + round_up256(static_cast<size_t>(T) * 4);
     if (odd_width(K)) n += aligned_bytes(T, K) + aligned_bytes(info->adapters * R, K);
     return n;
 }
@@ -227,7 +228,7 @@ size_t bt_adapter_linear_backward_workspace(int64_t T, int64_t K, int64_t N, int
                                             const bt_adapter_plan_info *info) {
     if (sizes_fit(T, K, N, R) != BT_OK || info == nullptr || !plan_fits(*info, T)) return 0;
     const size_t slot = round_up256(static_cast<size_t>(R * K) * 4) + round_up256(static_cast<size_t>(R * N) * 4);
-    size_t n = 2 * split_bytes(T, static_cast<int>(R)) + static_cast<size_t>(info->slots) * slot + arrived_bytes(*info, K, N);
+    size_t n = 6 * split_bytes(T, R) + static_cast<size_t>(info->slots) * slot + arrived_bytes(*info, K, N);
     if (odd_width(N)) n += aligned_bytes(T, N);
     if (odd_width(K)) n += aligned_bytes(T, K) + aligned_bytes(info->adapters * R, K);
     return n;
@@ -272,9 +273,10 @@ bt_status bt_adapter_linear_backward(const void *x, int64_t ldx, const void *g, 
     const AdapterPlanLayout lay = adapter_plan_layout(T, info->adapters);
     const Plan tiles{pw + lay.rows, reinterpret_cast<const AdapterTile *>(pw + lay.tiles)};
     const Plan parts{pw + lay.rows, reinterpret_cast<const AdapterTile *>(pw + lay.parts)};
-    const size_t split = split_bytes(T, static_cast<int>(R));
+    const size_t split = 3 * split_bytes(T, R);
     uint8_t *ws = static_cast<uint8_t *>(workspace);
-    const SplitRows du = split_rows(ws, T, static_cast<int>(R), false), us = split_rows(ws + split, T, static_cast<int>(R), false);
+    const SplitRows du = split_rows(ws, T, static_cast<int>(R), true, false);
+    const SplitRows us = split_rows(ws + split, T, static_cast<int>(R), true, false);
     float *slots = reinterpret_cast<float *>(ws + 2 * split);
     const int64_t off_b = static_cast<int64_t>(round_up256(static_cast<size_t>(R * K) * 4) / 4);
     const int64_t stride = off_b + static_cast<int64_t>(round_up256(static_cast<size_t>(R * N) * 4) / 4);

@@ -178,6 +178,7 @@ cudaError_t launch_pass(bt_dtype t, bool out_f32, const PassArgs &a, cudaStream_
 // a power of two of the row's own, whose inverse is in unpower.
 struct SplitRows {
     uint16_t *hi, *lo;         // [T, RP]
+    uint16_t *rest;            // what the two leave, a third value: for the fp32 gradients; NULL: dropped
     float *unpower;            // [T], NULL: 1
 };
 inline int padded_rank(int R) { return R <= 16 ? 16 : R <= 32 ? 32 : R <= 64 ? 64 : 128; }

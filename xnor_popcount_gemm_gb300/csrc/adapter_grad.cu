@@ -5,27 +5,30 @@ namespace bt {
 namespace adapter {
 namespace {
 
-// A CTA takes 128 columns of x (or g) and a part of one adapter's tokens, 64 at
-// a time: D (128 columns x twice the rank, fp32, tensor memory) += X^T (U_hi |
-// U_lo), the two halves of D being added when it is read. Both operands lie as
-// they arrive, a token a row, and go to the tensor cores MN-major: nothing is
-// transposed. Eight warps gather, a ninth issues the
-// products. A part that is its adapter's only one writes the gradient; the
-// others write their sums to the workspace, and whichever ends last adds them up
-// in the parts' order: the result does not depend on which that is. Both
+// A CTA takes 128 columns of x (or g) and a part of one adapter's tokens, 64 or
+// 32 at a time: D (128 columns x twice the rank, fp32, tensor memory) += X^T (U_hi
+// | U_lo), and U_rest onto the second half; the halves are added when D is
+// read. (fp32 gradients: two 16-bit values of U alone left them 2.5e-6 off, three
+// do not show.) Both operands lie as they arrive, a token a row, and go to the
+// tensor cores MN-major: nothing is transposed. Eight warps gather, a ninth
+// issues the products. A part that is its adapter's only one writes the gradient;
+// the others write their sums to the workspace, and whichever ends last adds
+// them up in the parts' order: the result does not depend on which that is. Both
 // products run in one launch, so that neither leaves the machine half empty at
 // its end. x and g are asked for before the previous kernel, which works out
 // dU, has ended.
 using T = __nv_bfloat16;
-constexpr int kCols = 128, kTok = 64;
+constexpr int kCols = 128;
 constexpr int kWarps = 9;
-constexpr int kXBytes = 2 * kAtom;                          // 64 tokens x 128 columns
-template <int RP> constexpr int kUBytes = (RP <= 32 ? 1 : RP / 32) * kAtom;   // hi and lo side by side, 64 ranks an atom
-template <int RP> constexpr int kStageBytes = kXBytes + kUBytes<RP>;
-template <int RP> constexpr int kStages = RP <= 64 ? 3 : 4;
+template <int RP> constexpr int kTok = RP <= 16 ? 64 : 32;
+template <int RP> constexpr int kTokAtom = kTok<RP> * 128;                  // the tokens' rows of 128 bytes
+template <int RP> constexpr int kXBytes = 2 * kTokAtom<RP>;                 // 128 columns
+template <int RP> constexpr int kUBytes = (3 * RP + 63) / 64 * kTokAtom<RP>;  // hi, lo, rest side by side, 64 ranks an atom
+template <int RP> constexpr int kStageBytes = kXBytes<RP> + kUBytes<RP>;
+template <int RP> constexpr int kStages = RP <= 16 ? 3 : 4;
 template <int RP> constexpr int kLag = kStages<RP> - 2;     // see adapter_shrink.cu
 // Sums of their own for the 16-token steps of a stage, see adapter_shrink.cu.
-template <int RP> constexpr int kSums = RP <= 16 ? 4 : RP <= 64 ? 2 : 1;
+template <int RP> constexpr int kSums = kTok<RP> / 16;
 template <int RP> constexpr int kSmem = kStages<RP> * kStageBytes<RP> + 1024;
 
 template <int RP, int MODE>
@@ -44,7 +47,7 @@ __global__ void __launch_bounds__(32 * kWarps, RP <= 32 ? 3 : RP <= 64 ? 2 : 1) 
     // what that kernel writes has to be waited for.
     if (a.alone) pdl_wait();
     const AdapterTile part = a.plan.tiles[blockIdx.x / both];
-    const int n = (part.n + kTok - 1) / kTok;
+    const int n = (part.n + kTok<RP> - 1) / kTok<RP>;
     if (warp == kWarps - 1) {
         pdl_wait();                                         // before tensor memory is taken, see shrink_kernel
         tc::tmem_alloc(smem_u32(&tmem_slot), kTmem);
@@ -63,28 +66,29 @@ __global__ void __launch_bounds__(32 * kWarps, RP <= 32 ? 3 : RP <= 64 ? 2 : 1) 
         const int32_t *rows = a.plan.rows + part.first;
         // this thread's chunks of X: column chunk tid % 16 of tokens tid / 16 + 16 i
         const int cj = tid & 15, ct = tid >> 4;
-        int xrow[4];
+        constexpr int kMine = kTok<RP> / 16;
+        int xrow[kMine];
         auto fetch_rows = [&](int s) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int at = s * kTok + ct + 16 * i;
+            for (int i = 0; i < kMine; ++i) {
+                const int at = s * kTok<RP> + ct + 16 * i;
                 xrow[i] = at < part.n ? rows[at] : -1;
             }
         };
         const int left = p.C - c0 - 8 * cj;
         const uint16_t *x = p.x + c0 + 8 * cj;
-        uint4 held[MODE == kRows2 ? 4 : 1];                 // (kRows2) the next stage, on its way
+        uint4 held[MODE == kRows2 ? kMine : 1];                 // (kRows2) the next stage, on its way
         auto hold = [&]() {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < kMine; ++i)
                 held[MODE == kRows2 ? i : 0] = xrow[i] >= 0 && left > 0 ? load8(x + static_cast<int64_t>(xrow[i]) * p.ldx, left)
                                                                         : make_uint4(0u, 0u, 0u, 0u);
         };
         auto load_x = [&](int s) {
             uint8_t *xs = smem + (s % S) * kStageBytes<RP>;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                uint8_t *dst = xs + (cj >> 3) * kAtom + sw128(ct + 16 * i, cj & 7);
+            for (int i = 0; i < kMine; ++i) {
+                uint8_t *dst = xs + (cj >> 3) * kTokAtom<RP> + sw128(ct + 16 * i, cj & 7);
                 if (MODE == kRows2) {
                     *reinterpret_cast<uint4 *>(dst) = held[MODE == kRows2 ? i : 0];
                 } else {
@@ -115,15 +119,17 @@ __global__ void __launch_bounds__(32 * kWarps, RP <= 32 ? 3 : RP <= 64 ? 2 : 1) 
                     wait_landed(empty[s % S], static_cast<uint32_t>(s / S - 1) & 1u, &abort_flag, a.err, a.limit_ns);
                     load_x(s);
                 }
-                uint8_t *us = smem + (s % S) * kStageBytes<RP> + kXBytes;
-                // U: its two parts, RP / 8 chunks of 64 tokens
+                uint8_t *us = smem + (s % S) * kStageBytes<RP> + kXBytes<RP>;
+                // U: its three values, RP / 8 chunks of a token each
+                constexpr int kChunks = kTok<RP> * (RP / 8);
 #pragma unroll
-                for (int i = 0; i < 2 * kTok * (RP / 8) / 256; ++i) {
-                    const int at = tid + 256 * i, part2 = at / (kTok * (RP / 8)), k = at % (kTok * (RP / 8));
-                    const int tok = k / (RP / 8), j = k % (RP / 8), row = s * kTok + tok;
-                    const uint16_t *u = part2 ? p.u.lo : p.u.hi;
-                    const int at8 = part2 * (RP / 8) + j;   // its chunk of the token's row
-                    cp_async_16(us + (at8 >> 3) * kAtom + sw128(tok, at8 & 7),
+                for (int i = 0; i < (3 * kChunks + 255) / 256; ++i) {
+                    const int at = tid + 256 * i, part3 = at / kChunks, k = at % kChunks;
+                    if (part3 >= 3) break;
+                    const int tok = k / (RP / 8), j = k % (RP / 8), row = s * kTok<RP> + tok;
+                    const uint16_t *u = part3 == 0 ? p.u.hi : part3 == 1 ? p.u.lo : p.u.rest;
+                    const int at8 = part3 * (RP / 8) + j;   // its chunk of the token's row
+                    cp_async_16(us + (at8 >> 3) * kTokAtom<RP> + sw128(tok, at8 & 7),
                                 row < part.n ? u + static_cast<int64_t>(part.first + row) * RP + 8 * j : u, row < part.n ? 16 : 0);
                 }
             }
@@ -142,17 +148,23 @@ __global__ void __launch_bounds__(32 * kWarps, RP <= 32 ? 3 : RP <= 64 ? 2 : 1) 
     tc::fence_after_sync();
     const uint32_t tmem = tmem_slot;
     if (warp == kWarps - 1 && lane == 0) {
-        // fp32 sums, bf16 operands, both MN-major, N = 2 RP, M = 128
-        constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 15) | (1u << 16) |
-                                    ((static_cast<uint32_t>(2 * RP) >> 3) << 17) | ((128u >> 4) << 24);
+        // fp32 sums, bf16 operands, both MN-major, N = 2 RP (hi, lo) or RP (rest), M = 128
+        constexpr uint32_t kCommon = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 15) | (1u << 16) | ((128u >> 4) << 24);
+        constexpr uint32_t kTwo = kCommon | ((static_cast<uint32_t>(2 * RP) >> 3) << 17);
+        constexpr uint32_t kOne = kCommon | ((static_cast<uint32_t>(RP) >> 3) << 17);
+        // where rest begins: after 2 RP ranks, 64 to an atom, 2 bytes each
+        constexpr uint32_t kRest = (2 * RP / 64) * kTokAtom<RP> + (2 * RP % 64) * 2;
         for (int s = 0; s < n; ++s) {
             wait_landed(full[s % S], static_cast<uint32_t>(s / S) & 1u, &abort_flag, a.err, a.limit_ns);
             tc::fence_after_sync();
-            const uint32_t xs = smem_u32(smem + (s % S) * kStageBytes<RP>), us = xs + kXBytes;
+            const uint32_t xs = smem_u32(smem + (s % S) * kStageBytes<RP>), us = xs + kXBytes<RP>;
 #pragma unroll
-            for (int k = 0; k < 4; ++k)                     // 16 tokens: 16 rows of either operand
-                tc::mma_f16(tmem + (k % kSums<RP>) * 2 * RP, tc::sw128_mnmajor_desc(xs + 2048 * k, kAtom),
-                            tc::sw128_mnmajor_desc(us + 2048 * k, kAtom), kIdesc, s != 0 || k >= kSums<RP>);
+            for (int k = 0; k < kTok<RP> / 16; ++k) {       // 16 tokens: 16 rows of either operand
+                const uint64_t da = tc::sw128_mnmajor_desc(xs + 2048 * k, kTokAtom<RP>);
+                const uint32_t d = tmem + k * 2 * RP;
+                tc::mma_f16(d, da, tc::sw128_mnmajor_desc(us + 2048 * k, kTokAtom<RP>), kTwo, s != 0);
+                tc::mma_f16(d + RP, da, tc::sw128_mnmajor_desc(us + kRest + 2048 * k, kTokAtom<RP>), kOne, 1);
+            }
             tc::mma_commit(smem_u32(&empty[s % S]));
         }
         if (n > 0) tc::mma_commit(smem_u32(&done));

@@ -49,6 +49,12 @@ __device__ __forceinline__ void put_split(const SplitRows &o, int64_t at, int r,
     if (ok) {
         *reinterpret_cast<uint2 *>(o.hi + at * RP + r) = h;
         *reinterpret_cast<uint2 *>(o.lo + at * RP + r) = l;
+        if (o.rest != nullptr) {
+            const float2 h0 = unpack2<T>(h.x), h1 = unpack2<T>(h.y), l0 = unpack2<T>(l.x), l1 = unpack2<T>(l.y);
+            auto left = [&](float v, float a, float b) { return isinf(a) ? 0.0f : (v * p - a) - b; };
+            *reinterpret_cast<uint2 *>(o.rest + at * RP + r) = make_uint2(pack2<T>(left(f[0], h0.x, l0.x), left(f[1], h0.y, l0.y)),
+                                                                          pack2<T>(left(f[2], h1.x, l1.x), left(f[3], h1.y, l1.y)));
+        }
     }
 }
 
