@@ -691,9 +691,8 @@ typedef struct {
     int32_t used;              /* adapters that have tokens */
     int32_t most_tokens;       /* tokens of the one that has most */
     int32_t without;           /* tokens without an adapter */
-    int32_t tiles;             /* tiles of up to 128 tokens of one adapter; */
-    int32_t large_tiles;       /*   the first of them, of adapters with more than 32 tokens */
-    int32_t small_tiles;       /* tiles of up to 16 tokens, of the other adapters; */
+    int32_t tiles;             /* tiles of up to 128 tokens of one adapter */
+    int32_t small_tiles;       /* the same tokens in tiles of up to 16; */
     int32_t small_most;        /*   tokens of the fullest of them */
     int32_t parts, slots;      /* parts of a gradient's tokens; those that are summed afterwards */
 } bt_adapter_plan_info;
@@ -715,9 +714,9 @@ size_t bt_adapter_plan_bytes(int64_t T, int64_t L);
 bt_status bt_adapter_plan(const int32_t *adapter, int64_t T, int64_t L, void *plan, size_t plan_bytes,
                           bt_adapter_plan_info *info);
 
-/* Workspace bytes of bt_adapter_linear (0 when no adapter has more than 32
- * tokens, or for sizes out of range). */
-size_t bt_adapter_linear_workspace(int64_t T, int64_t K, int64_t R, const bt_adapter_plan_info *info);
+/* Workspace bytes of bt_adapter_linear (0 for a batch that it serves in one
+ * kernel, and for sizes out of range). */
+size_t bt_adapter_linear_workspace(int64_t T, int64_t K, int64_t N, int64_t R, const bt_adapter_plan_info *info);
 
 /*
  * bt_adapter_linear -- the formula above for x [T, K].
@@ -736,7 +735,7 @@ size_t bt_adapter_linear_workspace(int64_t T, int64_t K, int64_t R, const bt_ada
  * rounded once. Any sizes and element alignments are served; rows that start
  * at multiples of 16 bytes (and R a multiple of 8) are faster. 1 <= R <= 128;
  * T, K, N < 2^24. T = 0 or N = 0 does nothing. workspace:
- * bt_adapter_linear_workspace(T, K, R, info) bytes, 256-byte aligned.
+ * bt_adapter_linear_workspace(T, K, N, R, info) bytes, 256-byte aligned.
  * Equal calls give equal results.
  * Errors: INVALID_ARG, ALIGNMENT, WORKSPACE, UNSUPPORTED, CUDA.
  */

@@ -9,7 +9,7 @@ import torch
 
 import xnor_popcount_gemm_gb300 as bt
 
-TILE, SMALL, SMALL_MOST, PARTS = 128, 16, 32, 8
+TILE, SMALL, PARTS = 128, 16, 8
 
 
 def _plan(ids, L):
@@ -50,8 +50,7 @@ def test_plan_covers_every_token_once(T, L, none, skew):
         assert sorted(seen) == [t for t in range(T) if ids[t] in adapters]
 
     covered(tiles, TILE, [a for a in range(L) if count[a]])
-    covered(tiles[:info.large_tiles], TILE, [a for a in range(L) if count[a] > SMALL_MOST])
-    covered(small, SMALL, [a for a in range(L) if 0 < count[a] <= SMALL_MOST])
+    covered(small, SMALL, [a for a in range(L) if count[a]])
     assert info.small_most == max([n for _, _, n, _ in small], default=0)
     # every adapter has its parts, one after the other; those of split ones come first and have the slots in order
     length = max(256, (-(-T // PARTS) + 63) // 64 * 64)
@@ -122,7 +121,7 @@ def _bwd(**kw):
     return bt._c_abwd(*a.values())
 
 
-def test_forward_refusals():
+def test_forward_refusals(monkeypatch):
     for bad in (dict(xt=bt.BT_F32), dict(xt=bt.BT_I32), dict(ot=bt.BT_F16), dict(ot=bt.BT_I32), dict(K=0, ldx=64),
                 dict(T=-1), dict(N=-1), dict(R=0), dict(ldx=63), dict(ldo=31), dict(base=256, ldb=31),
                 dict(base=256, ldb=32, bt_=bt.BT_F16), dict(info=None), dict(T=5), dict(info=_info(T=3)), dict(x=None),
@@ -136,16 +135,26 @@ def test_forward_refusals():
     for bad in (dict(x=257), dict(A=513), dict(B=1025), dict(s=2050), dict(plan=4100), dict(out=8193), dict(u=2),
                 dict(ot=bt.BT_F32, out=8194), dict(base=258, ldb=32, bt_=bt.BT_F32)):
         assert _fwd(**bad) == bt.BT_ERR_ALIGNMENT, bad
+    monkeypatch.setenv("BT_ADAPTER_PATH", "large")
     large = dict(T=40, info=_info(T=40))
     assert _fwd(**large, ws=None) == _fwd(**large, wsb=2 * 1280 + 256 - 1) == bt.BT_ERR_WORKSPACE
     assert _fwd(**large, ws=16384 + 16) == bt.BT_ERR_ALIGNMENT
+    monkeypatch.delenv("BT_ADAPTER_PATH")
     assert _fwd(T=0, info=_info(T=0), x=None) == _fwd(N=0, out=None) == bt.BT_OK
-    few, many = (bt.bt_adapter_plan([0] * n, 2, device="cpu") for n in (4, 40))
-    assert bt.bt_adapter_linear_workspace(40, 64, 8, many) == 2 * 1280 + 256         # two 16-bit values of 16 ranks, a power
+
+
+def test_workspace_queries(monkeypatch):
+    ws = bt.bt_adapter_linear_workspace
+    one, many, most = (bt.bt_adapter_plan([0] * n, 2, device="cpu") for n in (1, 40, 8192))
+    assert ws(1, 4096, 4096, 16, one) == 0                       # one kernel
+    assert ws(8192, 4096, 4096, 64, most) == 2 * 8192 * 128 + 8192 * 4
+    monkeypatch.setenv("BT_ADAPTER_PATH", "large")
+    assert ws(40, 64, 32, 8, many) == 2 * 1280 + 256             # two 16-bit values of 16 ranks, a power
     # a width that is no multiple of 4: room for the rows of x and A at 16-byte multiples
-    assert bt.bt_adapter_linear_workspace(40, 66, 8, many) == 2 * 1280 + 256 + 5888 + 2304
-    assert bt.bt_adapter_linear_workspace(40, 64, 129, many) == 0
-    assert bt.bt_adapter_linear_workspace(4, 64, 8, few) == 0
+    assert ws(40, 66, 32, 8, many) == 2 * 1280 + 256 + 5888 + 2304
+    assert ws(40, 64, 32, 129, many) == ws(41, 64, 32, 8, many) == 0
+    monkeypatch.setenv("BT_ADAPTER_PATH", "small")
+    assert ws(8192, 4096, 4096, 64, most) == 0
 
 
 def test_backward_refusals():

@@ -26,6 +26,13 @@ def _device_clean():
     assert bt.bt_device_status() == 0
 
 
+@pytest.fixture(params=["small", "large"])
+def path(request, monkeypatch):
+    """Either forward, whatever the rule on sizes says."""
+    monkeypatch.setenv("BT_ADAPTER_PATH", request.param)
+    return request.param
+
+
 def _ids(T, L, kind, seed):
     gen = torch.Generator().manual_seed(seed)
     if kind == "runs":
@@ -93,7 +100,7 @@ def _check_forward(x, a, b, s, ids, base, out_dtype, **kw):
     (129, 260, 128, 128, 2, "some"), (300, 67, 129, 100, 3, "skew"), (500, 192, 200, 40, 4, "skew"),
     (257, 1024, 96, 16, 1, "runs"), (40, 2048, 1100, 64, 40, "some"),
 ])
-def test_forward(T, K, N, R, L, kind, dtype):
+def test_forward(T, K, N, R, L, kind, dtype, path):
     x, a, b, s = _inputs(T, K, N, R, L, dtype, seed=T + K)
     ids = _ids(T, L, kind, T)
     gen = torch.Generator().manual_seed(1)
@@ -106,7 +113,7 @@ def test_forward(T, K, N, R, L, kind, dtype):
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
 @pytest.mark.parametrize("T", [3, 200])
-def test_strides_in_place_and_views(T, dtype):
+def test_strides_in_place_and_views(T, dtype, path):
     K, N, R, L = 72, 104, 16, 3
     x, a, b, s = _inputs(T, K, N, R, L, dtype, seed=3)
     ids = _ids(T, L, "some", 4)
@@ -129,7 +136,7 @@ def test_strides_in_place_and_views(T, dtype):
         assert torch.equal(apart[:, :N], want) and (apart[:, N:] == 33).all()
 
 
-def test_nobody_has_an_adapter():
+def test_nobody_has_an_adapter(path):
     x, a, b, s = _inputs(9, 64, 48, 8, 2, torch.bfloat16)
     ids = torch.full((9,), -1)
     base = torch.randn(9, 48)
@@ -155,7 +162,7 @@ def test_no_tokens():
 
 
 @pytest.mark.parametrize("T", [4, 70])
-def test_nan_and_infinity_stay_in_their_rows(T):
+def test_nan_and_infinity_stay_in_their_rows(T, path):
     x, a, b, s = _inputs(T, 128, 72, 16, 1, torch.bfloat16, seed=5)
     ids = torch.zeros(T, dtype=torch.int64)
     clean = _check_forward(x, a, b, s, ids, None, torch.float32)
@@ -168,7 +175,7 @@ def test_nan_and_infinity_stay_in_their_rows(T):
 
 
 @pytest.mark.parametrize("T", [3, 80])
-def test_half_precision_reaches_beyond_its_range_inside(T):
+def test_half_precision_reaches_beyond_its_range_inside(T, path):
     """u beyond 65504 and far below 2^-24 in half precision: u is fp32 and enters the second product by rows."""
     K, N, R = 256, 64, 8
     x, a, b, s = _inputs(T, K, N, R, 1, torch.float16, seed=6)
@@ -265,7 +272,7 @@ def test_gradients_against_differences():
             assert abs(d - got) <= (eh + el) / 2 + 2.0 ** -8 * abs(got), (which, at, d, got)
 
 
-def test_another_stream_and_a_graph():
+def test_another_stream_and_a_graph(path):
     T, K, N, R, L = 200, 256, 264, 16, 3
     x, a, b, s = (t.to(DEV) for t in _inputs(T, K, N, R, L, torch.bfloat16, seed=11))
     ids = _ids(T, L, "some", 12)
@@ -285,7 +292,7 @@ def test_another_stream_and_a_graph():
     assert torch.equal(out, want)
 
 
-def test_offsets_beyond_32_bits():
+def test_offsets_beyond_32_bits(path):
     T, K, N, R = 70000, 32768, 64, 8                          # x holds 2.3e9 elements
     x = torch.zeros(T, K, dtype=torch.bfloat16, device=DEV)
     xs, a, b, s = _inputs(2, K, N, R, 2, torch.bfloat16, seed=13)

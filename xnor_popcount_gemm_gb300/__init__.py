@@ -102,13 +102,13 @@ _c_distill_step = _sig("bt_distill_topk_step", _i, [_p, _p, _i, _i64, _i64, _i64
 class AdapterPlanInfo(ctypes.Structure):
     """bt_adapter_plan_info: what bt_adapter_plan says of a batch."""
     _fields_ = [("tokens", _i64), ("adapters", _i64)] + [(n, ctypes.c_int32) for n in (
-        "used", "most_tokens", "without", "tiles", "large_tiles", "small_tiles", "small_most", "parts", "slots")]
+        "used", "most_tokens", "without", "tiles", "small_tiles", "small_most", "parts", "slots")]
 
 
 _pinfo = ctypes.POINTER(AdapterPlanInfo)
 _c_aplan_bytes = _sig("bt_adapter_plan_bytes", _sz, [_i64, _i64])
 _c_aplan = _sig("bt_adapter_plan", _i, [_p, _i64, _i64, _p, _sz, _pinfo])
-_c_alin_ws = _sig("bt_adapter_linear_workspace", _sz, [_i64, _i64, _i64, _pinfo])
+_c_alin_ws = _sig("bt_adapter_linear_workspace", _sz, [_i64, _i64, _i64, _i64, _pinfo])
 _c_alin = _sig("bt_adapter_linear", _i, [_p, _i, _i64, _p, _p, _p, _p, _pinfo, _i64, _i64, _i64, _i64, _p, _i, _i64,
                                          _p, _i, _i64, _p, _p, _sz, _p])
 _c_abwd_ws = _sig("bt_adapter_linear_backward_workspace", _sz, [_i64, _i64, _i64, _i64, _pinfo])
@@ -729,8 +729,8 @@ def _adapter_args(x, a, b, scale, plan):
     return T, K, N, R
 
 
-def bt_adapter_linear_workspace(T: int, K: int, R: int, plan: AdapterPlan) -> int:
-    return int(_c_alin_ws(T, K, R, plan._ref))
+def bt_adapter_linear_workspace(T: int, K: int, N: int, R: int, plan: AdapterPlan) -> int:
+    return int(_c_alin_ws(T, K, N, R, plan._ref))
 
 
 def bt_adapter_linear(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, scale: torch.Tensor, plan: AdapterPlan,
@@ -754,7 +754,7 @@ def bt_adapter_linear(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, scale: 
     ldo = _rows(out, "out", T, N, _HALVES[dt] if out_dtype is None else (out_dtype,))
     if u is not None:
         _dense(u, "u", (T, R), torch.float32)
-    need = _c_alin_ws(T, K, R, plan._ref)
+    need = _c_alin_ws(T, K, N, R, plan._ref)
     if need and (workspace is None or workspace.numel() < need):
         workspace = _empty((need,), torch.uint8, x.device, stream)
     _check(_c_alin(x.data_ptr(), _DT[dt], ldx, a.data_ptr(), b.data_ptr(), scale.data_ptr(), plan.buffer.data_ptr(),

@@ -18,7 +18,8 @@
 //
 // Tokens of an adapter are gathered through the plan's row list: a tile's rows
 // lie anywhere in the batch.
-#include <cmath>
+#include <cstdlib>
+#include <cstring>
 
 #include "adapter.cuh"
 
@@ -37,7 +38,7 @@ constexpr int64_t kMaxSide = int64_t(1) << 24;
 
 bool plan_fits(const bt_adapter_plan_info &p, int64_t T) {
     return p.tokens == T && p.adapters >= 1 && p.adapters <= kAdapterMaxAdapters && p.without >= 0 && p.without <= T &&
-           p.tiles >= 0 && p.tiles <= T && p.large_tiles >= 0 && p.large_tiles <= p.tiles && p.small_tiles >= 0 &&
+           p.tiles >= 0 && p.tiles <= T && p.small_tiles >= 0 &&
            p.small_tiles <= T && p.small_most >= 0 && p.small_most <= kAdapterSmall && p.parts >= 1 && p.parts <= 2 * kAdapterParts + p.adapters + 1 && p.slots >= 0 &&
            p.slots <= 2 * kAdapterParts;
 }
@@ -74,6 +75,26 @@ cudaError_t align_weights(const uint16_t *src, int R, int64_t C, const AdapterTi
     return launch_align(a, s);
 }
 
+// Which forward a batch takes: everything in one kernel of small tiles, or in two of large ones. Small tiles read an
+// adapter's weights once for 16 tokens, large ones once for 128, but two kernels cost more to begin and to join.
+// Microseconds, fitted on GB300 in graphs (1 to 6000 tokens, 1 to 48 adapters, ranks 8 to 128): one kernel 2.3, for
+// each wave of CTAs 0.7 and its piece of the weights at 42 bytes a nanosecond, and x, base and out at 4.2 TB/s; two
+// kernels 8, 0.3 for every 512 of K, and the longer of x, base and out at 4.5 TB/s and 0.7 a tile. One kernel against
+// two, 4096 x 4096, rank 16: one token 3.9 and 10.1, 768 tokens of one adapter 8.7 and 13.2, 6000 51.6 and 43.3; rank
+// 64: 256 tokens 10.2 and 12.5, 2048 28.1 and 23.3; 64 tokens of 48 adapters 11.7 and 37.0. BT_ADAPTER_PATH=small|large
+// in the environment decides instead.
+bool takes_small(const bt_adapter_plan_info &p, int64_t T, int64_t K, int64_t N, int64_t R) {
+    if (const char *e = std::getenv("BT_ADAPTER_PATH")) {
+        if (std::strcmp(e, "small") == 0) return true;
+        if (std::strcmp(e, "large") == 0) return false;
+    }
+    double small;
+    small_cluster(p.small_tiles, p.small_most, K, N, R, &small);
+    const double bytes = static_cast<double>(T) * static_cast<double>(K + 2 * N) * 2.0;
+    const double rows = bytes / 4.5e6, tiles = 0.7 * static_cast<double>(p.tiles);
+    return small + bytes / 4.2e6 < 8.0 + 0.3 * static_cast<double>((K + 511) / 512) + (rows > tiles ? rows : tiles);
+}
+
 struct Forward {
     const uint16_t *x, *A, *B;
     int64_t ldx, ldb, ldo;
@@ -87,7 +108,7 @@ struct Forward {
     void *out;
     float *u;                  // NULL: not wanted
     void *workspace;
-    bool out_f32;
+    bool out_f32, small;
     bt_dtype type;
     unsigned int *err;
 };
@@ -108,9 +129,9 @@ cudaError_t forward(const Forward &f, cudaStream_t s) {
     pa.out = f.out == f.base ? nullptr : f.out; pa.ldo = f.ldo;
     pa.u = f.u;
     if (pa.out == nullptr && pa.u == nullptr) pa.n = 0;
-    const bool pass_along = f.info->small_tiles > 0 || f.info->large_tiles > 0;
     cudaError_t e;
-    if (f.info->small_tiles > 0) {
+    if (f.info->tiles == 0) return launch_pass(t, of32, pa, s);
+    if (f.small) {
         SmallArgs sm = {};
         sm.plan = Plan{plan.rows, reinterpret_cast<const AdapterTile *>(f.plan + lay.small)};
         sm.x = f.x; sm.A = f.A; sm.B = f.B; sm.ldx = f.ldx;
@@ -124,10 +145,8 @@ cudaError_t forward(const Forward &f, cudaStream_t s) {
         sm.out = f.out; sm.ldo = f.ldo;
         sm.u = f.u;
         sm.pass = pa;
-        e = launch_small(t, of32, sm, f.info->small_tiles, f.info->small_most, s);
-        if (e != cudaSuccess) return e;
+        return launch_small(t, of32, sm, f.info->small_tiles, f.info->small_most, s);
     }
-    if (f.info->large_tiles == 0) return pass_along ? cudaSuccess : launch_pass(t, of32, pa, s);
     ShrinkArgs sh = {};
     sh.plan = plan;
     sh.x = f.x; sh.ldx = f.ldx;
@@ -147,18 +166,18 @@ cudaError_t forward(const Forward &f, cudaStream_t s) {
     sh.C = f.K; sh.R = f.R; sh.u = f.u;
     sh.out = split_rows(f.workspace, f.T, f.R, false, t == BT_F16);
     sh.err = f.err; sh.limit_ns = wait_limit_ns();
-    e = launch_shrink(t, false, sh, f.info->large_tiles, s);
+    e = launch_shrink(t, false, sh, f.info->tiles, s);
     if (e != cudaSuccess) return e;
     ExpandArgs ex = {};
     ex.plan = plan;
-    if (f.info->small_tiles == 0) ex.pass = pa;
+    ex.pass = pa;
     ex.u = sh.out; ex.w = f.B; ex.aw = align_of(f.B, int64_t(f.R) * 2);
     ex.C = f.N; ex.R = f.R; ex.scale = f.scale;
     ex.base = f.base; ex.base_f32 = f.base_f32; ex.ldb = f.ldb;
     ex.out = f.out; ex.ldo = f.ldo;
     ex.wide = wide;
     ex.err = f.err; ex.limit_ns = wait_limit_ns();
-    return launch_expand(t, false, of32, ex, f.info->large_tiles, s);
+    return launch_expand(t, false, of32, ex, f.info->tiles, s);
 }
 
 }  // namespace
@@ -169,8 +188,9 @@ using namespace bt::adapter;
 
 extern "C" {
 
-size_t bt_adapter_linear_workspace(int64_t T, int64_t K, int64_t R, const bt_adapter_plan_info *info) {
-    if (sizes_fit(T, K, 0, R) != BT_OK || info == nullptr || info->large_tiles == 0) return 0;
+size_t bt_adapter_linear_workspace(int64_t T, int64_t K, int64_t N, int64_t R, const bt_adapter_plan_info *info) {
+    if (sizes_fit(T, K, N, R) != BT_OK || info == nullptr || !plan_fits(*info, T) || info->tiles == 0 || takes_small(*info, T, K, N, R))
+        return 0;
     size_t n = 2 * split_bytes(T, R) + round_up256(static_cast<size_t>(T) * 4);
     if (odd_width(K)) n += aligned_bytes(T, K) + aligned_bytes(info->adapters * R, K);
     return n;
@@ -196,7 +216,7 @@ bt_status bt_adapter_linear(const void *x, bt_dtype x_dtype, int64_t ldx, const 
     if (!aligned(x, 2) || !aligned(A, 2) || !aligned(B, 2) || !aligned(scale, 4) || !aligned(plan, 16) || !aligned(u, 16) ||
         !aligned(out, dtype_bytes(out_dtype)) || (base != nullptr && !aligned(base, dtype_bytes(base_dtype))))
         return BT_ERR_ALIGNMENT;
-    const size_t need = bt_adapter_linear_workspace(T, K, R, info);
+    const size_t need = bt_adapter_linear_workspace(T, K, N, R, info);
     if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return BT_ERR_WORKSPACE;
     if (need > 0 && !aligned(workspace, 256)) return BT_ERR_ALIGNMENT;
     Forward f = {};
@@ -215,7 +235,8 @@ bt_status bt_adapter_linear(const void *x, bt_dtype x_dtype, int64_t ldx, const 
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     f.out_f32 = out_dtype == BT_F32;
     f.type = x_dtype;
-    if (info->large_tiles > 0 && (f.err = device_error_word()) == nullptr) return BT_ERR_CUDA;
+    f.small = need == 0;
+    if (!f.small && (f.err = device_error_word()) == nullptr) return BT_ERR_CUDA;
     const cudaError_t e = forward(f, s);
     return e == cudaSuccess ? BT_OK : BT_ERR_CUDA;
 }

@@ -291,7 +291,8 @@ struct SmallArgs {
     int tiles, cluster;
     PassArgs pass;             // rows that the CTAs after the tiles' take along (n = 0: none)
 };
-// most: tokens of the fullest tile
+// CTAs a tile (1, 2, 4, 8) and what the launch takes then, in microseconds; most: tokens of the fullest tile
+int small_cluster(int64_t tiles, int most, int64_t K, int64_t N, int64_t R, double *us);
 cudaError_t launch_small(bt_dtype t, bool out_f32, const SmallArgs &a, int tiles, int most, cudaStream_t s);
 
 template <typename K> cudaError_t allow_smem(K kern, int bytes, std::once_flag &once, cudaError_t &err) {

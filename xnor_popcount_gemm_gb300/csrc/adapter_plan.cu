@@ -76,22 +76,16 @@ bt_status bt_adapter_plan(const int32_t *adapter, int64_t T, int64_t L, void *pl
         }
         return k;
     };
-    // Adapters with many tokens first: the forward takes those tiles alone, the backward all.
-    for (int pass = 0; pass < 2; ++pass) {
-        for (int64_t a = 0; a < L; ++a) {
-            const int32_t first = a == 0 ? 0 : last[a - 1], n = last[a] - first;
-            if (n == 0 || (n > kAdapterSmallMost) != (pass == 0)) continue;
-            r.tiles += even(tiles + r.tiles, static_cast<int32_t>(a), first, n, kAdapterTile);
-            if (pass == 1) {
-                const int32_t k = even(small + r.small_tiles, static_cast<int32_t>(a), first, n, kAdapterSmall);
-                for (int32_t i = 0; i < k; ++i)
-                    if (small[r.small_tiles + i].n > r.small_most) r.small_most = small[r.small_tiles + i].n;
-                r.small_tiles += k;
-            }
-            if (n > r.most_tokens) r.most_tokens = n;
-            ++r.used;
-        }
-        if (pass == 0) r.large_tiles = r.tiles;
+    for (int64_t a = 0; a < L; ++a) {
+        const int32_t first = a == 0 ? 0 : last[a - 1], n = last[a] - first;
+        if (n == 0) continue;
+        r.tiles += even(tiles + r.tiles, static_cast<int32_t>(a), first, n, kAdapterTile);
+        const int32_t k = even(small + r.small_tiles, static_cast<int32_t>(a), first, n, kAdapterSmall);
+        for (int32_t i = 0; i < k; ++i)
+            if (small[r.small_tiles + i].n > r.small_most) r.small_most = small[r.small_tiles + i].n;
+        r.small_tiles += k;
+        if (n > r.most_tokens) r.most_tokens = n;
+        ++r.used;
     }
     r.without = static_cast<int32_t>(T) - last[L - 1];
 

@@ -291,9 +291,8 @@ template <typename T, int RB, int NB, bool FAST> cudaError_t launch_f(SmallArgs 
     static std::once_flag once;
     static cudaError_t err = cudaSuccess;
     if (allow_smem(kern, smem, once, err) != cudaSuccess) return err;
-    int c = 1;
-    // the widest cluster with which two CTAs an SM hold all tiles
-    while (c < 8 && tiles * c <= device_sm_count()) c *= 2;
+    double us;
+    const int c = small_cluster(tiles, 8 * NB, a.K, a.N, a.R, &us);
     a.cluster = c;
     a.tiles = tiles;
     const int64_t pieces = pass_pieces(a.pass);
@@ -327,6 +326,24 @@ template <typename T> cudaError_t launch_t(const SmallArgs &a, bool out_f32, int
 }
 
 }  // namespace
+
+int small_cluster(int64_t tiles, int most, int64_t K, int64_t N, int64_t R, double *us) {
+    // the model of takes_small (adapter.cu); two CTAs an SM, but one where their registers do not allow it; clusters do not fill every group of SMs
+    const int per_sm = padded_rank(static_cast<int>(R)) / 16 * (most <= 8 ? 1 : 2) <= 4 ? 2 : 1;
+    const double fill[4] = {1.0, 0.97, 0.9, per_sm == 2 ? 0.88 : 0.75};
+    int best = 1;
+    for (int i = 0; i < 4; ++i) {
+        const int c = 1 << i;
+        const double slots = device_sm_count() * per_sm * fill[i];
+        const double waves = static_cast<double>(static_cast<int64_t>((static_cast<double>(tiles) * c + slots - 1.0) / slots));
+        const double t = 2.3 + (waves < 1.0 ? 1.0 : waves) * (0.7 + static_cast<double>(R) * static_cast<double>(K + N) * 2.0 / c / 42e3);
+        if (i == 0 || t < *us) {
+            *us = t;
+            best = c;
+        }
+    }
+    return best;
+}
 
 cudaError_t launch_small(bt_dtype t, bool out_f32, const SmallArgs &a, int tiles, int most, cudaStream_t s) {
     if (tiles == 0) return cudaSuccess;
