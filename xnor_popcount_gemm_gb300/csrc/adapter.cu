@@ -92,7 +92,10 @@ bool takes_small(const bt_adapter_plan_info &p, int64_t T, int64_t K, int64_t N,
     small_cluster(p.small_tiles, p.small_most, K, N, R, &small);
     const double bytes = static_cast<double>(T) * static_cast<double>(K + 2 * N) * 2.0;
     const double rows = bytes / 4.5e6, tiles = 0.7 * static_cast<double>(p.tiles);
-    return small + bytes / 4.2e6 < 8.0 + 0.3 * static_cast<double>((K + 511) / 512) + (rows > tiles ? rows : tiles);
+    // widths that are no multiples of 8: one kernel fetches and stores by elements (777 tokens of 12 adapters, 4100 x
+    // 4093, rank 24: 32.8 us against 26.1)
+    const double slow = (K | N | R) % 8 == 0 ? 1.0 : 3.0;
+    return slow * (small + bytes / 4.2e6) < 8.0 + 0.3 * static_cast<double>((K + 511) / 512) + (rows > tiles ? rows : tiles);
 }
 
 struct Forward {
