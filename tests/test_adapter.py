@@ -53,7 +53,7 @@ def test_plan_covers_every_token_once(T, L, none, skew):
     covered(small, SMALL, [a for a in range(L) if count[a]])
     assert info.small_most == max([n for _, _, n, _ in small], default=0)
     # every adapter has its parts, one after the other; those of split ones come first and have the slots in order
-    length = max(256, (-(-T // PARTS) + 63) // 64 * 64)
+    length = max(256, (-(-T // (PARTS if info.used <= 2 else PARTS // 2)) + 63) // 64 * 64)
     assert sorted({a for a, *_ in parts}) == list(range(L))
     slots = [p[3] for p in parts]
     assert slots == list(range(info.slots)) + [-1] * (len(parts) - info.slots) and info.slots <= 2 * PARTS

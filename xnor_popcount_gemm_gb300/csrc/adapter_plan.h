@@ -7,7 +7,7 @@ namespace bt {
 
 constexpr int kAdapterTile = 128;        // rows of a tile of the two-kernel forward and of the backward
 constexpr int kAdapterSmall = 16;        // rows of a tile of the one-kernel forward
-constexpr int kAdapterParts = 8;         // parts the tokens of a gradient are cut into
+constexpr int kAdapterParts = 8;         // parts the tokens of a gradient are cut into, at most
 constexpr int64_t kAdapterMaxTokens = int64_t(1) << 24;
 constexpr int64_t kAdapterMaxAdapters = int64_t(1) << 16;
 constexpr int kAdapterMaxRank = 128;
