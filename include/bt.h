@@ -731,12 +731,14 @@ size_t bt_adapter_linear_workspace(int64_t T, int64_t K, int64_t N, int64_t R, c
  *              needs; 0 for a token without an adapter.
  *   ldx, ldb, ldo  elements from one row to the next, >= K, N, N.
  * A_a x is summed in fp32 and enters the second product as the sum of two
- * 16-bit values, so that 16 bits of it or more count; base + scale * sum is
- * rounded once. Any sizes and element alignments are served; rows that start
+ * 16-bit values (three BF16 ones for an F32 out), so that 16 bits of it or more
+ * count (for an F32 out 22); base + scale * sum is rounded once. Any sizes and element alignments are served; rows that start
  * at multiples of 16 bytes (and R a multiple of 8) are faster. 1 <= R <= 128;
  * T, K, N < 2^24. T = 0 or N = 0 does nothing. workspace:
  * bt_adapter_linear_workspace(T, K, N, R, info) bytes, 256-byte aligned.
- * Equal calls give equal results.
+ * Equal calls give equal results. Batches with few tokens of each adapter go
+ * through one kernel, others through two; BT_ADAPTER_PATH=small or large in
+ * the environment decides instead (the same for this call and its workspace's).
  * Errors: INVALID_ARG, ALIGNMENT, WORKSPACE, UNSUPPORTED, CUDA.
  */
 bt_status bt_adapter_linear(const void *x, bt_dtype x_dtype, int64_t ldx, const void *A, const void *B,

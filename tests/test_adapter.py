@@ -137,7 +137,7 @@ def test_forward_refusals(monkeypatch):
         assert _fwd(**bad) == bt.BT_ERR_ALIGNMENT, bad
     monkeypatch.setenv("BT_ADAPTER_PATH", "large")
     large = dict(T=40, info=_info(T=40))
-    assert _fwd(**large, ws=None) == _fwd(**large, wsb=2 * 1280 + 256 - 1) == bt.BT_ERR_WORKSPACE
+    assert _fwd(**large, ws=None) == _fwd(**large, wsb=3 * 1280 - 1) == bt.BT_ERR_WORKSPACE
     assert _fwd(**large, ws=16384 + 16) == bt.BT_ERR_ALIGNMENT
     monkeypatch.delenv("BT_ADAPTER_PATH")
     assert _fwd(T=0, info=_info(T=0), x=None) == _fwd(N=0, out=None) == bt.BT_OK
@@ -147,11 +147,11 @@ def test_workspace_queries(monkeypatch):
     ws = bt.bt_adapter_linear_workspace
     one, many, most = (bt.bt_adapter_plan([0] * n, 2, device="cpu") for n in (1, 40, 8192))
     assert ws(1, 4096, 4096, 16, one) == 0                       # one kernel
-    assert ws(8192, 4096, 4096, 64, most) == 2 * 8192 * 128 + 8192 * 4
+    assert ws(8192, 4096, 4096, 64, most) == 3 * 8192 * 128
     monkeypatch.setenv("BT_ADAPTER_PATH", "large")
-    assert ws(40, 64, 32, 8, many) == 2 * 1280 + 256             # two 16-bit values of 16 ranks, a power
+    assert ws(40, 64, 32, 8, many) == 3 * 1280                   # two 16-bit values of 16 ranks, and a third or a power
     # a width that is no multiple of 4: room for the rows of x and A at 16-byte multiples
-    assert ws(40, 66, 32, 8, many) == 2 * 1280 + 256 + 5888 + 2304
+    assert ws(40, 66, 32, 8, many) == 3 * 1280 + 5888 + 2304
     assert ws(40, 64, 32, 129, many) == ws(41, 64, 32, 8, many) == 0
     monkeypatch.setenv("BT_ADAPTER_PATH", "small")
     assert ws(8192, 4096, 4096, 64, most) == 0

@@ -112,6 +112,20 @@ def test_forward(T, K, N, R, L, kind, dtype, path):
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("T,R,kind", [(1, 16, "all"), (24, 24, "all"), (40, 64, "some"), (300, 8, "runs"), (300, 100, "skew")])
+def test_fp32_results_are_not_rounded_between_the_products(T, R, kind, dtype, path):
+    """In the 2-norm. u: 512 terms in sums of at most 8 steps that drop less than 2^-23 of a sum each, 4e-7 of it on
+    average if all dropped half of that; the second product as much at most in as many steps; u's values in the second
+    product 2^-22 and less. They are independent: 8e-7 together. (Two bf16 values of u alone: 2^-18 at most, 1.2e-6.)"""
+    x, a, b, s = _inputs(T, 512, 384, R, 3, dtype, seed=R)
+    ids = _ids(T, 3, kind, 5)
+    want = _forward(x, a, b, s, ids, None)[0]
+    plan = bt.bt_adapter_plan(ids, 3)
+    got = bt.bt_adapter_linear(*(v.to(DEV) for v in (x, a, b, s)), plan, out_dtype=torch.float32).double().cpu()
+    assert (got - want).norm() <= 8e-7 * want.norm()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
 @pytest.mark.parametrize("T", [3, 200])
 def test_strides_in_place_and_views(T, dtype, path):
     K, N, R, L = 72, 104, 16, 3

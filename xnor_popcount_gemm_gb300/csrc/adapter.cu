@@ -13,7 +13,7 @@
 //   adapter_small.cu    the whole forward for a few tokens of each adapter
 // The 16-bit operands go to the matrix instructions as they are; u and dU, fp32
 // sums, go as the sum of two 16-bit values (16 bits or more of mantissa; three
-// for the fp32 gradients), so that the only rounding to 16 bits is the result's
+// bf16 ones for fp32 results), so that the only rounding to 16 bits is the result's
 // own.
 //
 // Tokens of an adapter are gathered through the plan's row list: a tile's rows
@@ -48,7 +48,8 @@ bt_status sizes_fit(int64_t T, int64_t K, int64_t N, int64_t R) {
     return BT_OK;
 }
 
-// u as two or three 16-bit values a rank, in a workspace: the bytes of one, and where they lie.
+// u as two or three 16-bit values a rank, in a workspace: the bytes of one, and where they lie (unpower has the
+// third one's place).
 size_t split_bytes(int64_t T, int64_t R) { return round_up256(static_cast<size_t>(T) * padded_rank(static_cast<int>(R)) * 2); }
 SplitRows split_rows(void *p, int64_t T, int R, bool rest, bool unpower) {
     const size_t one = split_bytes(T, R);
@@ -155,7 +156,7 @@ cudaError_t forward(const Forward &f, cudaStream_t s) {
     sh.x = f.x; sh.ldx = f.ldx;
     sh.w = f.A; sh.ldw = f.K;
     if (odd_width(f.K)) {
-        uint8_t *ws = static_cast<uint8_t *>(f.workspace) + 2 * split_bytes(f.T, f.R) + round_up256(static_cast<size_t>(f.T) * 4);
+        uint8_t *ws = static_cast<uint8_t *>(f.workspace) + 3 * split_bytes(f.T, f.R);
         uint16_t *xa = reinterpret_cast<uint16_t *>(ws), *Aa = reinterpret_cast<uint16_t *>(ws + aligned_bytes(f.T, f.K));
         e = align_rows(f.x, f.ldx, f.T, f.K, xa, s);
         if (e == cudaSuccess)
@@ -167,7 +168,7 @@ cudaError_t forward(const Forward &f, cudaStream_t s) {
     sh.ax = align_of(sh.x, sh.ldx * 2);
     sh.aw = align_of(sh.w, sh.ldw * 2);
     sh.C = f.K; sh.R = f.R; sh.u = f.u;
-    sh.out = split_rows(f.workspace, f.T, f.R, false, t == BT_F16);
+    sh.out = split_rows(f.workspace, f.T, f.R, t == BT_BF16 && of32, t == BT_F16);
     sh.err = f.err; sh.limit_ns = wait_limit_ns();
     e = launch_shrink(t, false, sh, f.info->tiles, s);
     if (e != cudaSuccess) return e;
@@ -194,7 +195,7 @@ extern "C" {
 size_t bt_adapter_linear_workspace(int64_t T, int64_t K, int64_t N, int64_t R, const bt_adapter_plan_info *info) {
     if (sizes_fit(T, K, N, R) != BT_OK || info == nullptr || !plan_fits(*info, T) || info->tiles == 0 || takes_small(*info, T, K, N, R))
         return 0;
-    size_t n = 2 * split_bytes(T, R) + round_up256(static_cast<size_t>(T) * 4);
+    size_t n = 3 * split_bytes(T, R);
     if (odd_width(K)) n += aligned_bytes(T, K) + aligned_bytes(info->adapters * R, K);
     return n;
 }

@@ -51,6 +51,13 @@ template <typename T> __device__ __forceinline__ void split2(float v0, float v1,
     const float2 h = unpack2<T>(hi);
     lo = pack2<T>(isinf(h.x) ? 0.0f : v0 - h.x, isinf(h.y) ? 0.0f : v1 - h.y);
 }
+// What the two leave of v, given them.
+template <typename T> __device__ __forceinline__ uint32_t split_rest(float v0, float v1, uint32_t hi, uint32_t lo) {
+    const float2 h = unpack2<T>(hi), l = unpack2<T>(lo);
+    return pack2<T>(isinf(h.x) ? 0.0f : (v0 - h.x) - l.x, isinf(h.y) ? 0.0f : (v1 - h.y) - l.y);
+}
+// bf16 results are rounded to 8 bits, fp32 ones show the 17 of two bf16 values: u enters them as three.
+template <typename T, bool OF32> constexpr bool kRestCounts = OF32 && std::is_same<T, __nv_bfloat16>::value;
 // Half precision reaches 65504 and ends at 2^-24: rows of u are brought to a
 // largest value of about 2^14 by a power of two first (taken out again in fp32).
 template <typename T> __device__ __forceinline__ float row_power(float amax) {
@@ -178,7 +185,7 @@ cudaError_t launch_pass(bt_dtype t, bool out_f32, const PassArgs &a, cudaStream_
 // a power of two of the row's own, whose inverse is in unpower.
 struct SplitRows {
     uint16_t *hi, *lo;         // [T, RP]
-    uint16_t *rest;            // what the two leave, a third value: for the fp32 gradients; NULL: dropped
+    uint16_t *rest;            // what the two leave, a third value: for fp32 results; NULL: dropped
     float *unpower;            // [T], NULL: 1
 };
 inline int padded_rank(int R) { return R <= 16 ? 16 : R <= 32 ? 32 : R <= 64 ? 64 : 128; }

@@ -6,8 +6,8 @@ namespace adapter {
 namespace {
 
 // A CTA keeps its tile's 128 rows of U in shared memory, as two 16-bit values
-// each, and walks a range of columns, 128 at a time: D (128 rows x 128 columns,
-// fp32, tensor memory, two of them) = U_hi W + U_lo W. While one D is added to
+// each (three bf16 ones for fp32 results), side by side, and walks a range of columns, 128 at a time: D (128 rows x 128 columns,
+// fp32, tensor memory, two of them) = U_hi W + U_lo W (+ U_rest W). While one D is added to
 // base and written, the next is worked out, and the columns of W after that and
 // base's next values arrive.
 // Bound: base and out. D is read in the layout in which a quad's four lanes hold
@@ -15,15 +15,19 @@ namespace {
 // a quad's words are turned so that a lane loads and stores 16 bytes. Otherwise a
 // warp's 16 x 64 results pass through shared memory and every lane walks a
 // column, so that a row's elements still travel together.
-// (The same with warp-level matrix instructions and U in registers: 8192 x 4096,
-// rank 64, 53 us.)
+// 8192 x 4096 bf16, rank 64: 35 us, 3.8 TB/s of base and out (with warp-level
+// matrix instructions and U in registers 53 us). Neither memory (29 % busy) nor
+// the issue slots (42 %) nor L1 (44 %) is full: 8 warps an SM, of which every one
+// takes D, base and the result through its registers, do not hide each other's
+// waits, and two D of 128 columns leave room for no third CTA. 4096 x 4096 with
+// base, rank 16: 20 us.
 constexpr int kTile = 128;                 // columns
 template <int RP> constexpr int kParts = RP <= 64 ? 1 : 2;                  // of 64 ranks
-template <int RP> constexpr int kUBytes = kParts<RP> * 2 * kAtom;           // one of hi, lo: 128 rows of 128 bytes
+template <int RP, int VALS> constexpr int kUBytes = (VALS * RP + 63) / 64 * 2 * kAtom;    // 128 rows of 128 bytes for every 64 ranks
 template <int RP, bool WT> constexpr int kWBytes = WT ? 2 * RP * 128 : kParts<RP> * 2 * kAtom;
 constexpr int kTurnPitch = 64 + 4;         // floats of a row of a warp's results
-template <int RP, bool WT, bool WIDE> constexpr int kSmem =
-    2 * kUBytes<RP> + 2 * kWBytes<RP, WT> + (WIDE ? 0 : kThreads / 32 * 16 * kTurnPitch * 4) + 1024;
+template <int RP, bool WT, bool WIDE, int VALS> constexpr int kSmem =
+    kUBytes<RP, VALS> + 2 * kWBytes<RP, WT> + (WIDE ? 0 : kThreads / 32 * 16 * kTurnPitch * 4) + 1024;
 
 // 4 x 4 transpose of words across a quad: lane t gives word j to lane j's word t.
 __device__ __forceinline__ void quad_transpose(uint32_t (&w)[4], int t) {
@@ -60,7 +64,8 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) expand_kernel(cons
     __shared__ uint32_t tmem_slot, abort_flag;
     __shared__ int64_t rows_s[FAST ? 1 : 128];
     __shared__ float mul_s[FAST ? 1 : 128];
-    uint8_t *us = dyn + ((1024u - (smem_u32(dyn) & 1023u)) & 1023u), *wbuf = us + 2 * kUBytes<RP>;
+    constexpr int VALS = kRestCounts<T, OF32> ? 3 : 2;      // of U
+    uint8_t *us = dyn + ((1024u - (smem_u32(dyn) & 1023u)) & 1023u), *wbuf = us + kUBytes<RP, VALS>;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     float *turn = reinterpret_cast<float *>(wbuf + 2 * kWBytes<RP, WT>) + warp * 16 * kTurnPitch;
     // The plan, W and base were there before this call's first kernel began, which waited for all before it: only
@@ -141,13 +146,13 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) expand_kernel(cons
     load_base(s0, 0);
     load_base(s0, 1);
     pdl_wait();                                             // before tensor memory is taken, see shrink_kernel
-    // U: 128 rows of RP ranks, hi and lo
+    // U: 128 rows of RP ranks, hi, lo (and rest)
 #pragma unroll
-    for (int i = 0; i < 2 * 128 * (RP / 8) / kThreads; ++i) {
-        const int at = tid + kThreads * i, half = at / (128 * (RP / 8)), k = at % (128 * (RP / 8));
-        const int m = k / (RP / 8), j = k % (RP / 8);
-        const uint16_t *u = half ? a.u.lo : a.u.hi;
-        cp_async_16(us + half * kUBytes<RP> + (j >> 3) * 2 * kAtom + sw128(m, j & 7),
+    for (int i = 0; i < VALS * 128 * (RP / 8) / kThreads; ++i) {
+        const int at = tid + kThreads * i, val = at / (128 * (RP / 8)), k = at % (128 * (RP / 8));
+        const int m = k / (RP / 8), j = k % (RP / 8), to = val * (RP / 8) + j;
+        const uint16_t *u = val == 0 ? a.u.hi : val == 1 ? a.u.lo : a.u.rest;
+        cp_async_16(us + (to >> 3) * 2 * kAtom + sw128(m, to & 7),
                     m < tile.n ? u + static_cast<int64_t>(tile.first + m) * RP + 8 * j : u, m < tile.n ? 16 : 0);
     }
     cp_async_commit();
@@ -182,13 +187,14 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) expand_kernel(cons
         tc::fence_after_sync();
         const uint32_t u0 = smem_u32(us), w0 = smem_u32(wbuf + (st & 1) * kWBytes<RP, WT>);
 #pragma unroll
-        for (int half = 0; half < 2; ++half)
+        for (int val = 0; val < VALS; ++val)
 #pragma unroll
             for (int k = 0; k < RP / 16; ++k) {             // 16 ranks
-                const uint64_t da = tc::sw128_kmajor_desc(u0 + half * kUBytes<RP> + (k >> 2) * 2 * kAtom + 32 * (k & 3));
+                const int from = val * (RP / 16) + k;
+                const uint64_t da = tc::sw128_kmajor_desc(u0 + (from >> 2) * 2 * kAtom + 32 * (from & 3));
                 const uint64_t db = WT ? tc::sw128_mnmajor_desc(w0 + 2048 * k, RP * 128)
                                        : tc::sw128_kmajor_desc(w0 + (k >> 2) * 2 * kAtom + 32 * (k & 3));
-                tc::mma_f16(tmem + (st & 1) * kTile, da, db, kIdesc, (half | k) != 0);
+                tc::mma_f16(tmem + (st & 1) * kTile, da, db, kIdesc, (val | k) != 0);
             }
         tc::mma_commit(smem_u32(&ready[st & 1]));
     };
@@ -317,7 +323,7 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) expand_kernel(cons
 template <typename T, int RP, bool WT, bool OF32, bool FAST, bool BF32>
 cudaError_t launch_rp(const ExpandArgs &a, cudaStream_t s) {
     auto kern = expand_kernel<T, RP, WT, OF32, FAST, BF32>;
-    constexpr int smem = kSmem<RP, WT, FAST>;
+    constexpr int smem = kSmem<RP, WT, FAST, kRestCounts<T, OF32> ? 3 : 2>;
     static std::once_flag once;
     static cudaError_t err = cudaSuccess;
     if (allow_smem(kern, smem, once, err) != cudaSuccess) return err;

@@ -17,6 +17,11 @@ namespace {
 // products run in one launch, so that neither leaves the machine half empty at
 // its end. x and g are asked for before the previous kernel, which works out
 // dU, has ended.
+// Bound: x and g, read once. 4096 tokens of 8 adapters, 4096 x 4096, rank 16:
+// 26 us alone, 2.6 TB/s, with DRAM, L2 and issue all under half: 704 short CTAs
+// (16 stages at most), which wait for their first copies and, where parts are
+// summed, for one another's sums. 64 tokens a stage at rank 16, 32 from rank 32
+// on, where U takes more of it.
 using T = __nv_bfloat16;
 constexpr int kCols = 128;
 constexpr int kWarps = 9;

@@ -92,8 +92,9 @@ bt_status bt_adapter_plan(const int32_t *adapter, int64_t T, int64_t L, void *pl
     // The gradients' parts: at most a quarter of the tokens each, or an eighth where
     // one or two adapters have them all (whole 64s, at least 256), every adapter once
     // at least, so that one without tokens gets its zeros. (4096 tokens of 8 adapters,
-    // 4096 x 4096, rank 16: quarters 53.4 us, eighths 56.6, halves 55.1.) A split adapter's parts have a slot each for their sums. Adapters with
-    // many tokens first: their parts begin first, and what ends last is short.
+    // 4096 x 4096, rank 16, backward: quarters 53.4 us, eighths 56.6, halves 55.1.) A
+    // split adapter's parts have a slot each for their sums. Adapters with many tokens
+    // first: their parts begin first, and what ends last is short.
     const int64_t cut = r.used <= 2 ? kAdapterParts : kAdapterParts / 2;
     int32_t len = static_cast<int32_t>((T + cut - 1) / cut);
     len = len < 256 ? 256 : (len + 63) / 64 * 64;

@@ -19,6 +19,11 @@ namespace {
 // Second: 16 tokens are its rows, and the columns 8t + 2j + {0, 1} of a unit of
 // 32 are its columns 2t, 2t + 1 in the unit's instruction j, so that a lane ends
 // up with 8 consecutive results of a token.
+//
+// Bound: the adapters' weights, read once, and latency. One token, 4096 x 4096,
+// rank 16: 3.9 us. 64 tokens of 48 adapters, 4096 x 11008, rank 32: 12.3 us for
+// 50 MB, 4.0 TB/s; warps wait for memory half of their time, in a few trips one
+// after another (plan, tokens and A, exchange, B).
 
 // Elements k .. k + 7 of a row of n, zeros beyond. al: bytes the rows start at multiples of (FAST: 16).
 template <bool FAST> __device__ __forceinline__ uint4 row8(const uint16_t *p, int k, int n, int al) {
@@ -38,7 +43,8 @@ struct Base8 {
 };
 
 // RB: blocks of 16 ranks; NB: blocks of 8 tokens. FAST: every row starts at a 16-byte multiple and holds whole vectors.
-template <typename T, int RB, int NB, bool FAST>
+// REST: u as three values, for fp32 results.
+template <typename T, int RB, int NB, bool FAST, bool REST>
 __global__ void __launch_bounds__(kThreads, RB * NB <= 4 ? 2 : 1) small_kernel(const SmallArgs a, int out_f32) {
     constexpr int RP = 16 * RB, TOK = 8 * NB, UP = RP + 4;
     constexpr int RK = (RB + 1) / 2;                        // 32-rank pieces of B's rows
@@ -187,7 +193,7 @@ __global__ void __launch_bounds__(kThreads, RB * NB <= 4 ? 2 : 1) small_kernel(c
     __syncthreads();
     // its fragments: lane t of a quad holds ranks 32q + 8t .. + 7 of token g (and g + 8)
     const float s = a.scale[tile.adapter];
-    uint32_t uh[RK][NB][4], ul[RK][NB][4];
+    uint32_t uh[RK][NB][4], ul[RK][NB][4], ur[RK][NB][4];
     float mul[NB];
 #pragma unroll
     for (int j = 0; j < NB; ++j) {
@@ -207,7 +213,11 @@ __global__ void __launch_bounds__(kThreads, RB * NB <= 4 ? 2 : 1) small_kernel(c
 #pragma unroll
         for (int q = 0; q < RK; ++q)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) split2<T>(v[q][2 * e] * p, v[q][2 * e + 1] * p, uh[q][j][e], ul[q][j][e]);
+            for (int e = 0; e < 4; ++e) {
+                const float v0 = v[q][2 * e] * p, v1 = v[q][2 * e + 1] * p;
+                split2<T>(v0, v1, uh[q][j][e], ul[q][j][e]);
+                if constexpr (REST) ur[q][j][e] = split_rest<T>(v0, v1, uh[q][j][e], ul[q][j][e]);
+            }
     }
     for (int first = n0 + warp; first < n1; first += 8 * PRE) {
 #pragma unroll
@@ -222,14 +232,15 @@ __global__ void __launch_bounds__(kThreads, RB * NB <= 4 ? 2 : 1) small_kernel(c
                 for (int q = 0; q < RK; ++q) {
                     const uint4 w = wb[i][j][q];
                     // rows 8..15 are tokens 8..15, where there are any
-                    const uint32_t h0[4] = {uh[q][0][0], NB > 1 ? uh[q][NB - 1][0] : 0u, uh[q][0][1], NB > 1 ? uh[q][NB - 1][1] : 0u};
-                    const uint32_t h1[4] = {uh[q][0][2], NB > 1 ? uh[q][NB - 1][2] : 0u, uh[q][0][3], NB > 1 ? uh[q][NB - 1][3] : 0u};
-                    const uint32_t l0[4] = {ul[q][0][0], NB > 1 ? ul[q][NB - 1][0] : 0u, ul[q][0][1], NB > 1 ? ul[q][NB - 1][1] : 0u};
-                    const uint32_t l1[4] = {ul[q][0][2], NB > 1 ? ul[q][NB - 1][2] : 0u, ul[q][0][3], NB > 1 ? ul[q][NB - 1][3] : 0u};
-                    mma<T>(d[j], h0, w.x, w.y);
-                    mma<T>(d[j], h1, w.z, w.w);
-                    mma<T>(d[j], l0, w.x, w.y);
-                    mma<T>(d[j], l1, w.z, w.w);
+                    auto add = [&](const uint32_t (&f)[NB][4]) {
+                        const uint32_t f0[4] = {f[0][0], NB > 1 ? f[NB - 1][0] : 0u, f[0][1], NB > 1 ? f[NB - 1][1] : 0u};
+                        const uint32_t f1[4] = {f[0][2], NB > 1 ? f[NB - 1][2] : 0u, f[0][3], NB > 1 ? f[NB - 1][3] : 0u};
+                        mma<T>(d[j], f0, w.x, w.y);
+                        mma<T>(d[j], f1, w.z, w.w);
+                    };
+                    add(uh[q]);
+                    add(ul[q]);
+                    if constexpr (REST) add(ur[q]);
                 }
             }
             load_b(unit + 8 * PRE, wb[i]);
@@ -285,8 +296,9 @@ __global__ void __launch_bounds__(kThreads, RB * NB <= 4 ? 2 : 1) small_kernel(c
     }
 }
 
-template <typename T, int RB, int NB, bool FAST> cudaError_t launch_f(SmallArgs a, bool out_f32, int tiles, cudaStream_t s) {
-    auto kern = small_kernel<T, RB, NB, FAST>;
+template <typename T, int RB, int NB, bool FAST, bool REST>
+cudaError_t launch_f(SmallArgs a, bool out_f32, int tiles, cudaStream_t s) {
+    auto kern = small_kernel<T, RB, NB, FAST, REST>;
     constexpr int smem = 8 * 8 * NB * (32 * RB + 4) * static_cast<int>(sizeof(float));
     static std::once_flag once;
     static cudaError_t err = cudaSuccess;
@@ -313,7 +325,11 @@ template <typename T, int RB, int NB, bool FAST> cudaError_t launch_f(SmallArgs 
 }
 template <typename T, int RB, int NB> cudaError_t launch_rn(const SmallArgs &a, bool out_f32, int tiles, cudaStream_t s) {
     const bool fast = a.ax == 16 && a.aa == 16 && a.ab == 16 && a.wide;
-    return fast ? launch_f<T, RB, NB, true>(a, out_f32, tiles, s) : launch_f<T, RB, NB, false>(a, out_f32, tiles, s);
+    if constexpr (kRestCounts<T, true>) {
+        if (out_f32)
+            return fast ? launch_f<T, RB, NB, true, true>(a, true, tiles, s) : launch_f<T, RB, NB, false, true>(a, true, tiles, s);
+    }
+    return fast ? launch_f<T, RB, NB, true, false>(a, out_f32, tiles, s) : launch_f<T, RB, NB, false, false>(a, out_f32, tiles, s);
 }
 template <typename T, int NB> cudaError_t launch_n(const SmallArgs &a, bool out_f32, int tiles, cudaStream_t s) {
     if (a.R <= 16) return launch_rn<T, 1, NB>(a, out_f32, tiles, s);
@@ -328,7 +344,8 @@ template <typename T> cudaError_t launch_t(const SmallArgs &a, bool out_f32, int
 }  // namespace
 
 int small_cluster(int64_t tiles, int most, int64_t K, int64_t N, int64_t R, double *us) {
-    // the model of takes_small (adapter.cu); two CTAs an SM, but one where their registers do not allow it; clusters do not fill every group of SMs
+    // the model of takes_small (adapter.cu); two CTAs an SM, but one where their registers do not allow it; clusters
+    // do not fill every group of SMs
     const int per_sm = padded_rank(static_cast<int>(R)) / 16 * (most <= 8 ? 1 : 2) <= 4 ? 2 : 1;
     const double fill[4] = {1.0, 0.97, 0.9, per_sm == 2 ? 0.88 : 0.75};
     int best = 1;
