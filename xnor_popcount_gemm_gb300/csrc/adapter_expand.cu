@@ -6,15 +6,16 @@ namespace adapter {
 namespace {
 
 // A CTA keeps its tile's 128 rows of U in shared memory, as two 16-bit values
-// each (three bf16 ones for fp32 results), side by side, and walks a range of columns, 128 at a time: D (128 rows x 128 columns,
-// fp32, tensor memory, two of them) = U_hi W + U_lo W (+ U_rest W). While one D is added to
-// base and written, the next is worked out, and the columns of W after that and
-// base's next values arrive.
+// each (three bf16 ones for fp32 results), side by side, and walks a range of
+// columns, 128 at a time: D (128 rows x 128 columns, fp32, tensor memory, two of
+// them) = U_hi W + U_lo W (+ U_rest W). While one D is added to base and written,
+// the next is worked out, and the columns of W after that and base's next values
+// arrive.
 // Bound: base and out. D is read in the layout in which a quad's four lanes hold
 // 8 columns of a row. WIDE (rows of base and out start at 16-byte multiples):
 // a quad's words are turned so that a lane loads and stores 16 bytes. Otherwise a
-// warp's 16 x 64 results pass through shared memory and every lane walks a
-// column, so that a row's elements still travel together.
+// warp's results pass through shared memory and every lane walks a column, so
+// that a row's elements still travel together.
 // 8192 x 4096 bf16, rank 64: 35 us, 3.8 TB/s of base and out (with warp-level
 // matrix instructions and U in registers 53 us). Neither memory (29 % busy) nor
 // the issue slots (42 %) nor L1 (44 %) is full: 8 warps an SM, of which every one
@@ -26,8 +27,11 @@ template <int RP> constexpr int kParts = RP <= 64 ? 1 : 2;                  // o
 template <int RP, int VALS> constexpr int kUBytes = (VALS * RP + 63) / 64 * 2 * kAtom;    // 128 rows of 128 bytes for every 64 ranks
 template <int RP, bool WT> constexpr int kWBytes = WT ? 2 * RP * 128 : kParts<RP> * 2 * kAtom;
 constexpr int kTurnPitch = 64 + 4;         // floats of a row of a warp's results
+// Rows of them at a time: 16, or 8 where two CTAs would not fit on an SM else (4096 x 4093 bf16 to fp32, rank 64: 65 us
+// against 105; 16 take 26 us where 8 take 27, 777 x 4093 f16, rank 24).
+template <int VALS> constexpr int kTurnRows = VALS == 3 ? 8 : 16;
 template <int RP, bool WT, bool WIDE, int VALS> constexpr int kSmem =
-    kUBytes<RP, VALS> + 2 * kWBytes<RP, WT> + (WIDE ? 0 : kThreads / 32 * 16 * kTurnPitch * 4) + 1024;
+    kUBytes<RP, VALS> + 2 * kWBytes<RP, WT> + (WIDE ? 0 : kThreads / 32 * kTurnRows<VALS> * kTurnPitch * 4) + 1024;
 
 // 4 x 4 transpose of words across a quad: lane t gives word j to lane j's word t.
 __device__ __forceinline__ void quad_transpose(uint32_t (&w)[4], int t) {
@@ -67,7 +71,7 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) expand_kernel(cons
     constexpr int VALS = kRestCounts<T, OF32> ? 3 : 2;      // of U
     uint8_t *us = dyn + ((1024u - (smem_u32(dyn) & 1023u)) & 1023u), *wbuf = us + kUBytes<RP, VALS>;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-    float *turn = reinterpret_cast<float *>(wbuf + 2 * kWBytes<RP, WT>) + warp * 16 * kTurnPitch;
+    float *turn = reinterpret_cast<float *>(wbuf + 2 * kWBytes<RP, WT>) + warp * kTurnRows<VALS> * kTurnPitch;
     // The plan, W and base were there before this call's first kernel began, which waited for all before it: only
     // U, which that kernel writes, has to be waited for.
     if (static_cast<int>(blockIdx.x) >= a.tiles * a.splits) {
@@ -270,13 +274,16 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) expand_kernel(cons
                     }
                 }
             } else {
+                constexpr int TURN = kTurnRows<VALS>;
+                if constexpr (TURN == 16) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
+                    for (int h = 0; h < 2; ++h)
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        *reinterpret_cast<uint2 *>(turn + (8 * h + g) * kTurnPitch + 8 * j + 2 * t) =
-                            make_uint2(acc[4 * j + 2 * h], acc[4 * j + 2 * h + 1]);
-                __syncwarp();
+                        for (int j = 0; j < 8; ++j)
+                            *reinterpret_cast<uint2 *>(turn + (8 * h + g) * kTurnPitch + 8 * j + 2 * t) =
+                                make_uint2(acc[4 * j + 2 * h], acc[4 * j + 2 * h + 1]);
+                    __syncwarp();
+                }
                 // eight rows at a time: their base first, all on its way at once
 #pragma unroll 1
                 for (int m8 = 0; m8 < 16; m8 += 8) {
@@ -292,6 +299,14 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) expand_kernel(cons
                             else v[m][e] = ok ? Elem<T>::to_f32(static_cast<const T *>(a.base)[r + 32 * e]) : 0.0f;
                         }
                     }
+                    if constexpr (TURN == 8) {
+                        __syncwarp();                       // the eight before have been read
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            *reinterpret_cast<uint2 *>(turn + g * kTurnPitch + 8 * j + 2 * t) =
+                                m8 == 0 ? make_uint2(acc[4 * j], acc[4 * j + 1]) : make_uint2(acc[4 * j + 2], acc[4 * j + 3]);
+                        __syncwarp();
+                    }
 #pragma unroll
                     for (int m = 0; m < 8; ++m) {
                         const int at = m0 + 16 * b + m8 + m;
@@ -300,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) expand_kernel(cons
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
                             if (at >= tile.n || c0 + lane + 32 * e >= a.C) continue;
-                            const float f = __fmaf_rn(turn[(m8 + m) * kTurnPitch + lane + 32 * e], ms, v[m][e]);
+                            const float f = __fmaf_rn(turn[(TURN == 16 ? m8 + m : m) * kTurnPitch + lane + 32 * e], ms, v[m][e]);
                             if constexpr (OF32) static_cast<float *>(a.out)[r + 32 * e] = f;
                             else static_cast<T *>(a.out)[r + 32 * e] = to16<T>(f);
                         }
