@@ -730,9 +730,9 @@ size_t bt_adapter_linear_workspace(int64_t T, int64_t K, int64_t N, int64_t R, c
  *   u          device fp32 [T, R] out, 16-byte aligned, or NULL: A_a x_t, what the backward
  *              needs; 0 for a token without an adapter.
  *   ldx, ldb, ldo  elements from one row to the next, >= K, N, N.
- * A_a x is summed in fp32 and enters the second product as the sum of two
- * 16-bit values (three BF16 ones for an F32 out), so that 16 bits of it or more
- * count (for an F32 out 22); base + scale * sum is rounded once. Any sizes and element alignments are served; rows that start
+ * A_a x is summed in fp32 and enters the second product as the sum of three
+ * BF16 values (all of its 24 bits) or two F16 ones (22 bits); base + scale * sum
+ * is rounded once. Any sizes and element alignments are served; rows that start
  * at multiples of 16 bytes (and R a multiple of 8) are faster. 1 <= R <= 128;
  * T, K, N < 2^24. T = 0 or N = 0 does nothing. workspace:
  * bt_adapter_linear_workspace(T, K, N, R, info) bytes, 256-byte aligned.
@@ -764,8 +764,7 @@ size_t bt_adapter_linear_backward_workspace(int64_t T, int64_t K, int64_t N, int
  *   grad_A     device fp32 [L, R, K] out; grad_B device fp32 [L, N, R] out, 16-byte aligned,
  *              both overwritten.
  *   ldx, ldg, ldgb, ldgx  elements from one row to the next.
- * Sums are fp32; dU and u enter the products as the sum of two (for grad_x)
- * or three (for grad_A and grad_B) BF16 values.
+ * Sums are fp32; dU and u enter the products as the sum of three BF16 values.
  * Tokens of an adapter are summed in a fixed order: equal calls give equal
  * results. Limits, workspace rules and errors as bt_adapter_linear.
  */

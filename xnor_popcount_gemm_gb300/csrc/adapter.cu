@@ -12,9 +12,8 @@
 //   adapter_grad.cu     dA, dB: reduce the tokens
 //   adapter_small.cu    the whole forward for a few tokens of each adapter
 // The 16-bit operands go to the matrix instructions as they are; u and dU, fp32
-// sums, go as the sum of two 16-bit values (16 bits or more of mantissa; three
-// bf16 ones for fp32 results), so that the only rounding to 16 bits is the result's
-// own.
+// sums, go as the sum of three bf16 values (all 24 bits of mantissa) or of two in
+// half precision (22 bits), so that the only rounding to 16 bits is the result's own.
 //
 // Tokens of an adapter are gathered through the plan's row list: a tile's rows
 // lie anywhere in the batch.
@@ -168,7 +167,7 @@ cudaError_t forward(const Forward &f, cudaStream_t s) {
     sh.ax = align_of(sh.x, sh.ldx * 2);
     sh.aw = align_of(sh.w, sh.ldw * 2);
     sh.C = f.K; sh.R = f.R; sh.u = f.u;
-    sh.out = split_rows(f.workspace, f.T, f.R, t == BT_BF16 && of32, t == BT_F16);
+    sh.out = split_rows(f.workspace, f.T, f.R, t == BT_BF16, t == BT_F16);
     sh.err = f.err; sh.limit_ns = wait_limit_ns();
     e = launch_shrink(t, false, sh, f.info->tiles, s);
     if (e != cudaSuccess) return e;

@@ -56,8 +56,10 @@ template <typename T> __device__ __forceinline__ uint32_t split_rest(float v0, f
     const float2 h = unpack2<T>(hi), l = unpack2<T>(lo);
     return pack2<T>(isinf(h.x) ? 0.0f : (v0 - h.x) - l.x, isinf(h.y) ? 0.0f : (v1 - h.y) - l.y);
 }
-// bf16 results are rounded to 8 bits, fp32 ones show the 17 of two bf16 values: u enters them as three.
-template <typename T, bool OF32> constexpr bool kRestCounts = OF32 && std::is_same<T, __nv_bfloat16>::value;
+// How many 16-bit values an fp32 sum enters a product as: three bf16 ones hold all of its 24 bits, two half-precision
+// ones 22. (Two bf16 values hold 16: no less than a bf16 result shows, but its rounding then falls the other way now
+// and then, and ranks that cancel show it in full.)
+template <typename T> constexpr int kValues = std::is_same<T, __nv_bfloat16>::value ? 3 : 2;
 // Half precision reaches 65504 and ends at 2^-24: rows of u are brought to a
 // largest value of about 2^14 by a power of two first (taken out again in fp32).
 template <typename T> __device__ __forceinline__ float row_power(float amax) {
@@ -181,11 +183,11 @@ template <typename T> __device__ void pass_rows(const PassArgs &a, bool out_f32,
 cudaError_t launch_pass(bt_dtype t, bool out_f32, const PassArgs &a, cudaStream_t s);
 
 // u and dU between the products: rows in the plan's order, padded to RP = 16,
-// 32, 64 or 128 ranks, as the sum of two 16-bit values; in half precision times
-// a power of two of the row's own, whose inverse is in unpower.
+// 32, 64 or 128 ranks, as the sum of three bf16 values or of two in half precision, these
+// times a power of two of the row's own, whose inverse is in unpower.
 struct SplitRows {
     uint16_t *hi, *lo;         // [T, RP]
-    uint16_t *rest;            // what the two leave, a third value: for fp32 results; NULL: dropped
+    uint16_t *rest;            // what the two leave, the third value (bf16)
     float *unpower;            // [T], NULL: 1
 };
 inline int padded_rank(int R) { return R <= 16 ? 16 : R <= 32 ? 32 : R <= 64 ? 64 : 128; }

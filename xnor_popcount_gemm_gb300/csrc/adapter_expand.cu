@@ -5,8 +5,8 @@ namespace bt {
 namespace adapter {
 namespace {
 
-// A CTA keeps its tile's 128 rows of U in shared memory, as two 16-bit values
-// each (three bf16 ones for fp32 results), side by side, and walks a range of
+// A CTA keeps its tile's 128 rows of U in shared memory, as three bf16 values
+// each (two in half precision), side by side, and walks a range of
 // columns, 128 at a time: D (128 rows x 128 columns, fp32, tensor memory, two of
 // them) = U_hi W + U_lo W (+ U_rest W). While one D is added to base and written,
 // the next is worked out, and the columns of W after that and base's next values
@@ -68,7 +68,7 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) expand_kernel(cons
     __shared__ uint32_t tmem_slot, abort_flag;
     __shared__ int64_t rows_s[FAST ? 1 : 128];
     __shared__ float mul_s[FAST ? 1 : 128];
-    constexpr int VALS = kRestCounts<T, OF32> ? 3 : 2;      // of U
+    constexpr int VALS = kValues<T>;                        // of U
     uint8_t *us = dyn + ((1024u - (smem_u32(dyn) & 1023u)) & 1023u), *wbuf = us + kUBytes<RP, VALS>;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     float *turn = reinterpret_cast<float *>(wbuf + 2 * kWBytes<RP, WT>) + warp * kTurnRows<VALS> * kTurnPitch;
@@ -338,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, RP <= 64 ? 2 : 1) expand_kernel(cons
 template <typename T, int RP, bool WT, bool OF32, bool FAST, bool BF32>
 cudaError_t launch_rp(const ExpandArgs &a, cudaStream_t s) {
     auto kern = expand_kernel<T, RP, WT, OF32, FAST, BF32>;
-    constexpr int smem = kSmem<RP, WT, FAST, kRestCounts<T, OF32> ? 3 : 2>;
+    constexpr int smem = kSmem<RP, WT, FAST, kValues<T>>;
     static std::once_flag once;
     static cudaError_t err = cudaSuccess;
     if (allow_smem(kern, smem, once, err) != cudaSuccess) return err;

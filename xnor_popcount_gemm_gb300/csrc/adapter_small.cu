@@ -43,8 +43,7 @@ struct Base8 {
 };
 
 // RB: blocks of 16 ranks; NB: blocks of 8 tokens. FAST: every row starts at a 16-byte multiple and holds whole vectors.
-// REST: u as three values, for fp32 results.
-template <typename T, int RB, int NB, bool FAST, bool REST>
+template <typename T, int RB, int NB, bool FAST>
 __global__ void __launch_bounds__(kThreads, RB * NB <= 4 ? 2 : 1) small_kernel(const SmallArgs a, int out_f32) {
     constexpr int RP = 16 * RB, TOK = 8 * NB, UP = RP + 4;
     constexpr int RK = (RB + 1) / 2;                        // 32-rank pieces of B's rows
@@ -193,6 +192,7 @@ __global__ void __launch_bounds__(kThreads, RB * NB <= 4 ? 2 : 1) small_kernel(c
     __syncthreads();
     // its fragments: lane t of a quad holds ranks 32q + 8t .. + 7 of token g (and g + 8)
     const float s = a.scale[tile.adapter];
+    constexpr bool REST = kValues<T> == 3;
     uint32_t uh[RK][NB][4], ul[RK][NB][4], ur[RK][NB][4];
     float mul[NB];
 #pragma unroll
@@ -296,9 +296,9 @@ __global__ void __launch_bounds__(kThreads, RB * NB <= 4 ? 2 : 1) small_kernel(c
     }
 }
 
-template <typename T, int RB, int NB, bool FAST, bool REST>
+template <typename T, int RB, int NB, bool FAST>
 cudaError_t launch_f(SmallArgs a, bool out_f32, int tiles, cudaStream_t s) {
-    auto kern = small_kernel<T, RB, NB, FAST, REST>;
+    auto kern = small_kernel<T, RB, NB, FAST>;
     constexpr int smem = 8 * 8 * NB * (32 * RB + 4) * static_cast<int>(sizeof(float));
     static std::once_flag once;
     static cudaError_t err = cudaSuccess;
@@ -325,11 +325,7 @@ cudaError_t launch_f(SmallArgs a, bool out_f32, int tiles, cudaStream_t s) {
 }
 template <typename T, int RB, int NB> cudaError_t launch_rn(const SmallArgs &a, bool out_f32, int tiles, cudaStream_t s) {
     const bool fast = a.ax == 16 && a.aa == 16 && a.ab == 16 && a.wide;
-    if constexpr (kRestCounts<T, true>) {
-        if (out_f32)
-            return fast ? launch_f<T, RB, NB, true, true>(a, true, tiles, s) : launch_f<T, RB, NB, false, true>(a, true, tiles, s);
-    }
-    return fast ? launch_f<T, RB, NB, true, false>(a, out_f32, tiles, s) : launch_f<T, RB, NB, false, false>(a, out_f32, tiles, s);
+    return fast ? launch_f<T, RB, NB, true>(a, out_f32, tiles, s) : launch_f<T, RB, NB, false>(a, out_f32, tiles, s);
 }
 template <typename T, int NB> cudaError_t launch_n(const SmallArgs &a, bool out_f32, int tiles, cudaStream_t s) {
     if (a.R <= 16) return launch_rn<T, 1, NB>(a, out_f32, tiles, s);
