@@ -260,23 +260,54 @@ template <typename T> __device__ __forceinline__ float max_of(const uint4 &q, co
 }
 
 // The running sum of one lane: 2^(f c - mc), mc being m c rounded; what that
-// misses comes back into the sum in the end. `seen` is the largest logit so
-// far, which m may trail by the slack.
+// misses, less than 2^-4, comes back into the sum in the end. Where m c is so
+// large that its rounding is an exponent of its own (`far`: a lane that has met
+// nothing but masked values yet, or a row of huge ones) the sum is relative to m
+// itself, 2^((f - m) c). `seen` is the largest logit so far, which m may trail by
+// the slack.
+constexpr float kNear = 1048576.0f;        // 2^20
 struct Running {
     float m, mc, s, seen;
+    bool far;
 };
-__device__ __forceinline__ Running running_empty(float c) { return Running{kMasked, __fmul_rn(kMasked, c), 0.0f, kMasked}; }
+__device__ __forceinline__ bool is_far(float mc) { return !(fabsf(mc) <= kNear); }
+__device__ __forceinline__ Running running_empty() { return Running{kMasked, 0.0f, 0.0f, kMasked, true}; }
+__device__ __forceinline__ Running running_from(const MaxSum &x, float c) {
+    const float mc = __fmul_rn(x.m, c);
+    const bool far = is_far(mc);
+    return Running{x.m, mc, far ? x.s : x.s * ex2(__fmaf_rn(x.m, c, -mc)), x.m, far};
+}
+// The sum relative to m itself.
+__device__ __forceinline__ MaxSum running_sum(const Running &r, float c) {
+    return MaxSum{r.m, r.far ? r.s : r.s * ex2(__fmaf_rn(-r.m, c, r.mc))};
+}
+// A larger reference.
+__device__ __forceinline__ void running_move(Running &r, float m, float c) {
+    const float mc = __fmul_rn(m, c);
+    if (r.far || is_far(mc)) {
+        MaxSum x = running_sum(r, c);
+        x.s *= ex2((x.m - m) * c);
+        x.m = m;
+        const float seen = r.seen;
+        r = running_from(x, c);
+        r.seen = seen;
+    } else {
+        r.s *= ex2(r.mc - mc);
+        r.m = m;
+        r.mc = mc;
+    }
+}
 template <typename T> __device__ __forceinline__ void running_add(Running &r, const uint4 &q, const Args &a) {
     constexpr int VEC = 16 / sizeof(T);
     float f[VEC];
     Elem<T>::unpack(q, f);
     const float mx = max_of<T>(q, f);
     r.seen = fmaxf(r.seen, mx);
-    if (mx > r.m + a.slack) {
-        const float to = __fmul_rn(mx, a.c);
-        r.s *= ex2(r.mc - to);
-        r.m = mx;
-        r.mc = to;
+    if (mx > r.m + a.slack) running_move(r, mx, a.c);
+    if (r.far) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) r.s += ex2((f[e] - r.m) * a.c);
+        return;
     }
     float2 sum;
 #pragma unroll
@@ -287,14 +318,24 @@ template <typename T> __device__ __forceinline__ void running_add(Running &r, co
     }
     r.s += sum.x + sum.y;
 }
-__device__ __forceinline__ MaxSum running_warp(const Running &r, float c) {
-    return ms_warp(MaxSum{r.m, r.s * ex2(__fmaf_rn(-r.m, c, r.mc))}, r.seen, c);
-}
+__device__ __forceinline__ MaxSum running_warp(const Running &r, float c) { return ms_warp(running_sum(r, c), r.seen, c); }
 
-// The gradient outside the slots: coef * 2^(z c1 - shift).
+// The gradient outside the slots: coef * 2^(z c1 - shift), or, where the
+// rounding of shift would be an exponent of its own (`far`, as above), coef *
+// 2^((z k1 - base) k2), c1 = k1 k2.
 struct Slope {
     float coef, c1, shift;
+    bool far;
+    float k1, base, k2;
 };
+__device__ __forceinline__ Slope slope_make(float coef, float c1, float k1, float base, float k2) {
+    const float shift = __fmul_rn(base, k2);                // the factor takes what the rounding misses
+    const bool far = is_far(shift);
+    return Slope{far ? coef : coef * ex2(__fmaf_rn(-base, k2, shift)), c1, shift, far, k1, base, k2};
+}
+// Nothing: 0 wherever the logits are masked.
+__device__ __forceinline__ Slope slope_none(float c1) { return Slope{0.0f, c1, 0.0f, false, 0.0f, 0.0f, 0.0f}; }
+// (not far)
 template <typename T> __device__ __forceinline__ void slope_vec(const Slope &g, const uint4 &q, float *f) {
     constexpr int VEC = 16 / sizeof(T);
     Elem<T>::unpack(q, f);
@@ -306,21 +347,26 @@ template <typename T> __device__ __forceinline__ void slope_vec(const Slope &g, 
         f[e + 1] = p.y;
     }
 }
-__device__ __forceinline__ float slope_of(const Slope &g, float v) { return g.coef * ex2(__fmaf_rn(v, g.c1, -g.shift)); }
+__device__ __forceinline__ float slope_of(const Slope &g, float v) {
+    return g.coef * ex2(g.far ? __fmaf_rn(v, g.k1, -g.base) * g.k2 : __fmaf_rn(v, g.c1, -g.shift));
+}
+template <typename T> __device__ __forceinline__ void slope_any(const Slope &g, const uint4 &q, float *f) {
+    if (g.far) {
+        Elem<T>::unpack(q, f);
+#pragma unroll
+        for (int e = 0; e < static_cast<int>(16 / sizeof(T)); ++e) f[e] = slope_of(g, f[e]);
+    } else {
+        slope_vec<T>(g, q, f);
+    }
+}
 
 // Both from a row's sums: over the slots, outside them, over all.
 __device__ __forceinline__ Slope slope_from(const Args &a, const Teacher &te, float w, const MaxSum &rest, const MaxSum &all) {
-    float coef, base;
-    if (a.tlse != nullptr) {
-        const float pr = rest.s * ex2((rest.m - all.m) * a.c) / all.s;
-        coef = rest.s == 0.0f ? 0.0f : w * (pr - te.qr) / rest.s;
-        base = rest.m;
-    } else {
-        coef = all.s == 0.0f ? 0.0f : w / all.s;
-        base = all.m;
-    }
-    const float shift = __fmul_rn(base, a.c);               // the factor takes what the rounding misses
-    return Slope{coef * ex2(__fmaf_rn(-base, a.c, shift)), a.c, shift};
+    const bool other = a.tlse != nullptr;
+    if (other ? rest.s == 0.0f : all.s == 0.0f) return slope_none(a.c);
+    if (!other) return slope_make(w / all.s, a.c, 1.0f, all.m, a.c);
+    const float pr = rest.s * ex2((rest.m - all.m) * a.c) / all.s;
+    return slope_make(w * (pr - te.qr) / rest.s, a.c, 1.0f, rest.m, a.c);
 }
 
 // One warp: the loss of a row from the statistics as they are returned (the
@@ -538,7 +584,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2) distill_stream_kernel(const
                     zt[k] = v;
                     ms_add(top, v, a.c);
                 };
-                Running run = running_empty(a.c);
+                Running run = running_empty();
                 if (edges) {
                     __syncwarp();
                     for (int l = lane; l < count; l += 32) {
@@ -550,9 +596,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2) distill_stream_kernel(const
                     __syncwarp();
                     MaxSum one = ms_empty();
                     ms_add(one, Elem<T>::to_f32(edge[lane]), a.c);
-                    run.m = run.seen = one.m;
-                    run.mc = __fmul_rn(one.m, a.c);
-                    run.s = one.s;
+                    run = running_from(one, a.c);
                 }
                 for (int i = 0; i < cur.mine; ++i) {
                     const uint32_t at = used % kRing;
@@ -603,7 +647,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2) distill_stream_kernel(const
                     const int j = warp + i * NW, n = min(kChunkVecs, cur.sp.nb - j * kChunkVecs);
                     const uint4 *q = reinterpret_cast<const uint4 *>(ring + at * kChunkVecs * 16);
                     T *out = grad + nhead + static_cast<int64_t>(j) * kChunkElems;
-                    if (n == kChunkVecs && wide) {
+                    if (n == kChunkVecs && wide && !slope.far) {
 #pragma unroll
                         for (int u = 0; u < kChunkVecs / 32; ++u) {
                             float f[VEC];
@@ -613,7 +657,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2) distill_stream_kernel(const
                     } else {
                         for (int v = lane; v < n; v += 32) {
                             float f[VEC];
-                            slope_vec<T>(slope, q[v], f);
+                            slope_any<T>(slope, q[v], f);
                             store_vec<T>(out + v * VEC, wide, f);
                         }
                     }
@@ -752,7 +796,7 @@ __global__ void __launch_bounds__(kRowThreads) distill_rows_kernel(const Args a)
         if (lane == 0) teacher = t;
     }
     MaxSum top = ms_empty();
-    Running run = running_empty(a.c);
+    Running run = running_empty();
     const uint32_t zt_rank0 = c > 1 ? tc::mapa(smem_u32(zt), 0) : 0u;
     auto take = [&](int k, T *p) {                          // take slot k's logit out of the row
         const float v = Elem<T>::to_f32(*p);
@@ -771,9 +815,7 @@ __global__ void __launch_bounds__(kRowThreads) distill_rows_kernel(const Args a)
         __syncwarp();
         MaxSum one = ms_empty();
         ms_add(one, Elem<T>::to_f32(edge[lane]), a.c);
-        run.m = run.seen = one.m;
-        run.mc = __fmul_rn(one.m, a.c);
-        run.s = one.s;
+        run = running_from(one, a.c);
     }
     for (int j = 0; j < pieces; ++j) {
         wait_landed(smem_u32(&bars[warp][j]), 0, &abort_flag, a);
@@ -814,7 +856,7 @@ __global__ void __launch_bounds__(kRowThreads) distill_rows_kernel(const Args a)
         const Slope slope = slope_from(a, te, w, rest, all);
         for (int v = w0 + lane; v < w1; v += 32) {
             float f[VEC];
-            slope_vec<T>(slope, reinterpret_cast<const uint4 *>(data)[v - v0], f);
+            slope_any<T>(slope, reinterpret_cast<const uint4 *>(data)[v - v0], f);
             store_vec<T>(grad + sp.head + v * VEC, wide, f);
         }
         if (edges) {
@@ -898,17 +940,16 @@ __global__ void __launch_bounds__(kBackThreads, 4) distill_backward_kernel(const
     __syncthreads();
     const Teacher te = teacher;
     const bool dead = !alive || lse == -INFINITY;
-    // exp(z / tau - base) as 2^(z c - base log2 e); the factor takes what the rounding misses
+    // exp(z / tau - base) as 2^(z c - base log2 e)
     const bool other = a.tlse != nullptr, none = dead || (other && r == -INFINITY);
-    const float base = none ? 0.0f : other ? r : lse, shift = __fmul_rn(base, kLog2e);
-    const float coef = none ? 0.0f : (other ? w * (expf(r - lse) - te.qr) : w) * ex2(__fmaf_rn(-base, kLog2e, shift));
-    const Slope slope{coef, a.c, shift};
+    const Slope slope = none ? slope_none(a.c)
+                             : slope_make(other ? w * (expf(r - lse) - te.qr) : w, a.c, a.inv_tau, other ? r : lse, kLog2e);
 #pragma unroll
     for (int i = 0; i < kBackLoads; ++i) {
         const int v = tid + kBackThreads * i;
         if (v >= n) continue;
         float f[VEC];
-        slope_vec<T>(slope, q[i], f);
+        slope_any<T>(slope, q[i], f);
         if (dead) {                                         // whatever the row holds
 #pragma unroll
             for (int e = 0; e < VEC; ++e) f[e] = 0.0f;
