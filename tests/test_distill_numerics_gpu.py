@@ -75,7 +75,7 @@ def definition(z, ids, top, tlse, tau, w):
     loss = term.sum(dim=1)
     far = torch.where(q > 0, lq - lp, 0.0).abs().nan_to_num(0.0, 0.0)
     lb = 2.0 ** -19 * (q * ((1 + far) * size_t + mag)).nan_to_num(0.0).sum(dim=1)
-    lpr = mr0 + sr0 - m0 - s0                        # log of what the student leaves
+    lpr = (mr0 - m0) + (sr0 - s0)                    # log of what the student leaves
     if tlse is not None:
         take = rest & (qr > 0)
         d = torch.where(take, qr.clamp(min=1e-300).log() - lpr, 0.0)
@@ -199,3 +199,27 @@ def test_nothing_outside_the_slots(T, V, tau):
             grad = check(only, ids, top, tlse, tau, w)[1]
             outside = torch.ones(T, V, dtype=torch.bool).scatter_(1, ids, False)
             assert not grad.cpu()[1:][outside[1:]].any()
+
+
+@pytest.mark.parametrize("tau", [1.0, 1.2, 2.5])
+@pytest.mark.parametrize("rest", [False, True])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("T,V", [(25, 3001), (175, 3001), (175, 61)])
+def test_gradients_of_rows_of_one_huge_value(T, V, dtype, rest, tau):
+    """The same of values whose log sum fp32 cannot tell from their largest: the step's gradient, which comes from the
+    sums, is the definition's, the backward's, from the statistics, is that of probabilities of at most one."""
+    z, ids, top, t, w = inputs(T, V, 9, dtype, seed=3)
+    for r, v in enumerate([-1e10, -1e15, -1e20, 1e10] * 3):
+        z[r] = v
+    z[3, 5] = -1e15                                  # and of one value beside another
+    z[9, : V // 2] = -3e15
+    z[11, V // 2:] = 2e10
+    tlse = torch.logsumexp(t / tau, 1) if rest else None
+    grad, es = (definition(z, ids, top, tlse, tau, w)[i] for i in (2, 4))
+    rel, sub = HALF[dtype]
+    args = [w.to(DEV), z.to(DEV), ids.to(DEV), top.to(DEV)]
+    tl = None if tlse is None else tlse.to(DEV)
+    stats = torch.empty(T, 2, device=DEV)
+    near(bt.bt_distill_topk_step(*args, tl, tau, stats=stats)[1], grad, es + rel * grad.abs() + sub, "step")
+    got = bt.bt_distill_topk_backward(*args, stats, tl, tau).cpu().double()
+    assert (got[:12].abs() <= (1 + rel) * w[:12, None].double().abs() / tau).all()

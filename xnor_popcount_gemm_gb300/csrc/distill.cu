@@ -322,7 +322,9 @@ __device__ __forceinline__ MaxSum running_warp(const Running &r, float c) { retu
 
 // The gradient outside the slots: coef * 2^(z c1 - shift), or, where the
 // rounding of shift would be an exponent of its own (`far`, as above), coef *
-// 2^((z k1 - base) k2), c1 = k1 k2.
+// 2^((z k1 - base) k2), c1 = k1 k2. base is a largest logit, or the log sum of
+// logits that it cannot tell from the largest: no such exponent is above 0 (in a
+// slot, which is written over, it may be).
 struct Slope {
     float coef, c1, shift;
     bool far;
@@ -333,6 +335,7 @@ __device__ __forceinline__ Slope slope_make(float coef, float c1, float k1, floa
     const bool far = is_far(shift);
     return Slope{far ? coef : coef * ex2(__fmaf_rn(-base, k2, shift)), c1, shift, far, k1, base, k2};
 }
+__device__ __forceinline__ float not_above_0(float x) { return x > 0.0f ? 0.0f : x; }   // a NaN stays one
 // Nothing: 0 wherever the logits are masked.
 __device__ __forceinline__ Slope slope_none(float c1) { return Slope{0.0f, c1, 0.0f, false, 0.0f, 0.0f, 0.0f}; }
 // (not far)
@@ -348,7 +351,7 @@ template <typename T> __device__ __forceinline__ void slope_vec(const Slope &g, 
     }
 }
 __device__ __forceinline__ float slope_of(const Slope &g, float v) {
-    return g.coef * ex2(g.far ? __fmaf_rn(v, g.k1, -g.base) * g.k2 : __fmaf_rn(v, g.c1, -g.shift));
+    return g.coef * ex2(g.far ? not_above_0(__fmul_rn(v, g.k1) - g.base) * g.k2 : __fmaf_rn(v, g.c1, -g.shift));
 }
 template <typename T> __device__ __forceinline__ void slope_any(const Slope &g, const uint4 &q, float *f) {
     if (g.far) {
@@ -375,8 +378,9 @@ __device__ __forceinline__ Slope slope_from(const Args &a, const Teacher &te, fl
 __device__ __forceinline__ void write_loss(const Args &a, int64_t row, const int *ids, const float *tt, const float *zt,
                                            const Teacher &te, const MaxSum &rest, const MaxSum &all, int lane) {
     const bool empty = all.s == 0.0f;                       // the student has nothing left
-    const float lse = empty ? -INFINITY : all.m * a.inv_tau + logf(all.s);
-    const float r = rest.s == 0.0f ? -INFINITY : rest.m * a.inv_tau + logf(rest.s);
+    // (rounded as the backward rounds z / tau: of a huge row lse is its largest)
+    const float lse = empty ? -INFINITY : __fadd_rn(__fmul_rn(all.m, a.inv_tau), logf(all.s));
+    const float r = rest.s == 0.0f ? -INFINITY : __fadd_rn(__fmul_rn(rest.m, a.inv_tau), logf(rest.s));
     float l = 0.0f;
     for (int k = lane; k < a.S; k += 32) {
         if (ids[k] < 0) continue;
@@ -967,7 +971,7 @@ __global__ void __launch_bounds__(kBackThreads, 4) distill_backward_kernel(const
     for (int k = tid; k < a.S; k += kBackThreads) {
         const int id = ids[k];
         if (!mine(id)) continue;
-        const float p = expf(__fmaf_rn(zt[k], a.inv_tau, -lse));
+        const float p = expf(slope.far ? not_above_0(__fmul_rn(zt[k], a.inv_tau) - lse) : __fmaf_rn(zt[k], a.inv_tau, -lse));
         grad[id] = from_f32<T>(w * (p - expf(log_q(a, te, tt[k]))));
     }
 }
