@@ -223,3 +223,30 @@ def test_gradients_of_rows_of_one_huge_value(T, V, dtype, rest, tau):
     near(bt.bt_distill_topk_step(*args, tl, tau, stats=stats)[1], grad, es + rel * grad.abs() + sub, "step")
     got = bt.bt_distill_topk_backward(*args, stats, tl, tau).cpu().double()
     assert (got[:12].abs() <= (1 + rel) * w[:12, None].double().abs() / tau).all()
+
+
+@pytest.mark.parametrize("tau", [1.0, 1.2, 2.5])
+@pytest.mark.parametrize("rest", [False, True])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("T,V", [(25, 3001), (175, 3001), (175, 61)])
+def test_rows_of_one_huge_value(T, V, dtype, rest, tau):
+    """The same of values whose logarithms do not show next to them: the loss comes from the sums."""
+    z, ids, top, t, w = inputs(T, V, 9, dtype, seed=3)
+    for r, v in enumerate([-1e10, -1e15, -1e20, 1e10] * 3):
+        z[r] = v
+    # and those with one value beside another
+    z[3, 5] = -1e15
+    z[9, : V // 2] = -3e15
+    z[11, V // 2:] = 2e10
+    check(z, ids, top, torch.logsumexp(t / tau, 1) if rest else None, tau, w)
+
+
+@pytest.mark.parametrize("rest", [False, True])
+@pytest.mark.parametrize("T,tau", [(20, 1.0), (20, 4.0), (180, 2.5)])
+def test_a_common_offset_does_not_show(T, tau, rest):
+    """What all logits of a row share changes its statistics, and its loss no more than by a rounding."""
+    z, ids, top, t, w = inputs(T, 4000, 24, torch.float32, seed=6)
+    z = (z * 1024).round() / 1024                    # the offsets below are exact
+    tlse = torch.logsumexp(t / tau, 1) if rest else None
+    for offset in (0.0, 24.0, 4096.0, -8192.0):
+        check(z + offset, ids, top, tlse, tau, w)

@@ -372,25 +372,31 @@ __device__ __forceinline__ Slope slope_from(const Args &a, const Teacher &te, fl
     return slope_make(w * (pr - te.qr) / rest.s, a.c, 1.0f, rest.m, a.c);
 }
 
-// One warp: the loss of a row from the statistics as they are returned (the
-// loss and its backward belong to the same lse and r), with the student's
-// logits of the slots in zt.
+// One warp: the loss of a row, with the student's logits of the slots in zt.
+// Where lse and r are below 16 it is taken from them as they are returned and as
+// the backward reads them: fp32 log probabilities, rounded by up to 5e-7. Larger
+// ones would be rounded by more (logits with a common offset of 4096: 2e-4,
+// beside losses of 1e-3), so that they are taken relative to the row's largest
+// logit then: the loss of a row does not depend on what all its logits share.
 __device__ __forceinline__ void write_loss(const Args &a, int64_t row, const int *ids, const float *tt, const float *zt,
                                            const Teacher &te, const MaxSum &rest, const MaxSum &all, int lane) {
     const bool empty = all.s == 0.0f;                       // the student has nothing left
     // (rounded as the backward rounds z / tau: of a huge row lse is its largest)
     const float lse = empty ? -INFINITY : __fadd_rn(__fmul_rn(all.m, a.inv_tau), logf(all.s));
     const float r = rest.s == 0.0f ? -INFINITY : __fadd_rn(__fmul_rn(rest.m, a.inv_tau), logf(rest.s));
+    const bool small = fmaxf(fabsf(lse), fabsf(r)) < 16.0f;
+    const float ref = small ? 0.0f : all.m, lse0 = small ? lse : logf(all.s);
     float l = 0.0f;
     for (int k = lane; k < a.S; k += 32) {
         if (ids[k] < 0) continue;
         const float q = expf(log_q(a, te, tt[k]));
-        if (!(q == 0.0f)) l += q * (logf(q) - (zt[k] * a.inv_tau - lse));
+        if (!(q == 0.0f)) l += q * (logf(q) - ((zt[k] - ref) * a.inv_tau - lse0));
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
     if (lane == 0) {
-        if (a.tlse != nullptr && rest.s != 0.0f && !(te.qr == 0.0f)) l += te.qr * (logf(te.qr) - (r - lse));
+        const float r0 = small ? r : (rest.m - ref) * a.inv_tau + logf(rest.s);
+        if (a.tlse != nullptr && rest.s != 0.0f && !(te.qr == 0.0f)) l += te.qr * (logf(te.qr) - (r0 - lse0));
         a.loss[row] = empty ? 0.0f : l;
         if (a.stats != nullptr) {
             a.stats[2 * row] = lse;
