@@ -250,3 +250,25 @@ def test_a_common_offset_does_not_show(T, tau, rest):
     tlse = torch.logsumexp(t / tau, 1) if rest else None
     for offset in (0.0, 24.0, 4096.0, -8192.0):
         check(z + offset, ids, top, tlse, tau, w)
+
+
+@pytest.mark.parametrize("rest", [False, True])
+@pytest.mark.parametrize("top_dtype", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("T", [12, 180])
+def test_teachers_at_their_types_lowest_value(T, top_dtype, rest):
+    """A slot is empty where its logit is -inf alone: lowest values among others have a probability of 0, lowest values
+    alone are all alike."""
+    V, S, tau = 2500, 40, 1.2
+    z, ids, top, t, w = inputs(T, V, S, torch.bfloat16, seed=7)
+    low = torch.finfo(top_dtype).min
+    tlse = torch.logsumexp(t / tau, 1) if rest else None
+    top = top.to(top_dtype)
+    top[0, 5:] = low
+    top[1, :-1] = low
+    top[2, ::2], top[2, 1::2] = -INF, low
+    if not rest:                                     # (a log sum of such a row is not an fp32 number)
+        top[3], top[T - 1] = low, low
+        top[4], ids[4, 7:] = low, -1
+        top[5, :3], top[5, 3:] = low, -INF
+    loss, grad = check(z, ids, top, tlse, tau, w)
+    assert loss.isfinite().all() and grad.isfinite().all()

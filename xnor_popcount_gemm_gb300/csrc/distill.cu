@@ -178,7 +178,7 @@ __device__ __forceinline__ float rest_of(float q) { return q < 1.0f ? 1.0f - q :
 __device__ __forceinline__ Teacher teacher_of(const Args &a, const int *ids, const float *t, int64_t row, int lane) {
     Teacher r;
     if (a.tlse == nullptr) {
-        MaxSum x = ms_empty();
+        MaxSum x{-INFINITY, 0.0f};                          // any finite logit counts, however low
         for (int k = lane; k < a.S; k += 32)
             if (ids[k] >= 0) ms_add(x, t[k], a.c);
         x = ms_warp(x, x.m, a.c);
