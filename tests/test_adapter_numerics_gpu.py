@@ -79,3 +79,47 @@ def test_ranks_that_cancel_show_no_rounding_of_du():
     got = bt.bt_adapter_linear_backward(x, g, u, a, b, torch.ones(L, device=DEV), plan)[0].cpu().double()
     want = (one.double() - two.double())[ids][:, None]
     assert ((got - want).abs() <= 12 * 2.0 ** -23 + 2.0 ** -8 * want.abs()).all(), (got - want).abs().max()
+
+
+def _signs(L, C, R, dtype):
+    """[L, C, R]: ranks of one sign for every c, which alternates."""
+    gen = torch.Generator().manual_seed(3)
+    return ((torch.rand(L, C, R, generator=gen) + 0.5) * (1 - 2 * (torch.arange(C) % 2))[:, None]).to(dtype)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("R", [1, 3, 8, 16, 24, 40, 100])
+@pytest.mark.parametrize("T", [4, 70])
+def test_an_infinity_goes_as_far_as_the_formula_says(T, R, dtype, path):
+    """An infinity in x makes u of its token infinite, and its results +inf or -inf with the sign of B's row; a rank that
+    is no 16, 32, 64 or 128 adds nothing of its padding."""
+    K, N = 72, 41
+    gen = torch.Generator().manual_seed(4)
+    x, a, b = torch.randn(T, K, generator=gen).to(dtype), torch.rand(1, R, K, generator=gen).to(dtype) + 0.5, _signs(1, N, R, dtype)
+    x[2, 9] = float("inf")
+    plan = bt.bt_adapter_plan([0] * T, 1, device=DEV)
+    u = torch.empty(T, R, device=DEV)
+    for out_dtype in (dtype, torch.float32):
+        out = bt.bt_adapter_linear(*(t.to(DEV) for t in (x, a, b)), torch.ones(1, device=DEV), plan, out_dtype=out_dtype, u=u).cpu()
+        want = (x.double() @ a[0].double().t()) @ b[0].double().t()
+        assert torch.equal(out[2].double(), want[2]) and want[2].isinf().all()
+        assert torch.cat([out[:2], out[3:]]).isfinite().all() and (u[2] == float("inf")).all()
+
+
+@pytest.mark.parametrize("R", [1, 3, 8, 16, 24, 40, 100])
+def test_an_infinity_in_the_backward(R):
+    """The same of g, dU, grad_x and grad_a."""
+    T, K, N = 70, 72, 41
+    gen = torch.Generator().manual_seed(5)
+    x, g = torch.randn(T, K, generator=gen).bfloat16(), torch.randn(T, N, generator=gen).bfloat16()
+    a, b = _signs(1, K, R, torch.bfloat16).transpose(1, 2).contiguous(), torch.rand(1, N, R, generator=gen).bfloat16() + 0.5
+    x[2][x[2] == 0] = 1.0
+    g[2, 7] = float("inf")
+    plan = bt.bt_adapter_plan([0] * T, 1, device=DEV)
+    u = torch.randn(T, R, generator=gen)
+    gx, ga, gb = bt.bt_adapter_linear_backward(*(t.to(DEV) for t in (x, g, u, a, b, torch.ones(1))), plan)
+    du = g.double() @ b[0].double()
+    assert torch.equal(gx[2].cpu().double(), (du @ a[0].double())[2]) and gx[2].isinf().all()
+    assert torch.cat([gx[:2], gx[3:]]).isfinite().all()
+    assert torch.equal(ga[0].cpu().double(), du.t() @ x.double())              # infinite all over, by x's sign
+    assert not gb[0, 7].isfinite().any() and torch.cat([gb[0, :7], gb[0, 8:]]).isfinite().all()

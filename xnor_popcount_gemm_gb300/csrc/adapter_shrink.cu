@@ -247,7 +247,10 @@ __global__ void __launch_bounds__(32 * kWarps, 2) shrink_kernel(const ShrinkArgs
                     v.x += p.x; v.y += p.y; v.z += p.z; v.w += p.w;
                 }
             }
-            const float f[4] = {v.x * mul, v.y * mul, v.z * mul, v.w * mul};
+            float f[4] = {v.x * mul, v.y * mul, v.z * mul, v.w * mul};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (r + e >= a.R) f[e] = 0.0f;              // an infinity among X makes NaN of it and the padding's zeros
             if (a.u != nullptr && ok) {
                 float *u = a.u + static_cast<int64_t>(rows[row]) * a.R + r;
 #pragma unroll

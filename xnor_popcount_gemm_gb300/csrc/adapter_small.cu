@@ -185,7 +185,7 @@ __global__ void __launch_bounds__(kThreads, RB * NB <= 4 ? 2 : 1) small_kernel(c
         const int tok = i / RP, r = i % RP;
         float v = 0.0f;
         for (int q = 0; q < c; ++q) v += slot[q][tok][r];
-        u[tok][r] = v;
+        u[tok][r] = r < a.R ? v : 0.0f;                     // an infinity among x makes NaN of it and the padding's zeros
         if (a.u != nullptr && rank == 0 && tok < tile.n && r < a.R)
             a.u[static_cast<int64_t>(a.plan.rows[tile.first + tok]) * a.R + r] = v;
     }
