@@ -123,3 +123,33 @@ def test_an_infinity_in_the_backward(R):
     assert torch.cat([gx[:2], gx[3:]]).isfinite().all()
     assert torch.equal(ga[0].cpu().double(), du.t() @ x.double())              # infinite all over, by x's sign
     assert not gb[0, 7].isfinite().any() and torch.cat([gb[0, :7], gb[0, 8:]]).isfinite().all()
+
+
+@pytest.mark.parametrize("K", [5, 8])
+def test_as_many_adapters_as_a_plan_takes(K, monkeypatch):
+    """65536 adapters of rank 1, most of them without a token, widths that are a multiple of 4 and one that is not."""
+    monkeypatch.setenv("BT_ADAPTER_PATH", "large")
+    L, T, N, R = 65536, 1400, 6, 1
+    gen = torch.Generator().manual_seed(6)
+    ids = torch.randint(0, L, (T,), generator=gen)
+    ids[:600], ids[600] = L - 1, 0                   # one whose tokens are split
+    x, a, b = (torch.randn(*s, generator=gen).bfloat16() for s in ((T, K), (L, R, K), (L, N, R)))
+    g = torch.randn(T, N, generator=gen).bfloat16()
+    d = [t.to(DEV) for t in (x, a, b, torch.ones(L))]
+    plan = bt.bt_adapter_plan(ids, L, device=DEV)
+    u = torch.empty(T, R, device=DEV)
+    out = bt.bt_adapter_linear(*d, plan, out_dtype=torch.float32, u=u).cpu().double()
+    xd, ad, bd, gd = x.double(), a.double()[ids], b.double()[ids], g.double()
+    ud = torch.einsum("tk,trk->tr", xd, ad)
+    size = torch.einsum("tk,trk->tr", xd.abs(), ad.abs())
+    assert ((out - torch.einsum("tr,tnr->tn", ud, bd)).abs() <= (K + 2) * 2.0 ** -22 * torch.einsum("tr,tnr->tn", size, bd.abs())).all()
+    nan = float("nan")
+    gx, ga, gb = bt.bt_adapter_linear_backward(d[0], g.to(DEV), u, *d[1:], plan, grad_a=torch.full(a.shape, nan, device=DEV),
+                                               grad_b=torch.full(b.shape, nan, device=DEV))
+    du, dsize = torch.einsum("tn,tnr->tr", gd, bd), torch.einsum("tn,tnr->tr", gd.abs(), bd.abs())
+    wx, sx = torch.einsum("tr,trk->tk", du, ad), torch.einsum("tr,trk->tk", dsize, ad.abs())
+    assert ((gx.cpu().double() - wx).abs() <= 2.0 ** -8 * wx.abs() + (N + 2) * 2.0 ** -22 * sx).all()
+    for got, left, mag, right in ((ga, du, dsize, xd), (gb.transpose(1, 2), ud, size, gd)):
+        want, bound = (torch.zeros(L, R, right.shape[1]).double().index_add_(0, ids, l[:, :, None] * r[:, None])
+                       for l, r in ((left, right), (mag, right.abs())))
+        assert ((got.cpu().double() - want).abs() <= 600 * 2.0 ** -22 * bound).all()

@@ -274,19 +274,20 @@ __global__ void __launch_bounds__(kThreads) align_kernel(const AlignArgs a) {
     pdl_wait();
     pdl_launch_dependents();
     const int chunks = (a.C + 7) / 8;
-    int64_t first = 0, rows = a.rows;
-    if (a.parts != nullptr) {
-        const AdapterTile part = a.parts[blockIdx.y];
-        if (part.n == 0 || (blockIdx.y > 0 && a.parts[blockIdx.y - 1].adapter == part.adapter)) return;
-        first = static_cast<int64_t>(part.adapter) * a.R;
-        rows = a.R;
-    }
-    const int64_t total = rows * chunks, step = static_cast<int64_t>(gridDim.x) * kThreads;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kThreads;
+    auto copy = [&](int64_t first, int64_t rows) {
 #pragma unroll 4
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < total; i += step) {
-        const int64_t row = first + i / chunks;
-        const int j = static_cast<int>(i % chunks) * 8;
-        *reinterpret_cast<uint4 *>(a.dst + row * a.ldd + j) = load8(a.src + row * a.lds + j, a.C - j);
+        for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < rows * chunks; i += step) {
+            const int64_t row = first + i / chunks;
+            const int j = static_cast<int>(i % chunks) * 8;
+            *reinterpret_cast<uint4 *>(a.dst + row * a.ldd + j) = load8(a.src + row * a.lds + j, a.C - j);
+        }
+    };
+    if (a.parts == nullptr) return copy(0, a.rows);
+    for (int i = blockIdx.y; i < a.nparts; i += gridDim.y) {
+        const AdapterTile part = a.parts[i];
+        if (part.n == 0) return;                            // adapters without tokens come last
+        if (i == 0 || a.parts[i - 1].adapter != part.adapter) copy(static_cast<int64_t>(part.adapter) * a.R, a.R);
     }
 }
 
@@ -330,8 +331,8 @@ cudaError_t launch_align(const AlignArgs &a, cudaStream_t s) {
     const int64_t total = (a.parts != nullptr ? a.R : a.rows) * ((a.C + 7) / 8);
     if (total == 0) return cudaSuccess;
     const int64_t blocks = (total + 4 * kThreads - 1) / (4 * kThreads), most = 8 * device_sm_count();
-    return launch_pdl(align_kernel, dim3(static_cast<unsigned>(blocks < most ? blocks : most), static_cast<unsigned>(a.parts != nullptr ? a.nparts : 1)),
-                      dim3(kThreads), s, a);
+    const int parts = a.parts == nullptr ? 1 : a.nparts < 1024 ? a.nparts : 1024;
+    return launch_pdl(align_kernel, dim3(static_cast<unsigned>(blocks < most ? blocks : most), static_cast<unsigned>(parts)), dim3(kThreads), s, a);
 }
 
 cudaError_t launch_shrink(bt_dtype t, bool wt, const ShrinkArgs &a, int tiles, cudaStream_t s) {
