@@ -1,7 +1,6 @@
 // Declarations and device helpers shared by the adapters' kernels (see adapter.cu).
 #pragma once
 
-#include <mutex>
 #include <type_traits>
 
 #include "adapter_plan.h"
@@ -303,12 +302,6 @@ struct SmallArgs {
 // CTAs a tile (1, 2, 4, 8) and what the launch takes then, in microseconds; most: tokens of the fullest tile
 int small_cluster(int64_t tiles, int most, int64_t K, int64_t N, int64_t R, double *us);
 cudaError_t launch_small(bt_dtype t, bool out_f32, const SmallArgs &a, int tiles, int most, cudaStream_t s);
-
-template <typename K> cudaError_t allow_smem(K kern, int bytes, std::once_flag &once, cudaError_t &err) {
-    std::call_once(once, [&] { err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes); });
-    return err;
-}
-
 
 // `grid` CTAs in clusters of c, programmatic dependent launch allowed.
 template <typename K, typename Args>

@@ -339,9 +339,8 @@ template <typename T, int RP, bool WT, bool OF32, bool FAST, bool BF32>
 cudaError_t launch_rp(const ExpandArgs &a, cudaStream_t s) {
     auto kern = expand_kernel<T, RP, WT, OF32, FAST, BF32>;
     constexpr int smem = kSmem<RP, WT, FAST, kValues<T>>;
-    static std::once_flag once;
-    static cudaError_t err = cudaSuccess;
-    if (allow_smem(kern, smem, once, err) != cudaSuccess) return err;
+    static ContextOnce once;
+    if (const cudaError_t err = allow_smem(kern, smem, once); err != cudaSuccess) return err;
     const int64_t pieces = pass_pieces(a.pass);
     const int pass = static_cast<int>(pieces < 2 * device_sm_count() ? pieces : 2 * device_sm_count());
     return launch_pdl_smem(kern, dim3(static_cast<unsigned>(a.tiles * a.splits + pass)), dim3(kThreads), smem, s, a);

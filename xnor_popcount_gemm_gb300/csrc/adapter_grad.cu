@@ -293,9 +293,8 @@ __global__ void __launch_bounds__(32 * kWarps, RP <= 32 ? 3 : RP <= 64 ? 2 : 1) 
 
 template <int RP, int MODE> cudaError_t launch_m(const GradArgs &a, int parts, cudaStream_t s) {
     auto kern = grad_kernel<RP, MODE>;
-    static std::once_flag once;
-    static cudaError_t err = cudaSuccess;
-    if (allow_smem(kern, kSmem<RP>, once, err) != cudaSuccess) return err;
+    static ContextOnce once;
+    if (const cudaError_t err = allow_smem(kern, kSmem<RP>, once); err != cudaSuccess) return err;
     return launch_pdl_smem(kern, dim3(static_cast<unsigned>(parts * (a.p[0].slices + a.p[1].slices))), dim3(32 * kWarps),
                            kSmem<RP>, s, a);
 }

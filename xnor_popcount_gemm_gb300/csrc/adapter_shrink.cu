@@ -293,9 +293,8 @@ __global__ void __launch_bounds__(kThreads) align_kernel(const AlignArgs a) {
 
 template <typename T, int RP, bool WT, int MODE> cudaError_t launch_m(ShrinkArgs a, int tiles, cudaStream_t s) {
     auto kern = shrink_kernel<T, RP, WT, MODE>;
-    static std::once_flag once;
-    static cudaError_t err = cudaSuccess;
-    if (allow_smem(kern, kSmem<RP, WT>, once, err) != cudaSuccess) return err;
+    static ContextOnce once;
+    if (const cudaError_t err = allow_smem(kern, kSmem<RP, WT>, once); err != cudaSuccess) return err;
     // CTAs a tile, as many as end soonest: in waves of two CTAs an SM, each of its steps and of what it
     // costs to begin, join and end, about six steps' time. (Half precision joins rows by whole warps:
     // powers of two.)

@@ -300,9 +300,8 @@ template <typename T, int RB, int NB, bool FAST>
 cudaError_t launch_f(SmallArgs a, bool out_f32, int tiles, cudaStream_t s) {
     auto kern = small_kernel<T, RB, NB, FAST>;
     constexpr int smem = 8 * 8 * NB * (32 * RB + 4) * static_cast<int>(sizeof(float));
-    static std::once_flag once;
-    static cudaError_t err = cudaSuccess;
-    if (allow_smem(kern, smem, once, err) != cudaSuccess) return err;
+    static ContextOnce once;
+    if (const cudaError_t err = allow_smem(kern, smem, once); err != cudaSuccess) return err;
     double us;
     const int c = small_cluster(tiles, 8 * NB, a.K, a.N, a.R, &us);
     a.cluster = c;

@@ -9,6 +9,7 @@
 #include <cudaTypedefs.h>
 
 #include "bt.h"
+#include "context_once.h"
 
 namespace bt {
 
@@ -303,6 +304,12 @@ cudaError_t launch_pack_rows_sum(const void *x, bt_dtype xt, int64_t R, int64_t 
                                  int64_t bias_len, bt_code code, void *out, double *abs_sum, cudaStream_t s);
 cudaError_t launch_pack_nhwc_sum(const void *x, bt_dtype xt, int64_t B, int64_t C, int64_t HW, const float *bias,
                                  int64_t bias_len, bt_code code, void *out, double *abs_sum, cudaStream_t s);
+
+// Opts `kern` into `bytes` of dynamic shared memory in the current context; `once` belongs to this kernel alone.
+template <typename K> cudaError_t allow_smem(K kern, int bytes, ContextOnce &once) {
+    return static_cast<cudaError_t>(
+        once.run(current_context_id, [&] { return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes); }));
+}
 
 // Launch attribute list allowing programmatic dependent launch (the kernel
 // overlaps its prologue with the previous kernel in the stream).

@@ -647,10 +647,8 @@ bool encode(const DgArgs &a, int64_t O, int k, const uint16_t *g, const uint16_t
 
 cudaError_t launch_kernel(const CUtensorMap &mg, const CUtensorMap &mw, const DgArgs &a, int smem, cudaStream_t s) {
     auto kern = dgrad_kernel;
-    static std::once_flag once;
-    static cudaError_t attr_err = cudaSuccess;
-    std::call_once(once, [&] { attr_err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax); });
-    if (attr_err != cudaSuccess) return attr_err;
+    static ContextOnce once;
+    if (const cudaError_t err = allow_smem(kern, kSmemMax, once); err != cudaSuccess) return err;
     int grid = device_sm_count();
     if (grid > a.units) grid = a.units;
     if (grid < 1) grid = 1;

@@ -24,7 +24,6 @@
 // to themselves), 8 x 32000 bf16 4.8 us; the backward, 2048 x 32000 bf16, 43.7
 // us, 5.4 TB/s, 300 x 50001 f16 11.1 us.
 #include <cmath>
-#include <mutex>
 #include <type_traits>
 
 #include "bt_device.cuh"
@@ -985,17 +984,11 @@ __global__ void __launch_bounds__(kBackThreads, 4) distill_backward_kernel(const
 int elem_bytes(bt_dtype t) { return t == BT_F32 ? 4 : 2; }
 bool float_type(int t) { return t == BT_F32 || t == BT_BF16 || t == BT_F16; }
 
-template <typename K> cudaError_t allow_smem(K kern, int bytes, std::once_flag &once, cudaError_t &err) {
-    std::call_once(once, [&] { err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes); });
-    return err;
-}
-
 template <typename T, bool STEP> cudaError_t launch_stream(const Args &a, cudaStream_t s) {
     auto kern = distill_stream_kernel<T, STEP>;
     const auto smem = [](int S) { return kStreamWarps * kRing * kChunkVecs * 16 + S * (9 * 4 + 2 * kStreamWarps); };
-    static std::once_flag once;
-    static cudaError_t err = cudaSuccess;
-    if (allow_smem(kern, smem(kMaxSlots), once, err) != cudaSuccess) return err;
+    static ContextOnce once;
+    if (const cudaError_t err = allow_smem(kern, smem(kMaxSlots), once); err != cudaSuccess) return err;
     const int64_t slots = 2 * device_sm_count();
     return launch_pdl_smem(kern, dim3(static_cast<unsigned>(a.rows < slots ? a.rows : slots)), dim3(kStreamThreads),
                            static_cast<size_t>(smem(a.S)), s, a);
@@ -1018,9 +1011,8 @@ int rows_cluster(int64_t rows, int64_t row_bytes, int sms) {
 
 template <typename T, bool STEP> cudaError_t launch_rows(Args a, cudaStream_t s) {
     auto kern = distill_rows_kernel<T, STEP>;
-    static std::once_flag once;
-    static cudaError_t err = cudaSuccess;
-    if (allow_smem(kern, kSliceMax + 16 + 12 * kMaxSlots, once, err) != cudaSuccess) return err;
+    static ContextOnce once;
+    if (const cudaError_t err = allow_smem(kern, kSliceMax + 16 + 12 * kMaxSlots, once); err != cudaSuccess) return err;
     a.shift = 0;
     while ((1 << a.shift) < a.cluster) ++a.shift;
     const int64_t bytes = a.V * static_cast<int64_t>(sizeof(T));

@@ -1094,12 +1094,8 @@ cudaError_t rows_t(const T *x, int64_t R, int64_t K, const float *bias, int64_t 
     unsigned int *err = device_error_word();
     if (vec && err != nullptr) {
         auto kern = pack_rows_staged_kernel<T, CODE>;
-        static std::once_flag once;
-        static cudaError_t attr = cudaSuccess;
-        std::call_once(once, [&] {
-            attr = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kStagedSmem);
-        });
-        if (attr != cudaSuccess) return attr;
+        static ContextOnce once;
+        if (const cudaError_t attr = allow_smem(kern, kStagedSmem, once); attr != cudaSuccess) return attr;
         const int seg = kSegBytes / static_cast<int>(sizeof(T));
         const int64_t upr = (K + seg - 1) / seg;
         const int sms = device_sm_count();
@@ -1371,10 +1367,8 @@ cudaError_t im2col_t(const T *x, const ConvGeom &g, const float *bias, int64_t b
     unsigned int *err = device_error_word();
     if (err == nullptr) return cudaErrorUnknown;
     auto kern = pack_im2col_kernel<T, CODE>;
-    static std::once_flag once;
-    static cudaError_t attr = cudaSuccess;
-    std::call_once(once, [&] { attr = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kUnfoldMaxSmem); });
-    if (attr != cudaSuccess) return attr;
+    static ContextOnce once;
+    if (const cudaError_t attr = allow_smem(kern, kUnfoldMaxSmem, once); attr != cudaSuccess) return attr;
     const int smem = unfold_smem(u);
     int per_sm = (227 * 1024) / (smem + 1024);
     if (per_sm < 1) per_sm = 1;

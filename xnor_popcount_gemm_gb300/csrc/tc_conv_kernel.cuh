@@ -1017,10 +1017,8 @@ struct ConvPlan {
 template <int CODE, int OUT, int SW, bool PAIRS, typename XT, bool CP>
 cudaError_t launch_cp(const CUtensorMap &ma, const CUtensorMap &mb, const ConvPlan &p, cudaStream_t s) {
     auto kern = conv_kernel<CODE, OUT, SW, PAIRS, XT, CP>;
-    static std::once_flag once;
-    static cudaError_t attr_err = cudaSuccess;
-    std::call_once(once, [&] { attr_err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax); });
-    if (attr_err != cudaSuccess) return attr_err;
+    static ContextOnce once;
+    if (const cudaError_t err = allow_smem(kern, kSmemMax, once); err != cudaSuccess) return err;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
     attr[0] = pdl_attribute();

@@ -823,10 +823,8 @@ cudaError_t launch_t(const Maps &mp, TcArgs a, cudaStream_t s) {
     a.wait_ns = wait_limit_ns();
     const int smem = smem_bytes(a.bn, PAIR, a.d, static_cast<int>(sizeof(typename OutT<OUT>::type)), a.epi_warps);
     if (a.stages < 2 || smem > kSmemMax) return cudaErrorInvalidValue;
-    static std::once_flag once;
-    static cudaError_t attr_err = cudaSuccess;
-    std::call_once(once, [&] { attr_err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax); });
-    if (attr_err != cudaSuccess) return attr_err;
+    static ContextOnce once;
+    if (const cudaError_t err = allow_smem(kern, kSmemMax, once); err != cudaSuccess) return err;
     const int csize = PAIR ? 2 : 1;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
