@@ -10,6 +10,7 @@ there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -544,10 +545,44 @@ def bt_scale_init(x: torch.Tensor, factor: float = 2.0, scale_dtype=None, out: t
 _ID_BYTES = {torch.int32: 4, torch.int64: 8}
 
 
-def _on_gpu(**tensors) -> None:
-    for name, t in tensors.items():
-        if t is not None and not t.is_cuda:
-            raise ValueError(f"{name} must be a CUDA tensor")
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
+def _on_device_of(name: str, at: int):
+    """Runs the call with the device of its operand `name` (the at-th argument) current: launches, workspace sizes and
+    kernel attributes belong to the current device."""
+    def wrap(fn):
+        @functools.wraps(fn)
+        def call(*args, **kw):
+            t = args[at] if at < len(args) else kw.get(name)
+            if type(t) is AdapterPlan:
+                t = t.buffer
+            device = t.get_device() if isinstance(t, torch.Tensor) else -1
+            if device < 0 or device == _current_device():
+                return fn(*args, **kw)
+            with torch.cuda.device(device):
+                return fn(*args, **kw)
+        return call
+    return wrap
+
+
+def _same_device(first, stream, *tensors) -> None:
+    at = first.get_device()
+    for t in tensors:
+        if t is not None and t.get_device() != at:
+            raise ValueError(f"operands must be on one device, {first.device} by the first: one is on {t.device}")
+    if stream is not None and stream.device != first.device:
+        raise ValueError(f"stream must be one of {first.device}, where the first operand is")
+
+
+def _scratch(workspace, need: int, device, stream):
+    """A workspace of need bytes: the one given, where it holds them."""
+    if workspace is not None:
+        if not workspace.is_cuda or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous CUDA tensor")
+        if workspace.numel() * workspace.element_size() >= need:
+            return workspace
+    return _empty((need,), torch.uint8, device, stream) if need else None
 
 
 def _on_stream(stream, device) -> int:
@@ -569,8 +604,9 @@ def _dense(t, name: str, shape: tuple, dtype) -> None:
     _contig(t, name)
 
 
-def _distill_args(logits, ids, top, teacher_lse):
-    _on_gpu(logits=logits, ids=ids, top=top, teacher_lse=teacher_lse)
+def _distill_args(logits, ids, top, teacher_lse, stream, *others):
+    if not logits.is_cuda:
+        raise ValueError("logits must be a CUDA tensor")
     if logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
         raise ValueError("logits must be [T, V] with elements of a row next to each other")
     T, V = logits.shape
@@ -582,6 +618,7 @@ def _distill_args(logits, ids, top, teacher_lse):
     _contig(top, "top")
     if teacher_lse is not None:
         _dense(teacher_lse, "teacher_lse", (T,), torch.float32)
+    _same_device(logits, stream, ids, top, teacher_lse, *others)
     return T, V, (logits.stride(0) if T > 1 else max(V, logits.stride(0)))
 
 
@@ -593,6 +630,7 @@ def _distill_grad(logits, grad, T, V, stream):
     return grad, (grad.stride(0) if T > 1 else max(V, grad.stride(0)))
 
 
+@_on_device_of("logits", 0)
 def bt_distill_topk(logits: torch.Tensor, ids: torch.Tensor, top: torch.Tensor, teacher_lse: torch.Tensor | None = None,
                     temperature: float = 1.0, loss: torch.Tensor | None = None, stats: torch.Tensor | None = None,
                     stream=None) -> tuple[torch.Tensor, torch.Tensor]:
@@ -602,7 +640,7 @@ def bt_distill_topk(logits: torch.Tensor, ids: torch.Tensor, top: torch.Tensor, 
     teacher's log-sum-exp of its logits / temperature, counts the teacher's
     remaining probability as one more outcome; without it the teacher is
     normalized over its slots."""
-    T, V, ld = _distill_args(logits, ids, top, teacher_lse)
+    T, V, ld = _distill_args(logits, ids, top, teacher_lse, stream, loss, stats)
     if loss is None:
         loss = _empty((T,), torch.float32, logits.device, stream)
     else:
@@ -617,12 +655,13 @@ def bt_distill_topk(logits: torch.Tensor, ids: torch.Tensor, top: torch.Tensor, 
     return loss, stats
 
 
+@_on_device_of("logits", 1)
 def bt_distill_topk_backward(grad_loss: torch.Tensor, logits: torch.Tensor, ids: torch.Tensor, top: torch.Tensor,
                              stats: torch.Tensor, teacher_lse: torch.Tensor | None = None, temperature: float = 1.0,
                              grad: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Gradient [T, V] (the logits' dtype) of bt_distill_topk's loss for
     grad_loss [T] and the forward's stats. grad may be the logits."""
-    T, V, ld = _distill_args(logits, ids, top, teacher_lse)
+    T, V, ld = _distill_args(logits, ids, top, teacher_lse, stream, grad_loss, stats, grad)
     _dense(grad_loss, "grad_loss", (T,), torch.float32)
     _dense(stats, "stats", (T, 2), torch.float32)
     grad, ldg = _distill_grad(logits, grad, T, V, stream)
@@ -632,13 +671,14 @@ def bt_distill_topk_backward(grad_loss: torch.Tensor, logits: torch.Tensor, ids:
     return grad
 
 
+@_on_device_of("logits", 1)
 def bt_distill_topk_step(grad_loss: torch.Tensor, logits: torch.Tensor, ids: torch.Tensor, top: torch.Tensor,
                          teacher_lse: torch.Tensor | None = None, temperature: float = 1.0,
                          loss: torch.Tensor | None = None, grad: torch.Tensor | None = None,
                          stats: torch.Tensor | None = None, stream=None) -> tuple[torch.Tensor, torch.Tensor]:
     """Loss [T] and gradient [T, V] in one read of the logits, for an upstream
     gradient grad_loss [T] known beforehand. grad may be the logits."""
-    T, V, ld = _distill_args(logits, ids, top, teacher_lse)
+    T, V, ld = _distill_args(logits, ids, top, teacher_lse, stream, grad_loss, loss, grad, stats)
     _dense(grad_loss, "grad_loss", (T,), torch.float32)
     if loss is None:
         loss = _empty((T,), torch.float32, logits.device, stream)
@@ -684,6 +724,8 @@ def bt_adapter_plan(adapter_ids, num_adapters: int, device="cuda", stream=None) 
         ids = ids.to(torch.int32)
     ids = ids.contiguous()
     T = ids.numel()
+    if stream is not None and torch.device(device) not in (torch.device("cuda"), stream.device):
+        raise ValueError(f"stream must be one of {device}")
     host = torch.empty(max(bt_adapter_plan_bytes(T, num_adapters) // 4, 1), dtype=torch.int32,
                        pin_memory=torch.device(device).type == "cuda")
     info = AdapterPlanInfo()
@@ -708,7 +750,7 @@ def _rows(t: torch.Tensor, name: str, T: int, C: int, dtypes) -> int:
     return ld if T > 1 else max(C, ld)
 
 
-def _adapter_args(x, a, b, scale, plan):
+def _adapter_args(x, a, b, scale, plan, stream, *others):
     if x.dim() != 2 or a.dim() != 3 or b.dim() != 3:
         raise ValueError("x must be [T, K], a [L, R, K] and b [L, N, R]")
     T, K = x.shape
@@ -726,13 +768,16 @@ def _adapter_args(x, a, b, scale, plan):
     _dense(scale, "scale", (L,), torch.float32)
     if type(plan) is not AdapterPlan or plan.tokens != T or plan.adapters != L or not plan.buffer.is_cuda:
         raise ValueError("plan must be bt_adapter_plan of these tokens and adapters, on the device")
+    _same_device(x, stream, a, b, scale, plan.buffer, *others)
     return T, K, N, R
 
 
+@_on_device_of("plan", 4)
 def bt_adapter_linear_workspace(T: int, K: int, N: int, R: int, plan: AdapterPlan) -> int:
     return int(_c_alin_ws(T, K, N, R, plan._ref))
 
 
+@_on_device_of("x", 0)
 def bt_adapter_linear(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, scale: torch.Tensor, plan: AdapterPlan,
                       base: torch.Tensor | None = None, out_dtype=None, u: torch.Tensor | None = None,
                       out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
@@ -741,7 +786,7 @@ def bt_adapter_linear(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, scale: 
     token of x [T, K] (bf16 or f16), a [L, R, K], b [L, N, R]: out [T, N] in
     out_dtype (base's type, else x's). out may be base. u [T, R] (float), if
     given, receives a[i] x_t for the backward."""
-    T, K, N, R = _adapter_args(x, a, b, scale, plan)
+    T, K, N, R = _adapter_args(x, a, b, scale, plan, stream, base, u, out, workspace)
     dt = x.dtype
     ldx = _rows(x, "x", T, K, (dt,))
     if base is None:
@@ -755,8 +800,7 @@ def bt_adapter_linear(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, scale: 
     if u is not None:
         _dense(u, "u", (T, R), torch.float32)
     need = _c_alin_ws(T, K, N, R, plan._ref)
-    if need and (workspace is None or workspace.numel() < need):
-        workspace = _empty((need,), torch.uint8, x.device, stream)
+    workspace = _scratch(workspace, need, x.device, stream)
     _check(_c_alin(x.data_ptr(), _DT[dt], ldx, a.data_ptr(), b.data_ptr(), scale.data_ptr(), plan.buffer.data_ptr(),
                    plan._ref, T, K, N, R, pbase, base_type, ldb, out.data_ptr(), _DT[out.dtype], ldo,
                    None if u is None else u.data_ptr(), None if workspace is None else workspace.data_ptr(), need,
@@ -764,10 +808,12 @@ def bt_adapter_linear(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, scale: 
     return out
 
 
+@_on_device_of("plan", 4)
 def bt_adapter_linear_backward_workspace(T: int, K: int, N: int, R: int, plan: AdapterPlan) -> int:
     return int(_c_abwd_ws(T, K, N, R, plan._ref))
 
 
+@_on_device_of("x", 0)
 def bt_adapter_linear_backward(x: torch.Tensor, g: torch.Tensor, u: torch.Tensor, a: torch.Tensor, b: torch.Tensor,
                                scale: torch.Tensor, plan: AdapterPlan, grad_base: torch.Tensor | None = None,
                                grad_x: torch.Tensor | None = None, grad_a: torch.Tensor | None = None,
@@ -776,7 +822,7 @@ def bt_adapter_linear_backward(x: torch.Tensor, g: torch.Tensor, u: torch.Tensor
     result), its input x and its u: (grad_x [T, K] bf16, grad_a [L, R, K],
     grad_b [L, N, R], both float). grad_base [T, K], the projection's own
     input gradient, is added to grad_x, which may be grad_base itself."""
-    T, K, N, R = _adapter_args(x, a, b, scale, plan)
+    T, K, N, R = _adapter_args(x, a, b, scale, plan, stream, g, u, grad_base, grad_x, grad_a, grad_b, workspace)
     ldx, ldg = _rows(x, "x", T, K, _BF16), _rows(g, "g", T, N, _BF16)
     _dense(u, "u", (T, R), torch.float32)
     ldgb = 0 if grad_base is None else _rows(grad_base, "grad_base", T, K, _BF16)
@@ -791,9 +837,8 @@ def bt_adapter_linear_backward(x: torch.Tensor, g: torch.Tensor, u: torch.Tensor
         grad_b = _empty(b.shape, torch.float32, x.device, stream)
     else:
         _dense(grad_b, "grad_b", tuple(b.shape), torch.float32)
-    need = bt_adapter_linear_backward_workspace(T, K, N, R, plan)
-    if need and (workspace is None or workspace.numel() < need):
-        workspace = _empty((need,), torch.uint8, x.device, stream)
+    need = _c_abwd_ws(T, K, N, R, plan._ref)
+    workspace = _scratch(workspace, need, x.device, stream)
     _check(_c_abwd(_ptr(x), ldx, _ptr(g), ldg, _ptr(u), _ptr(a), _ptr(b), _ptr(scale), _ptr(plan.buffer), plan._ref, T,
                    K, N, R, _ptr(grad_base), ldgb, _ptr(grad_x), ldgx, _ptr(grad_a), _ptr(grad_b), _ptr(workspace), need,
                    _on_stream(stream, x.device)))
