@@ -153,3 +153,36 @@ def test_as_many_adapters_as_a_plan_takes(K, monkeypatch):
         want, bound = (torch.zeros(L, R, right.shape[1]).double().index_add_(0, ids, l[:, :, None] * r[:, None])
                        for l, r in ((left, right), (mag, right.abs())))
         assert ((got.cpu().double() - want).abs() <= 600 * 2.0 ** -22 * bound).all()
+
+
+def test_a_wait_that_runs_out_is_reported(monkeypatch):
+    """With a limit of 1 ns the first wait for a copy or a product in flight gives up: TIMEOUT, once; what is in flight
+    still lands, and the next call is as always. (It may have landed by the first look: several calls, the first that did
+    not will do.)"""
+    monkeypatch.setenv("BT_ADAPTER_PATH", "large")
+    T, K, N, R, L = 600, 2048, 1024, 32, 3
+    gen = torch.Generator().manual_seed(7)
+    x, g = (torch.randn(T, c, generator=gen).bfloat16().to(DEV) for c in (K, N))
+    a, b = (torch.randn(*s, generator=gen).bfloat16().to(DEV) for s in ((L, R, K), (L, N, R)))
+    scale, plan, u = torch.ones(L, device=DEV), bt.bt_adapter_plan(torch.arange(T) % L, L, device=DEV), torch.empty(T, R, device=DEV)
+
+    def forward():
+        return [bt.bt_adapter_linear(x, a, b, scale, plan, u=u)]
+
+    def backward():
+        return list(bt.bt_adapter_linear_backward(x, g, u, a, b, scale, plan))
+
+    for call in (forward, backward):
+        want = call()
+        assert bt.bt_device_status() == 0
+        seen = []
+        bt.bt_set_wait_timeout(1)
+        try:
+            while bt.BT_ERR_TIMEOUT not in seen and len(seen) < 200:
+                call()
+                seen.append(bt.bt_device_status())
+        finally:
+            bt.bt_set_wait_timeout(0)
+        assert set(seen) <= {0, bt.BT_ERR_TIMEOUT} and seen[-1] == bt.BT_ERR_TIMEOUT
+        assert bt.bt_device_status() == 0
+        assert all(torch.equal(p, q) for p, q in zip(call(), want))
