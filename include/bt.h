@@ -818,11 +818,22 @@ bt_status bt_distill_topk(const void *logits, bt_dtype dtype, int64_t T, int64_t
                           float temperature, float *loss, float *stats, bt_stream stream);
 
 /*
- * bt_distill_topk_backward -- grad[t, v] = grad_loss[t] * d loss[t] / d z[t, v]:
+ * bt_distill_topk_backward -- grad[t, v] = grad_loss[t] times
  *   (1 / temperature) (exp(a_v - lse) - q_v)                 v in a slot
  *   (1 / temperature) exp(a_v - lse)                         else, teacher_lse NULL
  *   (1 / temperature) (exp(r - lse) - q_r) exp(a_v - r)      else, teacher_lse given
- * for the arguments of the forward and its stats; grad_loss device [T]. grad
+ * This is d loss[t] / d z[t, v] where the teacher's probabilities sum to one,
+ * sum q + q_r = 1, as they do by themselves without teacher_lse, and with it
+ * wherever sum q <= 1. Two cases are left, and there it is p - q as well, not the
+ * derivative Q p - q of a loss whose q sum to another Q:
+ *   sum q > 1 (q_r is 0 then): top kept in fewer bits than teacher_lse was
+ *     worked out with; top in BF16 reaches Q = 1.1 where the teacher is sure. A
+ *     teacher_lse raised to the log sum of exp(top / temperature) over the row's
+ *     slots, where that is larger, makes them sum to one again.
+ *   a student with nothing outside the slots: the loss leaves q_r's term, which
+ *     is infinite, out; the gradient is the limit of the whole loss's as what
+ *     the student leaves tends to 0.
+ * For the arguments of the forward and its stats; grad_loss device [T]. grad
  * [T, V] in the logits' dtype, rows ldg >= V elements apart, each value rounded
  * once; it may be the logits themselves (ldg = ld). Rows without a slot and
  * rows with nothing left get zeros.

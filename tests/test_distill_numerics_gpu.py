@@ -272,3 +272,39 @@ def test_teachers_at_their_types_lowest_value(T, top_dtype, rest):
         top[5, :3], top[5, 3:] = low, -INF
     loss, grad = check(z, ids, top, tlse, tau, w)
     assert loss.isfinite().all() and grad.isfinite().all()
+
+
+def _derivative(z, ids, top, tlse, tau, w):
+    """The loss's derivative by autograd, in 64 bits."""
+    z = z.double().requires_grad_()
+    lp = torch.log_softmax(z / tau, 1)
+    q = (top.double() / tau - tlse.double()[:, None]).exp()
+    qr = (1 - q.sum(1)).clamp(min=0)
+    inside = torch.zeros(z.shape, dtype=torch.bool).scatter_(1, ids, True)
+    lpr = torch.logsumexp(lp.masked_fill(inside, -INF), 1)
+    loss = (q * (q.log() - lp.gather(1, ids))).sum(1) + torch.where(qr > 0, qr * (qr.clamp(min=1e-300).log() - lpr), 0.0)
+    (loss * w.double()).sum().backward()
+    return z.grad, q.sum(1)
+
+
+@pytest.mark.parametrize("top_dtype", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("T", [30, 170])
+def test_a_teacher_in_few_bits(T, top_dtype):
+    """16-bit logits under a log sum of all of their bits: the gradient is p - q whatever the q sum to, as stated, and the
+    loss's derivative where they sum to one or less, which a raised log sum sees to."""
+    tau = 0.25
+    z, ids, top, t, w = inputs(T, 777, 20, torch.float32, seed=9)
+    top, tlse = top.to(top_dtype), torch.logsumexp(t / tau, 1)
+    check(z, ids, top, tlse, tau, w)
+    want, total = _derivative(z, ids, top, tlse, tau, w)
+    assert (total > 1.003).any() == (top_dtype != torch.float32)
+    es = definition(z, ids, top, tlse, tau, w)[4]
+    args = [v.to(DEV) for v in (w, z, ids, top)]
+    got = bt.bt_distill_topk_step(*args, tlse.to(DEV), tau)[1].cpu()
+    below = total <= 1
+    near(got[below], want[below], es[below] + 2.0 ** -23 * want[below].abs(), "gradient")
+    raised = torch.maximum(tlse, torch.logsumexp(top.float() / tau, 1))
+    want, total = _derivative(z, ids, top, raised, tau, w)
+    es = definition(z, ids, top, raised, tau, w)[4]
+    got = bt.bt_distill_topk_step(*args, raised.to(DEV), tau)[1].cpu()
+    near(got, want, es + 2.0 ** -22 * want.abs(), "gradient under a raised log sum")

@@ -660,7 +660,9 @@ def bt_distill_topk_backward(grad_loss: torch.Tensor, logits: torch.Tensor, ids:
                              stats: torch.Tensor, teacher_lse: torch.Tensor | None = None, temperature: float = 1.0,
                              grad: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Gradient [T, V] (the logits' dtype) of bt_distill_topk's loss for
-    grad_loss [T] and the forward's stats. grad may be the logits."""
+    grad_loss [T] and the forward's stats, for teachers whose probabilities
+    sum to one: with top in 16 bits, a teacher_lse below logsumexp(top /
+    temperature) is to be raised to it. grad may be the logits."""
     T, V, ld = _distill_args(logits, ids, top, teacher_lse, stream, grad_loss, stats, grad)
     _dense(grad_loss, "grad_loss", (T,), torch.float32)
     _dense(stats, "stats", (T, 2), torch.float32)

@@ -9,6 +9,9 @@
 //   d loss / d z_v = (exp(a_v - lse) - q_v) / tau                      v in a slot
 //                  = exp(a_v - lse) / tau                              else, without the rest
 //                  = (exp(r - lse) - q_r) exp(a_v - r) / tau           else, with it
+// for a teacher whose probabilities sum to one. Where stored logits of fewer bits
+// than teacher_lse sum to more, or the rest's term is left out since the student
+// has no rest, the gradient stays this one, not the derivative of what is left.
 // The slots' own logits are taken out of the running sum as the row is read,
 // so that r comes from a sum of its own and not from a difference that cancels
 // where the student is as sure as the teacher. Sums and statistics are fp32.
