@@ -92,9 +92,12 @@ bool takes_small(const bt_adapter_plan_info &p, int64_t T, int64_t K, int64_t N,
     small_cluster(p.small_tiles, p.small_most, K, N, R, &small);
     const double bytes = static_cast<double>(T) * static_cast<double>(K + 2 * N) * 2.0;
     const double rows = bytes / 4.5e6, tiles = 0.7 * static_cast<double>(p.tiles);
-    // widths that are no multiples of 8: one kernel fetches and stores by elements (777 tokens of 12 adapters, 4100 x
-    // 4093, rank 24: 32.8 us against 26.1)
-    const double slow = (K | N | R) % 8 == 0 ? 1.0 : 3.0;
+    // Widths that are no multiples of 8: one kernel fetches and stores by elements. Over 99 such sizes (515 to 11005
+    // wide, ranks 8 to 64, 1 to 2048 tokens of 1 to 48 adapters) the choice by this factor takes 1.3 % longer than the
+    // better of the two on average, 43 % at worst; by 2 and by 3 it is 1.6 and 9 %. One kernel against two, 4100 x
+    // 4093, rank 24: one token 8.8 and 14.5 us, 777 tokens of 12 adapters 31.2 and 25.8; 2050 x 2051, rank 16: 256
+    // tokens 12.5 and 18.8; 4093 x 11005, rank 32: 64 tokens of 12 adapters 21.7 and 35.3, of one 25.6 and 19.3.
+    const double slow = (K | N | R) % 8 == 0 ? 1.0 : 2.3;
     return slow * (small + bytes / 4.2e6) < 8.0 + 0.3 * static_cast<double>((K + 511) / 512) + (rows > tiles ? rows : tiles);
 }
 
