@@ -231,16 +231,24 @@ __global__ void __launch_bounds__(kThreads, RB * NB <= 4 ? 2 : 1) small_kernel(c
 #pragma unroll
                 for (int q = 0; q < RK; ++q) {
                     const uint4 w = wb[i][j][q];
-                    // rows 8..15 are tokens 8..15, where there are any
-                    auto add = [&](const uint32_t (&f)[NB][4]) {
-                        const uint32_t f0[4] = {f[0][0], NB > 1 ? f[NB - 1][0] : 0u, f[0][1], NB > 1 ? f[NB - 1][1] : 0u};
-                        const uint32_t f1[4] = {f[0][2], NB > 1 ? f[NB - 1][2] : 0u, f[0][3], NB > 1 ? f[NB - 1][3] : 0u};
+                    auto add = [&](const uint32_t (&lo)[4], const uint32_t (&hi)[4]) {     // rows 0..7 and 8..15
+                        const uint32_t f0[4] = {lo[0], hi[0], lo[1], hi[1]}, f1[4] = {lo[2], hi[2], lo[3], hi[3]};
                         mma<T>(d[j], f0, w.x, w.y);
                         mma<T>(d[j], f1, w.z, w.w);
                     };
-                    add(uh[q]);
-                    add(ul[q]);
-                    if constexpr (REST) add(ur[q]);
+                    if constexpr (NB == 1) {                // no tokens 8..15: the second value takes their rows
+                        const uint32_t none[4] = {0u, 0u, 0u, 0u};
+                        add(uh[q][0], ul[q][0]);
+                        if constexpr (REST) add(ur[q][0], none);
+                    } else {
+                        add(uh[q][0], uh[q][NB - 1]);
+                        add(ul[q][0], ul[q][NB - 1]);
+                        if constexpr (REST) add(ur[q][0], ur[q][NB - 1]);
+                    }
+                }
+                if constexpr (NB == 1) {
+                    d[j][0] += d[j][2];
+                    d[j][1] += d[j][3];
                 }
             }
             load_b(unit + 8 * PRE, wb[i]);
