@@ -866,11 +866,15 @@ __global__ void __launch_bounds__(kRowThreads) distill_rows_kernel(const Args a)
     if constexpr (STEP) {
         const float w = __ldg(a.w + row) * a.inv_tau;
         const Slope slope = slope_from(a, te, w, rest, all);
-        for (int v = w0 + lane; v < w1; v += 32) {
-            float f[VEC];
-            slope_any<T>(slope, reinterpret_cast<const uint4 *>(data)[v - v0], f);
-            store_vec<T>(grad + sp.head + v * VEC, wide, f);
-        }
+        auto write = [&](auto values) {
+            for (int v = w0 + lane; v < w1; v += 32) {
+                float f[VEC];
+                values(reinterpret_cast<const uint4 *>(data)[v - v0], f);
+                store_vec<T>(grad + sp.head + v * VEC, wide, f);
+            }
+        };
+        if (!slope.far) write([&](const uint4 &q, float *f) { slope_vec<T>(slope, q, f); });
+        else write([&](const uint4 &q, float *f) { slope_any<T>(slope, q, f); });
         if (edges) {
             const float f = slope_of(slope, Elem<T>::to_f32(edge[lane]));
             if (lane < nhead) grad[lane] = from_f32<T>(f);
