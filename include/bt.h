@@ -731,10 +731,13 @@ size_t bt_adapter_linear_workspace(int64_t T, int64_t K, int64_t N, int64_t R, c
  *              needs; 0 for a token without an adapter.
  *   ldx, ldb, ldo  elements from one row to the next, >= K, N, N.
  * A_a x is summed in fp32 and enters the second product as the sum of three
- * BF16 values (all of its 24 bits) or two F16 ones (22 bits); base + scale * sum
- * is rounded once. Any sizes and element alignments are served; rows that start
- * at multiples of 16 bytes (and R a multiple of 8) are faster. 1 <= R <= 128;
- * T, K, N < 2^24. T = 0 or N = 0 does nothing. workspace:
+ * BF16 values (all of its 24 bits) or two F16 ones (22 bits), in fp32 sums of the
+ * tensor cores, which cut off instead of rounding; base + scale * sum is rounded
+ * once. An infinity in x makes its token's row what the formula says; one in B (or
+ * in g and x for the gradients of B and A) meets u's values one by one, so that
+ * NaN may stand where the formula says infinity. Any sizes and element alignments
+ * are served; rows that start at multiples of 16 bytes (and R a multiple of 8) are
+ * faster. 1 <= R <= 128; T, K, N < 2^24. T = 0 or N = 0 does nothing. workspace:
  * bt_adapter_linear_workspace(T, K, N, R, info) bytes, 256-byte aligned.
  * Equal calls give equal results. Batches with few tokens of each adapter go
  * through one kernel, others through two; BT_ADAPTER_PATH=small or large in
@@ -807,8 +810,14 @@ bt_status bt_adapter_linear_backward(const void *x, int64_t ldx, const void *g, 
  *               is -inf. A NaN among a row's logits makes its loss NaN.
  *   stats       device [T, 2] out, or NULL: (lse, r), what
  *               bt_distill_topk_backward needs; zeros for a row without a slot.
- * The sums are fp32, in an order that depends on the sizes only: equal calls
- * give equal results. temperature finite and > 0. S <= 1024;
+ * The sums are fp32, of exp2 approximations within 2^-22, in an order that
+ * depends on the sizes only: equal calls give equal results. The loss is a sum of
+ * fp32 log probabilities: lse and r, where both are below 16, as they are
+ * returned, rounded by up to 5e-7 each, which shows in losses of 1e-2 and less;
+ * else it is relative to the row's largest logit, with the same error whatever
+ * the logits share. Where lse is so large that fp32 does not hold its parts
+ * (1e7 and more) the backward, which has nothing but the statistics, takes a
+ * logit that equals lse for certain. temperature finite and > 0. S <= 1024;
  * V <= 2^28, T <= 2^24: BT_ERR_UNSUPPORTED beyond. T = 0 does
  * nothing. Errors: INVALID_ARG, ALIGNMENT (a pointer not aligned to its
  * element), UNSUPPORTED, CUDA.
@@ -845,8 +854,11 @@ bt_status bt_distill_topk_backward(const float *grad_loss, const void *logits, b
 
 /*
  * bt_distill_topk_step -- both at once, for a caller that knows the upstream
- * gradient (a mean's 1 / tokens, a loss scale) beforehand: every logit is read
- * once and its gradient written once. stats may be NULL.
+ * gradient (a mean's 1 / tokens, a loss scale) beforehand. Few rows (up to half
+ * as many as the GPU has SMs) are read once, more of them twice, the second time
+ * out of L2 as far as the rows at work fit there (two for every SM at once);
+ * every gradient is written once. Its gradient comes from the row's sums and not
+ * from the statistics. stats may be NULL.
  */
 bt_status bt_distill_topk_step(const float *grad_loss, const void *logits, bt_dtype dtype, int64_t T, int64_t V,
                                int64_t ld, const void *ids, int ids_bytes, const void *top, bt_dtype top_dtype,

@@ -678,7 +678,8 @@ def bt_distill_topk_step(grad_loss: torch.Tensor, logits: torch.Tensor, ids: tor
                          teacher_lse: torch.Tensor | None = None, temperature: float = 1.0,
                          loss: torch.Tensor | None = None, grad: torch.Tensor | None = None,
                          stats: torch.Tensor | None = None, stream=None) -> tuple[torch.Tensor, torch.Tensor]:
-    """Loss [T] and gradient [T, V] in one read of the logits, for an upstream
+    """Loss [T] and gradient [T, V] in one kernel (few rows are read once, many
+    twice, the second time out of L2), for an upstream
     gradient grad_loss [T] known beforehand. grad may be the logits."""
     T, V, ld = _distill_args(logits, ids, top, teacher_lse, stream, grad_loss, loss, grad, stats)
     _dense(grad_loss, "grad_loss", (T,), torch.float32)

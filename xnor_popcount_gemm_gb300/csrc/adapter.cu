@@ -80,8 +80,8 @@ cudaError_t align_weights(const uint16_t *src, int R, int64_t C, const AdapterTi
 // Microseconds, fitted on GB300 in graphs (1 to 6000 tokens, 1 to 48 adapters, ranks 8 to 128): one kernel 2.3, for
 // each wave of CTAs 0.7 and its piece of the weights at 42 bytes a nanosecond, and x, base and out at 4.2 TB/s; two
 // kernels 8, 0.3 for every 512 of K, and the longer of x, base and out at 4.5 TB/s and 0.7 a tile. One kernel against
-// two, 4096 x 4096, rank 16: one token 3.9 and 10.1, 768 tokens of one adapter 8.7 and 13.2, 6000 51.6 and 43.3; rank
-// 64: 256 tokens 10.2 and 12.5, 2048 28.1 and 23.3; 64 tokens of 48 adapters 11.7 and 37.0. BT_ADAPTER_PATH=small|large
+// two, 4096 x 4096, rank 16: one token 4.0 and 10.0, 768 tokens of one adapter 9.4 and 13.4, 6000 54.0 and 43.4; rank
+// 64: 256 tokens 11.1 and 12.8, 2048 30.5 and 24.0; 64 tokens of 48 adapters 11.7 and 38.0. BT_ADAPTER_PATH=small|large
 // in the environment decides instead.
 bool takes_small(const bt_adapter_plan_info &p, int64_t T, int64_t K, int64_t N, int64_t R) {
     if (const char *e = std::getenv("BT_ADAPTER_PATH")) {

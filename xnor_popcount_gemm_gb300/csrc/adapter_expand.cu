@@ -16,12 +16,12 @@ namespace {
 // a quad's words are turned so that a lane loads and stores 16 bytes. Otherwise a
 // warp's results pass through shared memory and every lane walks a column, so
 // that a row's elements still travel together.
-// 8192 x 4096 bf16, rank 64: 35 us, 3.8 TB/s of base and out (with warp-level
+// 8192 x 4096 bf16, rank 64: 36 us, 3.7 TB/s of base and out (with warp-level
 // matrix instructions and U in registers 53 us). Neither memory (29 % busy) nor
-// the issue slots (42 %) nor L1 (44 %) is full: 8 warps an SM, of which every one
+// the issue slots (41 %) nor L1 (45 %) is full: 8 warps an SM, of which every one
 // takes D, base and the result through its registers, do not hide each other's
 // waits, and two D of 128 columns leave room for no third CTA. 4096 x 4096 with
-// base, rank 16: 20 us.
+// base, rank 16: 21 us.
 constexpr int kTile = 128;                 // columns
 template <int RP> constexpr int kParts = RP <= 64 ? 1 : 2;                  // of 64 ranks
 template <int RP, int VALS> constexpr int kUBytes = (VALS * RP + 63) / 64 * 2 * kAtom;    // 128 rows of 128 bytes for every 64 ranks

@@ -14,7 +14,7 @@ namespace {
 // take it K-major or MN-major. The pieces are added in a fixed order through
 // distributed shared memory: u leaves once, no partial sum touches memory.
 //
-// Bound: the long rows, read once. 8192 x 11008 bf16, rank 64: 41 us, 4.4 TB/s,
+// Bound: the long rows, read once. 8192 x 11008 bf16, rank 64: 42 us, 4.3 TB/s,
 // with the issue slots half busy (a 16-byte copy and its address for every 8
 // elements: rows are gathered, they have no box) and 264 of 304 CTAs' places
 // taken. 4096 x 4096, rank 16: 16 us alone, with the join and the beginning as

@@ -21,7 +21,7 @@ namespace {
 // up with 8 consecutive results of a token.
 //
 // Bound: the adapters' weights, read once, and latency. One token, 4096 x 4096,
-// rank 16: 3.9 us. 64 tokens of 48 adapters, 4096 x 11008, rank 32: 12.3 us for
+// rank 16: 4.0 us. 64 tokens of 48 adapters, 4096 x 11008, rank 32: 12.5 us for
 // 50 MB, 4.0 TB/s; warps wait for memory half of their time, in a few trips one
 // after another (plan, tokens and A, exchange, B).
 

@@ -20,12 +20,11 @@
 // moves 4 bytes, 0.17 clocks of an SM's share of the memory; its two passes take
 // ten instructions, 0.08 clocks, and two exp2, 0.12 clocks at 16 a clock.
 //
-// Measured, of the bytes that each must move: the step, 4096 x 131072 bf16, 390
-// us, 5.2 TB/s (issue slots 68 % busy, memory 73 %, the second read's misses
-// among it); 16 x 131072 f32 9.9 us; the loss alone, 512 x 50001 f32, 29 us, 3.2
-// TB/s (304 CTAs take one or two rows each: the second ones have the machine half
-// to themselves), 8 x 32000 bf16 4.8 us; the backward, 2048 x 32000 bf16, 43.7
-// us, 5.4 TB/s, 300 x 50001 f16 11.1 us.
+// Measured, of the bytes that each must move: the step, 4096 x 131072 bf16, 396
+// us, 5.2 TB/s (issue slots two thirds busy); 16 x 131072 f32 10.5 us; the loss
+// alone, 512 x 50001 f32, 29 us, 3.2 TB/s (304 CTAs take one or two rows each: the
+// second ones have the machine half to themselves), 8 x 32000 bf16 4.8 us; the
+// backward, 2048 x 32000 bf16, 44 us, 5.4 TB/s, 300 x 50001 f16 10.9 us.
 #include <cmath>
 #include <type_traits>
 
@@ -424,7 +423,7 @@ __device__ __forceinline__ void wait_landed(uint32_t bar, uint32_t parity, uint3
 // ring runs on over the join between the two passes and into the next row, so
 // that the copies never pause; two CTAs an SM take turns with arithmetic. A
 // cluster that holds the row in its CTAs' shared memory, read once, was slower
-// (4096 x 131072 bf16: 505 us, 570 with the next row's prefetch, against 390):
+// (4096 x 131072 bf16: 505 us, 570 with the next row's prefetch, against 396):
 // its per-row joins idle more of the machine than the second read costs.
 // ---------------------------------------------------------------------------
 constexpr int kStreamWarps = 12, kStreamThreads = 32 * kStreamWarps;
@@ -899,7 +898,7 @@ __global__ void __launch_bounds__(kRowThreads) distill_rows_kernel(const Args a)
 // (32 KB in, 32 KB out), all asked for at once; meanwhile it works out the
 // teacher's side and reads the slots' logits, before anything is written, so
 // that the gradient may take the logits' place. (A warp of its own for every
-// 4 KB, which waits for no other, took 46 us for 2048 x 32000 bf16 against 42:
+// 4 KB, which waits for no other, took 46 us for 2048 x 32000 bf16 against 44:
 // every warp then goes through the slots. One warp alone at the slots: 49 us.)
 // ---------------------------------------------------------------------------
 constexpr int kBackThreads = 256, kBackLoads = 8;
