@@ -186,3 +186,20 @@ def test_a_wait_that_runs_out_is_reported(monkeypatch):
         assert set(seen) <= {0, bt.BT_ERR_TIMEOUT} and seen[-1] == bt.BT_ERR_TIMEOUT
         assert bt.bt_device_status() == 0
         assert all(torch.equal(p, q) for p, q in zip(call(), want))
+
+
+@pytest.mark.parametrize("T", [4, 70])
+def test_an_infinite_rank_beside_large_ones_in_half_precision(T, path):
+    """u_0 = inf beside u_1 = -1e5 and u_2 = -3e5, beyond half precision's range: the results are +inf, not NaN."""
+    K, N, R = 32, 24, 16
+    x, a, b = torch.ones(T, K).half(), torch.zeros(1, R, K).half(), torch.ones(1, N, R).half()
+    a[0, 0, 3] = float("inf")
+    a[0, 1], a[0, 2] = -1e5 / K, -3e5 / K
+    plan = bt.bt_adapter_plan([0] * T, 1, device=DEV)
+    d = [t.to(DEV) for t in (x, a, b, torch.ones(1))]
+    for out_dtype in (torch.float16, torch.float32):
+        assert (bt.bt_adapter_linear(*d, plan, out_dtype=out_dtype) == float("inf")).all()
+    a[0, 0, 3] = 0
+    out = bt.bt_adapter_linear(d[0], a.to(DEV), *d[2:], plan, out_dtype=torch.float32)
+    want = (x.double() @ a[0].double().t()).sum(1)[:, None]
+    assert ((out.cpu().double() - want).abs() <= K * 2.0 ** -22 * want.abs()).all()

@@ -61,9 +61,11 @@ template <typename T> __device__ __forceinline__ uint32_t split_rest(float v0, f
 template <typename T> constexpr int kValues = std::is_same<T, __nv_bfloat16>::value ? 3 : 2;
 // Half precision reaches 65504 and ends at 2^-24: rows of u are brought to a
 // largest value of about 2^14 by a power of two first (taken out again in fp32).
+// An infinity is one at any scale: the others count.
+__device__ __forceinline__ float finite_size(float v) { return isinf(v) ? 0.0f : fabsf(v); }
 template <typename T> __device__ __forceinline__ float row_power(float amax) {
     if constexpr (std::is_same<T, __half>::value) {
-        if (!(amax > 0.0f) || isinf(amax)) return 1.0f;
+        if (!(amax > 0.0f)) return 1.0f;
         int e = 14 - ilogbf(amax);
         e = e > 100 ? 100 : e < -100 ? -100 : e;
         return exp2f(static_cast<float>(e));

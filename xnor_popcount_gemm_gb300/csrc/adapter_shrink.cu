@@ -41,7 +41,7 @@ template <typename T, int RP>
 __device__ __forceinline__ void put_split(const SplitRows &o, int64_t at, int r, const float (&f)[4], bool ok) {
     float p = 1.0f;
     if constexpr (std::is_same<T, __half>::value) {
-        float amax = fmaxf(fmaxf(fabsf(f[0]), fabsf(f[1])), fmaxf(fabsf(f[2]), fabsf(f[3])));
+        float amax = fmaxf(fmaxf(finite_size(f[0]), finite_size(f[1])), fmaxf(finite_size(f[2]), finite_size(f[3])));
 #pragma unroll
         for (int d = 1; d < RP / 4; d *= 2) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, d));
         p = row_power<T>(amax);

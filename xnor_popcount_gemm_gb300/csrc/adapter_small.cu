@@ -204,7 +204,7 @@ __global__ void __launch_bounds__(kThreads, RB * NB <= 4 ? 2 : 1) small_kernel(c
             for (int e = 0; e < 8; ++e) {
                 const int r = 32 * q + 8 * t + e;
                 v[q][e] = r < RP ? u[8 * j + g][r] : 0.0f;
-                amax = fmaxf(amax, fabsf(v[q][e]));
+                amax = fmaxf(amax, finite_size(v[q][e]));
             }
         amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
         amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
