@@ -865,6 +865,172 @@ bt_status bt_distill_topk_step(const float *grad_loss, const void *logits, bt_dt
                                int64_t S, const float *teacher_lse, float temperature, float *loss, float *stats,
                                void *grad, int64_t ldg, bt_stream stream);
 
+/* ------------------------------------------------------------------------
+ * Microscaled operands (OCP MX): what the projections that cannot do with signs
+ * run on. Blocks of 32 consecutive values of a row share a power of two; the
+ * values are E4M3 (8 bits) or E2M1 (4 bits) multiples of it. The pages have no
+ * counterpart.
+ *
+ * For a block with the largest magnitude m:
+ *   scale  = 2^e, e = max(floor(log2 m) - E, -127), E = 8 (E4M3: up to 448) or 2 (E2M1: up to 6);
+ *   value  = x / scale rounded to the nearest of the format's, ties to the even code, larger
+ *            ones to its largest (m / scale lies below 2^(E+1): in E4M3 what is above 448, in
+ *            E2M1 what is above 6).
+ * The quotient is exact, so the codes are those of the definition, on any input. A
+ * block with a NaN or an infinity has the NaN scale: its 32 values are NaN.
+ *
+ * An operand [R, K] in code BT_CODE_E4M3 or BT_CODE_E2M1 is
+ *   codes   [R, bt_mx_row_bytes(K, code)] bytes, a multiple of 128 a row; E2M1: element 2i in
+ *           the low nibble of byte i; zeros past K;
+ *   scales  bt_mx_scale_bytes(R, K, code) bytes, one a block, the biased exponent (255: NaN), in
+ *           the order that the tensor cores take: row r, block b lies at byte
+ *           ((r / 128) * A + b / 4) * 512 + (r % 32) * 16 + (r / 32 % 4) * 4 + b % 4,
+ *           A = bt_mx_row_bytes / 128 (E4M3) or / 64 (E2M1). Rows past R are not written.
+ * Both device, 16-byte aligned. R, K < 2^24; R * K below about 2^34.
+ * ------------------------------------------------------------------------ */
+
+/* Bytes of a row of codes, and of all scales; 0 for sizes out of range. */
+int64_t bt_mx_row_bytes(int64_t K, bt_code code);
+size_t bt_mx_scale_bytes(int64_t R, int64_t K, bt_code code);
+
+/*
+ * bt_mx_quantize -- x [R, K] of x_dtype (F32, BF16, F16; device, rows ldx >= K elements
+ * apart, any element alignment; 16-byte rows are faster) to an operand. R = 0 does
+ * nothing. Errors: INVALID_ARG, ALIGNMENT, UNSUPPORTED (sizes), CUDA.
+ */
+bt_status bt_mx_quantize(const void *x, bt_dtype x_dtype, int64_t ldx, int64_t R, int64_t K, bt_code code, void *codes,
+                         void *scales, bt_stream stream);
+
+/*
+ * bt_mx_dequantize -- the values of an operand: out [R, K] of out_dtype (F32, BF16,
+ * F16), rows ldo >= K elements apart. Exact in F32 and BF16 but for scales next to
+ * the ends of their range; F16 rounds and overflows as a conversion does.
+ */
+bt_status bt_mx_dequantize(const void *codes, const void *scales, int64_t R, int64_t K, bt_code code, void *out,
+                           bt_dtype out_dtype, int64_t ldo, bt_stream stream);
+
+/* Workspace bytes of bt_mx_linear for x of float type (0 for BT_PACKED and for
+ * sizes out of range). */
+size_t bt_mx_linear_workspace(int64_t M, int64_t N, int64_t K, bt_dtype x_dtype, bt_code code);
+
+/*
+ * bt_mx_linear -- out [M, N] = X W^T on tcgen05 (kind::mxf4 or kind::mxf8f6f4, block
+ * scales applied by the tensor cores, fp32 sums, which cut off instead of rounding),
+ * rounded once to out_dtype (F32, BF16, F16).
+ *   x        device; of float type: [M, K], rows ldx elements apart, quantised to
+ *            `code` by the call; BT_PACKED: an operand's codes (ldx ignored), with
+ *            x_scales.
+ *   w        device, the operand [N, K] in `code`, with w_scales.
+ *   out      rows ldo >= N elements apart; 16-byte rows are faster.
+ * A NaN block makes its row of out (its column, in W) NaN. M = 0 or N = 0 does
+ * nothing. workspace: bt_mx_linear_workspace(M, N, K, x_dtype, code) bytes, 256-byte
+ * aligned. Equal calls give equal results. Errors: INVALID_ARG, ALIGNMENT,
+ * WORKSPACE, UNSUPPORTED, CUDA.
+ */
+bt_status bt_mx_linear(const void *x, bt_dtype x_dtype, int64_t ldx, const void *x_scales, const void *w,
+                       const void *w_scales, bt_code code, int64_t M, int64_t N, int64_t K, void *out, bt_dtype out_dtype,
+                       int64_t ldo, void *workspace, size_t workspace_bytes, bt_stream stream);
+
+/*
+ * bt_mx_transpose -- an operand [R, K] as bf16 [K, ld], transposed, zeros for the columns
+ * R to ld (ld >= R, a multiple of 8; bt_backward_weight_ld(R) will do): the weight of
+ * bt_mx_linear_backward, built once.
+ */
+bt_status bt_mx_transpose(const void *codes, const void *scales, int64_t R, int64_t K, bt_code code, int64_t ld,
+                          void *out, bt_stream stream);
+
+/* Workspace bytes of bt_mx_linear_backward (needed where g's rows do not start at
+ * 16-byte multiples or N is no multiple of 8; 0 for sizes out of range). */
+size_t bt_mx_linear_backward_workspace(int64_t M, int64_t N);
+
+/*
+ * bt_mx_linear_backward -- grad_x [M, K] = g W for the upstream gradient g [M, N] (device,
+ * BF16, rows ldg elements apart) and wt = bt_mx_transpose(W) with pitch ldw (zeros past
+ * N up to a multiple of 8): the gradient of bt_mx_linear's result with the rounding
+ * of x taken as the identity (straight through). bf16 products, fp32 sums; grad_x
+ * dense, BF16 or F32. The weights are constants. M = 0 does nothing, N = 0 gives
+ * zeros. Errors as bt_mx_linear.
+ */
+bt_status bt_mx_linear_backward(const void *g, int64_t ldg, const void *wt, int64_t ldw, int64_t M, int64_t N, int64_t K,
+                                void *grad_x, bt_dtype grad_x_dtype, void *workspace, size_t workspace_bytes,
+                                bt_stream stream);
+
+/* ------------------------------------------------------------------------
+ * Root-mean-square norm before a projection. The pages have no counterpart.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * bt_rms_norm -- for every row x_t of x [T, N] (dtype F32, BF16 or F16):
+ *   h = cast(x_t + residual_t)                 (x_t without a residual), kept in sum
+ *   y = cast(fp32(h * weight / sqrt(mean h^2 + eps)))
+ * y goes to out [T, N] (dtype) and / or, as an operand in `code`, to codes and
+ * scales: equal to bt_mx_quantize of out, which need not be written for it.
+ *   weight    device [N] in F32 or dtype, or NULL for 1.
+ *   residual  device [T, N] or NULL; sum device [T, N] or NULL (not wanted; needs a
+ *             residual), may be x or residual.
+ *   out       device [T, N] or NULL; codes and scales both or neither; one of out and
+ *             codes at least. out may be x or, without sum there, residual.
+ *   ldx, ldr, lds, ldo  elements from one row to the next, >= N.
+ * The fp32 value under the last cast is the correctly rounded one but for about one
+ * in 2^24, so that the codes do not depend on how the sum of squares was taken. Rows
+ * whose squares leave fp32's range are scaled first. eps >= 0, finite. A row with a
+ * NaN is NaN, one with an infinity NaN there and 0 elsewhere; with eps = 0 a row of zeros is NaN. Any element
+ * alignment; 16-byte rows with N a multiple of 8 are faster. T = 0 does nothing.
+ * T, N < 2^24. Errors: INVALID_ARG, ALIGNMENT, UNSUPPORTED, CUDA.
+ */
+bt_status bt_rms_norm(const void *x, bt_dtype dtype, int64_t ldx, const void *residual, int64_t ldr, const void *weight,
+                      bt_dtype weight_dtype, int64_t T, int64_t N, double eps, void *sum, int64_t lds, void *out,
+                      int64_t ldo, bt_code code, void *codes, void *scales, bt_stream stream);
+
+/* Workspace bytes of bt_rms_norm_backward (0 for sizes out of range). */
+size_t bt_rms_norm_backward_workspace(int64_t T, int64_t N);
+
+/*
+ * bt_rms_norm_backward -- for the upstream gradient g [T, N] of y and the forward's h
+ * (sum, or x without a residual), r = 1 / sqrt(mean h^2 + eps), n = h r:
+ *   grad_x_t    = cast(r (g w - n mean(g w n)) + grad_sum_t)
+ *   grad_weight = sum over the rows of g n          (fp32 [N], or NULL: not wanted)
+ * grad_x is the gradient of x and of the residual alike; grad_sum [T, N], the gradient
+ * that comes back along the residual stream, or NULL. g, h, grad_sum and grad_x have
+ * dtype; grad_x may be one of the other three (with its pitch). Codes take the
+ * gradient straight through. Rows are summed in an order that the sizes decide: equal
+ * calls give equal results. T = 0 zeroes grad_weight. workspace:
+ * bt_rms_norm_backward_workspace(T, N) bytes, 256-byte aligned. Limits and errors as
+ * bt_rms_norm.
+ */
+bt_status bt_rms_norm_backward(const void *g, bt_dtype dtype, int64_t ldg, const void *h, int64_t ldh, const void *weight,
+                               bt_dtype weight_dtype, int64_t T, int64_t N, double eps, const void *grad_sum, int64_t ldgs,
+                               void *grad_x, int64_t ldgx, float *grad_weight, void *workspace, size_t workspace_bytes,
+                               bt_stream stream);
+
+/* ------------------------------------------------------------------------
+ * Clipping by the global norm: the last step before the optimiser's. The pages
+ * have no counterpart.
+ * ------------------------------------------------------------------------ */
+
+/* Workspace bytes of bt_clip_grads for `count` tensors (0 for counts out of range). */
+size_t bt_clip_grads_workspace(int64_t count);
+
+/*
+ * bt_clip_grads -- norm = sqrt(sum of the squares of every element of every tensor),
+ * written to *norm (device fp32), and each tensor times
+ * min(1, max_norm / (norm + eps)), in place, rounded once.
+ *   grads, numels, dtypes  host arrays of `count` <= 2^20 tensors: device pointers
+ *             (aligned to their elements), elements (each dense; 0: ignored) and
+ *             bt_dtype (F32, BF16 or F16 each). They must not overlap, which is
+ *             checked: an element of two tensors would be scaled twice.
+ *   max_norm  >= 0; +inf: the norm alone is computed. eps >= 0.
+ * The arrays are read before the call returns and the addresses go with the launches:
+ * a captured graph keeps them. A norm that is infinite makes the factor 0, a NaN norm
+ * makes every gradient NaN, as the formula says. Where the factor is not below one
+ * the tensors are not written. Squares are summed in fp32 over at most 64 values, then
+ * in fp64, in an order that the sizes decide: equal calls give equal results. workspace:
+ * bt_clip_grads_workspace(count) bytes, 256-byte aligned. count = 0 gives the norm 0.
+ * Errors: INVALID_ARG (overlaps among them), ALIGNMENT, WORKSPACE, UNSUPPORTED, CUDA.
+ */
+bt_status bt_clip_grads(void *const *grads, const int64_t *numels, const int32_t *dtypes, int64_t count, float max_norm,
+                        float eps, float *norm, void *workspace, size_t workspace_bytes, bt_stream stream);
+
 /*
  * bt_device_status -- synchronizes `stream`, then reads and clears the
  * device error word of the current device: BT_ERR_TIMEOUT if a kernel's

@@ -29,6 +29,10 @@ __all__ = [
     "bt_binary_conv2d_dscale_init", "bt_distill_topk", "bt_distill_topk_backward", "bt_distill_topk_step",
     "AdapterPlan", "bt_adapter_plan", "bt_adapter_plan_bytes", "bt_adapter_linear", "bt_adapter_linear_workspace",
     "bt_adapter_linear_backward", "bt_adapter_linear_backward_workspace",
+    "MxRows", "bt_mx_row_bytes", "bt_mx_scale_bytes", "bt_mx_quantize", "bt_mx_dequantize", "bt_mx_linear",
+    "bt_mx_linear_workspace", "bt_mx_transpose", "bt_mx_linear_backward", "bt_mx_linear_backward_workspace",
+    "bt_rms_norm", "bt_rms_norm_backward", "bt_rms_norm_backward_workspace", "bt_clip_grads",
+    "bt_clip_grads_workspace",
 ]
 
 BT_OK, BT_ERR_INVALID_ARG, BT_ERR_UNSUPPORTED, BT_ERR_ALIGNMENT = 0, -1, -2, -3
@@ -115,6 +119,22 @@ _c_alin = _sig("bt_adapter_linear", _i, [_p, _i, _i64, _p, _p, _p, _p, _pinfo, _
 _c_abwd_ws = _sig("bt_adapter_linear_backward_workspace", _sz, [_i64, _i64, _i64, _i64, _pinfo])
 _c_abwd = _sig("bt_adapter_linear_backward", _i, [_p, _i64, _p, _i64, _p, _p, _p, _p, _p, _pinfo, _i64, _i64, _i64,
                                                  _i64, _p, _i64, _p, _i64, _p, _p, _p, _sz, _p])
+_c_mx_rb = _sig("bt_mx_row_bytes", _i64, [_i64, _i])
+_c_mx_sb = _sig("bt_mx_scale_bytes", _sz, [_i64, _i64, _i])
+_c_mx_q = _sig("bt_mx_quantize", _i, [_p, _i, _i64, _i64, _i64, _i, _p, _p, _p])
+_c_mx_dq = _sig("bt_mx_dequantize", _i, [_p, _p, _i64, _i64, _i, _p, _i, _i64, _p])
+_c_mx_lin_ws = _sig("bt_mx_linear_workspace", _sz, [_i64, _i64, _i64, _i, _i])
+_c_mx_lin = _sig("bt_mx_linear", _i, [_p, _i, _i64, _p, _p, _p, _i, _i64, _i64, _i64, _p, _i, _i64, _p, _sz, _p])
+_c_mx_t = _sig("bt_mx_transpose", _i, [_p, _p, _i64, _i64, _i, _i64, _p, _p])
+_c_mx_bwd_ws = _sig("bt_mx_linear_backward_workspace", _sz, [_i64, _i64])
+_c_mx_bwd = _sig("bt_mx_linear_backward", _i, [_p, _i64, _p, _i64, _i64, _i64, _i64, _p, _i, _p, _sz, _p])
+_c_rms = _sig("bt_rms_norm", _i, [_p, _i, _i64, _p, _i64, _p, _i, _i64, _i64, ctypes.c_double, _p, _i64, _p, _i64, _i, _p,
+                                  _p, _p])
+_c_rms_bwd_ws = _sig("bt_rms_norm_backward_workspace", _sz, [_i64, _i64])
+_c_rms_bwd = _sig("bt_rms_norm_backward", _i, [_p, _i, _i64, _p, _i64, _p, _i, _i64, _i64, ctypes.c_double, _p, _i64, _p,
+                                               _i64, _p, _p, _sz, _p])
+_c_clip_ws = _sig("bt_clip_grads_workspace", _sz, [_i64])
+_c_clip = _sig("bt_clip_grads", _i, [_p, _p, _p, _i64, _f, _f, _p, _p, _sz, _p])
 _c_plan = _sig("bt_plan", _i, [_i, _i64, _i64, _i64, ctypes.POINTER(_i), ctypes.POINTER(_i)])
 
 
@@ -153,7 +173,10 @@ EXPORTED = ["bt_version", "bt_status_string", "bt_packed_row_bytes", "bt_pack_si
             "bt_w8a8_conv2d", "bt_set_wait_timeout", "bt_binary_linear_dscale_init", "bt_binary_conv2d_dscale_init",
             "bt_distill_topk", "bt_distill_topk_backward", "bt_distill_topk_step", "bt_adapter_plan_bytes",
             "bt_adapter_plan", "bt_adapter_linear_workspace", "bt_adapter_linear",
-            "bt_adapter_linear_backward_workspace", "bt_adapter_linear_backward"]
+            "bt_adapter_linear_backward_workspace", "bt_adapter_linear_backward",
+            "bt_mx_row_bytes", "bt_mx_scale_bytes", "bt_mx_quantize", "bt_mx_dequantize", "bt_mx_linear_workspace",
+            "bt_mx_linear", "bt_mx_transpose", "bt_mx_linear_backward_workspace", "bt_mx_linear_backward", "bt_rms_norm",
+            "bt_rms_norm_backward_workspace", "bt_rms_norm_backward", "bt_clip_grads_workspace", "bt_clip_grads"]
 
 
 class BtError(RuntimeError):
@@ -557,6 +580,10 @@ def _on_device_of(name: str, at: int):
             t = args[at] if at < len(args) else kw.get(name)
             if type(t) is AdapterPlan:
                 t = t.buffer
+            elif type(t) is MxRows:
+                t = t.codes
+            elif type(t) in (list, tuple):
+                t = t[0] if t else None
             device = t.get_device() if isinstance(t, torch.Tensor) else -1
             if device < 0 or device == _current_device():
                 return fn(*args, **kw)
@@ -846,6 +873,286 @@ def bt_adapter_linear_backward(x: torch.Tensor, g: torch.Tensor, u: torch.Tensor
                    K, N, R, _ptr(grad_base), ldgb, _ptr(grad_x), ldgx, _ptr(grad_a), _ptr(grad_b), _ptr(workspace), need,
                    _on_stream(stream, x.device)))
     return grad_x, grad_a, grad_b
+
+
+class MxRows:
+    """A microscaled operand [R, K]: `codes` uint8 [R, bt_mx_row_bytes(K, code)] and `scales` uint8
+    [bt_mx_scale_bytes(R, K, code)] on the device, `code` BT_CODE_E4M3 or BT_CODE_E2M1."""
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor, K: int, code: int):
+        row = bt_mx_row_bytes(K, code)
+        if row == 0:
+            raise ValueError("code must be BT_CODE_E4M3 or BT_CODE_E2M1 and K in [1, 2^24)")
+        if codes.dim() != 2 or codes.shape[1] != row or codes.dtype != torch.uint8 or not codes.is_cuda:
+            raise ValueError(f"codes must be a uint8 CUDA tensor of shape [R, {row}]")
+        _contig(codes, "codes")
+        _dense(scales, "scales", (bt_mx_scale_bytes(codes.shape[0], K, code),), torch.uint8)
+        self.codes, self.scales, self.K, self.code = codes, scales, K, code
+
+    @property
+    def shape(self) -> tuple[int, int]:
+        return self.codes.shape[0], self.K
+
+    @property
+    def device(self) -> torch.device:
+        return self.codes.device
+
+    def __repr__(self) -> str:
+        return f"MxRows({list(self.shape)}, {'E4M3' if self.code == BT_CODE_E4M3 else 'E2M1'}, {self.device})"
+
+
+def bt_mx_row_bytes(K: int, code: int) -> int:
+    return int(_c_mx_rb(K, code))
+
+
+def bt_mx_scale_bytes(R: int, K: int, code: int) -> int:
+    return int(_c_mx_sb(R, K, code))
+
+
+_FLOATS = (torch.float32, torch.bfloat16, torch.float16)
+
+
+def _float_rows(t: torch.Tensor, name: str, dtypes=_FLOATS) -> int:
+    """Elements from one row of a 2-D operand to the next."""
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D")
+    return _rows(t, name, t.shape[0], t.shape[1], dtypes)
+
+
+def _mx(q, name: str):
+    if type(q) is not MxRows:
+        raise ValueError(f"{name} must be MxRows")
+    return q
+
+
+def _new_mx(R: int, K: int, code: int, device, stream) -> MxRows:
+    row = bt_mx_row_bytes(K, code)
+    if row == 0:
+        raise BtError(BT_ERR_INVALID_ARG)
+    return MxRows(_empty((R, row), torch.uint8, device, stream),
+                  _empty((bt_mx_scale_bytes(R, K, code),), torch.uint8, device, stream), K, code)
+
+
+@_on_device_of("x", 0)
+def bt_mx_quantize(x: torch.Tensor, code: int, out: MxRows | None = None, stream=None) -> MxRows:
+    """x [R, K] in blocks of 32 along K that share a power of two, as E4M3 or E2M1 values."""
+    ld = _float_rows(x, "x")
+    R, K = x.shape
+    if out is not None:
+        if _mx(out, "out").shape != (R, K) or out.code != code:
+            raise ValueError("out must be MxRows of x's shape and the code")
+        _same_device(x, stream, out.codes, out.scales)
+    else:
+        _same_device(x, stream)
+        out = _new_mx(R, K, code, x.device, stream)
+    _check(_c_mx_q(x.data_ptr(), _DT[x.dtype], ld, R, K, code, out.codes.data_ptr(), out.scales.data_ptr(),
+                   _on_stream(stream, x.device)))
+    return out
+
+
+@_on_device_of("q", 0)
+def bt_mx_dequantize(q: MxRows, out_dtype=torch.float32, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The values [R, K] of an operand in out_dtype."""
+    R, K = _mx(q, "q").shape
+    _same_device(q.codes, stream, q.scales, out)
+    if out is None:
+        out = _empty((R, K), out_dtype, q.device, stream)
+    ldo = _rows(out, "out", R, K, _FLOATS)
+    _check(_c_mx_dq(q.codes.data_ptr(), q.scales.data_ptr(), R, K, q.code, out.data_ptr(), _DT[out.dtype], ldo,
+                    _on_stream(stream, q.device)))
+    return out
+
+
+def bt_mx_linear_workspace(M: int, N: int, K: int, x_dtype: int, code: int) -> int:
+    return int(_c_mx_lin_ws(M, N, K, x_dtype, code))
+
+
+@_on_device_of("x", 0)
+def bt_mx_linear(x, w: MxRows, out_dtype=None, out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                 stream=None) -> torch.Tensor:
+    """out [M, N] = x w^T for a weight operand w [N, K] and x [M, K]: a float tensor (quantised to w's code by the
+    call) or MxRows in w's code. out_dtype: x's type, bfloat16 for MxRows."""
+    N, K = _mx(w, "w").shape
+    code = w.code
+    if type(x) is MxRows:
+        if x.code != code or x.K != K:
+            raise ValueError("x and w must agree on K and the code")
+        M, xt, ldx, xp, xs = x.codes.shape[0], BT_PACKED, K, x.codes, x.scales
+        dt = torch.bfloat16
+    else:
+        ldx = _float_rows(x, "x")
+        if x.shape[1] != K:
+            raise ValueError("x and w must agree on K")
+        M, xt, xp, xs = x.shape[0], _DT[x.dtype], x, None
+        dt = x.dtype
+    _same_device(xp, stream, xs, w.codes, w.scales, out, workspace)
+    if out is None:
+        out = _empty((M, N), dt if out_dtype is None else out_dtype, xp.device, stream)
+    ldo = _rows(out, "out", M, N, _FLOATS if out_dtype is None else (out_dtype,))
+    need = _c_mx_lin_ws(M, N, K, xt, code)
+    workspace = _scratch(workspace, need, xp.device, stream)
+    _check(_c_mx_lin(xp.data_ptr(), xt, ldx, None if xs is None else xs.data_ptr(), w.codes.data_ptr(), w.scales.data_ptr(),
+                     code, M, N, K, out.data_ptr(), _DT[out.dtype], ldo, None if workspace is None else workspace.data_ptr(),
+                     need, _on_stream(stream, xp.device)))
+    return out
+
+
+@_on_device_of("w", 0)
+def bt_mx_transpose(w: MxRows, ld: int | None = None, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """An operand w [N, K] as bf16 [K, ld], transposed, zeros past N: the weight of bt_mx_linear_backward
+    (ld defaults to bt_backward_weight_ld(N))."""
+    N, K = _mx(w, "w").shape
+    ld = bt_backward_weight_ld(N) if ld is None else ld
+    _same_device(w.codes, stream, w.scales, out)
+    if out is None:
+        out = _empty((K, ld), torch.bfloat16, w.device, stream)
+    else:
+        _dense(out, "out", (K, ld), torch.bfloat16)
+    _check(_c_mx_t(w.codes.data_ptr(), w.scales.data_ptr(), N, K, w.code, ld, out.data_ptr(), _on_stream(stream, w.device)))
+    return out
+
+
+def bt_mx_linear_backward_workspace(M: int, N: int) -> int:
+    return int(_c_mx_bwd_ws(M, N))
+
+
+@_on_device_of("g", 0)
+def bt_mx_linear_backward(g: torch.Tensor, wt: torch.Tensor, out_dtype=torch.bfloat16, grad_x: torch.Tensor | None = None,
+                          workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The input gradient [M, K] of bt_mx_linear for the upstream gradient g [M, N] (bf16), wt = bt_mx_transpose(w)."""
+    ldg = _float_rows(g, "g", _BF16)
+    M, N = g.shape
+    if wt.dim() != 2 or wt.dtype != torch.bfloat16 or not wt.is_cuda or wt.shape[1] < N:
+        raise ValueError("wt must be bt_mx_transpose(w) for g's N columns")
+    _contig(wt, "wt")
+    K, ldw = wt.shape
+    _same_device(g, stream, wt, grad_x, workspace)
+    if grad_x is None:
+        grad_x = _empty((M, K), out_dtype, g.device, stream)
+    elif grad_x.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("grad_x must be bfloat16 or float32")
+    _dense(grad_x, "grad_x", (M, K), grad_x.dtype)
+    need = _c_mx_bwd_ws(M, N)
+    if ldg % 8 == 0 and N % 8 == 0 and g.data_ptr() % 16 == 0:
+        need = 0
+    workspace = _scratch(workspace, need, g.device, stream)
+    _check(_c_mx_bwd(g.data_ptr(), ldg, wt.data_ptr(), ldw, M, N, K, grad_x.data_ptr(), _DT[grad_x.dtype],
+                     None if workspace is None else workspace.data_ptr(), need, _on_stream(stream, g.device)))
+    return grad_x
+
+
+def _norm_weight(weight, N: int, dtype) -> int:
+    if weight is None:
+        return BT_F32
+    if weight.dtype not in (dtype, torch.float32):
+        raise ValueError("weight must be of x's type or float32")
+    _dense(weight, "weight", (N,), weight.dtype)
+    return _DT[weight.dtype]
+
+
+@_on_device_of("x", 0)
+def bt_rms_norm(x: torch.Tensor, weight: torch.Tensor | None = None, eps: float = 1e-6,
+                residual: torch.Tensor | None = None, want_out: bool = True, code: int | None = None,
+                sum: torch.Tensor | None = None, out: torch.Tensor | None = None, q: MxRows | None = None, stream=None):
+    """h = x + residual (in x's type), y = h * weight / sqrt(mean(h^2) + eps) along the rows of x [T, N]: returns
+    (y, h, codes). y is None unless want_out; h (which may be written over x or residual: sum) None without a
+    residual; codes, y as MxRows in `code`, None without a code."""
+    ldx = _float_rows(x, "x")
+    T, N = x.shape
+    dt = (x.dtype,)
+    if q is not None:
+        if _mx(q, "q").shape != (T, N) or (code is not None and q.code != code):
+            raise ValueError("q must be MxRows of x's shape and the code")
+        code = q.code
+    if out is not None and not want_out:
+        raise ValueError("out is given and not wanted")
+    if sum is not None and residual is None:
+        raise ValueError("sum needs a residual")
+    _same_device(x, stream, weight, residual, sum, out, None if q is None else q.codes, None if q is None else q.scales)
+    wt = _norm_weight(weight, N, x.dtype)
+    ldr = lds = ldo = 0
+    if residual is not None:
+        ldr = _rows(residual, "residual", T, N, dt)
+        if sum is None:
+            sum = _empty((T, N), x.dtype, x.device, stream)
+        lds = _rows(sum, "sum", T, N, dt)
+    if want_out:
+        if out is None:
+            out = _empty((T, N), x.dtype, x.device, stream)
+        ldo = _rows(out, "out", T, N, dt)
+    if code is not None and q is None:
+        q = _new_mx(T, N, code, x.device, stream)
+    _check(_c_rms(x.data_ptr(), _DT[x.dtype], ldx, _ptr(residual), ldr, _ptr(weight), wt, T, N, eps, _ptr(sum), lds, _ptr(out),
+                  ldo, 0 if q is None else code, None if q is None else q.codes.data_ptr(),
+                  None if q is None else q.scales.data_ptr(), _on_stream(stream, x.device)))
+    return out, sum, q
+
+
+def bt_rms_norm_backward_workspace(T: int, N: int) -> int:
+    return int(_c_rms_bwd_ws(T, N))
+
+
+@_on_device_of("g", 0)
+def bt_rms_norm_backward(g: torch.Tensor, h: torch.Tensor, weight: torch.Tensor | None = None, eps: float = 1e-6,
+                         grad_sum: torch.Tensor | None = None, want_grad_weight: bool = True,
+                         grad_x: torch.Tensor | None = None, grad_weight: torch.Tensor | None = None,
+                         workspace: torch.Tensor | None = None, stream=None):
+    """Gradients of bt_rms_norm for the upstream gradient g [T, N] of y, h what was normed (its sum, or x) and grad_sum
+    the gradient of h that comes along the residual stream: (grad_x [T, N], of x and of the residual alike,
+    grad_weight [N] float, None unless wanted)."""
+    ldg = _float_rows(g, "g")
+    T, N = g.shape
+    dt = (g.dtype,)
+    ldh = _rows(h, "h", T, N, dt)
+    _same_device(g, stream, h, weight, grad_sum, grad_x, grad_weight, workspace)
+    wt = _norm_weight(weight, N, g.dtype)
+    ldgs = 0 if grad_sum is None else _rows(grad_sum, "grad_sum", T, N, dt)
+    if grad_x is None:
+        grad_x = _empty((T, N), g.dtype, g.device, stream)
+    ldgx = _rows(grad_x, "grad_x", T, N, dt)
+    if grad_weight is not None:
+        if not want_grad_weight:
+            raise ValueError("grad_weight is given and not wanted")
+        _dense(grad_weight, "grad_weight", (N,), torch.float32)
+    elif want_grad_weight:
+        grad_weight = _empty((N,), torch.float32, g.device, stream)
+    need = _c_rms_bwd_ws(T, N)
+    workspace = _scratch(workspace, need, g.device, stream)
+    _check(_c_rms_bwd(g.data_ptr(), _DT[g.dtype], ldg, h.data_ptr(), ldh, _ptr(weight), wt, T, N, eps, _ptr(grad_sum), ldgs,
+                      grad_x.data_ptr(), ldgx, _ptr(grad_weight), _ptr(workspace), need, _on_stream(stream, g.device)))
+    return grad_x, grad_weight
+
+
+def bt_clip_grads_workspace(count: int) -> int:
+    return int(_c_clip_ws(count))
+
+
+@_on_device_of("grads", 0)
+def bt_clip_grads(grads, max_norm: float, eps: float = 1e-6, norm: torch.Tensor | None = None,
+                  workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The norm of all of grads (a list of contiguous CUDA tensors, float32, bfloat16 or float16) as a device float, and
+    each of them times min(1, max_norm / (norm + eps)), in place. max_norm = inf: the norm alone."""
+    grads = list(grads)
+    if not grads:
+        raise ValueError("grads must hold a tensor")
+    n = len(grads)
+    first = grads[0]
+    _same_device(first, stream, *grads, norm, workspace)
+    for g in grads:
+        if g.dtype not in _FLOATS or not g.is_cuda:
+            raise ValueError("grads must be CUDA tensors of float32, bfloat16 or float16")
+        if not g.is_contiguous():
+            raise ValueError("grads must be contiguous")
+    if norm is None:
+        norm = _empty((), torch.float32, first.device, stream)
+    else:
+        _dense(norm, "norm", (), torch.float32)
+    need = _c_clip_ws(n)
+    workspace = _scratch(workspace, need, first.device, stream)
+    _check(_c_clip((_p * n)(*[g.data_ptr() for g in grads]), (_i64 * n)(*[g.numel() for g in grads]),
+                   (ctypes.c_int32 * n)(*[_DT[g.dtype] for g in grads]), n, max_norm, eps, norm.data_ptr(), _ptr(workspace),
+                   need, _on_stream(stream, first.device)))
+    return norm
 
 
 def bt_binary_linear_noalloc_max_bytes() -> int:

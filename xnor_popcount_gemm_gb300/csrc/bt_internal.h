@@ -311,6 +311,13 @@ template <typename K> cudaError_t allow_smem(K kern, int bytes, ContextOnce &onc
         once.run(current_context_id, [&] { return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes); }));
 }
 
+// Microscaled operands (mx_quant.cu): whether [R, K] is a size they have, and rows to one. x [R, K] of float type xt, rows
+// ldx elements apart; q and scales as bt_mx_quantize writes them. The kernel lets the one after it begin only when
+// everything before it has ended.
+bt_status mx_sides(int64_t R, int64_t K, bt_code code);
+cudaError_t launch_mx_quantize(const void *x, bt_dtype xt, int64_t ldx, int64_t R, int64_t K, bt_code code, void *q, void *scales,
+                               cudaStream_t s);
+
 // Launch attribute list allowing programmatic dependent launch (the kernel
 // overlaps its prologue with the previous kernel in the stream).
 inline cudaLaunchAttribute pdl_attribute() {

@@ -1,0 +1,163 @@
+// Microscaled operands (OCP MX): 32 consecutive values of a row share a power of
+// two 2^(s - 127), s one byte, and are E4M3 (8 bits) or E2M1 (4 bits) values of it.
+//   s     = max(exponent of the block's largest magnitude - the format's largest exponent + 127, 0)
+//   value = x / 2^(s - 127) rounded to nearest, ties to even, beyond the largest value to that
+// x / 2^(s - 127) is exact but for values below 2^-126, far below half a step, so
+// the codes do not depend on who computes them. A NaN or infinity among the 32
+// makes s = 255, the NaN of these scales, and the block NaN.
+//
+// Codes: rows of a multiple of 128 bytes (128 E4M3 or 256 E2M1 values), zero past
+// K; E2M1: element 2i in the low nibble of byte i. Scales: what the tensor cores take. An atom of
+// 512 bytes holds 128 rows x 4 blocks: row r's block b at (r % 32) * 16 +
+// (r / 32) * 4 + b, which one tcgen05.cp brings to 32 lanes x 4 columns of TMEM.
+// Atoms lie in row order of [rows / 128, blocks / 4], a whole number of them (1 or 2) for 128 bytes of codes.
+#pragma once
+
+#include <type_traits>
+
+#include <cuda_fp4.h>
+#include <cuda_fp8.h>
+
+#include "bt_device.cuh"
+#include "mx_layout.h"
+
+namespace bt {
+namespace mx {
+
+template <int CODE> struct Format;
+template <> struct Format<BT_CODE_E4M3> {
+    static constexpr int kMaxExp = 8;          // 448 = 1.75 * 2^8
+    static constexpr int kBytes8 = 8;          // bytes of eight codes
+};
+template <> struct Format<BT_CODE_E2M1> {
+    static constexpr int kMaxExp = 2;          // 6 = 1.5 * 2^2
+    static constexpr int kBytes8 = 4;
+};
+
+// Bits of |v|: their order is that of the magnitudes, infinity and then NaN last.
+__device__ __forceinline__ uint32_t mag_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+constexpr uint32_t kInfBits = 0x7F800000u;
+constexpr uint32_t kNanScale = 255u;
+
+// The scale byte of a block whose largest magnitude has the bits `top`.
+template <int CODE> __device__ __forceinline__ uint32_t scale_of(uint32_t top) {
+    if (top >= kInfBits) return kNanScale;
+    const int e = static_cast<int>(top >> 23) - Format<CODE>::kMaxExp;
+    return static_cast<uint32_t>(e > 0 ? e : 0);
+}
+// 2^(127 - s), what values are multiplied by; 0 for the NaN scale (codes 0 then).
+__device__ __forceinline__ float inverse_of(uint32_t s) {
+    return s == kNanScale ? 0.0f : __uint_as_float((254u - s) << 23);
+}
+// 2^(s - 127).
+__device__ __forceinline__ float power_of(uint32_t s) {
+    return __uint_as_float(s == 0u ? 0x00400000u : s == kNanScale ? 0x7FFFFFFFu : s << 23);
+}
+
+// Two codes: lo in the low byte (nibble).
+template <int CODE> __device__ __forceinline__ uint32_t code2(float lo, float hi) {
+    if constexpr (CODE == BT_CODE_E4M3)
+        return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
+    else
+        return __nv_cvt_float2_to_fp4x2(make_float2(lo, hi), __NV_E2M1, cudaRoundNearest);
+}
+// Eight codes of v * inv; zeros where inv is 0 (a NaN block).
+template <int CODE> __device__ __forceinline__ uint2 code8(const float (&v)[8], float inv) {
+    if (inv == 0.0f) return make_uint2(0u, 0u);
+    if constexpr (CODE == BT_CODE_E4M3) {
+        return make_uint2(code2<CODE>(v[0] * inv, v[1] * inv) | (code2<CODE>(v[2] * inv, v[3] * inv) << 16),
+                          code2<CODE>(v[4] * inv, v[5] * inv) | (code2<CODE>(v[6] * inv, v[7] * inv) << 16));
+    } else {
+        return make_uint2(code2<CODE>(v[0] * inv, v[1] * inv) | (code2<CODE>(v[2] * inv, v[3] * inv) << 8) |
+                              (code2<CODE>(v[4] * inv, v[5] * inv) << 16) | (code2<CODE>(v[6] * inv, v[7] * inv) << 24),
+                          0u);
+    }
+}
+template <int CODE> __device__ __forceinline__ void store8(uint8_t *p, const uint2 &c) {
+    if constexpr (CODE == BT_CODE_E4M3) *reinterpret_cast<uint2 *>(p) = c;
+    else *reinterpret_cast<uint32_t *>(p) = c.x;
+}
+// The values of eight codes.
+template <int CODE> __device__ __forceinline__ void value8(const uint2 &c, float (&v)[8]) {
+    if constexpr (CODE == BT_CODE_E4M3) {
+        const uint32_t w[2] = {c.x, c.y};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w[i >> 1] >> (16 * (i & 1))), __NV_E4M3);
+            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+            v[2 * i] = f.x;
+            v[2 * i + 1] = f.y;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __half2_raw h = __nv_cvt_fp4x2_to_halfraw2(static_cast<__nv_fp4x2_storage_t>(c.x >> (8 * i)), __NV_E2M1);
+            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+            v[2 * i] = f.x;
+            v[2 * i + 1] = f.y;
+        }
+    }
+}
+template <int CODE> __device__ __forceinline__ uint2 load8(const uint8_t *p) {
+    if constexpr (CODE == BT_CODE_E4M3) return *reinterpret_cast<const uint2 *>(p);
+    else return make_uint2(*reinterpret_cast<const uint32_t *>(p), 0u);
+}
+
+// fp32 to an element type, rounded to nearest.
+template <typename T> __device__ __forceinline__ T from_f32(float v);
+template <> __device__ __forceinline__ float from_f32<float>(float v) { return v; }
+template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+template <> __device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
+
+// Eight consecutive elements as 16 or 32 bytes.
+template <typename T> struct Raw8;
+template <> struct Raw8<float> { uint4 a, b; };
+template <> struct Raw8<__nv_bfloat16> { uint4 a; };
+template <> struct Raw8<__half> { uint4 a; };
+template <typename T> __device__ __forceinline__ Raw8<T> raw_load(const T *p) {
+    Raw8<T> r;
+    r.a = __ldg(reinterpret_cast<const uint4 *>(p));
+    if constexpr (sizeof(T) == 4) r.b = __ldg(reinterpret_cast<const uint4 *>(p) + 1);
+    return r;
+}
+template <typename T> __device__ __forceinline__ void raw_unpack(const Raw8<T> &r, float (&v)[8]) {
+    Elem<T>::unpack(r.a, v);
+    if constexpr (sizeof(T) == 4) Elem<T>::unpack(r.b, v + 4);
+}
+template <typename T> __device__ __forceinline__ Raw8<T> raw_pack(const float (&v)[8]) {
+    Raw8<T> r;
+    if constexpr (sizeof(T) == 4) {
+        r.a = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+        r.b = make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7]));
+    } else {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (std::is_same<T, __half>::value) {
+                const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+                w[i] = *reinterpret_cast<const uint32_t *>(&h);
+            } else {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+                w[i] = *reinterpret_cast<const uint32_t *>(&h);
+            }
+        }
+        r.a = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    return r;
+}
+template <typename T> __device__ __forceinline__ void raw_store(T *p, const Raw8<T> &r) {
+    *reinterpret_cast<uint4 *>(p) = r.a;
+    if constexpr (sizeof(T) == 4) *(reinterpret_cast<uint4 *>(p) + 1) = r.b;
+}
+// A NaN as the compiler's conversions leave it is as good as any: nothing here goes by a NaN's bits.
+
+// Four lanes next to one another hold a block: its largest magnitude, in all of them.
+__device__ __forceinline__ uint32_t quad_max(uint32_t m) {
+    uint32_t o = __shfl_xor_sync(0xFFFFFFFFu, m, 1);
+    m = m > o ? m : o;
+    o = __shfl_xor_sync(0xFFFFFFFFu, m, 2);
+    return m > o ? m : o;
+}
+
+}  // namespace mx
+}  // namespace bt

@@ -251,6 +251,45 @@ __device__ __forceinline__ void mma_mxf4(uint32_t d, uint64_t a, uint64_t b, uin
         : "memory");
 }
 
+// The same for E4M3 operands: one scale for the instruction's 32 values of K, the byte that the descriptor names.
+__device__ __forceinline__ void mma_mxf8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                         uint32_t accumulate) {
+    asm volatile(
+        "{\n"
+        ".reg .pred p;\n"
+        "setp.ne.b32 p, %6, 0;\n"
+        "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n"
+        "}\n" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void mma_mxf8_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                              uint32_t accumulate) {
+    asm volatile(
+        "{\n"
+        ".reg .pred p;\n"
+        "setp.ne.b32 p, %6, 0;\n"
+        "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n"
+        "}\n" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+}
+
+// 32 rows of 16 bytes in shared memory (512 contiguous bytes) to 4 columns of TMEM, the 32 rows repeated in each
+// quarter of the lanes: the scales of 128 operand rows. Ordered before the same thread's later tcgen05.mma. The pair
+// form copies in both CTAs, each from its own shared memory at the descriptor's offset.
+__device__ __forceinline__ uint64_t scale_atom_desc(uint32_t saddr) {
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);       // start address
+    d |= static_cast<uint64_t>(128u >> 4) << 32;                // 8 rows of 16 bytes to the next 8
+    d |= static_cast<uint64_t>(1u) << 46;                       // descriptor version; no swizzle
+    return d;
+}
+__device__ __forceinline__ void cp_scales(uint32_t taddr, uint64_t desc) {
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+__device__ __forceinline__ void cp_scales_pair(uint32_t taddr, uint64_t desc) {
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+
 // CTA-pair forms (issued by the pair's even CTA): M = 256, A rows 0..127 and
 // B rows (N columns) 0..N/2-1 in this CTA's shared memory, the other halves at
 // the same offsets in the peer's; D rows 0..127 in this CTA's TMEM, 128..255
