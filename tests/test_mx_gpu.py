@@ -162,13 +162,33 @@ def test_linear_types(code, dtype, out_dtype, M, N, K):
 
 
 @pytest.mark.parametrize("config", ["256,1", "128,1", "256,2", "128,2", "128,3", "pair,256,1", "pair,128,1", "pair,256,2", "pair,128,2",
-                                    "pair,256,3", "pair,128,4"])
+                                    "pair,128,3", "256,1,4", "pair,256,1,4", "pair,128,2,4"])
 @pytest.mark.parametrize("code", CODES)
 def test_linear_every_shape_of_tiles(code, config, monkeypatch):
     monkeypatch.setenv("BT_MX_CONFIG", config)
     for M, N, K in [(1, 1, 1), (300, 517, 777), (515, 1290, 2300), (1500, 2600, 1300)]:
         check_linear(M, N, K, code, out_dtype=F32)
     check_linear(4000, 5000, 520, code)                     # several tiles a CTA
+
+
+@pytest.mark.parametrize("split", [1, 2, 4, 8])
+@pytest.mark.parametrize("code", CODES)
+def test_linear_few_rows_every_split(code, split, monkeypatch):
+    monkeypatch.setenv("BT_MX_CONFIG", f"small,{split}")
+    for M, N, K in [(1, 1, 1), (1, 300, 2000), (7, 129, 1300), (16, 260, 4100), (17, 100, 3333), (32, 513, 2560), (31, 128, 9000)]:
+        for packed in (False, True):
+            check_linear(M, N, K, code, F32, F32, packed=packed)
+            check_linear(M, N, K, code, F16, BF16, packed=packed)
+
+
+@pytest.mark.parametrize("code", CODES)
+def test_linear_few_rows_of_strided_x(code):
+    for M, K, ld, skip in [(3, 1000, 1003, 1), (20, 257, 300, 4), (32, 512, 513, 0)]:
+        for dtype in (F32, BF16, F16):
+            buf = torch.randn(M * ld + skip).to(dtype).cuda()
+            x = buf[skip:].as_strided((M, K), (ld, 1))
+            wq = bt.bt_mx_quantize(torch.randn(200, K).cuda(), code)
+            assert torch.equal(bt.bt_mx_linear(x, wq, out_dtype=F32), bt.bt_mx_linear(bt.bt_mx_quantize(x, code), wq, out_dtype=F32))
 
 
 @pytest.mark.parametrize("code", CODES)

@@ -7,20 +7,20 @@
 // X and of all the tile's rows of W.
 //   warp 0 lane 0   TMA: stages of D 128-byte slices of K, operands (128-byte
 //                   swizzle) and atoms of scales
-//   warp 1 lane 0   scales of a slice to TMEM (tcgen05.cp), its four MMAs
-//   warps 2..9      epilogue: two a TMEM lane quarter, 32 columns at a time, through
+//   warp 1          scales of a slice to TMEM (tcgen05.cp), its four MMAs
+//   warps 2..9      epilogue: two (or one) a TMEM lane quarter, 32 columns at a time, through
 //                   shared memory so that whole row pieces are stored
-// TMEM: two accumulators and 32 columns of scales. At BN = 256 the accumulators
-// share 32 columns: a tile's epilogue takes those first, and the next tile's MMAs
-// begin when they are free.
+// TMEM: two accumulators and two times 32 columns of scales. At BN = 256 the
+// accumulators share 64 columns: a tile's epilogue takes those first, and the next
+// tile's MMAs begin when they are free.
+// Copies of scales and MMAs run in order, so that scales need no barrier; two sets of
+// columns in turn cost nothing.
 // Every wait is bounded, as in the other tensor-core kernels.
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
 
-#include "bt_internal.h"
-#include "mx.cuh"
-#include "tc_ptx.cuh"
+#include "mx_linear.cuh"
 
 namespace bt {
 namespace {
@@ -29,17 +29,15 @@ using namespace mx;
 
 constexpr int kBM = 128;
 constexpr int kRowB = 128;
-constexpr int kEpiWarps = 8;
+constexpr int kEpiWarps = 8;                    // at most
 constexpr int kThreads = 64 + 32 * kEpiWarps;
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kSfCol = 480;                // 32 columns: at most 2 atoms x (4 of X + 8 of W)
-constexpr int kSmemMax = 232448;
+constexpr uint32_t kSfCol = 448;                // two times 32 columns: at most 2 atoms x (4 of X + 8 of W)
 constexpr int kReserve = 1024 + 256;            // alignment, barriers
 constexpr int kMaxStages = 8;
-__host__ __device__ constexpr int staging_bytes(int elem) { return kEpiWarps * 32 * 32 * elem; }
-__host__ __device__ constexpr int atoms_a_slice(int code) { return code == BT_CODE_E2M1 ? 2 : 1; }
+__host__ __device__ constexpr int staging_bytes(int elem, int epi) { return epi * 32 * 32 * elem; }
 // Rows of W that a CTA brings.
-__host__ __device__ __forceinline__ int b_rows(int bn, bool pair) { return pair ? bn / 2 : bn; }
+__host__ __device__ constexpr int b_rows(int bn, bool pair) { return pair ? bn / 2 : bn; }
 __host__ __device__ __forceinline__ int slice_bytes(int code, int bn, bool pair) {
     return (kBM + b_rows(bn, pair)) * kRowB + atoms_a_slice(code) * (1 + bn / 128) * kAtomBytes;
 }
@@ -47,20 +45,13 @@ __host__ __device__ __forceinline__ int slice_bytes(int code, int bn, bool pair)
 struct MxArgs {
     int64_t M, N, ldo;
     int slices, d, nk, stages;                  // slices of K, of a stage; stages of a tile, of the ring
-    int bn, num_n, num_tiles;
+    int bn, num_n, num_tiles, epi;              // epi: epilogue warps, 4 or 8
     uint32_t idesc;
     void *out;
     int vec;                                    // out's rows start at 16-byte multiples and N is a whole number of 16 bytes
     unsigned int *err;
     unsigned long long wait_ns;
 };
-
-// D = F32, K-major, UE8M0 scales; `id`: the byte of its 32-bit columns that an MMA's scales lie in (from) for X and W.
-uint32_t make_idesc(int code, int m, int bn) {
-    const uint32_t mn = ((static_cast<uint32_t>(bn) >> 3) << 17) | ((static_cast<uint32_t>(m) >> 7) << 27) | (1u << 23);
-    return code == BT_CODE_E2M1 ? mn | (1u << 7) | (1u << 10) : mn;
-}
-__device__ __forceinline__ uint32_t with_id(uint32_t idesc, uint32_t id) { return idesc | (id << 4) | (id << 29); }
 
 template <typename T> __device__ __forceinline__ uint4 chunk16(const uint32_t (&r)[32], int j0) {
     if constexpr (sizeof(T) == 4) {
@@ -77,16 +68,18 @@ template <int ELEM> __device__ __forceinline__ uint32_t box_chunk(int q, int row
     return ELEM == 4 ? static_cast<uint32_t>(q ^ (row & 7)) : static_cast<uint32_t>(q ^ ((row >> 1) & 3));
 }
 
-template <int CODE, typename T, bool PAIR>
+template <int CODE, typename T, bool PAIR, int BN>
 __global__ void __launch_bounds__(kThreads, 1)
 mx_linear_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                  const __grid_constant__ CUtensorMap tmSa, const __grid_constant__ CUtensorMap tmSb, const MxArgs a) {
     constexpr int kElem = sizeof(T);
     constexpr int kBoxInner = 32 * kElem;
     constexpr int kAtoms = atoms_a_slice(CODE);
+    constexpr bool kE2M1 = CODE == BT_CODE_E2M1;
     constexpr uint32_t kASlice = kBM * kRowB;
-    const int S = a.stages, bn = a.bn, D = a.d;
-    const uint32_t kBSlice = static_cast<uint32_t>(b_rows(bn, PAIR) * kRowB);
+    constexpr int bn = BN;
+    const int S = a.stages, D = a.d;
+    constexpr uint32_t kBSlice = static_cast<uint32_t>(b_rows(bn, PAIR) * kRowB);
     const uint32_t kSaStage = static_cast<uint32_t>(kAtoms * D * kAtomBytes), kSbStage = kSaStage * static_cast<uint32_t>(bn / 128);
 
     extern __shared__ uint8_t smem_raw[];
@@ -94,7 +87,7 @@ mx_linear_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
     const uint32_t sA = (raw + 1023u) & ~1023u, sB = sA + S * kASlice * D;
     const uint32_t sSa = sB + S * kBSlice * D, sSb = sSa + S * kSaStage;
     const uint32_t sStage = sSb + S * kSbStage;
-    const uint32_t bars = sStage + staging_bytes(kElem);
+    const uint32_t bars = sStage + staging_bytes(kElem, a.epi);
     uint8_t *gbars = smem_raw + (bars - raw);
     volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(gbars + 8 * (2 * kMaxStages + 6));
     volatile uint32_t *abort_flag = tmem_slot + 1;
@@ -105,21 +98,20 @@ mx_linear_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
     const uint32_t shared_read = bars + 8u * (2 * kMaxStages + 4);              // a tile's shared columns read
     const uint32_t drain = bars + 8u * (2 * kMaxStages + 5);
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t crank = PAIR ? tc::cluster_ctarank() : 0u;
+    const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+    const uint32_t crank = PAIR ? __shfl_sync(0xFFFFFFFFu, tc::cluster_ctarank(), 0) : 0u;
     const bool leader = !PAIR || crank == 0;
 
     if (threadIdx.x == 0) {
-        pdl_launch_dependents();
         for (int s = 0; s < S; ++s) {
             tc::mbar_init(full(s), 1);
             tc::mbar_init(empty(s), 1);
         }
         for (int b = 0; b < 2; ++b) {
             tc::mbar_init(tfull(b), 1);
-            tc::mbar_init(tempty(b), (PAIR ? 2 : 1) * kEpiWarps);
+            tc::mbar_init(tempty(b), (PAIR ? 2 : 1) * a.epi);
         }
-        tc::mbar_init(shared_read, (PAIR ? 2 : 1) * 4);     // one warp of each lane quarter
+        tc::mbar_init(shared_read, (PAIR ? 2 : 1) * a.epi);
         tc::mbar_init(drain, 1);
         *abort_flag = 0u;
         tc::fence_mbar_init();
@@ -128,6 +120,9 @@ mx_linear_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
         tc::prefetch_map(&tmSa);
         tc::prefetch_map(&tmSb);
     }
+    // Tensor memory is taken after the grids before this one have ended and before the next may begin: none waits for
+    // columns that are held by one that waits for it.
+    pdl_wait();
     if (warp == 1) {
         if (PAIR) {
             tc::tmem_alloc_pair(smem_u32(const_cast<uint32_t *>(tmem_slot)), kTmemCols);
@@ -141,18 +136,18 @@ mx_linear_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
     __syncthreads();
     if (PAIR) tc::cluster_sync();
     tc::fence_after_sync();
-    const uint32_t tmem = *tmem_slot;
-    const bool shared = bn == 256;                          // the accumulators overlap
-    auto acc_col = [&](int buf) { return static_cast<uint32_t>(buf) * (shared ? 224u : 256u); };
+    if (threadIdx.x == 0) pdl_launch_dependents();
+    const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *tmem_slot, 0);
+    constexpr bool shared = bn == 256;                      // the accumulators overlap
+    auto acc_col = [&](int buf) { return static_cast<uint32_t>(buf) * (shared ? 192u : 256u); };
 
-    const int unit = PAIR ? static_cast<int>(tc::cluster_id_x()) : static_cast<int>(blockIdx.x);
-    const int nunits = PAIR ? static_cast<int>(tc::num_clusters_x()) : static_cast<int>(gridDim.x);
+    const int unit = PAIR ? static_cast<int>(blockIdx.x >> 1) : static_cast<int>(blockIdx.x);
+    const int nunits = PAIR ? static_cast<int>(gridDim.x >> 1) : static_cast<int>(gridDim.x);
     const int tile_rows = PAIR ? 2 * kBM : kBM;
     auto slice_count = [&](int kb) { return a.slices - kb * D < D ? a.slices - kb * D : D; };
 
     if (warp == 0) {
         if (lane == 0) {
-            pdl_wait();
             const uint32_t bytes = static_cast<uint32_t>((PAIR ? 2 : 1) * D) * ((kASlice + kBSlice) + static_cast<uint32_t>(kAtoms * (1 + bn / 128) * kAtomBytes));
             int s = 0;
             uint32_t ph = 0, last_phase[kMaxStages];
@@ -184,80 +179,76 @@ mx_linear_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                     if (++s == S) { s = 0; ph ^= 1u; }
                 }
             }
-            if (!ok && leader) {
-                // let what was asked for land before shared memory is given back
+            // whatever happens elsewhere, what was asked for (a pair's: on the even CTA's barriers) lands before shared
+            // memory is given back
+            if (leader) {
                 for (int i = 0; i < S; ++i) {
-                    if (last_phase[i] < 2u) {
-                        const unsigned long long t0 = globaltimer_ns();
-                        while (!tc::mbar_try_wait(full(i), last_phase[i]) && globaltimer_ns() - t0 < kWaitNs) {}
-                    }
+                    uint32_t never = 0;
+                    if (last_phase[i] < 2u) tc::wait_bounded(full(i), last_phase[i], &never, a.err);
                 }
             }
         }
         __syncwarp();
     } else if (warp == 1) {
-        if (lane == 0 && leader) {
+        if (leader) {
+            const uint32_t me = tc::elect_one();
+            // the low words of the descriptors: one addition an instruction
+            const uint64_t op0 = tc::sw128_kmajor_desc(0), sf0 = tc::scale_atom_desc(0);
+            auto desc = [](uint64_t d, uint32_t at) { return d + at; };
+            auto copy_sf = [&](uint32_t col, uint32_t at) { tc::cp_scales<PAIR>(me, col, desc(sf0, at)); };
+            uint32_t id[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) id[k] = with_id(a.idesc, CODE == BT_CODE_E2M1 ? 2 * (k & 1) : k);
             int s = 0, local = 0;
-            uint32_t ph = 0;
+            uint32_t ph = 0, turn = 0;
             bool ok = true;
             for (int tl = unit; tl < a.num_tiles && ok; tl += nunits, ++local) {
                 const int buf = local & 1;
-                if (local >= 2 && !tc::wait_fast(tempty(buf), static_cast<uint32_t>((local - 2) >> 1) & 1u, abort_flag, a.err, a.wait_ns)) break;
-                if (shared && local >= 1 && !tc::wait_fast(shared_read, static_cast<uint32_t>(local - 1) & 1u, abort_flag, a.err, a.wait_ns)) break;
+                if (local >= 2 && !tc::wait_warp(tempty(buf), static_cast<uint32_t>((local - 2) >> 1) & 1u, abort_flag, a.err, a.wait_ns)) break;
+                if (shared && local >= 1 && !tc::wait_warp(shared_read, static_cast<uint32_t>(local - 1) & 1u, abort_flag, a.err, a.wait_ns)) break;
                 tc::fence_after_sync();
                 const uint32_t acc = tmem + acc_col(buf);
                 for (int kb = 0; kb < a.nk; ++kb) {
-                    if (!tc::wait_fast(full(s), ph, abort_flag, a.err, a.wait_ns)) { ok = false; break; }
+                    if (!tc::wait_warp(full(s), ph, abort_flag, a.err, a.wait_ns)) { ok = false; break; }
                     tc::fence_after_sync();
                     const int cnt = slice_count(kb);
-                    const uint32_t ad = sA + s * kASlice * D, bd = sB + s * kBSlice * D, sa = sSa + s * kSaStage, sb = sSb + s * kSbStage;
+                    uint32_t la = (sA + s * kASlice * D) >> 4, lb = (sB + s * kBSlice * D) >> 4;
+                    uint32_t lsa = (sSa + s * kSaStage) >> 4, lsb = (sSb + s * kSbStage) >> 4;
+                    const uint32_t next = static_cast<uint32_t>(kAtoms * D * kAtomBytes / 16);      // the other 128 rows of W
                     for (int i = 0; i < cnt; ++i) {
                         // the slice's scales: X's 128 rows 4 columns an atom, then W's bn rows 8 (4)
-                        const uint32_t sfa = tmem + kSfCol, sfb = sfa + 4 * kAtoms;
+                        const uint32_t sfa = tmem + kSfCol + (turn ^= 32u), sfb = sfa + 4 * kAtoms;
 #pragma unroll
                         for (int j = 0; j < kAtoms; ++j) {
-                            const uint64_t da = tc::scale_atom_desc(sa + (i * kAtoms + j) * kAtomBytes);
-                            if (PAIR) tc::cp_scales_pair(sfa + 4 * j, da);
-                            else tc::cp_scales(sfa + 4 * j, da);
-                            for (int h = 0; h < bn / 128; ++h) {
-                                const uint64_t db = tc::scale_atom_desc(sb + (h * kAtoms * D + i * kAtoms + j) * kAtomBytes);
-                                if (PAIR) tc::cp_scales_pair(sfb + 8 * j + 4 * h, db);
-                                else tc::cp_scales(sfb + 8 * j + 4 * h, db);
-                            }
+                            copy_sf(sfa + 4 * j, lsa + 32 * j);
+                            copy_sf(sfb + 8 * j, lsb + 32 * j);
+                            if (bn == 256) copy_sf(sfb + 8 * j + 4, lsb + next + 32 * j);
                         }
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk) {
-                            const uint64_t da = tc::sw128_kmajor_desc(ad + i * kASlice + kk * 32);
-                            const uint64_t db = tc::sw128_kmajor_desc(bd + i * kBSlice + kk * 32);
-                            const uint32_t more = (kb | i | kk) != 0 ? 1u : 0u;
-                            if constexpr (CODE == BT_CODE_E2M1) {       // 64 values: two bytes, from 0 or 2
-                                const uint32_t id = with_id(a.idesc, (kk & 1) * 2), fa = sfa + 4 * (kk >> 1), fb = sfb + 8 * (kk >> 1);
-                                if (PAIR) tc::mma_mxf4_pair(acc, da, db, id, fa, fb, more);
-                                else tc::mma_mxf4(acc, da, db, id, fa, fb, more);
-                            } else {                                    // 32 values: byte kk
-                                const uint32_t id = with_id(a.idesc, kk);
-                                if (PAIR) tc::mma_mxf8_pair(acc, da, db, id, sfa, sfb, more);
-                                else tc::mma_mxf8(acc, da, db, id, sfa, sfb, more);
-                            }
+                            const uint32_t more = kk != 0 || (kb | i) != 0 ? 1u : 0u;
+                            // E2M1: 64 values, two bytes from 0 or 2 of one of two columns; E4M3: 32 values, byte kk
+                            const uint32_t fa = kE2M1 ? sfa + 4 * (kk >> 1) : sfa, fb = kE2M1 ? sfb + 8 * (kk >> 1) : sfb;
+                            tc::mma_scaled<kE2M1, PAIR>(me, acc, desc(op0, la + 2 * kk), desc(op0, lb + 2 * kk), id[kE2M1 ? kk & 1 : kk], fa, fb, more);
                         }
+                        la += kASlice / 16;
+                        lb += kBSlice / 16;
+                        lsa += 32 * kAtoms;
+                        lsb += 32 * kAtoms;
                     }
-                    if (PAIR) tc::mma_commit_pair(empty(s), 0x3);
-                    else tc::mma_commit(empty(s));
+                    tc::commit_warp<PAIR>(me, empty(s), 0x3);
                     if (++s == S) { s = 0; ph ^= 1u; }
                 }
                 if (ok) {
-                    if (PAIR) tc::mma_commit_pair(tfull(buf), 0x3);
-                    else tc::mma_commit(tfull(buf));
+                    tc::commit_warp<PAIR>(me, tfull(buf), 0x3);
                 }
             }
-            if (PAIR) tc::mma_commit_pair(drain, 0x1);
-            else tc::mma_commit(drain);
+            tc::commit_warp<PAIR>(me, drain, 0x1);
             const unsigned long long t0 = globaltimer_ns();
             while (!tc::mbar_try_wait(drain, 0u) && globaltimer_ns() - t0 < kWaitNs) {}
         }
         __syncwarp();
     } else {
-        pdl_wait();                                         // the previous kernel may still use `out`
         const int quarter = warp & 3, half = (warp - 2) >> 2;
         const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
         const uint32_t sbox = sStage + static_cast<uint32_t>((warp - 2) * 32 * kBoxInner);
@@ -273,7 +264,8 @@ mx_linear_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
             tc::fence_after_sync();
             const uint32_t tbase = tmem + lane_base + acc_col(buf);
             // accumulator 0 backwards, 1 forwards: the columns that they share come first
-            auto box_of = [&](int j) { return buf == 0 ? boxes - 1 - half - 2 * j : half + 2 * j; };
+            const int per = a.epi / 4, steps = boxes / per;
+            auto box_of = [&](int j) { return buf == 0 ? boxes - 1 - half - per * j : half + per * j; };
             auto give = [&](uint32_t bar) {
                 tc::fence_before_sync();
                 __syncwarp();
@@ -282,7 +274,6 @@ mx_linear_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                     else tc::mbar_arrive(bar);
                 }
             };
-            const int steps = boxes / 2;
             auto emit = [&](const uint32_t (&r)[32], int box) {
                 constexpr int kChunks = kBoxInner / 16;
                 const int64_t c0 = n0 + 32 * box, cend = n0 + ncols;
@@ -332,16 +323,23 @@ mx_linear_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                     }
                 }
             };
-            uint32_t r[2][32];
-            if (box_of(0) < live) tc::tmem_ld32(tbase + 32 * box_of(0), r[0]);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                if (j >= steps) break;
-                tc::tmem_ld_wait();
-                if (j == 0 && half == 0) give(shared_read); // this warp's first box is the shared one
-                if (j + 1 < steps && box_of(j + 1) < live) tc::tmem_ld32(tbase + 32 * box_of(j + 1), r[(j + 1) & 1]);
-                if (j + 1 == steps) give(tempty(buf));
-                if (box_of(j) < live) emit(r[j & 1], box_of(j));
+            uint32_t r0[32], r1[32];
+            if (box_of(0) < live) tc::tmem_ld32(tbase + 32 * box_of(0), r0);
+            if (box_of(1) < live) tc::tmem_ld32(tbase + 32 * box_of(1), r1);
+            tc::tmem_ld_wait();
+            give(shared_read);                              // two boxes a warp hold all that is shared
+            if (steps == 2) give(tempty(buf));
+#pragma unroll 1
+            for (int j = 0; j < steps; j += 2) {
+                if (j > 0) tc::tmem_ld_wait();              // box j + 1
+                if (j > 0 && j + 2 == steps) give(tempty(buf));
+                if (box_of(j) < live) emit(r0, box_of(j));
+                if (j + 2 < steps && box_of(j + 2) < live) tc::tmem_ld32(tbase + 32 * box_of(j + 2), r0);
+                if (box_of(j + 1) < live) emit(r1, box_of(j + 1));
+                if (j + 2 < steps) {
+                    tc::tmem_ld_wait();
+                    if (box_of(j + 3) < live) tc::tmem_ld32(tbase + 32 * box_of(j + 3), r1);
+                }
             }
         }
     }
@@ -360,65 +358,72 @@ mx_linear_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
 // host side
 // ---------------------------------------------------------------------------
 
-// Codes [rows, slices * 128 bytes] as {128, rows, slices}: one copy brings d slices of `box_rows` rows.
-bool map_codes(CUtensorMap *m, const void *p, int64_t rows, int64_t slices, int box_rows, int d) {
-    auto fn = tensor_map_encoder();
-    if (fn == nullptr) return false;
-    cuuint64_t dims[3] = {kRowB, static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(slices)};
-    cuuint64_t strides[2] = {static_cast<cuuint64_t>(slices) * kRowB, kRowB};
-    cuuint32_t box[3] = {kRowB, static_cast<cuuint32_t>(box_rows), static_cast<cuuint32_t>(d)};
-    cuuint32_t one[3] = {1, 1, 1};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(p), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-// Scales as words {128 (an atom), atoms of a row, rows / 128}: `box_atoms` of `box_rows` 128-row groups.
-bool map_scales(CUtensorMap *m, const void *p, int64_t rows, int64_t atoms, int box_rows, int box_atoms) {
-    auto fn = tensor_map_encoder();
-    if (fn == nullptr) return false;
-    cuuint64_t dims[3] = {kAtomBytes / 4, static_cast<cuuint64_t>(atoms), static_cast<cuuint64_t>((rows + 127) / 128)};
-    cuuint64_t strides[2] = {kAtomBytes, static_cast<cuuint64_t>(atoms) * kAtomBytes};
-    cuuint32_t box[3] = {kAtomBytes / 4, static_cast<cuuint32_t>(box_atoms), static_cast<cuuint32_t>(box_rows)};
-    cuuint32_t one[3] = {1, 1, 1};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, const_cast<void *>(p), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-struct Product {
-    const uint8_t *x, *xs, *w, *ws;
-    bt_code code;
-    int64_t M, N, K;
-    void *out;
-    int64_t ldo;
-    bt_dtype out_t;
-    unsigned int *err;
-};
-
+// How a product is cut: rows of a tile (256 on a pair of CTAs, else 128), its columns, slices a stage, epilogue warps.
 struct Shape {
     bool pair;
-    int bn, d;
+    int bn, d, epi;
 };
 int num_stages(int code, const Shape &sh, int elem) {
-    const int n = (kSmemMax - kReserve - staging_bytes(elem)) / (slice_bytes(code, sh.bn, sh.pair) * sh.d);
+    const int n = (kSmemMax - kReserve - staging_bytes(elem, sh.epi)) / (slice_bytes(code, sh.bn, sh.pair) * sh.d);
     return n > kMaxStages ? kMaxStages : n;
 }
-Shape choose(const Product &p) {
-    if (const char *e = std::getenv("BT_MX_CONFIG")) {      // "pair,bn,d" or "bn,d"
-        int bn = 0, d = 0;
-        const bool pair = std::strncmp(e, "pair,", 5) == 0;
-        if (std::sscanf(pair ? e + 5 : e, "%d,%d", &bn, &d) == 2 && (bn == 128 || bn == 256) && d >= 1 && d <= 4 &&
-            num_stages(p.code, Shape{pair, bn, d}, dtype_bytes(p.out_t)) >= 2)
-            return Shape{pair, bn, d};
-    }
-    return Shape{false, 256, 1};
+
+// Whether few rows go through mx_small.cu. One row to 32 against tiles of 128: see there.
+bool takes_small(int64_t M) {
+    if (const char *e = std::getenv("BT_MX_CONFIG")) return std::strncmp(e, "small", 5) == 0 && M <= kSmallRows;
+    return M <= kSmallRows;
 }
 
-template <int CODE, typename T, bool PAIR> cudaError_t launch(const Product &p, const Shape &sh, cudaStream_t s) {
+// The fastest of four shapes by a model of their times in ns, fitted on GB300 (E2M1 and E4M3, 128 to 8192 rows): a slice of
+// K, what a tile costs beside its slices, the epilogue (which the next tile's MMAs overlap), the launch. Model and measured,
+// us: 8192 x 4096 x 11008 E2M1 pairs of 256 columns 107 and 102 (single CTAs 120 and 113, pairs of 128 133 and 131); 4096^3
+// pairs of 128 29.7 and 29.8 (30.0 and 32.3; 30.2 and 31.0); 1024 x 4096 x 4096 single CTAs of 256 9.7 and 8.8 (11.7 and
+// 11.7 with 128); 256 x 4096 x 4096 single CTAs of 128 7.3 and 7.2; 8192 x 11008 x 512 single CTAs of 256 42 and 39.5
+// (pairs 61). Two slices a stage at 128 columns halve what a stage costs its issuer (162 and 182 us), at 256 they leave too
+// few stages. BT_MX_CONFIG="[pair,]columns,slices[,epilogue warps]" or "small[,split]" in the environment decides instead.
+struct Timing {
+    bool pair;
+    int bn, d;
+    double slice, tile, epilogue, launch;
+};
+constexpr Timing kTimings[] = {{true, 256, 1, 310, 1300, 3200, 5000}, {false, 256, 1, 347, 1300, 2080, 2800},
+                               {true, 128, 2, 213, 200, 2190, 4500},  {false, 128, 2, 265, 200, 1090, 2900}};
+Shape choose(const Product &p) {
+    const int elem = dtype_bytes(p.out_t);
+    if (const char *e = std::getenv("BT_MX_CONFIG")) {
+        int bn = 0, d = 0, epi = 8;
+        const bool pair = std::strncmp(e, "pair,", 5) == 0;
+        if (std::sscanf(pair ? e + 5 : e, "%d,%d,%d", &bn, &d, &epi) >= 2 && (bn == 128 || bn == 256) && d >= 1 && d <= 4 && (epi == 4 || epi == 8) &&
+            num_stages(p.code, Shape{pair, bn, d, epi}, elem) >= 2)
+            return Shape{pair, bn, d, epi};
+    }
+    const bool wide = aligned(p.out, 16) && (p.ldo * elem) % 16 == 0 && (p.N * elem) % 16 == 0;
+    const int64_t k = slices(p.K, p.code), sms = device_sm_count();
+    Shape best = {};
+    double least = -1.0;
+    for (const Timing &t : kTimings) {
+        const int rows = t.pair ? 2 * kBM : kBM;
+        const int64_t tiles = ((p.M + rows - 1) / rows) * ((p.N + t.bn - 1) / t.bn), units = t.pair ? sms / 2 : sms;
+        const double main = static_cast<double>(k) * t.slice + t.tile, epi = t.epilogue * (elem == 4 ? 1.7 : 1.0) * (wide ? 1.0 : 1.5);
+        const double us = static_cast<double>((tiles + units - 1) / units) * (main > epi ? main : epi) + t.launch;
+        if (least < 0.0 || us < least) {
+            least = us;
+            best = Shape{t.pair, t.bn, t.d, 8};
+        }
+    }
+    // four epilogue warps make room for a sixth stage (8192 x 4096 x 11008 E2M1 102.6 -> 99.4 us) where a tile is long enough to hide them
+    if (best.pair && best.bn == 256 && p.code == BT_CODE_E2M1 && k >= 24 && wide && elem == 2) best.epi = 4;
+    return best;
+}
+
+template <int CODE, typename T, bool PAIR, int BN> cudaError_t launch(const Product &p, const Shape &sh, cudaStream_t s) {
     MxArgs a = {};
     a.M = p.M; a.N = p.N; a.ldo = p.ldo;
     a.slices = static_cast<int>(slices(p.K, CODE));
     a.d = sh.d;
     a.nk = (a.slices + a.d - 1) / a.d;
     a.bn = sh.bn;
+    a.epi = sh.epi;
     const int rows = PAIR ? 2 * kBM : kBM, elem = sizeof(T);
     const int64_t num_m = (p.M + rows - 1) / rows, num_n = (p.N + a.bn - 1) / a.bn;
     if (num_m * num_n > (int64_t(1) << 30)) return cudaErrorInvalidValue;
@@ -432,14 +437,14 @@ template <int CODE, typename T, bool PAIR> cudaError_t launch(const Product &p, 
     const int stage = slice_bytes(CODE, a.bn, PAIR) * a.d;
     a.stages = num_stages(CODE, sh, elem);
     if (a.stages < 2) return cudaErrorInvalidValue;
-    const int smem = a.stages * stage + staging_bytes(elem) + kReserve;
+    const int smem = a.stages * stage + staging_bytes(elem, a.epi) + kReserve;
     CUtensorMap ma, mb, sa, sb;
     const int64_t atoms = k_atoms(p.K, CODE);
     const int step = a.d * atoms_a_slice(CODE);
     if (!map_codes(&ma, p.x, p.M, a.slices, kBM, a.d) || !map_codes(&mb, p.w, p.N, a.slices, b_rows(a.bn, PAIR), a.d) ||
         !map_scales(&sa, p.xs, p.M, atoms, 1, step) || !map_scales(&sb, p.ws, p.N, atoms, a.bn / 128, step))
         return cudaErrorInvalidValue;
-    auto kern = mx_linear_kernel<CODE, T, PAIR>;
+    auto kern = mx_linear_kernel<CODE, T, PAIR, BN>;
     static ContextOnce once;
     if (const cudaError_t e = allow_smem(kern, kSmemMax, once); e != cudaSuccess) return e;
     int units = device_sm_count() / (PAIR ? 2 : 1);
@@ -451,19 +456,30 @@ template <int CODE, typename T, bool PAIR> cudaError_t launch(const Product &p, 
     attr[1].val.clusterDim.x = PAIR ? 2 : 1;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.gridDim = dim3(static_cast<unsigned>(units * (PAIR ? 2 : 1)));
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(static_cast<unsigned>(64 + 32 * a.epi));
     cfg.dynamicSmemBytes = static_cast<size_t>(smem);
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = PAIR ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kern, ma, mb, sa, sb, static_cast<const MxArgs>(a));
 }
+template <int CODE, typename T> cudaError_t launch_shape(const Product &p, const Shape &sh, cudaStream_t s) {
+    if (sh.bn == 256) return sh.pair ? launch<CODE, T, true, 256>(p, sh, s) : launch<CODE, T, false, 256>(p, sh, s);
+    return sh.pair ? launch<CODE, T, true, 128>(p, sh, s) : launch<CODE, T, false, 128>(p, sh, s);
+}
 template <int CODE> cudaError_t launch_out(const Product &p, const Shape &sh, cudaStream_t s) {
-    if (p.out_t == BT_F32) return sh.pair ? launch<CODE, float, true>(p, sh, s) : launch<CODE, float, false>(p, sh, s);
-    if (p.out_t == BT_BF16) return sh.pair ? launch<CODE, __nv_bfloat16, true>(p, sh, s) : launch<CODE, __nv_bfloat16, false>(p, sh, s);
-    return sh.pair ? launch<CODE, __half, true>(p, sh, s) : launch<CODE, __half, false>(p, sh, s);
+    if (p.out_t == BT_F32) return launch_shape<CODE, float>(p, sh, s);
+    if (p.out_t == BT_BF16) return launch_shape<CODE, __nv_bfloat16>(p, sh, s);
+    return launch_shape<CODE, __half>(p, sh, s);
 }
 cudaError_t product(const Product &p, cudaStream_t s) {
+    if (takes_small(p.M)) {
+        int split = 0;
+        if (const char *e = std::getenv("BT_MX_CONFIG")) {
+            if (std::sscanf(e, "small,%d", &split) != 1 || (split != 1 && split != 2 && split != 4 && split != 8)) split = 0;
+        }
+        return launch_small(p, split, s);
+    }
     const Shape sh = choose(p);
     return p.code == BT_CODE_E2M1 ? launch_out<BT_CODE_E2M1>(p, sh, s) : launch_out<BT_CODE_E4M3>(p, sh, s);
 }
@@ -493,7 +509,7 @@ using namespace bt::mx;
 extern "C" {
 
 size_t bt_mx_linear_workspace(int64_t M, int64_t N, int64_t K, bt_dtype x_dtype, bt_code code) {
-    if (!float_type(x_dtype) || mx_sides(M, K, code) != BT_OK || M < 1 || N < 1) return 0;
+    if (!float_type(x_dtype) || mx_sides(M, K, code) != BT_OK || M < 1 || N < 1 || takes_small(M)) return 0;
     return codes_room(M, K, code) + round_up256(scale_bytes(M, K, code));
 }
 
@@ -520,13 +536,16 @@ bt_status bt_mx_linear(const void *x, bt_dtype x_dtype, int64_t ldx, const void 
     p.err = device_error_word();
     if (p.err == nullptr) return BT_ERR_CUDA;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    p.x = static_cast<const uint8_t *>(x);
+    p.x = x;
+    p.x_t = x_dtype;
+    p.ldx = ldx;
     p.xs = static_cast<const uint8_t *>(x_scales);
-    if (!packed) {
+    if (need > 0) {
         uint8_t *q = static_cast<uint8_t *>(workspace), *sc = q + codes_room(M, K, code);
         if (launch_mx_quantize(x, x_dtype, ldx, M, K, code, q, sc, s) != cudaSuccess) return BT_ERR_CUDA;
         p.x = q;
         p.xs = sc;
+        p.x_t = BT_PACKED;
     }
     p.w = static_cast<const uint8_t *>(w);
     p.ws = static_cast<const uint8_t *>(w_scales);

@@ -568,9 +568,9 @@ bt_status bt_rms_norm(const void *x, bt_dtype dtype, int64_t ldx, const void *re
     if (ldx < N || (res && ldr < N) || (sum != nullptr && lds < N) || (out != nullptr && ldo < N)) return BT_ERR_INVALID_ARG;
     const int64_t far = int64_t(1) << 36;
     if (ldx > far || (res && ldr > far) || (sum != nullptr && lds > far) || (out != nullptr && ldo > far)) return BT_ERR_UNSUPPORTED;
+    if (T == 0) return BT_OK;
     if ((sum != nullptr && !res) || (q == nullptr) != (scales == nullptr)) return BT_ERR_INVALID_ARG;
     if (out == nullptr && q == nullptr) return BT_ERR_INVALID_ARG;
-    if (T == 0) return BT_OK;
     if (x == nullptr) return BT_ERR_INVALID_ARG;
     // in place: row for row
     if ((sum != nullptr && sum == x && lds != ldx) || (sum != nullptr && sum == residual && lds != ldr) || (out != nullptr && out == x && ldo != ldx) ||

@@ -251,45 +251,6 @@ __device__ __forceinline__ void mma_mxf4(uint32_t d, uint64_t a, uint64_t b, uin
         : "memory");
 }
 
-// The same for E4M3 operands: one scale for the instruction's 32 values of K, the byte that the descriptor names.
-__device__ __forceinline__ void mma_mxf8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
-                                         uint32_t accumulate) {
-    asm volatile(
-        "{\n"
-        ".reg .pred p;\n"
-        "setp.ne.b32 p, %6, 0;\n"
-        "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n"
-        "}\n" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
-        : "memory");
-}
-__device__ __forceinline__ void mma_mxf8_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
-                                              uint32_t accumulate) {
-    asm volatile(
-        "{\n"
-        ".reg .pred p;\n"
-        "setp.ne.b32 p, %6, 0;\n"
-        "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n"
-        "}\n" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
-        : "memory");
-}
-
-// 32 rows of 16 bytes in shared memory (512 contiguous bytes) to 4 columns of TMEM, the 32 rows repeated in each
-// quarter of the lanes: the scales of 128 operand rows. Ordered before the same thread's later tcgen05.mma. The pair
-// form copies in both CTAs, each from its own shared memory at the descriptor's offset.
-__device__ __forceinline__ uint64_t scale_atom_desc(uint32_t saddr) {
-    uint64_t d = 0;
-    d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);       // start address
-    d |= static_cast<uint64_t>(128u >> 4) << 32;                // 8 rows of 16 bytes to the next 8
-    d |= static_cast<uint64_t>(1u) << 46;                       // descriptor version; no swizzle
-    return d;
-}
-__device__ __forceinline__ void cp_scales(uint32_t taddr, uint64_t desc) {
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
-}
-__device__ __forceinline__ void cp_scales_pair(uint32_t taddr, uint64_t desc) {
-    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
-}
-
 // CTA-pair forms (issued by the pair's even CTA): M = 256, A rows 0..127 and
 // B rows (N columns) 0..N/2-1 in this CTA's shared memory, the other halves at
 // the same offsets in the peer's; D rows 0..127 in this CTA's TMEM, 128..255
@@ -398,6 +359,66 @@ __device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t saddr, uint32_t 
     d |= static_cast<uint64_t>(1u) << 46;                       // descriptor version
     d |= static_cast<uint64_t>(2u) << 61;                       // 128-byte swizzle
     return d;
+}
+
+// ---------------------------------------------------------------------------
+// Forms for a whole converged warp: every lane has the same operands, and one lane, which has `me` set (elect_one),
+// issues. Operands that the compiler can see to be the same in all lanes stay in uniform registers, where these
+// instructions want them; in a branch of one lane each is moved there first, which costs more than the instruction
+// (block-scaled product of 8192 x 4096 x 11008, E2M1: 160 us with the one, 104 with the other).
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t r;
+    asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xFFFFFFFF;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+    return r;
+}
+// wait_fast by all lanes, with one answer.
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile uint32_t *abort_flag, unsigned int *err,
+                                          unsigned long long limit_ns) {
+    return __all_sync(0xFFFFFFFFu, mbar_test_wait(bar, parity)) ||
+           __all_sync(0xFFFFFFFFu, wait_bounded(bar, parity, abort_flag, err, limit_ns));
+}
+// D (fp32, TMEM) (+)= A * B^T on block-scaled operands with scales sfa, sfb in TMEM: E2M1, 64 values of K, two scales a row
+// (the bytes from the descriptor's id on), or E4M3, 32 values, the byte that the id names.
+template <bool E2M1, bool PAIR>
+__device__ __forceinline__ void mma_scaled(uint32_t me, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
+                                           uint32_t sfb, uint32_t accumulate) {
+#define BT_MMA_SCALED(GROUP, KIND)                                                                                   \
+    asm volatile("{\n.reg .pred p, q;\nsetp.ne.b32 p, %6, 0;\nsetp.ne.b32 q, %7, 0;\n"                               \
+                 "@q tcgen05.mma.cta_group::" GROUP ".kind::" KIND " [%0], %1, %2, %3, [%4], [%5], p;\n}\n"          \
+                 ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate), "r"(me)                  \
+                 : "memory")
+    if constexpr (E2M1 && PAIR) BT_MMA_SCALED("2", "mxf4.block_scale.scale_vec::2X");
+    else if constexpr (E2M1) BT_MMA_SCALED("1", "mxf4.block_scale.scale_vec::2X");
+    else if constexpr (PAIR) BT_MMA_SCALED("2", "mxf8f6f4.block_scale.scale_vec::1X");
+    else BT_MMA_SCALED("1", "mxf8f6f4.block_scale.scale_vec::1X");
+#undef BT_MMA_SCALED
+}
+// 32 rows of 16 bytes in shared memory (512 contiguous bytes) to 4 columns of TMEM, the 32 rows repeated in each
+// quarter of the lanes: the scales of 128 operand rows. In order with the same thread's tcgen05.mma. The pair form
+// copies in both CTAs, each from its own shared memory at the descriptor's offset.
+__device__ __forceinline__ uint64_t scale_atom_desc(uint32_t saddr) {
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);       // start address
+    d |= static_cast<uint64_t>(128u >> 4) << 32;                // 8 rows of 16 bytes to the next 8
+    d |= static_cast<uint64_t>(1u) << 46;                       // descriptor version; no swizzle
+    return d;
+}
+template <bool PAIR> __device__ __forceinline__ void cp_scales(uint32_t me, uint32_t taddr, uint64_t desc) {
+    if constexpr (PAIR)
+        asm volatile("{\n.reg .pred q;\nsetp.ne.b32 q, %2, 0;\n@q tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;\n}\n"
+                     ::"r"(taddr), "l"(desc), "r"(me) : "memory");
+    else
+        asm volatile("{\n.reg .pred q;\nsetp.ne.b32 q, %2, 0;\n@q tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n}\n"
+                     ::"r"(taddr), "l"(desc), "r"(me) : "memory");
+}
+// The mbarrier (in every CTA of `mask`, for a pair) gets an arrival when what was issued before has completed.
+template <bool PAIR> __device__ __forceinline__ void commit_warp(uint32_t me, uint32_t bar, uint16_t mask) {
+    if (me) {
+        if (PAIR) mma_commit_pair(bar, mask);
+        else mma_commit(bar);
+    }
+    __syncwarp();
 }
 
 }  // namespace tc
