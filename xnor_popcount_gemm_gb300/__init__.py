@@ -9,8 +9,10 @@ there is no fallback.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import functools
+import operator
 import os
 
 import torch
@@ -581,7 +583,7 @@ def _on_device_of(name: str, at: int):
             if type(t) is AdapterPlan:
                 t = t.buffer
             elif type(t) is MxRows:
-                t = t.codes
+                t = t._tensors()[0]
             elif type(t) in (list, tuple):
                 t = t[0] if t else None
             device = t.get_device() if isinstance(t, torch.Tensor) else -1
@@ -879,6 +881,8 @@ class MxRows:
     """A microscaled operand [R, K]: `codes` uint8 [R, bt_mx_row_bytes(K, code)] and `scales` uint8
     [bt_mx_scale_bytes(R, K, code)] on the device, `code` BT_CODE_E4M3 or BT_CODE_E2M1."""
 
+    __slots__ = ("K", "code", "_rows", "_row", "_codes", "_scales", "_buffer")
+
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor, K: int, code: int):
         row = bt_mx_row_bytes(K, code)
         if row == 0:
@@ -887,15 +891,51 @@ class MxRows:
             raise ValueError(f"codes must be a uint8 CUDA tensor of shape [R, {row}]")
         _contig(codes, "codes")
         _dense(scales, "scales", (bt_mx_scale_bytes(codes.shape[0], K, code),), torch.uint8)
-        self.codes, self.scales, self.K, self.code = codes, scales, K, code
+        self._codes, self._scales, self._buffer, self.K, self.code = codes, scales, None, K, code
+        self._rows, self._row = codes.shape[0], row
+
+    @classmethod
+    def _new(cls, R: int, K: int, code: int, device, stream) -> "MxRows":
+        """One of the library's own: codes, then scales, in one allocation."""
+        if code not in (BT_CODE_E4M3, BT_CODE_E2M1) or not 1 <= K < 1 << 24:
+            raise BtError(BT_ERR_INVALID_ARG)
+        q = cls.__new__(cls)
+        q.K, q.code, q._rows = K, code, R
+        q._row = row = (K + 255) // 256 * 128 if code == BT_CODE_E2M1 else (K + 127) // 128 * 128
+        q._codes = q._scales = None
+        # 512 bytes of scales for 128 rows and 128 values of K
+        q._buffer = _empty((R * row + (R + 127) // 128 * (row * (8 if code == BT_CODE_E2M1 else 4)),), torch.uint8, device, stream)
+        return q
+
+    @property
+    def codes(self) -> torch.Tensor:
+        if self._codes is None:
+            self._codes = self._buffer[:self._rows * self._row].view(self._rows, self._row)
+        return self._codes
+
+    @property
+    def scales(self) -> torch.Tensor:
+        if self._scales is None:
+            self._scales = self._buffer[self._rows * self._row:]
+        return self._scales
 
     @property
     def shape(self) -> tuple[int, int]:
-        return self.codes.shape[0], self.K
+        return self._rows, self.K
 
     @property
     def device(self) -> torch.device:
-        return self.codes.device
+        return self._tensors()[0].device
+
+    def _tensors(self):
+        """What holds its memory."""
+        return (self._codes, self._scales) if self._buffer is None else (self._buffer,)
+
+    def _pointers(self):
+        if self._buffer is None:
+            return self._codes.data_ptr(), self._scales.data_ptr()
+        p = self._buffer.data_ptr()
+        return p, p + self._rows * self._row
 
     def __repr__(self) -> str:
         return f"MxRows({list(self.shape)}, {'E4M3' if self.code == BT_CODE_E4M3 else 'E2M1'}, {self.device})"
@@ -925,14 +965,6 @@ def _mx(q, name: str):
     return q
 
 
-def _new_mx(R: int, K: int, code: int, device, stream) -> MxRows:
-    row = bt_mx_row_bytes(K, code)
-    if row == 0:
-        raise BtError(BT_ERR_INVALID_ARG)
-    return MxRows(_empty((R, row), torch.uint8, device, stream),
-                  _empty((bt_mx_scale_bytes(R, K, code),), torch.uint8, device, stream), K, code)
-
-
 @_on_device_of("x", 0)
 def bt_mx_quantize(x: torch.Tensor, code: int, out: MxRows | None = None, stream=None) -> MxRows:
     """x [R, K] in blocks of 32 along K that share a power of two, as E4M3 or E2M1 values."""
@@ -941,12 +973,11 @@ def bt_mx_quantize(x: torch.Tensor, code: int, out: MxRows | None = None, stream
     if out is not None:
         if _mx(out, "out").shape != (R, K) or out.code != code:
             raise ValueError("out must be MxRows of x's shape and the code")
-        _same_device(x, stream, out.codes, out.scales)
+        _same_device(x, stream, *out._tensors())
     else:
         _same_device(x, stream)
-        out = _new_mx(R, K, code, x.device, stream)
-    _check(_c_mx_q(x.data_ptr(), _DT[x.dtype], ld, R, K, code, out.codes.data_ptr(), out.scales.data_ptr(),
-                   _on_stream(stream, x.device)))
+        out = MxRows._new(R, K, code, x.device, stream)
+    _check(_c_mx_q(x.data_ptr(), _DT[x.dtype], ld, R, K, code, *out._pointers(), _on_stream(stream, x.device)))
     return out
 
 
@@ -954,12 +985,12 @@ def bt_mx_quantize(x: torch.Tensor, code: int, out: MxRows | None = None, stream
 def bt_mx_dequantize(q: MxRows, out_dtype=torch.float32, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """The values [R, K] of an operand in out_dtype."""
     R, K = _mx(q, "q").shape
-    _same_device(q.codes, stream, q.scales, out)
+    first, *others = q._tensors()
+    _same_device(first, stream, *others, out)
     if out is None:
-        out = _empty((R, K), out_dtype, q.device, stream)
+        out = _empty((R, K), out_dtype, first.device, stream)
     ldo = _rows(out, "out", R, K, _FLOATS)
-    _check(_c_mx_dq(q.codes.data_ptr(), q.scales.data_ptr(), R, K, q.code, out.data_ptr(), _DT[out.dtype], ldo,
-                    _on_stream(stream, q.device)))
+    _check(_c_mx_dq(*q._pointers(), R, K, q.code, out.data_ptr(), _DT[out.dtype], ldo, _on_stream(stream, first.device)))
     return out
 
 
@@ -977,23 +1008,23 @@ def bt_mx_linear(x, w: MxRows, out_dtype=None, out: torch.Tensor | None = None, 
     if type(x) is MxRows:
         if x.code != code or x.K != K:
             raise ValueError("x and w must agree on K and the code")
-        M, xt, ldx, xp, xs = x.codes.shape[0], BT_PACKED, K, x.codes, x.scales
-        dt = torch.bfloat16
+        M, xt, ldx, dt = x._rows, BT_PACKED, K, torch.bfloat16
+        first, *others = x._tensors()
+        xp, xs = x._pointers()
     else:
         ldx = _float_rows(x, "x")
         if x.shape[1] != K:
             raise ValueError("x and w must agree on K")
-        M, xt, xp, xs = x.shape[0], _DT[x.dtype], x, None
-        dt = x.dtype
-    _same_device(xp, stream, xs, w.codes, w.scales, out, workspace)
+        M, xt, dt, first, others, xp, xs = x.shape[0], _DT[x.dtype], x.dtype, x, (), x.data_ptr(), None
+    _same_device(first, stream, *others, *w._tensors(), out, workspace)
+    device = first.device
     if out is None:
-        out = _empty((M, N), dt if out_dtype is None else out_dtype, xp.device, stream)
+        out = _empty((M, N), dt if out_dtype is None else out_dtype, device, stream)
     ldo = _rows(out, "out", M, N, _FLOATS if out_dtype is None else (out_dtype,))
     need = _c_mx_lin_ws(M, N, K, xt, code)
-    workspace = _scratch(workspace, need, xp.device, stream)
-    _check(_c_mx_lin(xp.data_ptr(), xt, ldx, None if xs is None else xs.data_ptr(), w.codes.data_ptr(), w.scales.data_ptr(),
-                     code, M, N, K, out.data_ptr(), _DT[out.dtype], ldo, None if workspace is None else workspace.data_ptr(),
-                     need, _on_stream(stream, xp.device)))
+    workspace = _scratch(workspace, need, device, stream)
+    _check(_c_mx_lin(xp, xt, ldx, xs, *w._pointers(), code, M, N, K, out.data_ptr(), _DT[out.dtype], ldo,
+                     None if workspace is None else workspace.data_ptr(), need, _on_stream(stream, device)))
     return out
 
 
@@ -1003,12 +1034,13 @@ def bt_mx_transpose(w: MxRows, ld: int | None = None, out: torch.Tensor | None =
     (ld defaults to bt_backward_weight_ld(N))."""
     N, K = _mx(w, "w").shape
     ld = bt_backward_weight_ld(N) if ld is None else ld
-    _same_device(w.codes, stream, w.scales, out)
+    first, *others = w._tensors()
+    _same_device(first, stream, *others, out)
     if out is None:
-        out = _empty((K, ld), torch.bfloat16, w.device, stream)
+        out = _empty((K, ld), torch.bfloat16, first.device, stream)
     else:
         _dense(out, "out", (K, ld), torch.bfloat16)
-    _check(_c_mx_t(w.codes.data_ptr(), w.scales.data_ptr(), N, K, w.code, ld, out.data_ptr(), _on_stream(stream, w.device)))
+    _check(_c_mx_t(*w._pointers(), N, K, w.code, ld, out.data_ptr(), _on_stream(stream, first.device)))
     return out
 
 
@@ -1068,7 +1100,7 @@ def bt_rms_norm(x: torch.Tensor, weight: torch.Tensor | None = None, eps: float 
         raise ValueError("out is given and not wanted")
     if sum is not None and residual is None:
         raise ValueError("sum needs a residual")
-    _same_device(x, stream, weight, residual, sum, out, None if q is None else q.codes, None if q is None else q.scales)
+    _same_device(x, stream, weight, residual, sum, out, *(() if q is None else q._tensors()))
     wt = _norm_weight(weight, N, x.dtype)
     ldr = lds = ldo = 0
     if residual is not None:
@@ -1081,10 +1113,10 @@ def bt_rms_norm(x: torch.Tensor, weight: torch.Tensor | None = None, eps: float 
             out = _empty((T, N), x.dtype, x.device, stream)
         ldo = _rows(out, "out", T, N, dt)
     if code is not None and q is None:
-        q = _new_mx(T, N, code, x.device, stream)
+        q = MxRows._new(T, N, code, x.device, stream)
+    codes, scales = (None, None) if q is None else q._pointers()
     _check(_c_rms(x.data_ptr(), _DT[x.dtype], ldx, _ptr(residual), ldr, _ptr(weight), wt, T, N, eps, _ptr(sum), lds, _ptr(out),
-                  ldo, 0 if q is None else code, None if q is None else q.codes.data_ptr(),
-                  None if q is None else q.scales.data_ptr(), _on_stream(stream, x.device)))
+                  ldo, 0 if q is None else code, codes, scales, _on_stream(stream, x.device)))
     return out, sum, q
 
 
@@ -1127,31 +1159,38 @@ def bt_clip_grads_workspace(count: int) -> int:
     return int(_c_clip_ws(count))
 
 
+_dtype_of = operator.attrgetter("dtype")
+
+
 @_on_device_of("grads", 0)
 def bt_clip_grads(grads, max_norm: float, eps: float = 1e-6, norm: torch.Tensor | None = None,
                   workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """The norm of all of grads (a list of contiguous CUDA tensors, float32, bfloat16 or float16) as a device float, and
     each of them times min(1, max_norm / (norm + eps)), in place. max_norm = inf: the norm alone."""
     grads = list(grads)
-    if not grads:
-        raise ValueError("grads must hold a tensor")
-    n = len(grads)
-    first = grads[0]
-    _same_device(first, stream, *grads, norm, workspace)
-    for g in grads:
-        if g.dtype not in _FLOATS or not g.is_cuda:
-            raise ValueError("grads must be CUDA tensors of float32, bfloat16 or float16")
-        if not g.is_contiguous():
-            raise ValueError("grads must be contiguous")
+    if not grads or not all(issubclass(t, torch.Tensor) for t in set(map(type, grads))):
+        raise ValueError("grads must be tensors, one at least")
+    # (maps, sets and arrays: hundreds of tensors are looked at before a launch of microseconds)
+    n, first = len(grads), grads[0]
+    dtypes = list(map(_dtype_of, grads))
+    if not set(dtypes).issubset(_FLOATS) or not first.is_cuda:
+        raise ValueError("grads must be CUDA tensors of float32, bfloat16 or float16")
+    _same_device(first, stream, norm, workspace)
+    if set(map(torch.Tensor.get_device, grads)) != {first.get_device()}:
+        raise ValueError(f"grads must be on one device, {first.device} by the first")
+    if not all(map(torch.Tensor.is_contiguous, grads)):
+        raise ValueError("grads must be contiguous")
     if norm is None:
         norm = _empty((), torch.float32, first.device, stream)
     else:
         _dense(norm, "norm", (), torch.float32)
     need = _c_clip_ws(n)
     workspace = _scratch(workspace, need, first.device, stream)
-    _check(_c_clip((_p * n)(*[g.data_ptr() for g in grads]), (_i64 * n)(*[g.numel() for g in grads]),
-                   (ctypes.c_int32 * n)(*[_DT[g.dtype] for g in grads]), n, max_norm, eps, norm.data_ptr(), _ptr(workspace),
-                   need, _on_stream(stream, first.device)))
+    pointers = array.array("Q", map(torch.Tensor.data_ptr, grads))
+    numels = array.array("q", map(torch.Tensor.numel, grads))
+    types = array.array("i", map(_DT.__getitem__, dtypes))
+    _check(_c_clip(pointers.buffer_info()[0], numels.buffer_info()[0], types.buffer_info()[0], n, max_norm, eps, norm.data_ptr(),
+                   _ptr(workspace), need, _on_stream(stream, first.device)))
     return norm
 
 

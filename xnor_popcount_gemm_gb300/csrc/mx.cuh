@@ -149,7 +149,98 @@ template <typename T> __device__ __forceinline__ void raw_store(T *p, const Raw8
     *reinterpret_cast<uint4 *>(p) = r.a;
     if constexpr (sizeof(T) == 4) *(reinterpret_cast<uint4 *>(p) + 1) = r.b;
 }
-// A NaN as the compiler's conversions leave it is as good as any: nothing here goes by a NaN's bits.
+// The same at any element address: `valid` of them are there (<= 0: none), the rest zeros. al: what p is a multiple of
+// (16, 8, 4 or 2; smaller than 16 goes by the widest loads that it allows).
+template <typename T> __device__ __forceinline__ Raw8<T> raw_load_any(const T *p, int valid, int al) {
+    if (al == 16 && valid >= 8) return raw_load<T>(p);
+    uint32_t w[sizeof(T) * 2] = {};
+    if (valid >= 8 && al == 8) {
+#pragma unroll
+        for (int i = 0; i < static_cast<int>(sizeof(T)); ++i) {
+            const uint2 v = __ldg(reinterpret_cast<const uint2 *>(p) + i);
+            w[2 * i] = v.x;
+            w[2 * i + 1] = v.y;
+        }
+    } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < valid) w[i] = __float_as_uint(__ldg(p + i));
+    } else {
+        // from the aligned words that hold a valid one
+        const int odd = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 2) >> 1;
+        const uint32_t *q = reinterpret_cast<const uint32_t *>(reinterpret_cast<const uint16_t *>(p) - odd);
+        uint32_t r[5];
+#pragma unroll
+        for (int i = 0; i < 5; ++i) r[i] = 2 * i - odd < valid && (i < 4 || odd) ? __ldg(q + i) : 0u;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t v = odd ? __funnelshift_r(r[i], r[i + 1], 16) : r[i];
+            w[i] = valid - 2 * i >= 2 ? v : valid - 2 * i == 1 ? v & 0xFFFFu : 0u;
+        }
+    }
+    Raw8<T> r;
+    r.a = make_uint4(w[0], w[1], w[2], w[3]);
+    if constexpr (sizeof(T) == 4) r.b = make_uint4(w[4], w[5], w[6], w[7]);
+    return r;
+}
+template <typename T> __device__ __forceinline__ void raw_store_any(T *p, const Raw8<T> &r, int valid, int al) {
+    if (al == 16 && valid >= 8) return raw_store<T>(p, r);
+    uint32_t w[sizeof(T) * 2];
+    w[0] = r.a.x; w[1] = r.a.y; w[2] = r.a.z; w[3] = r.a.w;
+    if constexpr (sizeof(T) == 4) { w[4] = r.b.x; w[5] = r.b.y; w[6] = r.b.z; w[7] = r.b.w; }
+    if (valid >= 8 && al == 8) {
+#pragma unroll
+        for (int i = 0; i < static_cast<int>(sizeof(T)); ++i) reinterpret_cast<uint2 *>(p)[i] = make_uint2(w[2 * i], w[2 * i + 1]);
+    } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < valid) p[i] = __uint_as_float(w[i]);
+    } else {
+        uint16_t *h = reinterpret_cast<uint16_t *>(p);
+        if (valid >= 8) {
+            if ((reinterpret_cast<uintptr_t>(p) & 2) == 0) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) reinterpret_cast<uint32_t *>(p)[i] = w[i];
+            } else {
+                h[0] = static_cast<uint16_t>(w[0]);
+#pragma unroll
+                for (int i = 0; i < 3; ++i) reinterpret_cast<uint32_t *>(h + 1)[i] = __funnelshift_r(w[i], w[i + 1], 16);
+                h[7] = static_cast<uint16_t>(w[3] >> 16);
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (e < valid) h[e] = static_cast<uint16_t>(w[e >> 1] >> (16 * (e & 1)));
+        }
+    }
+}
+// The largest of 16, 8, 4, 2 bytes that p and every multiple of ld elements share.
+template <typename T> inline int rows_align(const T *p, int64_t ld, int elem) {
+    const uintptr_t v = reinterpret_cast<uintptr_t>(p) | static_cast<uintptr_t>(ld * elem);
+    return v % 16 == 0 ? 16 : v % 8 == 0 ? 8 : v % 4 == 0 ? 4 : 2;
+}
+
+// Two fp32 operations an instruction.
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n.reg .b64 x, y, r;\nmov.b64 x, {%2, %3};\nmov.b64 y, {%4, %5};\nadd.rn.f32x2 r, x, y;\nmov.b64 {%0, %1}, r;\n}\n"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n.reg .b64 x, y, r;\nmov.b64 x, {%2, %3};\nmov.b64 y, {%4, %5};\nmul.rn.f32x2 r, x, y;\nmov.b64 {%0, %1}, r;\n}\n"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n.reg .b64 x, y, z, r;\nmov.b64 x, {%2, %3};\nmov.b64 y, {%4, %5};\nmov.b64 z, {%6, %7};\nfma.rn.f32x2 r, x, y, z;\n"
+        "mov.b64 {%0, %1}, r;\n}\n"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 sub2(float2 a, float2 b) { return fma2(b, make_float2(-1.0f, -1.0f), a); }
 
 // Four lanes next to one another hold a block: its largest magnitude, in all of them.
 __device__ __forceinline__ uint32_t quad_max(uint32_t m) {
@@ -157,6 +248,11 @@ __device__ __forceinline__ uint32_t quad_max(uint32_t m) {
     m = m > o ? m : o;
     o = __shfl_xor_sync(0xFFFFFFFFu, m, 2);
     return m > o ? m : o;
+}
+// Sixteen lanes hold an atom's four blocks of a row, quad by quad: their scale bytes as one word, in the first of them.
+__device__ __forceinline__ uint32_t atom_word(uint32_t s) {
+    s |= __shfl_down_sync(0xFFFFFFFFu, s, 4) << 8;
+    return s | (__shfl_down_sync(0xFFFFFFFFu, s, 8) << 16);
 }
 
 }  // namespace mx

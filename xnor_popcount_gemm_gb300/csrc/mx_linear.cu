@@ -20,6 +20,7 @@
 #include <cstdlib>
 #include <cstring>
 
+#include "adapter.cuh"
 #include "mx_linear.cuh"
 
 namespace bt {
@@ -368,11 +369,14 @@ int num_stages(int code, const Shape &sh, int elem) {
     return n > kMaxStages ? kMaxStages : n;
 }
 
-// Whether few rows go through mx_small.cu. One row to 32 against tiles of 128: see there.
-bool takes_small(int64_t M) {
+// Whether few rows go through mx_small.cu (its figures there): always up to 16, and up to 32 where its tiles of W are not
+// more than half of the SMs, so that a cluster shares each.
+bool takes_small(int64_t M, int64_t N) {
     if (const char *e = std::getenv("BT_MX_CONFIG")) return std::strncmp(e, "small", 5) == 0 && M <= kSmallRows;
-    return M <= kSmallRows;
+    return M <= kOwnRows || (M <= kSmallRows && (N + 127) / 128 * 2 <= device_sm_count());
 }
+// Whether x is quantised by a kernel before the product's.
+bool quantises_first(int64_t M, int64_t N) { return !takes_small(M, N) || M > kOwnRows; }
 
 // The fastest of four shapes by a model of their times in ns, fitted on GB300 (E2M1 and E4M3, 128 to 8192 rows): a slice of
 // K, what a tile costs beside its slices, the epilogue (which the next tile's MMAs overlap), the launch. Model and measured,
@@ -473,7 +477,7 @@ template <int CODE> cudaError_t launch_out(const Product &p, const Shape &sh, cu
     return launch_shape<CODE, __half>(p, sh, s);
 }
 cudaError_t product(const Product &p, cudaStream_t s) {
-    if (takes_small(p.M)) {
+    if (takes_small(p.M, p.N)) {
         int split = 0;
         if (const char *e = std::getenv("BT_MX_CONFIG")) {
             if (std::sscanf(e, "small,%d", &split) != 1 || (split != 1 && split != 2 && split != 4 && split != 8)) split = 0;
@@ -487,16 +491,6 @@ cudaError_t product(const Product &p, cudaStream_t s) {
 bool float_type(bt_dtype t) { return t == BT_F32 || t == BT_BF16 || t == BT_F16; }
 size_t codes_room(int64_t M, int64_t K, bt_code code) { return round_up256(static_cast<size_t>(M) * static_cast<size_t>(code_bytes(K, code))); }
 
-// g [M, N] at 16-byte rows, zeros up to a multiple of 8.
-__global__ void __launch_bounds__(256) pad_rows_kernel(const uint16_t *g, int64_t ldg, int N, uint16_t *out, int ld) {
-    if (threadIdx.x == 0) pdl_launch_dependents();
-    pdl_wait();
-    const int64_t row = blockIdx.x;
-    for (int c = threadIdx.x; c < ld / 2; c += 256) {
-        const uint32_t lo = 2 * c < N ? g[row * ldg + 2 * c] : 0, hi = 2 * c + 1 < N ? g[row * ldg + 2 * c + 1] : 0;
-        reinterpret_cast<uint32_t *>(out + row * ld)[c] = lo | (hi << 16);
-    }
-}
 int64_t pitch8(int64_t n) { return (n + 7) / 8 * 8; }
 bool plain_rows(const void *g, int64_t ldg, int64_t N) { return N % 8 == 0 && ldg % 8 == 0 && aligned(g, 16); }
 
@@ -509,7 +503,7 @@ using namespace bt::mx;
 extern "C" {
 
 size_t bt_mx_linear_workspace(int64_t M, int64_t N, int64_t K, bt_dtype x_dtype, bt_code code) {
-    if (!float_type(x_dtype) || mx_sides(M, K, code) != BT_OK || M < 1 || N < 1 || takes_small(M)) return 0;
+    if (!float_type(x_dtype) || mx_sides(M, K, code) != BT_OK || M < 1 || N < 1 || !quantises_first(M, N)) return 0;
     return codes_room(M, K, code) + round_up256(scale_bytes(M, K, code));
 }
 
@@ -579,9 +573,14 @@ bt_status bt_mx_linear_backward(const void *g, int64_t ldg, const void *wt, int6
         if (workspace == nullptr || workspace_bytes < need) return BT_ERR_WORKSPACE;
         if (!aligned(workspace, 256)) return BT_ERR_ALIGNMENT;
         pitch = pitch8(N);
-        if (launch_pdl(pad_rows_kernel, dim3(static_cast<unsigned>(M)), dim3(256), s, rows, ldg, static_cast<int>(N),
-                       static_cast<uint16_t *>(workspace), static_cast<int>(pitch)) != cudaSuccess)
-            return BT_ERR_CUDA;
+        adapter::AlignArgs al = {};         // (with zeros up to the pitch)
+        al.src = rows;
+        al.lds = ldg;
+        al.dst = static_cast<uint16_t *>(workspace);
+        al.ldd = pitch;
+        al.C = static_cast<int>(N);
+        al.rows = M;
+        if (adapter::launch_align(al, s) != cudaSuccess) return BT_ERR_CUDA;
         rows = static_cast<const uint16_t *>(workspace);
     }
     unsigned int *err = device_error_word();

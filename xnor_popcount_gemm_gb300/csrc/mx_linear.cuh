@@ -57,8 +57,9 @@ struct Product {
     unsigned int *err;
 };
 
-// Up to kSmallRows rows of x, quantised by the kernel itself. split: CTAs along K (1, 2, 4, 8; 0: chosen).
-constexpr int kSmallRows = 32;
+// Up to kSmallRows rows of x; of float type: quantised by the kernel itself, which pays up to kOwnRows. split: CTAs along K
+// (1, 2, 4, 8; 0: chosen).
+constexpr int kSmallRows = 32, kOwnRows = 16;
 cudaError_t launch_small(const Product &p, int split, cudaStream_t s);
 
 }  // namespace mx

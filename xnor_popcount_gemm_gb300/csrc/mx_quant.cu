@@ -18,7 +18,7 @@ constexpr int kGroups = 4;                  // groups of eight a thread takes, k
 struct QuantArgs {
     const void *x;
     int64_t ldx;
-    int R, K;
+    int R, K, al;                           // al: what x's rows start at multiples of
     uint32_t groups;                        // eights of a row, up to the end of its last atom
     FastDiv per_row;
     uint32_t total;
@@ -26,9 +26,7 @@ struct QuantArgs {
     uint8_t *q, *s;
 };
 
-// VEC: every eight of a row is 16-byte aligned.
-template <typename T, int CODE, bool VEC>
-__global__ void __launch_bounds__(kThreads) mx_quantize_kernel(const QuantArgs a) {
+template <typename T, int CODE> __global__ void __launch_bounds__(kThreads) mx_quantize_kernel(const QuantArgs a) {
     pdl_wait();
     pdl_launch_dependents();                // after the wait: what follows may rely on everything before this kernel
     const uint32_t first = blockIdx.x * (kThreads * kGroups) + threadIdx.x;
@@ -41,15 +39,7 @@ __global__ void __launch_bounds__(kThreads) mx_quantize_kernel(const QuantArgs a
         row[i] = fdiv(t < a.total ? t : 0u, a.per_row);
         g[i] = (t < a.total ? t : 0u) - row[i] * a.groups;
         const int k = static_cast<int>(g[i]) * 8;
-        const T *p = x + static_cast<int64_t>(row[i]) * a.ldx + k;
-        if (VEC && k + 8 <= a.K) {
-            raw[i] = raw_load<T>(p);
-        } else {
-            float v[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = k + e < a.K ? Elem<T>::to_f32(p[e]) : 0.0f;
-            raw[i] = raw_pack<T>(v);        // exact: they were of this type
-        }
+        raw[i] = raw_load_any<T>(x + static_cast<int64_t>(row[i]) * a.ldx + k, a.K - k, a.al);
     }
 #pragma unroll
     for (int i = 0; i < kGroups; ++i) {
@@ -61,12 +51,11 @@ __global__ void __launch_bounds__(kThreads) mx_quantize_kernel(const QuantArgs a
             const uint32_t m = mag_bits(v[e]);
             top = m > top ? m : top;
         }
-        top = quad_max(top);
-        if (first + i * kThreads >= a.total) continue;      // (whole quads: a row is a multiple of 16 groups)
-        const uint32_t s = scale_of<CODE>(top);
+        const uint32_t s = scale_of<CODE>(quad_max(top)), word = atom_word(s);
+        if (first + i * kThreads >= a.total) continue;      // (a row is a multiple of 16 groups)
         const int64_t at = static_cast<int64_t>(g[i]) * Format<CODE>::kBytes8;
         store8<CODE>(a.q + static_cast<int64_t>(row[i]) * a.row_bytes + at, code8<CODE>(v, inverse_of(s)));
-        if ((threadIdx.x & 3) == 0) a.s[scale_at(row[i], g[i] >> 2, a.atoms)] = static_cast<uint8_t>(s);
+        if ((threadIdx.x & 15) == 0) *reinterpret_cast<uint32_t *>(a.s + scale_at(row[i], g[i] >> 2, a.atoms)) = word;
     }
 }
 
@@ -79,10 +68,10 @@ struct DequantArgs {
     int64_t row_bytes, atoms;
     void *out;
     int64_t ldo;
+    int al;
 };
 
-template <typename T, int CODE, bool VEC>
-__global__ void __launch_bounds__(kThreads) mx_dequantize_kernel(const DequantArgs a) {
+template <typename T, int CODE> __global__ void __launch_bounds__(kThreads) mx_dequantize_kernel(const DequantArgs a) {
     if (threadIdx.x == 0) pdl_launch_dependents();
     pdl_wait();
     const uint32_t first = blockIdx.x * (kThreads * kGroups) + threadIdx.x;
@@ -105,14 +94,7 @@ __global__ void __launch_bounds__(kThreads) mx_dequantize_kernel(const DequantAr
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] *= p;
         const int k = static_cast<int>(g[i]) * 8;
-        T *o = static_cast<T *>(a.out) + static_cast<int64_t>(row[i]) * a.ldo + k;
-        if (VEC && k + 8 <= a.K) {
-            raw_store<T>(o, raw_pack<T>(v));
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (k + e < a.K) o[e] = from_f32<T>(v[e]);
-        }
+        raw_store_any<T>(static_cast<T *>(a.out) + static_cast<int64_t>(row[i]) * a.ldo + k, raw_pack<T>(v), a.K - k, a.al);
     }
 }
 
@@ -153,20 +135,15 @@ template <int CODE> __global__ void __launch_bounds__(kThreads) mx_transpose_ker
     }
 }
 
-bool wide_rows(const void *p, int64_t ld, bt_dtype t) {
-    return aligned(p, 16) && (ld * dtype_bytes(t)) % 16 == 0;
-}
 bool mx_code(bt_code c) { return c == BT_CODE_E4M3 || c == BT_CODE_E2M1; }
 bool float_type(bt_dtype t) { return t == BT_F32 || t == BT_BF16 || t == BT_F16; }
 unsigned blocks_of(uint32_t total) { return static_cast<unsigned>((static_cast<uint64_t>(total) + kThreads * kGroups - 1) / (kThreads * kGroups)); }
 
-template <typename T, int CODE> cudaError_t quantize(const QuantArgs &a, bool vec, cudaStream_t s) {
-    return launch_pdl(vec ? mx_quantize_kernel<T, CODE, true> : mx_quantize_kernel<T, CODE, false>, dim3(blocks_of(a.total)),
-                      dim3(kThreads), s, a);
+template <typename T, int CODE> cudaError_t quantize(const QuantArgs &a, cudaStream_t s) {
+    return launch_pdl(mx_quantize_kernel<T, CODE>, dim3(blocks_of(a.total)), dim3(kThreads), s, a);
 }
-template <typename T, int CODE> cudaError_t dequantize(const DequantArgs &a, bool vec, cudaStream_t s) {
-    return launch_pdl(vec ? mx_dequantize_kernel<T, CODE, true> : mx_dequantize_kernel<T, CODE, false>, dim3(blocks_of(a.total)),
-                      dim3(kThreads), s, a);
+template <typename T, int CODE> cudaError_t dequantize(const DequantArgs &a, cudaStream_t s) {
+    return launch_pdl(mx_dequantize_kernel<T, CODE>, dim3(blocks_of(a.total)), dim3(kThreads), s, a);
 }
 
 // What every call on such an operand checks of it.
@@ -191,14 +168,14 @@ cudaError_t launch_mx_quantize(const void *x, bt_dtype xt, int64_t ldx, int64_t 
     a.total = static_cast<uint32_t>(R) * a.groups;
     a.row_bytes = code_bytes(K, code);
     a.q = static_cast<uint8_t *>(q); a.s = static_cast<uint8_t *>(scales);
-    const bool vec = wide_rows(x, ldx, xt);
+    a.al = rows_align(static_cast<const char *>(x), ldx, dtype_bytes(xt));
     if (code == BT_CODE_E4M3)
-        return xt == BT_F32    ? quantize<float, BT_CODE_E4M3>(a, vec, s)
-               : xt == BT_BF16 ? quantize<__nv_bfloat16, BT_CODE_E4M3>(a, vec, s)
-                               : quantize<__half, BT_CODE_E4M3>(a, vec, s);
-    return xt == BT_F32    ? quantize<float, BT_CODE_E2M1>(a, vec, s)
-           : xt == BT_BF16 ? quantize<__nv_bfloat16, BT_CODE_E2M1>(a, vec, s)
-                           : quantize<__half, BT_CODE_E2M1>(a, vec, s);
+        return xt == BT_F32    ? quantize<float, BT_CODE_E4M3>(a, s)
+               : xt == BT_BF16 ? quantize<__nv_bfloat16, BT_CODE_E4M3>(a, s)
+                               : quantize<__half, BT_CODE_E4M3>(a, s);
+    return xt == BT_F32    ? quantize<float, BT_CODE_E2M1>(a, s)
+           : xt == BT_BF16 ? quantize<__nv_bfloat16, BT_CODE_E2M1>(a, s)
+                           : quantize<__half, BT_CODE_E2M1>(a, s);
 }
 
 }  // namespace bt
@@ -246,17 +223,17 @@ bt_status bt_mx_dequantize(const void *q, const void *scales, int64_t R, int64_t
     a.total = static_cast<uint32_t>(R) * a.groups;
     a.row_bytes = code_bytes(K, code);
     a.out = out; a.ldo = ldo;
-    const bool vec = wide_rows(out, ldo, out_dtype);
+    a.al = rows_align(static_cast<const char *>(out), ldo, dtype_bytes(out_dtype));
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e;
     if (code == BT_CODE_E4M3)
-        e = out_dtype == BT_F32    ? dequantize<float, BT_CODE_E4M3>(a, vec, s)
-            : out_dtype == BT_BF16 ? dequantize<__nv_bfloat16, BT_CODE_E4M3>(a, vec, s)
-                                   : dequantize<__half, BT_CODE_E4M3>(a, vec, s);
+        e = out_dtype == BT_F32    ? dequantize<float, BT_CODE_E4M3>(a, s)
+            : out_dtype == BT_BF16 ? dequantize<__nv_bfloat16, BT_CODE_E4M3>(a, s)
+                                   : dequantize<__half, BT_CODE_E4M3>(a, s);
     else
-        e = out_dtype == BT_F32    ? dequantize<float, BT_CODE_E2M1>(a, vec, s)
-            : out_dtype == BT_BF16 ? dequantize<__nv_bfloat16, BT_CODE_E2M1>(a, vec, s)
-                                   : dequantize<__half, BT_CODE_E2M1>(a, vec, s);
+        e = out_dtype == BT_F32    ? dequantize<float, BT_CODE_E2M1>(a, s)
+            : out_dtype == BT_BF16 ? dequantize<__nv_bfloat16, BT_CODE_E2M1>(a, s)
+                                   : dequantize<__half, BT_CODE_E2M1>(a, s);
     return e == cudaSuccess ? BT_OK : BT_ERR_CUDA;
 }
 

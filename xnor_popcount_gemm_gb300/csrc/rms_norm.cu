@@ -13,10 +13,10 @@
 // the second from one Newton step on the residual 1 - m q^2, which an fma gives
 // exactly. That is 13 operations a value where a plain norm has 4.
 #include <cmath>
-#include <cstdlib>
 
 #include "bt_internal.h"
 #include "mx.cuh"
+#include "tc_ptx.cuh"
 
 namespace bt {
 namespace {
@@ -42,14 +42,30 @@ struct NormArgs {
 // A sum and the rounding errors made in it.
 struct Sum2 {
     float s, c;
-    __device__ __forceinline__ void add(float p) {
-        const float t = s + p, b = t - s;
-        c += (s - (t - b)) + (p - b);
+    __device__ __forceinline__ void join(float os, float oc) {
+        const float t = s + os, b = t - s;
+        c += (s - (t - b)) + (os - b) + oc;
         s = t;
     }
-    __device__ __forceinline__ void join(float os, float oc) {
-        add(os);
-        c += oc;
+};
+// Two of them, side by side.
+struct Sums {
+    float2 s, c;
+    __device__ __forceinline__ void add(float2 p) {
+        const float2 t = add2(s, p), b = sub2(t, s);
+        c = add2(c, add2(sub2(s, sub2(t, b)), sub2(p, b)));
+        s = t;
+    }
+    // the square of two values; 16-bit ones have exact squares
+    template <bool EXACT> __device__ __forceinline__ void square(float2 v) {
+        const float2 p = mul2(v, v);
+        add(p);
+        if (!EXACT) c = add2(c, fma2(v, v, make_float2(-p.x, -p.y)));
+    }
+    __device__ __forceinline__ Sum2 joined() const {
+        Sum2 r{s.x, c.x};
+        r.join(s.y, c.y);
+        return r;
     }
 };
 
@@ -100,9 +116,11 @@ __device__ __forceinline__ Inverse inverse_rms(const Sum2 &v, const NormArgs &a,
     const float e = fmaf(-m, q, 1.0f) - fmaf(m, fmaf(r, r, -q), ml * q);
     return Inverse{r, r * (0.5f * e + 0.375f * e * e)};
 }
-__device__ __forceinline__ float normed(float v, float w, const Inverse &i) {
-    const float p = v * w;
-    return fmaf(p, i.hi, fmaf(p, i.lo, fmaf(v, w, -p) * i.hi));
+// v w / rms; exact: v w has no more than 24 bits.
+__device__ __forceinline__ float2 normed(float2 v, float2 w, const Inverse &i, bool exact) {
+    const float2 p = mul2(v, w), hi = make_float2(i.hi, i.hi), lo = make_float2(i.lo, i.lo);
+    const float2 rest = exact ? mul2(p, lo) : fma2(p, lo, mul2(fma2(v, w, make_float2(-p.x, -p.y)), hi));
+    return fma2(p, hi, rest);
 }
 
 // A row by its CTA, eight consecutive columns at a time: thread t has the eights
@@ -139,19 +157,15 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(const NormArgs a) {
         }
     }
     auto squares = [&](float k) {
-        Sum2 p{0.0f, 0.0f};
+        Sums p{};
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             float v[8];
             raw_unpack<T>(h[i], v);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float u = v[e] * k, sq = u * u;
-                p.add(sq);
-                if (sizeof(T) == 4) p.c += fmaf(u, u, -sq);      // (16-bit values have exact squares)
-            }
+            for (int e = 0; e < 8; e += 2) p.square<sizeof(T) == 2>(make_float2(v[e] * k, v[e + 1] * k));
         }
-        return p;
+        return p.joined();
     };
     Sum2 total = block_sum(squares(1.0f), red[0]);
     const float k = power_for(total.s, a.eps, a.N);
@@ -174,7 +188,11 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(const NormArgs a) {
                 raw_unpack<T>(raw_load<T>(static_cast<const T *>(a.w) + c), w);
             }
 #pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = normed(v[e] * k, w[e], inv);
+            for (int e = 0; e < 8; e += 2) {
+                const float2 n = normed(make_float2(v[e] * k, v[e + 1] * k), make_float2(w[e], w[e + 1]), inv, sizeof(T) == 2 && !a.w_f32);
+                y[e] = n.x;
+                y[e + 1] = n.y;
+            }
             const Raw8<T> o = raw_pack<T>(y);
             if (a.out != nullptr) raw_store<T>(static_cast<T *>(a.out) + row * a.ldo + c, o);
             raw_unpack<T>(o, y);
@@ -187,14 +205,13 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(const NormArgs a) {
             top = m > top ? m : top;
         }
         top = quad_max(top);
-        if (c >= a.cols) continue;
         const bool e4m3 = a.code == BT_CODE_E4M3;
-        const uint32_t s = e4m3 ? scale_of<BT_CODE_E4M3>(top) : scale_of<BT_CODE_E2M1>(top);
-        const int64_t at = static_cast<int64_t>(g) * (e4m3 ? 8 : 4);
-        uint8_t *p = a.q + row * a.row_bytes + at;
+        const uint32_t s = e4m3 ? scale_of<BT_CODE_E4M3>(top) : scale_of<BT_CODE_E2M1>(top), word = atom_word(s);
+        if (c >= a.cols) continue;
+        uint8_t *p = a.q + row * a.row_bytes + static_cast<int64_t>(g) * (e4m3 ? 8 : 4);
         if (e4m3) store8<BT_CODE_E4M3>(p, code8<BT_CODE_E4M3>(y, inverse_of(s)));
         else store8<BT_CODE_E2M1>(p, code8<BT_CODE_E2M1>(y, inverse_of(s)));
-        if ((threadIdx.x & 3) == 0) a.s[scale_at(row, g >> 2, a.atoms)] = static_cast<uint8_t>(s);
+        if ((threadIdx.x & 15) == 0) *reinterpret_cast<uint32_t *>(a.s + scale_at(row, g >> 2, a.atoms)) = word;
     }
 }
 
@@ -247,17 +264,12 @@ __global__ void __launch_bounds__(1024) rms_norm_any_kernel(const NormArgs a) {
             h[i] = Elem<T>::to_f32(t);
         }
     }
-    auto add = [&](Sum2 &p, float v, float k) {
-        const float u = v * k, sq = u * u;
-        p.add(sq);
-        if (sizeof(T) == 4) p.c += fmaf(u, u, -sq);
-    };
     auto squares = [&](float k, bool first) {
-        Sum2 p{0.0f, 0.0f};
+        Sums p{};
 #pragma unroll
-        for (int i = 0; i < E; ++i) add(p, h[i], k);
-        for (int c = threadIdx.x + E * step; c < a.N; c += step) add(p, first ? load(c, true) : again(c), k);
-        return p;
+        for (int i = 0; i < E; i += 2) p.square<sizeof(T) == 2>(make_float2(h[i] * k, h[i + 1] * k));
+        for (int c = threadIdx.x + E * step; c < a.N; c += step) p.square<sizeof(T) == 2>(make_float2((first ? load(c, true) : again(c)) * k, 0.0f));
+        return p.joined();
     };
     Sum2 total = block_sum(squares(1.0f, true), red[0]);
     const float k = power_for(total.s, a.eps, a.N);
@@ -269,7 +281,7 @@ __global__ void __launch_bounds__(1024) rms_norm_any_kernel(const NormArgs a) {
             const float w = a.w == nullptr ? 1.0f
                             : a.w_f32      ? __ldg(static_cast<const float *>(a.w) + c)
                                            : Elem<T>::to_f32(static_cast<const T *>(a.w)[c]);
-            const T o = from_f32<T>(normed(v * k, w, inv));
+            const T o = from_f32<T>(normed(make_float2(v * k, 0.0f), make_float2(w, 0.0f), inv, sizeof(T) == 2 && !a.w_f32).x);
             if (a.out != nullptr) static_cast<T *>(a.out)[row * a.ldo + c] = o;
             y = Elem<T>::to_f32(o);
         }
@@ -308,7 +320,10 @@ struct BackArgs {
     float *parts;                           // [chunks, N], NULL: gw not wanted
     float4 *rows;                           // (any) 1 / rms of the values times k, mean(g w n), k of every row
     int chunks;
+    int ahead, pitch;                       // rows of the ring, bytes of one of a row's arrays in it
+    unsigned int *err;
 };
+constexpr int kMostAhead = 3;
 
 __device__ __forceinline__ float2 block_pair(float2 v, float2 (&red)[32]) {
 #pragma unroll
@@ -333,112 +348,223 @@ __device__ __forceinline__ float inverse_plain(float s, const BackArgs &a, float
     return 1.0f / sqrtf(fmaf(s, a.n_inv, (a.eps * k) * k));
 }
 
-template <typename T> __device__ __forceinline__ void weight8(const void *w, int w_f32, int c, float (&o)[8]) {
-    if (w == nullptr) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] = 1.0f;
-    } else if (w_f32) {
-        raw_unpack<float>(raw_load<float>(static_cast<const float *>(w) + c), o);
-    } else {
-        raw_unpack<T>(raw_load<T>(static_cast<const T *>(w) + c), o);
-    }
-}
-
-// Aligned rows: a CTA takes rows blockIdx.x, + chunks, ... and keeps its threads'
-// columns of gw in registers; the next row's g and h are on their way meanwhile.
-template <typename T, int V>
-__global__ void __launch_bounds__(512) rms_back_kernel(const BackArgs a) {
-    __shared__ float2 red[4][32];
-    if (threadIdx.x == 0) pdl_launch_dependents();
-    pdl_wait();
-    float acc[V][8];
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) acc[i][e] = 0.0f;
-    Raw8<T> g[V], h[V], gn[V], hn[V];
-    auto fetch = [&](int row, Raw8<T> (&pg)[V], Raw8<T> (&ph)[V]) {
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int c = (threadIdx.x + i * blockDim.x) * 8;
-            pg[i] = ph[i] = Raw8<T>{};
-            if (c < a.N && row < a.T) {
-                pg[i] = raw_load<T>(static_cast<const T *>(a.g) + row * a.ldg + c);
-                ph[i] = raw_load<T>(static_cast<const T *>(a.h) + row * a.ldh + c);
+// Eight of a row's values: eight neighbours (VEC: rows 16-byte aligned, N a multiple of 8), thread t's i-th eight at
+// (t + i threads) 8, or, at any alignment, every `threads`-th from t + 8 i threads on, so that neighbours take neighbours.
+template <bool VEC> struct Columns {
+    int first, step, N;
+    __device__ __forceinline__ Columns(int i, int n, int threads)
+        : first(VEC ? (static_cast<int>(threadIdx.x) + i * threads) * 8 : static_cast<int>(threadIdx.x) + i * 8 * threads), step(VEC ? 1 : threads), N(n) {}
+    template <typename T> __device__ __forceinline__ Raw8<T> load(const T *row) const {
+        Raw8<T> r = {};
+        if constexpr (VEC) {
+            if (first < N) {
+                r.a = *reinterpret_cast<const uint4 *>(row + first);
+                if constexpr (sizeof(T) == 4) r.b = *(reinterpret_cast<const uint4 *>(row + first) + 1);
             }
-        }
-    };
-    fetch(blockIdx.x, g, h);
-    int odd = 0;
-    for (int row = blockIdx.x; row < a.T; row += gridDim.x, odd ^= 1) {
-        fetch(row + gridDim.x, gn, hn);
-        Raw8<T> gs[V];
-        if (a.gs != nullptr) {
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const int c = (threadIdx.x + i * blockDim.x) * 8;
-                if (c < a.N) gs[i] = raw_load<T>(static_cast<const T *>(a.gs) + row * a.ldgs + c);
-            }
-        }
-        auto sums = [&](float k) {
-            float2 p = make_float2(0.0f, 0.0f);
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const int c = (threadIdx.x + i * blockDim.x) * 8;
-                if (c >= a.N) continue;
-                float vg[8], vh[8], w[8];
-                raw_unpack<T>(g[i], vg);
-                raw_unpack<T>(h[i], vh);
-                weight8<T>(a.w, a.w_f32, c, w);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float u = vh[e] * k;
-                    p.x = fmaf(u, u, p.x);
-                    p.y = fmaf(vg[e] * w[e], u, p.y);
-                }
-            }
-            return p;
-        };
-        float2 p = block_pair(sums(1.0f), red[odd]);
-        const float k = power_for(p.x, a.eps, a.N);
-        if (k != 1.0f) p = block_pair(sums(k), red[2 + odd]);
-        const float inv = inverse_plain(p.x, a, k), mean = p.y * inv * a.n_inv;
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int c = (threadIdx.x + i * blockDim.x) * 8;
-            if (c >= a.N) continue;
-            float vg[8], vh[8], w[8], o[8];
-            raw_unpack<T>(g[i], vg);
-            raw_unpack<T>(h[i], vh);
-            weight8<T>(a.w, a.w_f32, c, w);
-            if (a.gs != nullptr) raw_unpack<T>(gs[i], o);
+        } else {
+            uint32_t w[sizeof(T) * 2] = {};
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const float n = vh[e] * k * inv;
-                acc[i][e] = fmaf(vg[e], n, acc[i][e]);
-                const float d = (inv * k) * fmaf(-n, mean, vg[e] * w[e]);
-                o[e] = a.gs != nullptr ? d + o[e] : d;
+                if (first + e * step >= N) continue;
+                if constexpr (sizeof(T) == 4) w[e] = __float_as_uint(row[first + e * step]);
+                else w[e / 2] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t *>(row)[first + e * step]) << (16 * (e & 1));
             }
-            raw_store<T>(static_cast<T *>(a.gx) + row * a.ldgx + c, raw_pack<T>(o));
+            r.a = make_uint4(w[0], w[1], w[2], w[3]);
+            if constexpr (sizeof(T) == 4) r.b = make_uint4(w[4], w[5], w[6], w[7]);
         }
+        return r;
+    }
+    template <typename T> __device__ __forceinline__ void store(T *row, const float (&v)[8]) const {
+        if constexpr (VEC) {
+            if (first < N) raw_store<T>(row + first, raw_pack<T>(v));
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (first + e * step < N) row[first + e * step] = from_f32<T>(v[e]);
+        }
+    }
+};
+
+// A CTA takes rows blockIdx.x, + gridDim.x, ..., keeps its threads' columns of gw in registers, and has the next two rows on
+// their way into a ring in shared memory: bulk copies of the 16-byte pieces that hold a row, asked for by a warp of its
+// own. Memory: 4096 x 4096 bf16 with gs 26.7 us (134 MB, 74 % of the copy rate), and 4 for the parts of gw and their sum;
+// with rows loaded when they are due 41.
+template <typename T, int V, int MOST, bool VEC>
+__global__ void __launch_bounds__(MOST + 32, MOST == 256 ? 2 : 1) rms_back_kernel(const BackArgs a) {
+    extern __shared__ __align__(16) uint8_t ring[];
+    __shared__ float2 red[2][2][16];
+    __shared__ uint64_t bars[2 * kMostAhead];
+    __shared__ uint32_t abort_word;
+    volatile uint32_t *abort_flag = &abort_word;
+    const int threads = static_cast<int>(blockDim.x) - 32, warps = threads >> 5;       // but for the last warp, which asks
+    const int rows = (a.T - static_cast<int>(blockIdx.x) + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x);
+    const int D = a.ahead, arrays = a.gs != nullptr ? 3 : 2, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    auto full = [&](int i) { return smem_u32(&bars[i]); };
+    auto empty = [&](int i) { return smem_u32(&bars[kMostAhead + i]); };
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < D; ++i) {
+            tc::mbar_init(full(i), 1);
+            tc::mbar_init(empty(i), static_cast<uint32_t>(warps));
+        }
+        abort_word = 0u;
+        tc::fence_mbar_init();
+    }
+    __syncthreads();
+    pdl_wait();
+    if (threadIdx.x == 0) pdl_launch_dependents();
+    const T *const src[3] = {static_cast<const T *>(a.g), static_cast<const T *>(a.h), static_cast<const T *>(a.gs)};
+    const int64_t lds[3] = {a.ldg, a.ldh, a.ldgs};
+    auto start = [&](int n, int k) { return reinterpret_cast<uintptr_t>(src[k] + (blockIdx.x + static_cast<int64_t>(n) * gridDim.x) * lds[k]); };
+
+    if (warp == warps) {
+        if (lane == 0) {
+            int n = 0, slot = 0;
+            uint32_t phase = 1;
+            for (; n < rows; ++n) {
+                if (!tc::wait_fast(empty(slot), phase, abort_flag, a.err)) break;
+                uint32_t to = smem_u32(ring) + static_cast<uint32_t>(slot * arrays * a.pitch), all = 0, bytes[3];
+                uintptr_t from[3];
+#pragma unroll
+                for (int k = 0; k < 3; ++k) {
+                    if (k >= arrays) continue;
+                    const uintptr_t p = start(n, k);
+                    from[k] = p & ~uintptr_t(15);
+                    bytes[k] = static_cast<uint32_t>(((p + static_cast<uintptr_t>(a.N) * sizeof(T) + 15) & ~uintptr_t(15)) - from[k]);
+                    all += bytes[k];
+                }
+                tc::mbar_arrive_expect_tx(full(slot), all);
+#pragma unroll
+                for (int k = 0; k < 3; ++k)
+                    if (k < arrays) tc::bulk_load(to + static_cast<uint32_t>(k * a.pitch), reinterpret_cast<const void *>(from[k]), bytes[k], full(slot));
+                if (++slot == D) {
+                    slot = 0;
+                    phase ^= 1u;
+                }
+            }
+            // whatever happens elsewhere, what was asked for lands before shared memory is given back
+            for (int m = n > D ? n - D : 0; m < n; ++m) {
+                uint32_t never = 0;
+                tc::wait_bounded(full(m % D), static_cast<uint32_t>(m / D) & 1u, &never, a.err);
+            }
+        }
+        return;
+    }
+
+    // the weight as floats behind the ring: each thread reads what it wrote
+    float *const weight = reinterpret_cast<float *>(ring + D * arrays * a.pitch) + 8 * V * threadIdx.x;
+    float2 acc[V][4];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const Columns<VEC> c(i, a.N, threads);
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = 1.0f;
+        if (a.w != nullptr && a.w_f32) raw_unpack<float>(c.template load<float>(static_cast<const float *>(a.w)), v);
+        else if (a.w != nullptr) raw_unpack<T>(c.template load<T>(static_cast<const T *>(a.w)), v);
+        raw_store<float>(weight + 8 * i, raw_pack<float>(v));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[i][e] = make_float2(0.0f, 0.0f);
+    }
+    auto weights = [&](int i, float2 (&w)[4]) {
+        const float4 lo = *reinterpret_cast<const float4 *>(weight + 8 * i), hi = *reinterpret_cast<const float4 *>(weight + 8 * i + 4);
+        w[0] = make_float2(lo.x, lo.y);
+        w[1] = make_float2(lo.z, lo.w);
+        w[2] = make_float2(hi.x, hi.y);
+        w[3] = make_float2(hi.z, hi.w);
+    };
+    // the block's sums, in every thread
+    auto together = [&](float2 v, float2 (&x)[16]) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            v.x += __shfl_xor_sync(0xFFFFFFFFu, v.x, o);
+            v.y += __shfl_xor_sync(0xFFFFFFFFu, v.y, o);
+        }
+        if (lane == 0) x[warp] = v;
+        asm volatile("bar.sync 1, %0;" ::"r"(threads) : "memory");
+        v = x[0];
+#pragma unroll
+        for (int i = 1; i < MOST / 32; ++i)
+            if (i < warps) v = add2(v, x[i]);
+        return v;
+    };
+    int slot = 0;
+    uint32_t phase = 0;
+    for (int n = 0; n < rows; ++n) {
+        // (a wait that runs out, which nothing but a fault elsewhere makes, is recorded; the loop goes on, so that all threads
+        // meet at the exchanges, and the results are incomplete)
+        tc::wait_fast(full(slot), phase, abort_flag, a.err);
+        auto row_of = [&](int k) {
+            const uint8_t *p = ring + (slot * arrays + k) * a.pitch;
+            return reinterpret_cast<const T *>(VEC ? p : p + (start(n, k) & 15));
+        };
+        Raw8<T> g[V], h[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            g[i] = gn[i];
-            h[i] = hn[i];
+            const Columns<VEC> c(i, a.N, threads);
+            g[i] = c.template load<T>(row_of(0));
+            h[i] = c.template load<T>(row_of(1));
+        }
+        auto sums = [&](float k) {
+            float2 s = make_float2(0.0f, 0.0f), d = s;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                float vg[8], vh[8];
+                raw_unpack<T>(g[i], vg);
+                raw_unpack<T>(h[i], vh);
+                float2 w[4];
+                weights(i, w);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float2 u = mul2(make_float2(vh[2 * e], vh[2 * e + 1]), make_float2(k, k));
+                    s = fma2(u, u, s);
+                    d = fma2(mul2(make_float2(vg[2 * e], vg[2 * e + 1]), w[e]), u, d);
+                }
+            }
+            return make_float2(s.x + s.y, d.x + d.y);
+        };
+        float2 p = together(sums(1.0f), red[0][n & 1]);
+        const float k = power_for(p.x, a.eps, a.N);
+        if (k != 1.0f) p = together(sums(k), red[1][n & 1]);
+        const float inv = inverse_plain(p.x, a, k), mean = p.y * inv * a.n_inv, n1 = k * inv;
+        T *gx = static_cast<T *>(a.gx) + (blockIdx.x + static_cast<int64_t>(n) * gridDim.x) * a.ldgx;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const Columns<VEC> c(i, a.N, threads);
+            float vg[8], vh[8], o[8];
+            raw_unpack<T>(g[i], vg);
+            raw_unpack<T>(h[i], vh);
+            if (a.gs != nullptr) raw_unpack<T>(c.template load<T>(row_of(2)), o);
+            float2 w[4];
+            weights(i, w);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                // (h k first: k brings it into range)
+                const float2 u = mul2(mul2(make_float2(vh[2 * e], vh[2 * e + 1]), make_float2(k, k)), make_float2(inv, inv));
+                const float2 gg = make_float2(vg[2 * e], vg[2 * e + 1]);
+                acc[i][e] = fma2(gg, u, acc[i][e]);
+                float2 d = mul2(fma2(u, make_float2(-mean, -mean), mul2(gg, w[e])), make_float2(n1, n1));
+                if (a.gs != nullptr) d = add2(d, make_float2(o[2 * e], o[2 * e + 1]));
+                o[2 * e] = d.x;
+                o[2 * e + 1] = d.y;
+            }
+            c.template store<T>(gx, o);
+        }
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(empty(slot));
+        if (++slot == D) {
+            slot = 0;
+            phase ^= 1u;
         }
     }
     if (a.parts == nullptr) return;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        const int c = (threadIdx.x + i * blockDim.x) * 8;
-        if (c < a.N) {
-            float *p = a.parts + static_cast<int64_t>(blockIdx.x) * a.N + c;
-            raw_store<float>(p, raw_pack<float>(acc[i]));
-        }
+        const float v[8] = {acc[i][0].x, acc[i][0].y, acc[i][1].x, acc[i][1].y, acc[i][2].x, acc[i][2].y, acc[i][3].x, acc[i][3].y};
+        Columns<VEC>(i, a.N, threads).template store<float>(a.parts + static_cast<int64_t>(blockIdx.x) * a.N, v);
     }
 }
 
-// Rows of any alignment and width: the rows' sums, then strips of columns.
+// Wider rows than that keeps: the rows' sums, then strips of columns.
 template <typename T> __device__ __forceinline__ float weight1(const BackArgs &a, int c) {
     return a.w == nullptr ? 1.0f : a.w_f32 ? __ldg(static_cast<const float *>(a.w) + c) : Elem<T>::to_f32(static_cast<const T *>(a.w)[c]);
 }
@@ -485,15 +611,22 @@ template <typename T> __global__ void __launch_bounds__(kStrip) rms_back_strips_
     if (a.parts != nullptr) a.parts[static_cast<int64_t>(blockIdx.y) * a.N + c] = acc;
 }
 
-// gw = the parts' sum: 32 columns a CTA, 32 rows of parts at a time.
+// gw = the parts' sum: 32 columns a CTA, 32 rows of parts at a time, eight of them on their way a thread.
 __global__ void __launch_bounds__(1024) rms_back_join_kernel(const float *parts, int chunks, int N, float *gw) {
     __shared__ float red[32][33];
     if (threadIdx.x == 0) pdl_launch_dependents();
     pdl_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
     float v = 0.0f;
-    if (c < N)
-        for (int i = warp; i < chunks; i += 32) v += parts[static_cast<int64_t>(i) * N + c];
+    if (c < N) {
+        for (int i = warp; i < chunks; i += 32 * 8) {
+            float p[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) p[k] = i + 32 * k < chunks ? parts[static_cast<int64_t>(i + 32 * k) * N + c] : 0.0f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v += p[k];
+        }
+    }
     red[warp][lane] = v;
     __syncthreads();
     v = red[lane][warp];
@@ -510,8 +643,9 @@ template <typename T> cudaError_t norm(const NormArgs &a, bool vec, cudaStream_t
     const dim3 grid(static_cast<unsigned>(a.T));
     if (vec) {
         const int64_t groups = (a.cols + 7) / 8;
-        // few rows: as many threads as there are loads; many: two loads a thread in flight
-        const int v = groups > 2048 ? 4 : groups > 1024 || a.T > 2 * device_sm_count() ? 2 : 1;
+        // few rows: as many threads as there are loads (16 x 4096: 2.8 us, 4.3 with four loads a thread); many: four loads
+        // a thread on their way (8192 x 4096 with codes: 53 us, 64 with one, 58.5 with two, 65 with eight)
+        const int v = groups > 2048 || a.T > 8 * device_sm_count() ? 4 : groups > 1024 || a.T > 2 * device_sm_count() ? 2 : 1;
         const dim3 block(whole_warps((groups + v - 1) / v));
         if (v == 1) return launch_pdl(rms_norm_kernel<T, 1>, grid, block, s, a);
         if (v == 2) return launch_pdl(rms_norm_kernel<T, 2>, grid, block, s, a);
@@ -521,25 +655,42 @@ template <typename T> cudaError_t norm(const NormArgs &a, bool vec, cudaStream_t
     return launch_pdl(rms_norm_any_kernel<T, 16>, grid, dim3(a.cols < 16384 ? whole_warps((a.cols + 15) / 16) : 1024), s, a);
 }
 
-constexpr int kBackMost = 512 * 8 * 4;      // the widest row that rms_back_kernel takes
+// Rows that rms_back_kernel takes: two of them (g, h and gs) fit in its ring.
+constexpr int kRingMost = 208 * 1024;
+constexpr int kBackCtas = 2;                // an SM: three hold fewer rows and leave more parts of gw (31 -> 40 us)
+int row_pitch(int64_t N, int elem) { return static_cast<int>((N * elem + 15) / 16 * 16 + 16); }
+int weight_bytes(int64_t N) { return static_cast<int>((N + 2047) / 2048 * 2048 * 4); }
+bool back_ring(int64_t N, int elem) { return N <= 16384 && 6 * row_pitch(N, elem) + weight_bytes(N) <= kRingMost; }
 
-int back_chunks(int64_t T, int64_t N, bool vec) {
-    const int64_t sms = device_sm_count();
-    int64_t n = vec ? 2 * sms : (8 * sms + (N + kStrip - 1) / kStrip - 1) / ((N + kStrip - 1) / kStrip);
+int back_chunks(int64_t T, int64_t N, int elem) {
+    const int64_t sms = device_sm_count(), strips = (N + kStrip - 1) / kStrip;
+    int64_t n = back_ring(N, elem) ? kBackCtas * sms : (8 * sms + strips - 1) / strips;
     if (n > T) n = T;
     return static_cast<int>(n < 1 ? 1 : n);
 }
 
+template <typename T, int V, int MOST, bool VEC> cudaError_t back_launch(const BackArgs &a, cudaStream_t s) {
+    auto kern = rms_back_kernel<T, V, MOST, VEC>;
+    static ContextOnce once;
+    if (const cudaError_t e = allow_smem(kern, kRingMost, once); e != cudaSuccess) return e;
+    const unsigned threads = whole_warps(((a.N + 7) / 8 + V - 1) / V) + 32;
+    const size_t smem = static_cast<size_t>(a.ahead) * (a.gs != nullptr ? 3 : 2) * static_cast<size_t>(a.pitch) + (threads - 32) * V * 32;
+    return launch_pdl_smem(kern, dim3(static_cast<unsigned>(a.chunks)), dim3(threads), smem, s, a);
+}
+template <typename T, bool VEC> cudaError_t back_rows(BackArgs a, cudaStream_t s) {
+    const int64_t groups = (a.N + 7) / 8;
+    a.pitch = row_pitch(a.N, sizeof(T));
+    const int per = (a.gs != nullptr ? 3 : 2) * a.pitch;
+    a.ahead = (kRingMost / kBackCtas - weight_bytes(a.N)) / per;
+    a.ahead = a.ahead < 2 ? 2 : a.ahead > 3 ? 3 : a.ahead;
+    if (groups <= 256) return back_launch<T, 1, 256, VEC>(a, s);
+    if (groups <= 512) return back_launch<T, 2, 256, VEC>(a, s);
+    if (groups <= 1024) return back_launch<T, 2, 512, VEC>(a, s);
+    return back_launch<T, 4, 512, VEC>(a, s);
+}
 template <typename T> cudaError_t backward(BackArgs a, bool vec, cudaStream_t s) {
-    a.chunks = back_chunks(a.T, a.N, vec);
-    if (vec) {
-        const int64_t groups = a.N / 8;
-        const int v = groups > 1024 ? 4 : groups > 256 ? 2 : 1;
-        const dim3 grid(static_cast<unsigned>(a.chunks)), block(whole_warps((groups + v - 1) / v));
-        if (v == 1) return launch_pdl(rms_back_kernel<T, 1>, grid, block, s, a);
-        if (v == 2) return launch_pdl(rms_back_kernel<T, 2>, grid, block, s, a);
-        return launch_pdl(rms_back_kernel<T, 4>, grid, block, s, a);
-    }
+    a.chunks = back_chunks(a.T, a.N, sizeof(T));
+    if (back_ring(a.N, sizeof(T))) return vec ? back_rows<T, true>(a, s) : back_rows<T, false>(a, s);
     const cudaError_t e = launch_pdl(rms_back_rows_kernel<T>, dim3(static_cast<unsigned>(a.T)), dim3(512), s, a);
     if (e != cudaSuccess) return e;
     return launch_pdl(rms_back_strips_kernel<T>,
@@ -608,11 +759,16 @@ bt_status bt_rms_norm(const void *x, bt_dtype dtype, int64_t ldx, const void *re
     return err == cudaSuccess ? BT_OK : BT_ERR_CUDA;
 }
 
-// The parts of gw (as many as either path has) and the rows' sums.
+// The parts of gw, and the sums of rows that are wider than a CTA keeps.
 size_t bt_rms_norm_backward_workspace(int64_t T, int64_t N) {
     if (T < 1 || N < 1 || T >= kMaxSide || N >= kMaxSide) return 0;
-    const int a = back_chunks(T, N, true), b = back_chunks(T, N, false);
-    return round_up256(static_cast<size_t>(T) * 16) + round_up256(static_cast<size_t>(a > b ? a : b) * static_cast<size_t>(N) * 4);
+    // (the largest that any type needs)
+    size_t most = 0;
+    for (int elem = 2; elem <= 4; elem += 2) {
+        const size_t n = (back_ring(N, elem) ? 0 : round_up256(static_cast<size_t>(T) * 16)) + static_cast<size_t>(back_chunks(T, N, elem)) * static_cast<size_t>(N) * 4;
+        most = n > most ? n : most;
+    }
+    return round_up256(most);
 }
 
 bt_status bt_rms_norm_backward(const void *g, bt_dtype dtype, int64_t ldg, const void *h, int64_t ldh, const void *weight,
@@ -647,14 +803,17 @@ bt_status bt_rms_norm_backward(const void *g, bt_dtype dtype, int64_t ldg, const
     a.eps = static_cast<float>(eps);
     a.gx = grad_x;
     a.rows = static_cast<float4 *>(workspace);
-    float *parts = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + round_up256(static_cast<size_t>(T) * 16));
+    const int elem = dtype_bytes(dtype);
+    float *parts = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + (back_ring(N, elem) ? 0 : round_up256(static_cast<size_t>(T) * 16)));
+    a.err = device_error_word();
+    if (a.err == nullptr) return BT_ERR_CUDA;
     a.parts = grad_weight == nullptr ? nullptr : parts;
-    const bool vec = N % 8 == 0 && N <= kBackMost && wide_rows(g, ldg, dtype) && wide_rows(h, ldh, dtype) && wide_rows(grad_sum, ldgs, dtype) &&
+    const bool vec = N % 8 == 0 && wide_rows(g, ldg, dtype) && wide_rows(h, ldh, dtype) && wide_rows(grad_sum, ldgs, dtype) &&
                      wide_rows(grad_x, ldgx, dtype) && aligned(weight, 16);
     cudaError_t err = dtype == BT_F32 ? backward<float>(a, vec, s) : dtype == BT_BF16 ? backward<__nv_bfloat16>(a, vec, s) : backward<__half>(a, vec, s);
     if (err == cudaSuccess && grad_weight != nullptr)
         err = launch_pdl(rms_back_join_kernel, dim3(static_cast<unsigned>((N + 31) / 32)), dim3(1024), s, static_cast<const float *>(parts),
-                         back_chunks(T, N, vec), static_cast<int>(N), grad_weight);
+                         back_chunks(T, N, elem), static_cast<int>(N), grad_weight);
     return err == cudaSuccess ? BT_OK : BT_ERR_CUDA;
 }
 
