@@ -1173,7 +1173,8 @@ def bt_clip_grads(grads, max_norm: float, eps: float = 1e-6, norm: torch.Tensor 
     # (maps, sets and arrays: hundreds of tensors are looked at before a launch of microseconds)
     n, first = len(grads), grads[0]
     dtypes = list(map(_dtype_of, grads))
-    if not set(dtypes).issubset(_FLOATS) or not first.is_cuda:
+    kinds = set(dtypes)
+    if not kinds.issubset(_FLOATS) or not first.is_cuda:
         raise ValueError("grads must be CUDA tensors of float32, bfloat16 or float16")
     _same_device(first, stream, norm, workspace)
     if set(map(torch.Tensor.get_device, grads)) != {first.get_device()}:
@@ -1188,7 +1189,7 @@ def bt_clip_grads(grads, max_norm: float, eps: float = 1e-6, norm: torch.Tensor 
     workspace = _scratch(workspace, need, first.device, stream)
     pointers = array.array("Q", map(torch.Tensor.data_ptr, grads))
     numels = array.array("q", map(torch.Tensor.numel, grads))
-    types = array.array("i", map(_DT.__getitem__, dtypes))
+    types = array.array("i", map(_DT.__getitem__, dtypes)) if len(kinds) > 1 else array.array("i", (_DT[first.dtype],)) * n
     _check(_c_clip(pointers.buffer_info()[0], numels.buffer_info()[0], types.buffer_info()[0], n, max_norm, eps, norm.data_ptr(),
                    _ptr(workspace), need, _on_stream(stream, first.device)))
     return norm

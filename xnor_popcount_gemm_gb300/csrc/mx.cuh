@@ -54,6 +54,28 @@ __device__ __forceinline__ float power_of(uint32_t s) {
     return __uint_as_float(s == 0u ? 0x00400000u : s == kNanScale ? 0x7FFFFFFFu : s << 23);
 }
 
+// Two fp32 operations an instruction.
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n.reg .b64 x, y, r;\nmov.b64 x, {%2, %3};\nmov.b64 y, {%4, %5};\nadd.rn.f32x2 r, x, y;\nmov.b64 {%0, %1}, r;\n}\n"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n.reg .b64 x, y, r;\nmov.b64 x, {%2, %3};\nmov.b64 y, {%4, %5};\nmul.rn.f32x2 r, x, y;\nmov.b64 {%0, %1}, r;\n}\n"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n.reg .b64 x, y, z, r;\nmov.b64 x, {%2, %3};\nmov.b64 y, {%4, %5};\nmov.b64 z, {%6, %7};\nfma.rn.f32x2 r, x, y, z;\n"
+        "mov.b64 {%0, %1}, r;\n}\n"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 sub2(float2 a, float2 b) { return fma2(b, make_float2(-1.0f, -1.0f), a); }
+
 // Two codes: lo in the low byte (nibble).
 template <int CODE> __device__ __forceinline__ uint32_t code2(float lo, float hi) {
     if constexpr (CODE == BT_CODE_E4M3)
@@ -64,14 +86,14 @@ template <int CODE> __device__ __forceinline__ uint32_t code2(float lo, float hi
 // Eight codes of v * inv; zeros where inv is 0 (a NaN block).
 template <int CODE> __device__ __forceinline__ uint2 code8(const float (&v)[8], float inv) {
     if (inv == 0.0f) return make_uint2(0u, 0u);
-    if constexpr (CODE == BT_CODE_E4M3) {
-        return make_uint2(code2<CODE>(v[0] * inv, v[1] * inv) | (code2<CODE>(v[2] * inv, v[3] * inv) << 16),
-                          code2<CODE>(v[4] * inv, v[5] * inv) | (code2<CODE>(v[6] * inv, v[7] * inv) << 16));
-    } else {
-        return make_uint2(code2<CODE>(v[0] * inv, v[1] * inv) | (code2<CODE>(v[2] * inv, v[3] * inv) << 8) |
-                              (code2<CODE>(v[4] * inv, v[5] * inv) << 16) | (code2<CODE>(v[6] * inv, v[7] * inv) << 24),
-                          0u);
+    uint32_t c[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 q = mul2(make_float2(v[2 * i], v[2 * i + 1]), make_float2(inv, inv));
+        c[i] = code2<CODE>(q.x, q.y);
     }
+    if constexpr (CODE == BT_CODE_E4M3) return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+    else return make_uint2(c[0] | (c[1] << 8) | (c[2] << 16) | (c[3] << 24), 0u);
 }
 template <int CODE> __device__ __forceinline__ void store8(uint8_t *p, const uint2 &c) {
     if constexpr (CODE == BT_CODE_E4M3) *reinterpret_cast<uint2 *>(p) = c;
@@ -152,6 +174,7 @@ template <typename T> __device__ __forceinline__ void raw_store(T *p, const Raw8
 // The same at any element address: `valid` of them are there (<= 0: none), the rest zeros. al: what p is a multiple of
 // (16, 8, 4 or 2; smaller than 16 goes by the widest loads that it allows).
 template <typename T> __device__ __forceinline__ Raw8<T> raw_load_any(const T *p, int valid, int al) {
+    if (valid <= 0) return Raw8<T>{};       // (p may lie anywhere then)
     if (al == 16 && valid >= 8) return raw_load<T>(p);
     uint32_t w[sizeof(T) * 2] = {};
     if (valid >= 8 && al == 8) {
@@ -220,34 +243,28 @@ template <typename T> inline int rows_align(const T *p, int64_t ld, int elem) {
     return v % 16 == 0 ? 16 : v % 8 == 0 ? 8 : v % 4 == 0 ? 4 : 2;
 }
 
-// Two fp32 operations an instruction.
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-    float2 d;
-    asm("{\n.reg .b64 x, y, r;\nmov.b64 x, {%2, %3};\nmov.b64 y, {%4, %5};\nadd.rn.f32x2 r, x, y;\nmov.b64 {%0, %1}, r;\n}\n"
-        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return d;
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-    float2 d;
-    asm("{\n.reg .b64 x, y, r;\nmov.b64 x, {%2, %3};\nmov.b64 y, {%4, %5};\nmul.rn.f32x2 r, x, y;\nmov.b64 {%0, %1}, r;\n}\n"
-        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return d;
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-    float2 d;
-    asm("{\n.reg .b64 x, y, z, r;\nmov.b64 x, {%2, %3};\nmov.b64 y, {%4, %5};\nmov.b64 z, {%6, %7};\nfma.rn.f32x2 r, x, y, z;\n"
-        "mov.b64 {%0, %1}, r;\n}\n"
-        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-    return d;
-}
-__device__ __forceinline__ float2 sub2(float2 a, float2 b) { return fma2(b, make_float2(-1.0f, -1.0f), a); }
-
-// Four lanes next to one another hold a block: its largest magnitude, in all of them.
-__device__ __forceinline__ uint32_t quad_max(uint32_t m) {
-    uint32_t o = __shfl_xor_sync(0xFFFFFFFFu, m, 1);
-    m = m > o ? m : o;
-    o = __shfl_xor_sync(0xFFFFFFFFu, m, 2);
-    return m > o ? m : o;
+// Four lanes next to one another hold a block: the bits of its largest magnitude as fp32, in all of them. 16-bit values go
+// two by two (the order of their bits is that of their magnitudes too).
+template <typename T> __device__ __forceinline__ uint32_t quad_top(const Raw8<T> &r) {
+    if constexpr (sizeof(T) == 4) {
+        const uint32_t w[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
+        uint32_t m = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) m = max(m, w[e] & 0x7FFFFFFFu);
+        m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+        return max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+    } else {
+        constexpr uint32_t kMag = 0x7FFF7FFFu;
+        uint32_t m = __vmaxu2(__vmaxu2(r.a.x & kMag, r.a.y & kMag), __vmaxu2(r.a.z & kMag, r.a.w & kMag));
+        m = __vmaxu2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+        m = __vmaxu2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+        m = max(m & 0xFFFFu, m >> 16);
+        if constexpr (std::is_same<T, __half>::value) {
+            const uint16_t h = static_cast<uint16_t>(m);
+            return __float_as_uint(__half2float(*reinterpret_cast<const __half *>(&h)));
+        }
+        return m << 16;
+    }
 }
 // Sixteen lanes hold an atom's four blocks of a row, quad by quad: their scale bytes as one word, in the first of them.
 __device__ __forceinline__ uint32_t atom_word(uint32_t s) {

@@ -83,6 +83,11 @@ template <int XB> __device__ __forceinline__ void values_of(const SmallArgs &a, 
     }
 }
 
+template <int XB> __device__ __forceinline__ uint32_t top_of(const SmallArgs &a, const X8<XB> &r) {
+    if constexpr (XB == 4) return quad_top<float>(Raw8<float>{r.a, r.b});
+    else return a.f16 ? quad_top<__half>(Raw8<__half>{r.a}) : quad_top<__nv_bfloat16>(Raw8<__nv_bfloat16>{r.a});
+}
+
 // Slice `slice` of the rows of x from `from` on, NB / 2 of them, as the MMA takes it: codes in rows of 128 bytes in the 128-byte swizzle, atoms of scales.
 // ready(): waits for the stage; false: it ran out.
 template <int CODE, int NB, int XB, typename F>
@@ -129,14 +134,8 @@ __device__ __forceinline__ void x_slice(const SmallArgs &a, int slice, int from,
                 const int row = r0 + i * kPer + row0;
                 if (r0 + i * kPer >= end) break;                              // (the same for all lanes)
                 float v[8];
+                const uint32_t top = top_of<XB>(a, raw[i]);
                 values_of<XB>(a, raw[i], v);
-                uint32_t top = 0;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const uint32_t m = mag_bits(v[e]);
-                    top = m > top ? m : top;
-                }
-                top = quad_max(top);
                 if (row >= end) continue;
                 const uint32_t s = scale_of<CODE>(top);
                 const uint2 c = code8<CODE>(v, inverse_of(s));

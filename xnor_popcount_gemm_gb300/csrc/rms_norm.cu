@@ -176,6 +176,7 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(const NormArgs a) {
         const int g = threadIdx.x + i * blockDim.x, c = g * 8;
         if (c - static_cast<int>(threadIdx.x & 31) * 8 >= a.cols) continue;      // (whole warps)
         float y[8] = {};
+        Raw8<T> o = {};
         if (c < a.N) {
             float v[8], w[8];
             raw_unpack<T>(h[i], v);
@@ -193,18 +194,12 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(const NormArgs a) {
                 y[e] = n.x;
                 y[e + 1] = n.y;
             }
-            const Raw8<T> o = raw_pack<T>(y);
+            o = raw_pack<T>(y);
             if (a.out != nullptr) raw_store<T>(static_cast<T *>(a.out) + row * a.ldo + c, o);
             raw_unpack<T>(o, y);
         }
         if (a.code == kNoCode) continue;
-        uint32_t top = 0;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const uint32_t m = mag_bits(y[e]);
-            top = m > top ? m : top;
-        }
-        top = quad_max(top);
+        const uint32_t top = quad_top<T>(o);
         const bool e4m3 = a.code == BT_CODE_E4M3;
         const uint32_t s = e4m3 ? scale_of<BT_CODE_E4M3>(top) : scale_of<BT_CODE_E2M1>(top), word = atom_word(s);
         if (c >= a.cols) continue;
