@@ -185,7 +185,7 @@ mx_linear_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
             if (leader) {
                 for (int i = 0; i < S; ++i) {
                     uint32_t never = 0;
-                    if (last_phase[i] < 2u) tc::wait_bounded(full(i), last_phase[i], &never, a.err);
+                    if (last_phase[i] < 2u && !tc::wait_bounded(full(i), last_phase[i], &never, a.err)) break;
                 }
             }
         }
@@ -522,10 +522,10 @@ bt_status bt_mx_linear(const void *x, bt_dtype x_dtype, int64_t ldx, const void 
     if (!aligned(w, 16) || !aligned(w_scales, 16) || !aligned(out, static_cast<size_t>(dtype_bytes(out_dtype))) ||
         !aligned(x, packed ? 16 : static_cast<size_t>(dtype_bytes(x_dtype))) || (packed && !aligned(x_scales, 16)))
         return BT_ERR_ALIGNMENT;
-    if (!tc_available()) return BT_ERR_UNSUPPORTED;
     const size_t need = packed ? 0 : bt_mx_linear_workspace(M, N, K, x_dtype, code);
     if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return BT_ERR_WORKSPACE;
     if (need > 0 && !aligned(workspace, 256)) return BT_ERR_ALIGNMENT;
+    if (!tc_available()) return BT_ERR_UNSUPPORTED;
     Product p = {};
     p.err = device_error_word();
     if (p.err == nullptr) return BT_ERR_CUDA;
@@ -565,13 +565,13 @@ bt_status bt_mx_linear_backward(const void *g, int64_t ldg, const void *wt, int6
     if (!aligned(g, 2) || !aligned(wt, 16) || !aligned(grad_x, e)) return BT_ERR_ALIGNMENT;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (N == 0) return cudaMemsetAsync(grad_x, 0, static_cast<size_t>(M) * static_cast<size_t>(K) * e, s) == cudaSuccess ? BT_OK : BT_ERR_CUDA;
+    const bool plain = plain_rows(g, ldg, N);
+    if (!plain && (workspace == nullptr || workspace_bytes < bt_mx_linear_backward_workspace(M, N))) return BT_ERR_WORKSPACE;
+    if (!plain && !aligned(workspace, 256)) return BT_ERR_ALIGNMENT;
     if (!tc_available()) return BT_ERR_UNSUPPORTED;
     const uint16_t *rows = static_cast<const uint16_t *>(g);
     int64_t pitch = ldg;
-    if (!plain_rows(g, ldg, N)) {
-        const size_t need = bt_mx_linear_backward_workspace(M, N);
-        if (workspace == nullptr || workspace_bytes < need) return BT_ERR_WORKSPACE;
-        if (!aligned(workspace, 256)) return BT_ERR_ALIGNMENT;
+    if (!plain) {
         pitch = pitch8(N);
         adapter::AlignArgs al = {};         // (with zeros up to the pitch)
         al.src = rows;

@@ -216,7 +216,7 @@ mx_small_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
             // whatever happens elsewhere, what was asked for lands before shared memory is given back
             for (int j = i > kStages ? i - kStages : 0; j < i; ++j) {
                 uint32_t never = 0;
-                tc::wait_bounded(w_full(j % kStages), static_cast<uint32_t>(j / kStages & 1), &never, a.err);
+                if (!tc::wait_bounded(w_full(j % kStages), static_cast<uint32_t>(j / kStages & 1), &never, a.err)) break;
             }
         }
         __syncwarp();
@@ -266,7 +266,8 @@ mx_small_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
 
     // The sums: through shared memory (the stages are free then), [row of x][row of W].
     float *part = reinterpret_cast<float *>(smem_raw + (sW - raw));
-    bool ok = tc::wait_warp(done, 0u, abort_flag, a.err, kWaitNs);
+    uint32_t never = 0;                                         // (also where a wait ran out: what was issued ends first)
+    bool ok = tc::wait_warp(done, 0u, &never, a.err, kWaitNs);
     __syncthreads();
     ok = ok && *abort_flag == 0u;
     const int quarter = warp & 3;
