@@ -974,7 +974,7 @@ bt_status bt_mx_linear_backward(const void *g, int64_t ldg, const void *wt, int6
  * The fp32 value under the last cast is the correctly rounded one but for about one
  * in 2^24, so that the codes do not depend on how the sum of squares was taken. Rows
  * whose squares leave fp32's range are scaled first. eps >= 0, finite. A row with a
- * NaN is NaN, one with an infinity NaN there and 0 elsewhere; with eps = 0 a row of zeros is NaN. Any element
+ * NaN is NaN, one with an infinity NaN there and 0 elsewhere; with eps = 0 a row of zeros is NaN. The weight is finite. Any element
  * alignment; 16-byte rows with N a multiple of 8 are faster. T = 0 does nothing.
  * T, N < 2^24. Errors: INVALID_ARG, ALIGNMENT, UNSUPPORTED, CUDA.
  */
@@ -1023,7 +1023,7 @@ size_t bt_clip_grads_workspace(int64_t count);
  * The arrays are read before the call returns and the addresses go with the launches:
  * a captured graph keeps them. A norm that is infinite makes the factor 0, a NaN norm
  * makes every gradient NaN, as the formula says. Where the factor is not below one
- * the tensors are not written. Squares are summed in fp32 over at most 64 values, then
+ * the tensors are not written. Squares are summed in fp32 over at most 33 values, then
  * in fp64, in an order that the sizes decide: equal calls give equal results. workspace:
  * bt_clip_grads_workspace(count) bytes, 256-byte aligned. count = 0 gives the norm 0.
  * Errors: INVALID_ARG (overlaps among them), ALIGNMENT, WORKSPACE, UNSUPPORTED, CUDA.

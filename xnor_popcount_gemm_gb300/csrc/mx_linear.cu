@@ -1,20 +1,22 @@
-// Y = X W^T on microscaled operands (see mx.cuh): E2M1 x E2M1 or E4M3 x E4M3, the
-// blocks' scales applied by the tensor cores, fp32 sums in TMEM.
+// Y = X W^T on microscaled operands (see mx.cuh): E2M1 x E2M1 or E4M3 x E4M3, the blocks' scales applied by the tensor
+// cores, fp32 sums in TMEM.
 //
-// Persistent and warp-specialised, one CTA per SM; tiles of 128 rows by BN columns
-// (256 or 128), or, on CTA pairs (tcgen05 cta_group::2), 256 by BN: each CTA brings
-// its 128 rows of X and half of the tile's rows of W, and the scales of its rows of
-// X and of all the tile's rows of W.
-//   warp 0 lane 0   TMA: stages of D 128-byte slices of K, operands (128-byte
-//                   swizzle) and atoms of scales
+// Persistent and warp-specialised, one CTA per SM; tiles of 128 rows by BN columns (256 or 128), or, on CTA pairs (tcgen05
+// cta_group::2), 256 by BN: each CTA brings its 128 rows of X and half of the tile's rows of W, and the scales of its rows
+// of X and of all the tile's rows of W.
+//   warp 0 lane 0   TMA: stages of D 128-byte slices of K, operands (128-byte swizzle) and atoms of scales
 //   warp 1          scales of a slice to TMEM (tcgen05.cp), its four MMAs
-//   warps 2..9      epilogue: two (or one) a TMEM lane quarter, 32 columns at a time, through
-//                   shared memory so that whole row pieces are stored
-// TMEM: two accumulators and two times 32 columns of scales. At BN = 256 the
-// accumulators share 64 columns: a tile's epilogue takes those first, and the next
-// tile's MMAs begin when they are free.
-// Copies of scales and MMAs run in order, so that scales need no barrier; two sets of
-// columns in turn cost nothing.
+//   warps 2..9      epilogue: two (or one) a TMEM lane quarter, 32 columns at a time, through shared memory so that whole
+//                   row pieces are stored
+// TMEM: two accumulators and two times 32 columns of scales. At BN = 256 the accumulators share 64 columns: a tile's
+// epilogue takes those first, and the next tile's MMAs begin when they are free.
+//
+// What bounds it: 8192 x 4096 x 11008 in E2M1 takes 100 us on pairs (7400 TFLOP/s), 640 clocks a slice where its MMAs need 512 and
+// its shared-memory traffic (copies in, operands out) about 650; the tensor pipe is 71 % busy. E4M3 204 to 230 us, by the
+// clock under load. Getting there: the issue of MMAs and copies from a whole warp with its operands in uniform registers
+// (tc_ptx.cuh) 160 -> 104 us. Copies of scales run in order with the MMAs and need no barrier. Not kept, same size: the
+// scales by tcgen05.st from four warps (a store waits about 1000 clocks under an MMA; 250 us on pairs), copies from a
+// warp of their own (157), a slice ahead of their MMAs (244), two slices' at once (175).
 // Every wait is bounded, as in the other tensor-core kernels.
 #include <cstdio>
 #include <cstdlib>

