@@ -188,7 +188,10 @@ template <int MOST> __global__ void __launch_bounds__(kThreads, kCtasPerSm) clip
     }
 }
 
-__global__ void clip_no_norm_kernel(float *norm) { *norm = 0.0f; }
+__global__ void clip_no_norm_kernel(float *norm) {
+    pdl_wait();
+    *norm = 0.0f;
+}
 
 // Tensors from `first` on, as many as go with one launch; returns how many it took (empty ones among them).
 template <int MOST> int64_t fill(Table<MOST> &t, void *const *p, const int64_t *n, const int32_t *type, int64_t first, int64_t count) {

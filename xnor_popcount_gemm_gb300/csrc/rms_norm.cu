@@ -125,7 +125,8 @@ __device__ __forceinline__ float2 normed(float2 v, float2 w, const Inverse &i, b
 
 // A row by its CTA, eight consecutive columns at a time: thread t has the eights
 // t, t + threads, ... (V of them). Rows 16-byte aligned, N a multiple of 8.
-template <typename T, int V>
+// WF: the weight is fp32 and T is not.
+template <typename T, int V, bool WF>
 __global__ void __launch_bounds__(1024) rms_norm_kernel(const NormArgs a) {
     __shared__ float2 red[2][32];
     const int64_t row = blockIdx.x;
@@ -175,34 +176,37 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(const NormArgs a) {
     for (int i = 0; i < V; ++i) {
         const int g = threadIdx.x + i * blockDim.x, c = g * 8;
         if (c - static_cast<int>(threadIdx.x & 31) * 8 >= a.cols) continue;      // (whole warps)
-        float y[8] = {};
         Raw8<T> o = {};
         if (c < a.N) {
-            float v[8], w[8];
+            using W = typename std::conditional<WF, float, T>::type;
+            float v[8], w[8], y[8];
             raw_unpack<T>(h[i], v);
-            if (a.w == nullptr) {
+            if (k != 1.0f) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] *= k;
+            }
+            if (a.w != nullptr) {
+                raw_unpack<W>(raw_load<W>(static_cast<const W *>(a.w) + c), w);
+            } else {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) w[e] = 1.0f;
-            } else if (a.w_f32) {
-                raw_unpack<float>(raw_load<float>(static_cast<const float *>(a.w) + c), w);
-            } else {
-                raw_unpack<T>(raw_load<T>(static_cast<const T *>(a.w) + c), w);
             }
 #pragma unroll
             for (int e = 0; e < 8; e += 2) {
-                const float2 n = normed(make_float2(v[e] * k, v[e + 1] * k), make_float2(w[e], w[e + 1]), inv, sizeof(T) == 2 && !a.w_f32);
+                const float2 n = normed(make_float2(v[e], v[e + 1]), make_float2(w[e], w[e + 1]), inv, sizeof(T) == 2 && !WF);
                 y[e] = n.x;
                 y[e + 1] = n.y;
             }
             o = raw_pack<T>(y);
             if (a.out != nullptr) raw_store<T>(static_cast<T *>(a.out) + row * a.ldo + c, o);
-            raw_unpack<T>(o, y);
         }
         if (a.code == kNoCode) continue;
         const uint32_t top = quad_top<T>(o);
         const bool e4m3 = a.code == BT_CODE_E4M3;
         const uint32_t s = e4m3 ? scale_of<BT_CODE_E4M3>(top) : scale_of<BT_CODE_E2M1>(top), word = atom_word(s);
         if (c >= a.cols) continue;
+        float y[8];
+        raw_unpack<T>(o, y);
         uint8_t *p = a.q + row * a.row_bytes + static_cast<int64_t>(g) * (e4m3 ? 8 : 4);
         if (e4m3) store8<BT_CODE_E4M3>(p, code8<BT_CODE_E4M3>(y, inverse_of(s)));
         else store8<BT_CODE_E2M1>(p, code8<BT_CODE_E2M1>(y, inverse_of(s)));
@@ -642,9 +646,10 @@ template <typename T> cudaError_t norm(const NormArgs &a, bool vec, cudaStream_t
         // a thread on their way (8192 x 4096 with codes: 53 us, 64 with one, 58.5 with two, 65 with eight)
         const int v = groups > 2048 || a.T > 8 * device_sm_count() ? 4 : groups > 1024 || a.T > 2 * device_sm_count() ? 2 : 1;
         const dim3 block(whole_warps((groups + v - 1) / v));
-        if (v == 1) return launch_pdl(rms_norm_kernel<T, 1>, grid, block, s, a);
-        if (v == 2) return launch_pdl(rms_norm_kernel<T, 2>, grid, block, s, a);
-        return launch_pdl(rms_norm_kernel<T, 4>, grid, block, s, a);
+        const bool wf = sizeof(T) == 2 && a.w != nullptr && a.w_f32;
+        if (v == 1) return launch_pdl(wf ? rms_norm_kernel<T, 1, true> : rms_norm_kernel<T, 1, false>, grid, block, s, a);
+        if (v == 2) return launch_pdl(wf ? rms_norm_kernel<T, 2, true> : rms_norm_kernel<T, 2, false>, grid, block, s, a);
+        return launch_pdl(wf ? rms_norm_kernel<T, 4, true> : rms_norm_kernel<T, 4, false>, grid, block, s, a);
     }
     if (a.cols <= 8192) return launch_pdl(rms_norm_any_kernel<T, 8>, grid, dim3(whole_warps((a.cols + 7) / 8)), s, a);
     return launch_pdl(rms_norm_any_kernel<T, 16>, grid, dim3(a.cols < 16384 ? whole_warps((a.cols + 15) / 16) : 1024), s, a);
