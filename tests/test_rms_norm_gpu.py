@@ -59,7 +59,8 @@ def test_norm(N, dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
-@pytest.mark.parametrize("T,N", [(1, 4096), (400, 4096), (700, 256), (330, 1001), (400, 12000)])
+@pytest.mark.parametrize("T,N", [(1, 4096), (400, 4096), (700, 256), (330, 1001), (400, 12000), (1300, 4093), (1300, 2048), (2500, 128), (5000, 64),
+                                 (30000, 96), (2600, 512), (2600, 1000), (2433, 1024), (2600, 90)])
 def test_norm_many_rows_and_weights(T, N, dtype):
     x = rows(T, T, N, dtype)
     for w in (None, torch.rand(N).cuda() + 0.5, (torch.rand(N).cuda() - 0.5).to(dtype)):
@@ -168,7 +169,8 @@ def test_backward(N, dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
-@pytest.mark.parametrize("T,N", [(1, 64), (3, 4096), (400, 512), (777, 1001), (1300, 96), (650, 4096), (40, 12000)])
+@pytest.mark.parametrize("T,N", [(1, 64), (3, 4096), (400, 512), (777, 1001), (1300, 96), (650, 4096), (40, 12000), (2500, 128), (2433, 8), (9000, 31),
+                                 (2600, 512), (2600, 1000), (2433, 1024), (2600, 777), (700, 8192), (310, 16384), (310, 11005)])
 def test_backward_many_rows(T, N, dtype):
     for residual, weight in ((True, True), (False, True), (False, False)):
         check_backward(T, N, dtype, residual, weight, seed=T)
@@ -228,6 +230,28 @@ def test_backward_is_the_gradient():
     u = torch.randn(N, generator=gen, dtype=torch.float64)
     diff = (loss(h, w + step * u) - loss(h, w - step * u)) / (2 * step)
     assert abs(float((gw.cpu().double() * u).sum()) - diff) <= 1e-6 * size
+
+
+def test_rows_far_apart():
+    # offsets beyond 32 bits, in every operand
+    ld, T, N = (1 << 30) + 24, 3, 200
+    def far(t):
+        buf = torch.empty((T - 1) * ld + N, dtype=BF16, device="cuda")
+        v = buf.as_strided((T, N), (ld, 1))
+        v.copy_(t)
+        return v
+    x, r, g = rows(1, T, N, BF16), rows(2, T, N, BF16), rows(3, T, N, BF16)
+    y, h, q = bt.bt_rms_norm(x, None, residual=r, code=E4M3)
+    gx, gw = bt.bt_rms_norm_backward(g, h)
+    fx, fr, fo = far(x), far(r), far(x)
+    y2, h2, q2 = bt.bt_rms_norm(fx, None, residual=fr, sum=fr, out=fo, code=E4M3)
+    assert torch.equal(y2, y) and torch.equal(h2, h) and same_operand(q, q2)
+    assert same_operand(q, bt.bt_mx_quantize(fo, E4M3))
+    bt.bt_mx_dequantize(q, out=fx)
+    assert torch.equal(fx, bt.bt_mx_dequantize(q, BF16))
+    fx.copy_(g)
+    gx2, gw2 = bt.bt_rms_norm_backward(fx, fr, grad_x=fo)
+    assert torch.equal(gx2, gx) and torch.equal(gw2, gw)
 
 
 def test_empty_and_graph():

@@ -37,6 +37,7 @@ struct NormArgs {
     uint8_t *q, *s;
     int64_t row_bytes, atoms;
     int cols;                               // N, or the columns up to the end of the last atom
+    int al_x, al_r, al_sum, al_out, al_w;   // what their rows start at multiples of
 };
 
 // A sum and the rounding errors made in it.
@@ -69,27 +70,24 @@ struct Sums {
     }
 };
 
-// The block's sum, in every thread, in an order that the thread count alone decides.
-__device__ __forceinline__ Sum2 block_sum(Sum2 v, float2 (&red)[32]) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        const float s = __shfl_xor_sync(0xFFFFFFFFu, v.s, o), c = __shfl_xor_sync(0xFFFFFFFFu, v.c, o);
-        v.join(s, c);
-    }
-    const int warps = blockDim.x >> 5;
-    if (warps == 1) return v;
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = make_float2(v.s, v.c);
-    __syncthreads();
-    const int lane = threadIdx.x & 31;
-    const float2 p = lane < warps ? red[lane] : make_float2(0.0f, 0.0f);
-    v.s = p.x;
-    v.c = p.y;
+// The warp's sum, and the block's, in every thread, in an order that the thread count alone decides.
+__device__ __forceinline__ Sum2 warp_sum(Sum2 v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         const float s = __shfl_xor_sync(0xFFFFFFFFu, v.s, o), c = __shfl_xor_sync(0xFFFFFFFFu, v.c, o);
         v.join(s, c);
     }
     return v;
+}
+__device__ __forceinline__ Sum2 block_sum(Sum2 v, float2 (&red)[32]) {
+    v = warp_sum(v);
+    const int warps = blockDim.x >> 5;
+    if (warps == 1) return v;
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = make_float2(v.s, v.c);
+    __syncthreads();
+    const int lane = threadIdx.x & 31;
+    const float2 p = lane < warps ? red[lane] : make_float2(0.0f, 0.0f);
+    return warp_sum(Sum2{p.x, p.y});
 }
 
 // Rows whose squares leave fp32 are summed again, their values times this power of two.
@@ -123,94 +121,118 @@ __device__ __forceinline__ float2 normed(float2 v, float2 w, const Inverse &i, b
     return fma2(p, hi, rest);
 }
 
-// A row by its CTA, eight consecutive columns at a time: thread t has the eights
-// t, t + threads, ... (V of them). Rows 16-byte aligned, N a multiple of 8.
-// WF: the weight is fp32 and T is not.
-template <typename T, int V, bool WF>
-__global__ void __launch_bounds__(1024) rms_norm_kernel(const NormArgs a) {
+// Rows eight consecutive columns at a time: thread t has the eights t, t + threads, ... (V of them).
+enum Kind {
+    kWide,          // rows 16-byte aligned, N a multiple of 8; a row by its CTA; the weight is of type T (or fp32 where T is)
+    kWideF32,       // the same with an fp32 weight beside 16-bit rows
+    kAligned2,      // 16-bit rows of any alignment and width, a row by its CTA
+    kWarp,          // as kWide with any weight; a row by a warp, for many short ones
+};
+template <typename T, int V, Kind KIND>
+__global__ void __launch_bounds__(KIND == kWarp ? 256 : 1024) rms_norm_kernel(const NormArgs a) {
     __shared__ float2 red[2][32];
-    const int64_t row = blockIdx.x;
-    const T *x = static_cast<const T *>(a.x) + row * a.ldx;
-    const T *r = static_cast<const T *>(a.r) + row * a.ldr;
+    constexpr bool kWhole = KIND != kAligned2;
+    const int threads = KIND == kWarp ? 32 : blockDim.x, tid = KIND == kWarp ? threadIdx.x & 31 : threadIdx.x;
+    const int rows = KIND == kWarp ? gridDim.x * (blockDim.x >> 5) : gridDim.x;
     if (threadIdx.x == 0) pdl_launch_dependents();
     pdl_wait();
-    Raw8<T> h[V], rr[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const int c = (threadIdx.x + i * blockDim.x) * 8;
-        h[i] = Raw8<T>{};
-        if (c >= a.N) continue;
-        h[i] = raw_load<T>(x + c);
-        if (a.r != nullptr) rr[i] = raw_load<T>(r + c);
-    }
-    if (a.r != nullptr) {
+    for (int64_t row = KIND == kWarp ? blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5) : blockIdx.x; row < a.T; row += rows) {
+        const T *x = static_cast<const T *>(a.x) + row * a.ldx;
+        const T *r = static_cast<const T *>(a.r) + row * a.ldr;
+        auto load = [&](const T *p, int c, int al) { return kWhole ? raw_load<T>(p + c) : raw_load_any<T>(p + c, a.N - c, al); };
+        auto store = [&](void *p, int64_t ld, int c, int al, const Raw8<T> &v) {
+            T *q = static_cast<T *>(p) + row * ld + c;
+            if (kWhole) raw_store<T>(q, v);
+            else raw_store_any<T>(q, v, a.N - c, al);
+        };
+        Raw8<T> h[V], rr[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const int c = (threadIdx.x + i * blockDim.x) * 8;
+            const int c = (tid + i * threads) * 8;
+            h[i] = Raw8<T>{};
             if (c >= a.N) continue;
-            float v[8], o[8];
-            raw_unpack<T>(h[i], v);
-            raw_unpack<T>(rr[i], o);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] += o[e];
-            h[i] = raw_pack<T>(v);
-            if (a.sum != nullptr) raw_store<T>(static_cast<T *>(a.sum) + row * a.lds + c, h[i]);
+            h[i] = load(x, c, a.al_x);
+            if (a.r != nullptr) rr[i] = load(r, c, a.al_r);
         }
-    }
-    auto squares = [&](float k) {
-        Sums p{};
+        if (a.r != nullptr) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const int c = (tid + i * threads) * 8;
+                if (c >= a.N) continue;
+                float v[8], o[8];
+                raw_unpack<T>(h[i], v);
+                raw_unpack<T>(rr[i], o);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] += o[e];
+                h[i] = raw_pack<T>(v);
+                if (a.sum != nullptr) store(a.sum, a.lds, c, a.al_sum, h[i]);
+            }
+        }
+        auto squares = [&](float k) {
+            Sums p{};
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                float v[8];
+                raw_unpack<T>(h[i], v);
+#pragma unroll
+                for (int e = 0; e < 8; e += 2) p.square<sizeof(T) == 2>(make_float2(v[e] * k, v[e + 1] * k));
+            }
+            return p.joined();
+        };
+        auto together = [&](Sum2 v, float2 (&x2)[32]) { return KIND == kWarp ? warp_sum(v) : block_sum(v, x2); };
+        Sum2 total = together(squares(1.0f), red[0]);
+        const float k = power_for(total.s, a.eps, a.N);
+        if (k != 1.0f) total = together(squares(k), red[1]);
+        const Inverse inv = inverse_rms(total, a, k);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            float v[8];
-            raw_unpack<T>(h[i], v);
+            const int g = tid + i * threads, c = g * 8;
+            if (c - (tid & 31) * 8 >= a.cols) continue;                 // (whole warps)
+            Raw8<T> o = {};
+            if (c < a.N) {
+                float v[8], w[8], y[8];
+                raw_unpack<T>(h[i], v);
+                if (k != 1.0f) {
 #pragma unroll
-            for (int e = 0; e < 8; e += 2) p.square<sizeof(T) == 2>(make_float2(v[e] * k, v[e + 1] * k));
+                    for (int e = 0; e < 8; ++e) v[e] *= k;
+                }
+                const bool f32 = KIND == kWideF32 || (sizeof(T) == 2 && (KIND == kAligned2 || KIND == kWarp) && a.w_f32);
+                if (a.w == nullptr) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) w[e] = 1.0f;
+                } else if (f32) {
+                    const float *p = static_cast<const float *>(a.w) + c;
+                    raw_unpack<float>(kWhole ? raw_load<float>(p) : raw_load_any<float>(p, a.N - c, a.al_w), w);
+                } else {
+                    raw_unpack<T>(load(static_cast<const T *>(a.w), c, a.al_w), w);
+                }
+                const bool exact = sizeof(T) == 2 && !f32;
+#pragma unroll
+                for (int e = 0; e < 8; e += 2) {
+                    const float2 n = normed(make_float2(v[e], v[e + 1]), make_float2(w[e], w[e + 1]), inv, exact);
+                    y[e] = n.x;
+                    y[e + 1] = n.y;
+                }
+                if (!kWhole) {                                          // (what is past N was zero: 0 / 0 stays out of the block)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) y[e] = c + e < a.N ? y[e] : 0.0f;
+                }
+                o = raw_pack<T>(y);
+                if (a.out != nullptr) store(a.out, a.ldo, c, a.al_out, o);
+            }
+            if (a.code == kNoCode) continue;
+            const uint32_t top = quad_top<T>(o);
+            const bool e4m3 = a.code == BT_CODE_E4M3;
+            const uint32_t s = e4m3 ? scale_of<BT_CODE_E4M3>(top) : scale_of<BT_CODE_E2M1>(top), word = atom_word(s);
+            if (c >= a.cols) continue;
+            float y[8];
+            raw_unpack<T>(o, y);
+            uint8_t *p = a.q + row * a.row_bytes + static_cast<int64_t>(g) * (e4m3 ? 8 : 4);
+            if (e4m3) store8<BT_CODE_E4M3>(p, code8<BT_CODE_E4M3>(y, inverse_of(s)));
+            else store8<BT_CODE_E2M1>(p, code8<BT_CODE_E2M1>(y, inverse_of(s)));
+            if ((tid & 15) == 0) *reinterpret_cast<uint32_t *>(a.s + scale_at(row, g >> 2, a.atoms)) = word;
         }
-        return p.joined();
-    };
-    Sum2 total = block_sum(squares(1.0f), red[0]);
-    const float k = power_for(total.s, a.eps, a.N);
-    if (k != 1.0f) total = block_sum(squares(k), red[1]);
-    const Inverse inv = inverse_rms(total, a, k);
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const int g = threadIdx.x + i * blockDim.x, c = g * 8;
-        if (c - static_cast<int>(threadIdx.x & 31) * 8 >= a.cols) continue;      // (whole warps)
-        Raw8<T> o = {};
-        if (c < a.N) {
-            using W = typename std::conditional<WF, float, T>::type;
-            float v[8], w[8], y[8];
-            raw_unpack<T>(h[i], v);
-            if (k != 1.0f) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] *= k;
-            }
-            if (a.w != nullptr) {
-                raw_unpack<W>(raw_load<W>(static_cast<const W *>(a.w) + c), w);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) w[e] = 1.0f;
-            }
-#pragma unroll
-            for (int e = 0; e < 8; e += 2) {
-                const float2 n = normed(make_float2(v[e], v[e + 1]), make_float2(w[e], w[e + 1]), inv, sizeof(T) == 2 && !WF);
-                y[e] = n.x;
-                y[e + 1] = n.y;
-            }
-            o = raw_pack<T>(y);
-            if (a.out != nullptr) raw_store<T>(static_cast<T *>(a.out) + row * a.ldo + c, o);
-        }
-        if (a.code == kNoCode) continue;
-        const uint32_t top = quad_top<T>(o);
-        const bool e4m3 = a.code == BT_CODE_E4M3;
-        const uint32_t s = e4m3 ? scale_of<BT_CODE_E4M3>(top) : scale_of<BT_CODE_E2M1>(top), word = atom_word(s);
-        if (c >= a.cols) continue;
-        float y[8];
-        raw_unpack<T>(o, y);
-        uint8_t *p = a.q + row * a.row_bytes + static_cast<int64_t>(g) * (e4m3 ? 8 : 4);
-        if (e4m3) store8<BT_CODE_E4M3>(p, code8<BT_CODE_E4M3>(y, inverse_of(s)));
-        else store8<BT_CODE_E2M1>(p, code8<BT_CODE_E2M1>(y, inverse_of(s)));
-        if ((threadIdx.x & 15) == 0) *reinterpret_cast<uint32_t *>(a.s + scale_at(row, g >> 2, a.atoms)) = word;
+        if (KIND != kWarp) break;                                       // (a row a CTA)
     }
 }
 
@@ -323,25 +345,24 @@ struct BackArgs {
     unsigned int *err;
 };
 constexpr int kMostAhead = 3;
+constexpr int kWarpRow = 512;               // the longest row that goes to a warp
 
-__device__ __forceinline__ float2 block_pair(float2 v, float2 (&red)[32]) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        v.x += __shfl_xor_sync(0xFFFFFFFFu, v.x, o);
-        v.y += __shfl_xor_sync(0xFFFFFFFFu, v.y, o);
-    }
-    const int warps = blockDim.x >> 5;
-    if (warps == 1) return v;
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-    __syncthreads();
-    const int lane = threadIdx.x & 31;
-    v = lane < warps ? red[lane] : make_float2(0.0f, 0.0f);
+__device__ __forceinline__ float2 warp_pair(float2 v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         v.x += __shfl_xor_sync(0xFFFFFFFFu, v.x, o);
         v.y += __shfl_xor_sync(0xFFFFFFFFu, v.y, o);
     }
     return v;
+}
+__device__ __forceinline__ float2 block_pair(float2 v, float2 (&red)[32]) {
+    v = warp_pair(v);
+    const int warps = blockDim.x >> 5;
+    if (warps == 1) return v;
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+    __syncthreads();
+    const int lane = threadIdx.x & 31;
+    return warp_pair(lane < warps ? red[lane] : make_float2(0.0f, 0.0f));
 }
 __device__ __forceinline__ float inverse_plain(float s, const BackArgs &a, float k) {
     return 1.0f / sqrtf(fmaf(s, a.n_inv, (a.eps * k) * k));
@@ -351,8 +372,7 @@ __device__ __forceinline__ float inverse_plain(float s, const BackArgs &a, float
 // (t + i threads) 8, or, at any alignment, every `threads`-th from t + 8 i threads on, so that neighbours take neighbours.
 template <bool VEC> struct Columns {
     int first, step, N;
-    __device__ __forceinline__ Columns(int i, int n, int threads)
-        : first(VEC ? (static_cast<int>(threadIdx.x) + i * threads) * 8 : static_cast<int>(threadIdx.x) + i * 8 * threads), step(VEC ? 1 : threads), N(n) {}
+    __device__ __forceinline__ Columns(int t, int i, int n, int threads) : first(VEC ? (t + i * threads) * 8 : t + i * 8 * threads), step(VEC ? 1 : threads), N(n) {}
     template <typename T> __device__ __forceinline__ Raw8<T> load(const T *row) const {
         Raw8<T> r = {};
         if constexpr (VEC) {
@@ -449,27 +469,39 @@ __global__ void __launch_bounds__(MOST + 32, MOST == 256 ? 2 : 1) rms_back_kerne
         return;
     }
 
-    // the weight as floats behind the ring: each thread reads what it wrote
+    // The weight as floats behind the ring, each thread reading what it wrote. Rows of more than 4096 values (MOST = 512) need the
+    // room: their weight comes from L2, and beyond 8192 (V = 4) g and h are read a second time too.
+    constexpr bool kKeep = MOST == 256, kHold = V < 4;
     float *const weight = reinterpret_cast<float *>(ring + D * arrays * a.pitch) + 8 * V * threadIdx.x;
     float2 acc[V][4];
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const Columns<VEC> c(i, a.N, threads);
-        float v[8];
+    auto weight_of = [&](int i, float (&v)[8]) {
+        const Columns<VEC> c(threadIdx.x, i, a.N, threads);
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] = 1.0f;
         if (a.w != nullptr && a.w_f32) raw_unpack<float>(c.template load<float>(static_cast<const float *>(a.w)), v);
         else if (a.w != nullptr) raw_unpack<T>(c.template load<T>(static_cast<const T *>(a.w)), v);
-        raw_store<float>(weight + 8 * i, raw_pack<float>(v));
+    };
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        if (kKeep) {
+            float v[8];
+            weight_of(i, v);
+            raw_store<float>(weight + 8 * i, raw_pack<float>(v));
+        }
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[i][e] = make_float2(0.0f, 0.0f);
     }
     auto weights = [&](int i, float2 (&w)[4]) {
-        const float4 lo = *reinterpret_cast<const float4 *>(weight + 8 * i), hi = *reinterpret_cast<const float4 *>(weight + 8 * i + 4);
-        w[0] = make_float2(lo.x, lo.y);
-        w[1] = make_float2(lo.z, lo.w);
-        w[2] = make_float2(hi.x, hi.y);
-        w[3] = make_float2(hi.z, hi.w);
+        float v[8];
+        if (kKeep) {
+            const float4 lo = *reinterpret_cast<const float4 *>(weight + 8 * i), hi = *reinterpret_cast<const float4 *>(weight + 8 * i + 4);
+            v[0] = lo.x; v[1] = lo.y; v[2] = lo.z; v[3] = lo.w;
+            v[4] = hi.x; v[5] = hi.y; v[6] = hi.z; v[7] = hi.w;
+        } else {
+            weight_of(i, v);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[e] = make_float2(v[2 * e], v[2 * e + 1]);
     };
     // the block's sums, in every thread
     auto together = [&](float2 v, float2 (&x)[16]) {
@@ -497,16 +529,20 @@ __global__ void __launch_bounds__(MOST + 32, MOST == 256 ? 2 : 1) rms_back_kerne
             return reinterpret_cast<const T *>(VEC ? p : p + (start(n, k) & 15));
         };
         Raw8<T> g[V], h[V];
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const Columns<VEC> c(i, a.N, threads);
+        auto take = [&](int i) {
+            const Columns<VEC> c(threadIdx.x, i, a.N, threads);
             g[i] = c.template load<T>(row_of(0));
             h[i] = c.template load<T>(row_of(1));
+        };
+        if (kHold) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) take(i);
         }
         auto sums = [&](float k) {
             float2 s = make_float2(0.0f, 0.0f), d = s;
 #pragma unroll
             for (int i = 0; i < V; ++i) {
+                if (!kHold) take(i);
                 float vg[8], vh[8];
                 raw_unpack<T>(g[i], vg);
                 raw_unpack<T>(h[i], vh);
@@ -528,7 +564,8 @@ __global__ void __launch_bounds__(MOST + 32, MOST == 256 ? 2 : 1) rms_back_kerne
         T *gx = static_cast<T *>(a.gx) + (blockIdx.x + static_cast<int64_t>(n) * gridDim.x) * a.ldgx;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const Columns<VEC> c(i, a.N, threads);
+            const Columns<VEC> c(threadIdx.x, i, a.N, threads);
+            if (!kHold) take(i);
             float vg[8], vh[8], o[8];
             raw_unpack<T>(g[i], vg);
             raw_unpack<T>(h[i], vh);
@@ -559,7 +596,95 @@ __global__ void __launch_bounds__(MOST + 32, MOST == 256 ? 2 : 1) rms_back_kerne
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const float v[8] = {acc[i][0].x, acc[i][0].y, acc[i][1].x, acc[i][1].y, acc[i][2].x, acc[i][2].y, acc[i][3].x, acc[i][3].y};
-        Columns<VEC>(i, a.N, threads).template store<float>(a.parts + static_cast<int64_t>(blockIdx.x) * a.N, v);
+        Columns<VEC>(threadIdx.x, i, a.N, threads).template store<float>(a.parts + static_cast<int64_t>(blockIdx.x) * a.N, v);
+    }
+}
+
+// Many short rows: one to a warp, V eights a lane, no exchange but the warp's own; the CTA's warps join their parts of gw
+// at the end.
+template <typename T, int V, bool VEC>
+__global__ void __launch_bounds__(256, 3) rms_back_warp_kernel(const BackArgs a) {
+    __shared__ float join[8][kWarpRow];
+    if (threadIdx.x == 0) pdl_launch_dependents();
+    pdl_wait();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    float2 acc[V][4], w[V][4];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const Columns<VEC> c(lane, i, a.N, 32);
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = 1.0f;
+        if (a.w != nullptr && a.w_f32) raw_unpack<float>(c.template load<float>(static_cast<const float *>(a.w)), v);
+        else if (a.w != nullptr) raw_unpack<T>(c.template load<T>(static_cast<const T *>(a.w)), v);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            w[i][e] = make_float2(v[2 * e], v[2 * e + 1]);
+            acc[i][e] = make_float2(0.0f, 0.0f);
+        }
+    }
+    for (int64_t row = blockIdx.x * 8 + warp; row < a.T; row += gridDim.x * 8) {
+        Raw8<T> g[V], h[V], gs[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const Columns<VEC> c(lane, i, a.N, 32);
+            g[i] = c.template load<T>(static_cast<const T *>(a.g) + row * a.ldg);
+            h[i] = c.template load<T>(static_cast<const T *>(a.h) + row * a.ldh);
+            if (a.gs != nullptr) gs[i] = c.template load<T>(static_cast<const T *>(a.gs) + row * a.ldgs);
+        }
+        auto sums = [&](float k) {
+            float2 s = make_float2(0.0f, 0.0f), d = s;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                float vg[8], vh[8];
+                raw_unpack<T>(g[i], vg);
+                raw_unpack<T>(h[i], vh);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float2 u = mul2(make_float2(vh[2 * e], vh[2 * e + 1]), make_float2(k, k));
+                    s = fma2(u, u, s);
+                    d = fma2(mul2(make_float2(vg[2 * e], vg[2 * e + 1]), w[i][e]), u, d);
+                }
+            }
+            return warp_pair(make_float2(s.x + s.y, d.x + d.y));
+        };
+        float2 p = sums(1.0f);
+        const float k = power_for(p.x, a.eps, a.N);
+        if (k != 1.0f) p = sums(k);
+        const float inv = inverse_plain(p.x, a, k), mean = p.y * inv * a.n_inv, n1 = k * inv;
+        T *gx = static_cast<T *>(a.gx) + row * a.ldgx;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            float vg[8], vh[8], o[8];
+            raw_unpack<T>(g[i], vg);
+            raw_unpack<T>(h[i], vh);
+            if (a.gs != nullptr) raw_unpack<T>(gs[i], o);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                // (h k first: k brings it into range)
+                const float2 u = mul2(mul2(make_float2(vh[2 * e], vh[2 * e + 1]), make_float2(k, k)), make_float2(inv, inv));
+                const float2 gg = make_float2(vg[2 * e], vg[2 * e + 1]);
+                acc[i][e] = fma2(gg, u, acc[i][e]);
+                float2 d = mul2(fma2(u, make_float2(-mean, -mean), mul2(gg, w[i][e])), make_float2(n1, n1));
+                if (a.gs != nullptr) d = add2(d, make_float2(o[2 * e], o[2 * e + 1]));
+                o[2 * e] = d.x;
+                o[2 * e + 1] = d.y;
+            }
+            Columns<VEC>(lane, i, a.N, 32).template store<T>(gx, o);
+        }
+    }
+    if (a.parts == nullptr) return;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const float v[8] = {acc[i][0].x, acc[i][0].y, acc[i][1].x, acc[i][1].y, acc[i][2].x, acc[i][2].y, acc[i][3].x, acc[i][3].y};
+        Columns<VEC>(lane, i, a.N, 32).template store<float>(join[warp], v);
+    }
+    __syncthreads();
+    for (int c = threadIdx.x; c < a.N; c += 256) {
+        float v = 0.0f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v += join[k][c];
+        a.parts[static_cast<int64_t>(blockIdx.x) * a.N + c] = v;
     }
 }
 
@@ -634,23 +759,39 @@ __global__ void __launch_bounds__(1024) rms_back_join_kernel(const float *parts,
     if (lane == 0 && blockIdx.x * 32 + warp < N) gw[blockIdx.x * 32 + warp] = v;
 }
 
+int rows_align(const void *p, int64_t ld, bt_dtype t) { return mx::rows_align(static_cast<const char *>(p), ld, dtype_bytes(t)); }
 bool float_type(bt_dtype t) { return t == BT_F32 || t == BT_BF16 || t == BT_F16; }
 bool wide_rows(const void *p, int64_t ld, bt_dtype t) { return p == nullptr || (aligned(p, 16) && (ld * dtype_bytes(t)) % 16 == 0); }
 unsigned whole_warps(int64_t n) { return static_cast<unsigned>((n + 31) / 32 * 32); }
 
-template <typename T> cudaError_t norm(const NormArgs &a, bool vec, cudaStream_t s) {
-    const dim3 grid(static_cast<unsigned>(a.T));
-    if (vec) {
-        const int64_t groups = (a.cols + 7) / 8;
-        // few rows: as many threads as there are loads (16 x 4096: 2.8 us, 4.3 with four loads a thread); many: four loads
-        // a thread on their way (8192 x 4096 with codes: 53 us, 64 with one, 58.5 with two, 65 with eight)
-        const int v = groups > 2048 || a.T > 8 * device_sm_count() ? 4 : groups > 1024 || a.T > 2 * device_sm_count() ? 2 : 1;
-        const dim3 block(whole_warps((groups + v - 1) / v));
-        const bool wf = sizeof(T) == 2 && a.w != nullptr && a.w_f32;
-        if (v == 1) return launch_pdl(wf ? rms_norm_kernel<T, 1, true> : rms_norm_kernel<T, 1, false>, grid, block, s, a);
-        if (v == 2) return launch_pdl(wf ? rms_norm_kernel<T, 2, true> : rms_norm_kernel<T, 2, false>, grid, block, s, a);
-        return launch_pdl(wf ? rms_norm_kernel<T, 4, true> : rms_norm_kernel<T, 4, false>, grid, block, s, a);
+// Many short rows go one to a warp: 131072 rows of 256 bf16 53 us (131 with a CTA each), backward 60 (231); of 1024 values the other
+// kernels are faster (with codes 48.5 and 52.7, backward 90 and 93).
+bool warp_rows(int64_t T, int64_t N) { return N <= kWarpRow && T >= 16 * device_sm_count(); }
+
+template <typename T, Kind KIND> cudaError_t norm_rows(const NormArgs &a, cudaStream_t s) {
+    const int64_t groups = (a.cols + 7) / 8, sms = device_sm_count();
+    if (KIND == kWarp) {
+        const int64_t ctas = (a.T + 7) / 8, most = 8 * sms;
+        const dim3 grid(static_cast<unsigned>(ctas < most ? ctas : most)), block(256);
+        return launch_pdl(groups <= 32 ? rms_norm_kernel<T, 1, KIND> : rms_norm_kernel<T, 2, KIND>, grid, block, s, a);
     }
+    // few rows: as many threads as there are loads (16 x 4096: 2.8 us, 4.3 with four loads a thread); many: four loads
+    // a thread on their way (8192 x 4096 with codes: 53 us, 64 with one, 58.5 with two, 65 with eight)
+    const int v = groups > 2048 || a.T > 8 * sms ? 4 : groups > 1024 || a.T > 2 * sms ? 2 : 1;
+    const dim3 grid(static_cast<unsigned>(a.T)), block(whole_warps((groups + v - 1) / v));
+    return launch_pdl(v == 1   ? rms_norm_kernel<T, 1, KIND>
+                      : v == 2 ? rms_norm_kernel<T, 2, KIND>
+                               : rms_norm_kernel<T, 4, KIND>, grid, block, s, a);
+}
+template <typename T> cudaError_t norm(const NormArgs &a, bool vec, cudaStream_t s) {
+    if (vec && warp_rows(a.T, a.cols)) return norm_rows<T, kWarp>(a, s);
+    if constexpr (sizeof(T) == 2) {
+        if (vec && a.w != nullptr && a.w_f32) return norm_rows<T, kWideF32>(a, s);
+        // (fp32 rows of odd alignments go by neighbours)
+        if (!vec && a.cols <= 32768) return norm_rows<T, kAligned2>(a, s);
+    }
+    if (vec) return norm_rows<T, kWide>(a, s);
+    const dim3 grid(static_cast<unsigned>(a.T));
     if (a.cols <= 8192) return launch_pdl(rms_norm_any_kernel<T, 8>, grid, dim3(whole_warps((a.cols + 7) / 8)), s, a);
     return launch_pdl(rms_norm_any_kernel<T, 16>, grid, dim3(a.cols < 16384 ? whole_warps((a.cols + 15) / 16) : 1024), s, a);
 }
@@ -659,12 +800,12 @@ template <typename T> cudaError_t norm(const NormArgs &a, bool vec, cudaStream_t
 constexpr int kRingMost = 208 * 1024;
 constexpr int kBackCtas = 2;                // an SM: three hold fewer rows and leave more parts of gw (31 -> 40 us)
 int row_pitch(int64_t N, int elem) { return static_cast<int>((N * elem + 15) / 16 * 16 + 16); }
-int weight_bytes(int64_t N) { return static_cast<int>((N + 2047) / 2048 * 2048 * 4); }
+int weight_bytes(int64_t N) { return N <= 4096 ? static_cast<int>((N + 2047) / 2048 * 2048 * 4) : 0; }
 bool back_ring(int64_t N, int elem) { return N <= 16384 && 6 * row_pitch(N, elem) + weight_bytes(N) <= kRingMost; }
 
 int back_chunks(int64_t T, int64_t N, int elem) {
     const int64_t sms = device_sm_count(), strips = (N + kStrip - 1) / kStrip;
-    int64_t n = back_ring(N, elem) ? kBackCtas * sms : (8 * sms + strips - 1) / strips;
+    int64_t n = warp_rows(T, N) ? 3 * sms : back_ring(N, elem) ? kBackCtas * sms : (8 * sms + strips - 1) / strips;
     if (n > T) n = T;
     return static_cast<int>(n < 1 ? 1 : n);
 }
@@ -674,7 +815,7 @@ template <typename T, int V, int MOST, bool VEC> cudaError_t back_launch(const B
     static ContextOnce once;
     if (const cudaError_t e = allow_smem(kern, kRingMost, once); e != cudaSuccess) return e;
     const unsigned threads = whole_warps(((a.N + 7) / 8 + V - 1) / V) + 32;
-    const size_t smem = static_cast<size_t>(a.ahead) * (a.gs != nullptr ? 3 : 2) * static_cast<size_t>(a.pitch) + (threads - 32) * V * 32;
+    const size_t smem = static_cast<size_t>(a.ahead) * (a.gs != nullptr ? 3 : 2) * static_cast<size_t>(a.pitch) + (MOST == 256 ? (threads - 32) * V * 32 : 0);
     return launch_pdl_smem(kern, dim3(static_cast<unsigned>(a.chunks)), dim3(threads), smem, s, a);
 }
 template <typename T, bool VEC> cudaError_t back_rows(BackArgs a, cudaStream_t s) {
@@ -688,8 +829,14 @@ template <typename T, bool VEC> cudaError_t back_rows(BackArgs a, cudaStream_t s
     if (groups <= 1024) return back_launch<T, 2, 512, VEC>(a, s);
     return back_launch<T, 4, 512, VEC>(a, s);
 }
+template <typename T, bool VEC> cudaError_t back_warps(const BackArgs &a, cudaStream_t s) {
+    const int64_t groups = (a.N + 7) / 8;
+    return launch_pdl(groups <= 32 ? rms_back_warp_kernel<T, 1, VEC> : rms_back_warp_kernel<T, 2, VEC>, dim3(static_cast<unsigned>(a.chunks)),
+                      dim3(256), s, a);
+}
 template <typename T> cudaError_t backward(BackArgs a, bool vec, cudaStream_t s) {
     a.chunks = back_chunks(a.T, a.N, sizeof(T));
+    if (warp_rows(a.T, a.N)) return vec ? back_warps<T, true>(a, s) : back_warps<T, false>(a, s);
     if (back_ring(a.N, sizeof(T))) return vec ? back_rows<T, true>(a, s) : back_rows<T, false>(a, s);
     const cudaError_t e = launch_pdl(rms_back_rows_kernel<T>, dim3(static_cast<unsigned>(a.T)), dim3(512), s, a);
     if (e != cudaSuccess) return e;
@@ -752,6 +899,11 @@ bt_status bt_rms_norm(const void *x, bt_dtype dtype, int64_t ldx, const void *re
         a.atoms = k_atoms(N, code);
         a.cols = static_cast<int>(a.atoms * 128);
     }
+    a.al_x = rows_align(x, ldx, dtype);
+    a.al_r = rows_align(residual, ldr, dtype);
+    a.al_sum = rows_align(sum, lds, dtype);
+    a.al_out = rows_align(out, ldo, dtype);
+    a.al_w = rows_align(weight, 0, weight_dtype);
     const bool vec = N % 8 == 0 && a.cols <= 32768 && wide_rows(x, ldx, dtype) && wide_rows(residual, ldr, dtype) &&
                      wide_rows(sum, lds, dtype) && wide_rows(out, ldo, dtype) && aligned(weight, 16);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
