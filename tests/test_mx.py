@@ -239,8 +239,9 @@ def test_the_operands_device_is_made_current(fake, monkeypatch):
             with pytest.raises((Entered, RuntimeError)):        # (a tensor without memory has no address)
                 call(**args, **more)
     fake.current = 0
-    with pytest.raises(Entered, match="device 1"):
-        bt.bt_clip_grads([fake.t(5), fake.t(7)], 1.0)
+    for grads in ([fake.t(5), fake.t(7)], (fake.t(5),), iter([fake.t(5)]), {"a": fake.t(5)}.values()):
+        with pytest.raises(Entered, match="device 1"):
+            bt.bt_clip_grads(grads, 1.0)
 
 
 def test_operands_of_several_devices_are_refused(fake):

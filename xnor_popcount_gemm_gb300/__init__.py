@@ -584,8 +584,6 @@ def _on_device_of(name: str, at: int):
                 t = t.buffer
             elif type(t) is MxRows:
                 t = t._tensors()[0]
-            elif type(t) in (list, tuple):
-                t = t[0] if t else None
             device = t.get_device() if isinstance(t, torch.Tensor) else -1
             if device < 0 or device == _current_device():
                 return fn(*args, **kw)
@@ -952,11 +950,15 @@ def bt_mx_scale_bytes(R: int, K: int, code: int) -> int:
 _FLOATS = (torch.float32, torch.bfloat16, torch.float16)
 
 
-def _float_rows(t: torch.Tensor, name: str, dtypes=_FLOATS) -> int:
-    """Elements from one row of a 2-D operand to the next."""
-    if t.dim() != 2:
-        raise ValueError(f"{name} must be 2-D")
-    return _rows(t, name, t.shape[0], t.shape[1], dtypes)
+def _float_rows(t: torch.Tensor, name: str, dtypes=_FLOATS):
+    """A 2-D operand's elements from one row to the next, its rows and its columns."""
+    if t.dim() != 2 or t.dtype not in dtypes or not t.is_cuda:
+        raise ValueError(f"{name} must be a 2-D CUDA tensor of type {' or '.join(map(str, dtypes))}")
+    T, C = t.shape
+    ld, one = t.stride()
+    if one != 1 and C > 1:
+        raise ValueError(f"{name} must have the elements of a row next to each other")
+    return (ld if T > 1 else max(C, ld)), T, C
 
 
 def _mx(q, name: str):
@@ -968,8 +970,7 @@ def _mx(q, name: str):
 @_on_device_of("x", 0)
 def bt_mx_quantize(x: torch.Tensor, code: int, out: MxRows | None = None, stream=None) -> MxRows:
     """x [R, K] in blocks of 32 along K that share a power of two, as E4M3 or E2M1 values."""
-    ld = _float_rows(x, "x")
-    R, K = x.shape
+    ld, R, K = _float_rows(x, "x")
     if out is not None:
         if _mx(out, "out").shape != (R, K) or out.code != code:
             raise ValueError("out must be MxRows of x's shape and the code")
@@ -1012,19 +1013,27 @@ def bt_mx_linear(x, w: MxRows, out_dtype=None, out: torch.Tensor | None = None, 
         first, *others = x._tensors()
         xp, xs = x._pointers()
     else:
-        ldx = _float_rows(x, "x")
-        if x.shape[1] != K:
+        ldx, M, columns = _float_rows(x, "x")
+        if columns != K:
             raise ValueError("x and w must agree on K")
-        M, xt, dt, first, others, xp, xs = x.shape[0], _DT[x.dtype], x.dtype, x, (), x.data_ptr(), None
+        dt, first, others, xp, xs = x.dtype, x, (), x.data_ptr(), None
+        xt = _DT[dt]
     _same_device(first, stream, *others, *w._tensors(), out, workspace)
     device = first.device
     if out is None:
         out = _empty((M, N), dt if out_dtype is None else out_dtype, device, stream)
     ldo = _rows(out, "out", M, N, _FLOATS if out_dtype is None else (out_dtype,))
+    call = (xp, xt, ldx, xs, *w._pointers(), code, M, N, K, out.data_ptr(), _DT[out.dtype], ldo)
+    raw = _on_stream(stream, device)
+    if M <= 16 and workspace is None:
+        # few rows need no workspace: the query costs a microsecond of a call's sixteen
+        status = _c_mx_lin(*call, None, 0, raw)
+        if status != BT_ERR_WORKSPACE:
+            _check(status)
+            return out
     need = _c_mx_lin_ws(M, N, K, xt, code)
     workspace = _scratch(workspace, need, device, stream)
-    _check(_c_mx_lin(xp, xt, ldx, xs, *w._pointers(), code, M, N, K, out.data_ptr(), _DT[out.dtype], ldo,
-                     None if workspace is None else workspace.data_ptr(), need, _on_stream(stream, device)))
+    _check(_c_mx_lin(*call, None if workspace is None else workspace.data_ptr(), need, raw))
     return out
 
 
@@ -1052,8 +1061,7 @@ def bt_mx_linear_backward_workspace(M: int, N: int) -> int:
 def bt_mx_linear_backward(g: torch.Tensor, wt: torch.Tensor, out_dtype=torch.bfloat16, grad_x: torch.Tensor | None = None,
                           workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """The input gradient [M, K] of bt_mx_linear for the upstream gradient g [M, N] (bf16), wt = bt_mx_transpose(w)."""
-    ldg = _float_rows(g, "g", _BF16)
-    M, N = g.shape
+    ldg, M, N = _float_rows(g, "g", _BF16)
     if wt.dim() != 2 or wt.dtype != torch.bfloat16 or not wt.is_cuda or wt.shape[1] < N:
         raise ValueError("wt must be bt_mx_transpose(w) for g's N columns")
     _contig(wt, "wt")
@@ -1064,9 +1072,7 @@ def bt_mx_linear_backward(g: torch.Tensor, wt: torch.Tensor, out_dtype=torch.bfl
     elif grad_x.dtype not in (torch.bfloat16, torch.float32):
         raise ValueError("grad_x must be bfloat16 or float32")
     _dense(grad_x, "grad_x", (M, K), grad_x.dtype)
-    need = _c_mx_bwd_ws(M, N)
-    if ldg % 8 == 0 and N % 8 == 0 and g.data_ptr() % 16 == 0:
-        need = 0
+    need = 0 if ldg % 8 == 0 and N % 8 == 0 and g.data_ptr() % 16 == 0 else _c_mx_bwd_ws(M, N)
     workspace = _scratch(workspace, need, g.device, stream)
     _check(_c_mx_bwd(g.data_ptr(), ldg, wt.data_ptr(), ldw, M, N, K, grad_x.data_ptr(), _DT[grad_x.dtype],
                      None if workspace is None else workspace.data_ptr(), need, _on_stream(stream, g.device)))
@@ -1076,10 +1082,10 @@ def bt_mx_linear_backward(g: torch.Tensor, wt: torch.Tensor, out_dtype=torch.bfl
 def _norm_weight(weight, N: int, dtype) -> int:
     if weight is None:
         return BT_F32
-    if weight.dtype not in (dtype, torch.float32):
-        raise ValueError("weight must be of x's type or float32")
-    _dense(weight, "weight", (N,), weight.dtype)
-    return _DT[weight.dtype]
+    t = weight.dtype
+    if t not in (dtype, torch.float32) or weight.shape != (N,) or not weight.is_cuda or not weight.is_contiguous():
+        raise ValueError(f"weight must be a contiguous CUDA tensor of shape {[N]} and of x's type or float32")
+    return _DT[t]
 
 
 @_on_device_of("x", 0)
@@ -1089,8 +1095,7 @@ def bt_rms_norm(x: torch.Tensor, weight: torch.Tensor | None = None, eps: float 
     """h = x + residual (in x's type), y = h * weight / sqrt(mean(h^2) + eps) along the rows of x [T, N]: returns
     (y, h, codes). y is None unless want_out; h (which may be written over x or residual: sum) None without a
     residual; codes, y as MxRows in `code`, None without a code."""
-    ldx = _float_rows(x, "x")
-    T, N = x.shape
+    ldx, T, N = _float_rows(x, "x")
     dt = (x.dtype,)
     if q is not None:
         if _mx(q, "q").shape != (T, N) or (code is not None and q.code != code):
@@ -1132,8 +1137,7 @@ def bt_rms_norm_backward(g: torch.Tensor, h: torch.Tensor, weight: torch.Tensor 
     """Gradients of bt_rms_norm for the upstream gradient g [T, N] of y, h what was normed (its sum, or x) and grad_sum
     the gradient of h that comes along the residual stream: (grad_x [T, N], of x and of the residual alike,
     grad_weight [N] float, None unless wanted)."""
-    ldg = _float_rows(g, "g")
-    T, N = g.shape
+    ldg, T, N = _float_rows(g, "g")
     dt = (g.dtype,)
     ldh = _rows(h, "h", T, N, dt)
     _same_device(g, stream, h, weight, grad_sum, grad_x, grad_weight, workspace)
@@ -1162,16 +1166,20 @@ def bt_clip_grads_workspace(count: int) -> int:
 _dtype_of = operator.attrgetter("dtype")
 
 
-@_on_device_of("grads", 0)
 def bt_clip_grads(grads, max_norm: float, eps: float = 1e-6, norm: torch.Tensor | None = None,
                   workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
-    """The norm of all of grads (a list of contiguous CUDA tensors, float32, bfloat16 or float16) as a device float, and
-    each of them times min(1, max_norm / (norm + eps)), in place. max_norm = inf: the norm alone."""
+    """The norm of all of grads (contiguous CUDA tensors, float32, bfloat16 or float16) as a device float, and each of them
+    times min(1, max_norm / (norm + eps)), in place. max_norm = inf: the norm alone."""
     grads = list(grads)
     if not grads or not all(issubclass(t, torch.Tensor) for t in set(map(type, grads))):
         raise ValueError("grads must be tensors, one at least")
+    return _clip_grads(grads[0], grads, max_norm, eps, norm, workspace, stream)
+
+
+@_on_device_of("first", 0)
+def _clip_grads(first, grads, max_norm, eps, norm, workspace, stream):
     # (maps, sets and arrays: hundreds of tensors are looked at before a launch of microseconds)
-    n, first = len(grads), grads[0]
+    n = len(grads)
     dtypes = list(map(_dtype_of, grads))
     kinds = set(dtypes)
     if not kinds.issubset(_FLOATS) or not first.is_cuda:
