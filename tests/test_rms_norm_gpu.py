@@ -270,3 +270,40 @@ def test_empty_and_graph():
         bt.bt_rms_norm_backward(g, x, grad_x=gx, grad_weight=gw, workspace=ws)
     graph.replay()
     assert all(torch.equal(a, b) for a, b in zip((y, gx, gw), want))
+
+
+# Several short rows to a warp: the last warp with some rows only, rows whose squares leave fp32 beside ordinary ones, rows of
+# zeros without eps, and what lies behind the last row left as it was.
+SHORT = [(2433, 128), (2435, 64), (2561, 120), (5003, 8), (2439, 72), (30001, 40)]
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+@pytest.mark.parametrize("T,N", SHORT)
+def test_norm_of_many_short_rows(T, N, dtype):
+    x = rows(T, T, N, dtype)
+    big, small = (0.0, 0.0) if dtype == F16 else (1e25, 1e-25)
+    if big:
+        x[5::7] = (x[5::7].float() / x[5::7].float().abs().amax(1, keepdim=True) * big).to(dtype)
+        x[3::11] = (x[3::11].float() / x[3::11].float().abs().amax(1, keepdim=True) * small).to(dtype)
+    w = (torch.rand(N, generator=torch.Generator().manual_seed(N)) + 0.5).cuda()
+    for code in (E4M3, E2M1):
+        buf = torch.full((T + 8, N), 7.0, dtype=dtype, device="cuda")
+        _, _, q = bt.bt_rms_norm(x, w, 0.0, out=buf[:T], code=code)
+        check_rounding(buf[:T], exact(x, w, 0.0))
+        assert bool((buf[T:] == 7.0).all())
+        assert same_operand(q, bt.bt_mx_quantize(buf[:T], code))
+    x[T - 1] = 0                                # 0 / 0
+    y, _, _ = bt.bt_rms_norm(x, w, 0.0)
+    assert bool(torch.isnan(y[T - 1]).all()) and torch.equal(y[:T - 1], buf[:T - 1])
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("T,N", SHORT + [(2433, 127), (2434, 33)])
+def test_backward_of_many_short_rows(T, N, dtype):
+    gx, gw, (h, g, gs, w) = check_backward(T, N, dtype, seed=T)
+    buf = torch.full((T + 8, N), 7.0, dtype=dtype, device="cuda")
+    a, b = bt.bt_rms_norm_backward(g, h, w, grad_sum=gs, grad_x=buf[:T])
+    assert torch.equal(a, gx) and torch.equal(b, gw) and bool((buf[T:] == 7.0).all())
+    # without eps: rows behind the last add nothing, not 0 / 0
+    a, b = bt.bt_rms_norm_backward(g, h, w, 0.0, grad_sum=gs)
+    assert bool(torch.isfinite(a).all()) and bool(torch.isfinite(b).all())

@@ -70,11 +70,16 @@ struct Sums {
     }
 };
 
-// The warp's sum, and the block's, in every thread, in an order that the thread count alone decides.
-__device__ __forceinline__ Sum2 warp_sum(Sum2 v) {
+// The lanes that hold a row, LANES neighbours of a warp.
+template <int LANES> __device__ __forceinline__ uint32_t row_lanes() {
+    return LANES == 32 ? 0xFFFFFFFFu : ((1u << (LANES & 31)) - 1u) << (threadIdx.x & 31 & ~(LANES - 1));
+}
+
+// Their sum, and the block's, in every thread, in an order that the thread count alone decides.
+template <int LANES = 32> __device__ __forceinline__ Sum2 warp_sum(Sum2 v) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        const float s = __shfl_xor_sync(0xFFFFFFFFu, v.s, o), c = __shfl_xor_sync(0xFFFFFFFFu, v.c, o);
+    for (int o = LANES / 2; o > 0; o >>= 1) {
+        const float s = __shfl_xor_sync(row_lanes<LANES>(), v.s, o), c = __shfl_xor_sync(row_lanes<LANES>(), v.c, o);
         v.join(s, c);
     }
     return v;
@@ -126,17 +131,21 @@ enum Kind {
     kWide,          // rows 16-byte aligned, N a multiple of 8; a row by its CTA; the weight is of type T (or fp32 where T is)
     kWideF32,       // the same with an fp32 weight beside 16-bit rows
     kAligned2,      // 16-bit rows of any alignment and width, a row by its CTA
-    kWarp,          // as kWide with any weight; a row by a warp, for many short ones
+    kWarp,          // as kWide with any weight; a row by LANES lanes of a warp, for many short ones
 };
-template <typename T, int V, Kind KIND>
+template <typename T, int V, Kind KIND, int LANES = 32>
 __global__ void __launch_bounds__(KIND == kWarp ? 256 : 1024) rms_norm_kernel(const NormArgs a) {
     __shared__ float2 red[2][32];
     constexpr bool kWhole = KIND != kAligned2;
-    const int threads = KIND == kWarp ? 32 : blockDim.x, tid = KIND == kWarp ? threadIdx.x & 31 : threadIdx.x;
-    const int rows = KIND == kWarp ? gridDim.x * (blockDim.x >> 5) : gridDim.x;
+    static_assert(LANES == 32 || (KIND == kWarp && V == 1), "several rows to a warp: one eight a lane");
+    const int threads = KIND == kWarp ? LANES : blockDim.x, tid = KIND == kWarp ? threadIdx.x & (LANES - 1) : threadIdx.x;
+    const int rows = KIND == kWarp ? gridDim.x * (256 / LANES) : gridDim.x;
     if (threadIdx.x == 0) pdl_launch_dependents();
     pdl_wait();
-    for (int64_t row = KIND == kWarp ? blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5) : blockIdx.x; row < a.T; row += rows) {
+    // (a warp's lanes stay together: first is its first row)
+    for (int64_t first = KIND == kWarp ? (blockIdx.x * 8 + (threadIdx.x >> 5)) * (32 / LANES) : blockIdx.x; first < a.T; first += rows) {
+        const int64_t row = LANES == 32 ? first : first + (threadIdx.x & 31) / LANES;
+        const int N = LANES < 32 && row >= a.T ? 0 : a.N, cols = LANES < 32 && row >= a.T ? 0 : a.cols;     // (behind the last: no columns)
         const T *x = static_cast<const T *>(a.x) + row * a.ldx;
         const T *r = static_cast<const T *>(a.r) + row * a.ldr;
         auto load = [&](const T *p, int c, int al) { return kWhole ? raw_load<T>(p + c) : raw_load_any<T>(p + c, a.N - c, al); };
@@ -150,7 +159,7 @@ __global__ void __launch_bounds__(KIND == kWarp ? 256 : 1024) rms_norm_kernel(co
         for (int i = 0; i < V; ++i) {
             const int c = (tid + i * threads) * 8;
             h[i] = Raw8<T>{};
-            if (c >= a.N) continue;
+            if (c >= N) continue;
             h[i] = load(x, c, a.al_x);
             if (a.r != nullptr) rr[i] = load(r, c, a.al_r);
         }
@@ -158,7 +167,7 @@ __global__ void __launch_bounds__(KIND == kWarp ? 256 : 1024) rms_norm_kernel(co
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 const int c = (tid + i * threads) * 8;
-                if (c >= a.N) continue;
+                if (c >= N) continue;
                 float v[8], o[8];
                 raw_unpack<T>(h[i], v);
                 raw_unpack<T>(rr[i], o);
@@ -179,7 +188,7 @@ __global__ void __launch_bounds__(KIND == kWarp ? 256 : 1024) rms_norm_kernel(co
             }
             return p.joined();
         };
-        auto together = [&](Sum2 v, float2 (&x2)[32]) { return KIND == kWarp ? warp_sum(v) : block_sum(v, x2); };
+        auto together = [&](Sum2 v, float2 (&x2)[32]) { return KIND == kWarp ? warp_sum<LANES>(v) : block_sum(v, x2); };
         Sum2 total = together(squares(1.0f), red[0]);
         const float k = power_for(total.s, a.eps, a.N);
         if (k != 1.0f) total = together(squares(k), red[1]);
@@ -189,7 +198,7 @@ __global__ void __launch_bounds__(KIND == kWarp ? 256 : 1024) rms_norm_kernel(co
             const int g = tid + i * threads, c = g * 8;
             if (c - (tid & 31) * 8 >= a.cols) continue;                 // (whole warps)
             Raw8<T> o = {};
-            if (c < a.N) {
+            if (c < N) {
                 float v[8], w[8], y[8];
                 raw_unpack<T>(h[i], v);
                 if (k != 1.0f) {
@@ -224,7 +233,7 @@ __global__ void __launch_bounds__(KIND == kWarp ? 256 : 1024) rms_norm_kernel(co
             const uint32_t top = quad_top<T>(o);
             const bool e4m3 = a.code == BT_CODE_E4M3;
             const uint32_t s = e4m3 ? scale_of<BT_CODE_E4M3>(top) : scale_of<BT_CODE_E2M1>(top), word = atom_word(s);
-            if (c >= a.cols) continue;
+            if (c >= cols) continue;
             float y[8];
             raw_unpack<T>(o, y);
             uint8_t *p = a.q + row * a.row_bytes + static_cast<int64_t>(g) * (e4m3 ? 8 : 4);
@@ -347,11 +356,11 @@ struct BackArgs {
 constexpr int kMostAhead = 3;
 constexpr int kWarpRow = 512;               // the longest row that goes to a warp
 
-__device__ __forceinline__ float2 warp_pair(float2 v) {
+template <int LANES = 32> __device__ __forceinline__ float2 warp_pair(float2 v) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        v.x += __shfl_xor_sync(0xFFFFFFFFu, v.x, o);
-        v.y += __shfl_xor_sync(0xFFFFFFFFu, v.y, o);
+    for (int o = LANES / 2; o > 0; o >>= 1) {
+        v.x += __shfl_xor_sync(row_lanes<LANES>(), v.x, o);
+        v.y += __shfl_xor_sync(row_lanes<LANES>(), v.y, o);
     }
     return v;
 }
@@ -600,18 +609,19 @@ __global__ void __launch_bounds__(MOST + 32, MOST == 256 ? 2 : 1) rms_back_kerne
     }
 }
 
-// Many short rows: one to a warp, V eights a lane, no exchange but the warp's own; the CTA's warps join their parts of gw
+// Many short rows: one to LANES lanes, V eights a lane, no exchange but theirs; the CTA's rows join their parts of gw
 // at the end.
-template <typename T, int V, bool VEC>
+template <typename T, int V, bool VEC, int LANES>
 __global__ void __launch_bounds__(256, 3) rms_back_warp_kernel(const BackArgs a) {
-    __shared__ float join[8][kWarpRow];
+    constexpr int kRow = LANES * 8 * V, kRows = 256 / LANES;
+    __shared__ __align__(16) float join[kRows][kRow];
     if (threadIdx.x == 0) pdl_launch_dependents();
     pdl_wait();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int part = threadIdx.x / LANES, lane = threadIdx.x & (LANES - 1);
     float2 acc[V][4], w[V][4];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        const Columns<VEC> c(lane, i, a.N, 32);
+        const Columns<VEC> c(lane, i, a.N, LANES);
         float v[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] = 1.0f;
@@ -623,11 +633,15 @@ __global__ void __launch_bounds__(256, 3) rms_back_warp_kernel(const BackArgs a)
             acc[i][e] = make_float2(0.0f, 0.0f);
         }
     }
-    for (int64_t row = blockIdx.x * 8 + warp; row < a.T; row += gridDim.x * 8) {
+    // (a warp's lanes stay together: first is its first row)
+    for (int64_t first = blockIdx.x * kRows + (threadIdx.x >> 5) * (32 / LANES); first < a.T; first += gridDim.x * kRows) {
+        const int64_t row = LANES == 32 ? first : first + (threadIdx.x & 31) / LANES;
+        const bool real = LANES == 32 || row < a.T;
+        const int N = real ? a.N : 0;                                   // (behind the last: no columns)
         Raw8<T> g[V], h[V], gs[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const Columns<VEC> c(lane, i, a.N, 32);
+            const Columns<VEC> c(lane, i, N, LANES);
             g[i] = c.template load<T>(static_cast<const T *>(a.g) + row * a.ldg);
             h[i] = c.template load<T>(static_cast<const T *>(a.h) + row * a.ldh);
             if (a.gs != nullptr) gs[i] = c.template load<T>(static_cast<const T *>(a.gs) + row * a.ldgs);
@@ -646,12 +660,12 @@ __global__ void __launch_bounds__(256, 3) rms_back_warp_kernel(const BackArgs a)
                     d = fma2(mul2(make_float2(vg[2 * e], vg[2 * e + 1]), w[i][e]), u, d);
                 }
             }
-            return warp_pair(make_float2(s.x + s.y, d.x + d.y));
+            return warp_pair<LANES>(make_float2(s.x + s.y, d.x + d.y));
         };
         float2 p = sums(1.0f);
         const float k = power_for(p.x, a.eps, a.N);
         if (k != 1.0f) p = sums(k);
-        const float inv = inverse_plain(p.x, a, k), mean = p.y * inv * a.n_inv, n1 = k * inv;
+        const float inv = real ? inverse_plain(p.x, a, k) : 0.0f, mean = p.y * inv * a.n_inv, n1 = k * inv;
         T *gx = static_cast<T *>(a.gx) + row * a.ldgx;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
@@ -670,20 +684,20 @@ __global__ void __launch_bounds__(256, 3) rms_back_warp_kernel(const BackArgs a)
                 o[2 * e] = d.x;
                 o[2 * e + 1] = d.y;
             }
-            Columns<VEC>(lane, i, a.N, 32).template store<T>(gx, o);
+            Columns<VEC>(lane, i, N, LANES).template store<T>(gx, o);
         }
     }
     if (a.parts == nullptr) return;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const float v[8] = {acc[i][0].x, acc[i][0].y, acc[i][1].x, acc[i][1].y, acc[i][2].x, acc[i][2].y, acc[i][3].x, acc[i][3].y};
-        Columns<VEC>(lane, i, a.N, 32).template store<float>(join[warp], v);
+        Columns<VEC>(lane, i, a.N, LANES).template store<float>(join[part], v);
     }
     __syncthreads();
     for (int c = threadIdx.x; c < a.N; c += 256) {
         float v = 0.0f;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v += join[k][c];
+        for (int k = 0; k < kRows; ++k) v += join[k][c];
         a.parts[static_cast<int64_t>(blockIdx.x) * a.N + c] = v;
     }
 }
@@ -768,13 +782,20 @@ unsigned whole_warps(int64_t n) { return static_cast<unsigned>((n + 31) / 32 * 3
 // kernels are faster (with codes 48.5 and 52.7, backward 90 and 93).
 bool warp_rows(int64_t T, int64_t N) { return N <= kWarpRow && T >= 16 * device_sm_count(); }
 
+// The lanes of a warp that take such a row: no more than it has eights, as a warp's other lanes would idle.
+int row_lanes_for(int64_t groups) { return groups <= 8 ? 8 : groups <= 16 ? 16 : 32; }
+
+template <typename T> cudaError_t norm_warps(const NormArgs &a, cudaStream_t s) {
+    const int64_t groups = (a.cols + 7) / 8;
+    const int lanes = row_lanes_for(groups);
+    const int64_t each = 256 / lanes, ctas = (a.T + each - 1) / each, most = 8 * device_sm_count();
+    return launch_pdl(groups > 32   ? rms_norm_kernel<T, 2, kWarp>
+                      : lanes == 32 ? rms_norm_kernel<T, 1, kWarp>
+                      : lanes == 16 ? rms_norm_kernel<T, 1, kWarp, 16>
+                                    : rms_norm_kernel<T, 1, kWarp, 8>, dim3(static_cast<unsigned>(ctas < most ? ctas : most)), dim3(256), s, a);
+}
 template <typename T, Kind KIND> cudaError_t norm_rows(const NormArgs &a, cudaStream_t s) {
     const int64_t groups = (a.cols + 7) / 8, sms = device_sm_count();
-    if (KIND == kWarp) {
-        const int64_t ctas = (a.T + 7) / 8, most = 8 * sms;
-        const dim3 grid(static_cast<unsigned>(ctas < most ? ctas : most)), block(256);
-        return launch_pdl(groups <= 32 ? rms_norm_kernel<T, 1, KIND> : rms_norm_kernel<T, 2, KIND>, grid, block, s, a);
-    }
     // few rows: as many threads as there are loads (16 x 4096: 2.8 us, 4.3 with four loads a thread); many: four loads
     // a thread on their way (8192 x 4096 with codes: 53 us, 64 with one, 58.5 with two, 65 with eight)
     const int v = groups > 2048 || a.T > 8 * sms ? 4 : groups > 1024 || a.T > 2 * sms ? 2 : 1;
@@ -784,7 +805,7 @@ template <typename T, Kind KIND> cudaError_t norm_rows(const NormArgs &a, cudaSt
                                : rms_norm_kernel<T, 4, KIND>, grid, block, s, a);
 }
 template <typename T> cudaError_t norm(const NormArgs &a, bool vec, cudaStream_t s) {
-    if (vec && warp_rows(a.T, a.cols)) return norm_rows<T, kWarp>(a, s);
+    if (vec && warp_rows(a.T, a.cols)) return norm_warps<T>(a, s);
     if constexpr (sizeof(T) == 2) {
         if (vec && a.w != nullptr && a.w_f32) return norm_rows<T, kWideF32>(a, s);
         // (fp32 rows of odd alignments go by neighbours)
@@ -831,8 +852,11 @@ template <typename T, bool VEC> cudaError_t back_rows(BackArgs a, cudaStream_t s
 }
 template <typename T, bool VEC> cudaError_t back_warps(const BackArgs &a, cudaStream_t s) {
     const int64_t groups = (a.N + 7) / 8;
-    return launch_pdl(groups <= 32 ? rms_back_warp_kernel<T, 1, VEC> : rms_back_warp_kernel<T, 2, VEC>, dim3(static_cast<unsigned>(a.chunks)),
-                      dim3(256), s, a);
+    const int lanes = row_lanes_for(groups);
+    return launch_pdl(groups > 32   ? rms_back_warp_kernel<T, 2, VEC, 32>
+                      : lanes == 32 ? rms_back_warp_kernel<T, 1, VEC, 32>
+                      : lanes == 16 ? rms_back_warp_kernel<T, 1, VEC, 16>
+                                    : rms_back_warp_kernel<T, 1, VEC, 8>, dim3(static_cast<unsigned>(a.chunks)), dim3(256), s, a);
 }
 template <typename T> cudaError_t backward(BackArgs a, bool vec, cudaStream_t s) {
     a.chunks = back_chunks(a.T, a.N, sizeof(T));
