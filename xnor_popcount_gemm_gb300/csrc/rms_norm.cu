@@ -137,7 +137,7 @@ template <typename T, int V, Kind KIND, int LANES = 32>
 __global__ void __launch_bounds__(KIND == kWarp ? 256 : 1024) rms_norm_kernel(const NormArgs a) {
     __shared__ float2 red[2][32];
     constexpr bool kWhole = KIND != kAligned2;
-    static_assert(LANES == 32 || (KIND == kWarp && V == 1), "several rows to a warp: one eight a lane");
+    static_assert(LANES == 32 || KIND == kWarp, "several rows to a warp");
     const int threads = KIND == kWarp ? LANES : blockDim.x, tid = KIND == kWarp ? threadIdx.x & (LANES - 1) : threadIdx.x;
     const int rows = KIND == kWarp ? gridDim.x * (256 / LANES) : gridDim.x;
     if (threadIdx.x == 0) pdl_launch_dependents();
@@ -229,7 +229,7 @@ __global__ void __launch_bounds__(KIND == kWarp ? 256 : 1024) rms_norm_kernel(co
                 o = raw_pack<T>(y);
                 if (a.out != nullptr) store(a.out, a.ldo, c, a.al_out, o);
             }
-            if (a.code == kNoCode) continue;
+            if (LANES < 16 || a.code == kNoCode) continue;              // (sixteen lanes make a word of scales)
             const uint32_t top = quad_top<T>(o);
             const bool e4m3 = a.code == BT_CODE_E4M3;
             const uint32_t s = e4m3 ? scale_of<BT_CODE_E4M3>(top) : scale_of<BT_CODE_E2M1>(top), word = atom_word(s);
@@ -782,17 +782,20 @@ unsigned whole_warps(int64_t n) { return static_cast<unsigned>((n + 31) / 32 * 3
 // kernels are faster (with codes 48.5 and 52.7, backward 90 and 93).
 bool warp_rows(int64_t T, int64_t N) { return N <= kWarpRow && T >= 16 * device_sm_count(); }
 
-// The lanes of a warp that take such a row: no more than it has eights, as a warp's other lanes would idle.
-int row_lanes_for(int64_t groups) { return groups <= 8 ? 8 : groups <= 16 ? 16 : 32; }
-
+// Two eights a lane on no more lanes than that takes: a row's exchange and its root then serve as many rows as a warp holds
+// (bf16, 134 MB: 524288 x 128 57 us, 82 with one eight on sixteen lanes and 156 with a warp each; 262144 x 256 66, 81 with a
+// warp each). A word of scales takes sixteen lanes.
 template <typename T> cudaError_t norm_warps(const NormArgs &a, cudaStream_t s) {
     const int64_t groups = (a.cols + 7) / 8;
-    const int lanes = row_lanes_for(groups);
-    const int64_t each = 256 / lanes, ctas = (a.T + each - 1) / each, most = 8 * device_sm_count();
-    return launch_pdl(groups > 32   ? rms_norm_kernel<T, 2, kWarp>
-                      : lanes == 32 ? rms_norm_kernel<T, 1, kWarp>
-                      : lanes == 16 ? rms_norm_kernel<T, 1, kWarp, 16>
-                                    : rms_norm_kernel<T, 1, kWarp, 8>, dim3(static_cast<unsigned>(ctas < most ? ctas : most)), dim3(256), s, a);
+    auto go = [&](void (*kern)(const NormArgs), int lanes) {
+        const int64_t each = 256 / lanes, ctas = (a.T + each - 1) / each, most = 8 * device_sm_count();
+        return launch_pdl(kern, dim3(static_cast<unsigned>(ctas < most ? ctas : most)), dim3(256), s, a);
+    };
+    if (groups <= 8) return go(rms_norm_kernel<T, 2, kWarp, 4>, 4);
+    if (groups <= 16 && a.code == kNoCode) return go(rms_norm_kernel<T, 2, kWarp, 8>, 8);
+    if (groups <= 16) return go(rms_norm_kernel<T, 1, kWarp, 16>, 16);
+    if (groups <= 32) return go(rms_norm_kernel<T, 2, kWarp, 16>, 16);
+    return go(rms_norm_kernel<T, 2, kWarp, 32>, 32);
 }
 template <typename T, Kind KIND> cudaError_t norm_rows(const NormArgs &a, cudaStream_t s) {
     const int64_t groups = (a.cols + 7) / 8, sms = device_sm_count();
@@ -852,11 +855,11 @@ template <typename T, bool VEC> cudaError_t back_rows(BackArgs a, cudaStream_t s
 }
 template <typename T, bool VEC> cudaError_t back_warps(const BackArgs &a, cudaStream_t s) {
     const int64_t groups = (a.N + 7) / 8;
-    const int lanes = row_lanes_for(groups);
-    return launch_pdl(groups > 32   ? rms_back_warp_kernel<T, 2, VEC, 32>
-                      : lanes == 32 ? rms_back_warp_kernel<T, 1, VEC, 32>
-                      : lanes == 16 ? rms_back_warp_kernel<T, 1, VEC, 16>
-                                    : rms_back_warp_kernel<T, 1, VEC, 8>, dim3(static_cast<unsigned>(a.chunks)), dim3(256), s, a);
+    // one eight a lane: with two its registers hide less of memory's delay (524288 x 128 bf16: 142 us, 93 with one)
+    return launch_pdl(groups <= 8    ? rms_back_warp_kernel<T, 1, VEC, 8>
+                      : groups <= 16 ? rms_back_warp_kernel<T, 1, VEC, 16>
+                      : groups <= 32 ? rms_back_warp_kernel<T, 1, VEC, 32>
+                                     : rms_back_warp_kernel<T, 2, VEC, 32>, dim3(static_cast<unsigned>(a.chunks)), dim3(256), s, a);
 }
 template <typename T> cudaError_t backward(BackArgs a, bool vec, cudaStream_t s) {
     a.chunks = back_chunks(a.T, a.N, sizeof(T));
