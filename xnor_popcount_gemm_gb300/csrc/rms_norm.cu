@@ -354,7 +354,10 @@ struct BackArgs {
     unsigned int *err;
 };
 constexpr int kMostAhead = 3;
-constexpr int kWarpRow = 512;               // the longest row that goes to a warp
+constexpr int kWarpRow = 512, kBackWarpRow = 256;   // the longest row that goes to a warp, forward and backward
+constexpr int kBackCtas = 2;                // an SM: three hold fewer rows and leave more parts of gw (31 -> 40 us)
+constexpr int kNarrowRow = 1024;            // up to which there are more of them
+constexpr int kNarrowCtas = 6;
 
 template <int LANES = 32> __device__ __forceinline__ float2 warp_pair(float2 v) {
 #pragma unroll
@@ -418,7 +421,7 @@ template <bool VEC> struct Columns {
 // own. Memory: 4096 x 4096 bf16 with gs 26.7 us (134 MB, 74 % of the copy rate), and 4 for the parts of gw and their sum;
 // with rows loaded when they are due 41.
 template <typename T, int V, int MOST, bool VEC>
-__global__ void __launch_bounds__(MOST + 32, MOST == 256 ? 2 : 1) rms_back_kernel(const BackArgs a) {
+__global__ void __launch_bounds__(MOST + 32, MOST == 128 ? kNarrowCtas : MOST == 256 ? kBackCtas : 1) rms_back_kernel(const BackArgs a) {
     extern __shared__ __align__(16) uint8_t ring[];
     __shared__ float2 red[2][2][16];
     __shared__ uint64_t bars[2 * kMostAhead];
@@ -480,7 +483,7 @@ __global__ void __launch_bounds__(MOST + 32, MOST == 256 ? 2 : 1) rms_back_kerne
 
     // The weight as floats behind the ring, each thread reading what it wrote. Rows of more than 4096 values (MOST = 512) need the
     // room: their weight comes from L2, and beyond 8192 (V = 4) g and h are read a second time too.
-    constexpr bool kKeep = MOST == 256, kHold = V < 4;
+    constexpr bool kKeep = MOST <= 256, kHold = V < 4;
     float *const weight = reinterpret_cast<float *>(ring + D * arrays * a.pitch) + 8 * V * threadIdx.x;
     float2 acc[V][4];
     auto weight_of = [&](int i, float (&v)[8]) {
@@ -702,25 +705,37 @@ __global__ void __launch_bounds__(256, 3) rms_back_warp_kernel(const BackArgs a)
     }
 }
 
-// Wider rows than that keeps: the rows' sums, then strips of columns.
-template <typename T> __device__ __forceinline__ float weight1(const BackArgs &a, int c) {
-    return a.w == nullptr ? 1.0f : a.w_f32 ? __ldg(static_cast<const float *>(a.w) + c) : Elem<T>::to_f32(static_cast<const T *>(a.w)[c]);
+// Wider rows than a ring holds: the rows' sums, then strips of columns, so that g and h are read twice.
+template <typename T, bool VEC> __device__ __forceinline__ void weight8(const BackArgs &a, const Columns<VEC> &c, float (&v)[8]) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = 1.0f;
+    if (a.w != nullptr && a.w_f32) raw_unpack<float>(c.template load<float>(static_cast<const float *>(a.w)), v);
+    else if (a.w != nullptr) raw_unpack<T>(c.template load<T>(static_cast<const T *>(a.w)), v);
 }
-template <typename T> __global__ void __launch_bounds__(512) rms_back_rows_kernel(const BackArgs a) {
+template <typename T, bool VEC> __global__ void __launch_bounds__(512) rms_back_rows_kernel(const BackArgs a) {
     __shared__ float2 red[2][32];
     if (threadIdx.x == 0) pdl_launch_dependents();
     pdl_wait();
     const int64_t row = blockIdx.x;
     const T *g = static_cast<const T *>(a.g) + row * a.ldg, *h = static_cast<const T *>(a.h) + row * a.ldh;
     auto sums = [&](float k) {
-        float2 p = make_float2(0.0f, 0.0f);
-#pragma unroll 4
-        for (int c = threadIdx.x; c < a.N; c += blockDim.x) {
-            const float u = Elem<T>::to_f32(h[c]) * k;
-            p.x = fmaf(u, u, p.x);
-            p.y = fmaf(Elem<T>::to_f32(g[c]) * weight1<T>(a, c), u, p.y);
+        float2 s = make_float2(0.0f, 0.0f), d = s;
+        const int eights = (a.N + 8 * 512 - 1) / (8 * 512);
+#pragma unroll 2
+        for (int i = 0; i < eights; ++i) {
+            const Columns<VEC> c(threadIdx.x, i, a.N, 512);
+            float vg[8], vh[8], w[8];
+            raw_unpack<T>(c.template load<T>(g), vg);
+            raw_unpack<T>(c.template load<T>(h), vh);
+            weight8<T, VEC>(a, c, w);
+#pragma unroll
+            for (int e = 0; e < 8; e += 2) {
+                const float2 u = mul2(make_float2(vh[e], vh[e + 1]), make_float2(k, k));
+                s = fma2(u, u, s);
+                d = fma2(mul2(make_float2(vg[e], vg[e + 1]), make_float2(w[e], w[e + 1])), u, d);
+            }
         }
-        return p;
+        return make_float2(s.x + s.y, d.x + d.y);
     };
     float2 p = block_pair(sums(1.0f), red[0]);
     const float k = power_for(p.x, a.eps, a.N);
@@ -728,25 +743,54 @@ template <typename T> __global__ void __launch_bounds__(512) rms_back_rows_kerne
     const float inv = inverse_plain(p.x, a, k);
     if (threadIdx.x == 0) a.rows[row] = make_float4(inv, p.y * inv * a.n_inv, k, 0.0f);
 }
-constexpr int kStrip = 128;
-template <typename T> __global__ void __launch_bounds__(kStrip) rms_back_strips_kernel(const BackArgs a) {
+constexpr int kStrip = 128, kStripColumns = kStrip * 8, kStripCtas = 5;     // threads, columns, CTAs an SM
+template <typename T, bool VEC> __global__ void __launch_bounds__(kStrip, kStripCtas) rms_back_strips_kernel(const BackArgs a) {
     if (threadIdx.x == 0) pdl_launch_dependents();
     pdl_wait();
-    const int c = blockIdx.x * kStrip + threadIdx.x;
-    if (c >= a.N) return;
-    const float w = weight1<T>(a, c);
-    float acc = 0.0f;
-#pragma unroll 4
-    for (int row = blockIdx.y; row < a.T; row += a.chunks) {
-        const float4 s = __ldg(a.rows + row);
-        const float vg = Elem<T>::to_f32(static_cast<const T *>(a.g)[row * a.ldg + c]);
-        const float n = Elem<T>::to_f32(static_cast<const T *>(a.h)[row * a.ldh + c]) * s.z * s.x;
-        acc = fmaf(vg, n, acc);
-        float d = (s.x * s.z) * fmaf(-n, s.y, vg * w);
-        if (a.gs != nullptr) d += Elem<T>::to_f32(static_cast<const T *>(a.gs)[row * a.ldgs + c]);
-        static_cast<T *>(a.gx)[row * a.ldgx + c] = from_f32<T>(d);
+    const Columns<VEC> c(threadIdx.x, blockIdx.x, a.N, kStrip);
+    float w[8];
+    weight8<T, VEC>(a, c, w);
+    float2 acc[4] = {};
+    // (two rows' loads before either's stores, which may go where they came from)
+    for (int64_t first = blockIdx.y; first < a.T; first += 2 * static_cast<int64_t>(a.chunks)) {
+        Raw8<T> g[2] = {}, h[2] = {}, gs[2] = {};
+        float4 s[2] = {};
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const int64_t row = first + r * static_cast<int64_t>(a.chunks);
+            if (row >= a.T) continue;
+            s[r] = __ldg(a.rows + row);
+            g[r] = c.template load<T>(static_cast<const T *>(a.g) + row * a.ldg);
+            h[r] = c.template load<T>(static_cast<const T *>(a.h) + row * a.ldh);
+            if (a.gs != nullptr) gs[r] = c.template load<T>(static_cast<const T *>(a.gs) + row * a.ldgs);
+        }
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const int64_t row = first + r * static_cast<int64_t>(a.chunks);
+            if (row >= a.T) continue;
+            const float n1 = s[r].x * s[r].z;
+            float vg[8], vh[8], o[8];
+            raw_unpack<T>(g[r], vg);
+            raw_unpack<T>(h[r], vh);
+            raw_unpack<T>(gs[r], o);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                // (h k first: k brings it into range)
+                const float2 u = mul2(mul2(make_float2(vh[2 * e], vh[2 * e + 1]), make_float2(s[r].z, s[r].z)), make_float2(s[r].x, s[r].x));
+                const float2 gg = make_float2(vg[2 * e], vg[2 * e + 1]);
+                acc[e] = fma2(gg, u, acc[e]);
+                float2 d = mul2(fma2(u, make_float2(-s[r].y, -s[r].y), mul2(gg, make_float2(w[2 * e], w[2 * e + 1]))), make_float2(n1, n1));
+                if (a.gs != nullptr) d = add2(d, make_float2(o[2 * e], o[2 * e + 1]));
+                o[2 * e] = d.x;
+                o[2 * e + 1] = d.y;
+            }
+            c.template store<T>(static_cast<T *>(a.gx) + row * a.ldgx, o);
+        }
     }
-    if (a.parts != nullptr) a.parts[static_cast<int64_t>(blockIdx.y) * a.N + c] = acc;
+    if (a.parts == nullptr) return;
+    const float v[8] = {acc[0].x, acc[0].y, acc[1].x, acc[1].y, acc[2].x, acc[2].y, acc[3].x, acc[3].y};
+    float *to = a.parts + static_cast<int64_t>(blockIdx.y) * a.N;
+    c.template store<float>(to, v);
 }
 
 // gw = the parts' sum: 32 columns a CTA, 32 rows of parts at a time, eight of them on their way a thread.
@@ -822,32 +866,43 @@ template <typename T> cudaError_t norm(const NormArgs &a, bool vec, cudaStream_t
 
 // Rows that rms_back_kernel takes: two of them (g, h and gs) fit in its ring.
 constexpr int kRingMost = 208 * 1024;
-constexpr int kBackCtas = 2;                // an SM: three hold fewer rows and leave more parts of gw (31 -> 40 us)
 int row_pitch(int64_t N, int elem) { return static_cast<int>((N * elem + 15) / 16 * 16 + 16); }
-int weight_bytes(int64_t N) { return N <= 4096 ? static_cast<int>((N + 2047) / 2048 * 2048 * 4) : 0; }
+int weight_bytes(int64_t N) { return N <= kNarrowRow ? static_cast<int>(whole_warps((N + 7) / 8) * 32) : N <= 4096 ? static_cast<int>((N + 2047) / 2048 * 2048 * 4) : 0; }
 bool back_ring(int64_t N, int elem) { return N <= 16384 && 6 * row_pitch(N, elem) + weight_bytes(N) <= kRingMost; }
 
+// CTAs an SM. A short row leaves its CTA waiting for its exchange, so there are as many as an SM holds at 64 registers a thread: fewer
+// than that are not spread evenly, and more than two leave more parts of gw than fewer than eight rows each are worth (32768 x 1024 bf16: 51 us with six, 61 with seven, 57 with five, 68 with four, 90 with two).
+int back_ctas(int64_t N) { return N > kNarrowRow ? kBackCtas : 32 / static_cast<int>(whole_warps((N + 7) / 8) / 32 + 1); }
+// (backward: the longest row that goes to a warp is shorter)
+bool back_warp_rows(int64_t T, int64_t N) { return N <= kBackWarpRow && warp_rows(T, N); }
+
 int back_chunks(int64_t T, int64_t N, int elem) {
-    const int64_t sms = device_sm_count(), strips = (N + kStrip - 1) / kStrip;
-    int64_t n = warp_rows(T, N) ? 3 * sms : back_ring(N, elem) ? kBackCtas * sms : (8 * sms + strips - 1) / strips;
+    const int64_t sms = device_sm_count(), strips = (N + kStripColumns - 1) / kStripColumns;
+    int64_t n = back_warp_rows(T, N) ? 3 * sms : back_ring(N, elem) ? (T < 8 * back_ctas(N) * sms ? kBackCtas : back_ctas(N)) * sms : (kStripCtas * sms + strips - 1) / strips;
     if (n > T) n = T;
     return static_cast<int>(n < 1 ? 1 : n);
 }
 
 template <typename T, int V, int MOST, bool VEC> cudaError_t back_launch(const BackArgs &a, cudaStream_t s) {
     auto kern = rms_back_kernel<T, V, MOST, VEC>;
-    static ContextOnce once;
+    static ContextOnce once, carve;
     if (const cudaError_t e = allow_smem(kern, kRingMost, once); e != cudaSuccess) return e;
+    // (what the driver sets aside by itself may hold fewer CTAs of small rings than there are)
+    if (const cudaError_t e = static_cast<cudaError_t>(carve.run(
+            current_context_id, [&] { return cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared); }));
+        e != cudaSuccess)
+        return e;
     const unsigned threads = whole_warps(((a.N + 7) / 8 + V - 1) / V) + 32;
-    const size_t smem = static_cast<size_t>(a.ahead) * (a.gs != nullptr ? 3 : 2) * static_cast<size_t>(a.pitch) + (MOST == 256 ? (threads - 32) * V * 32 : 0);
+    const size_t smem = static_cast<size_t>(a.ahead) * (a.gs != nullptr ? 3 : 2) * static_cast<size_t>(a.pitch) + (MOST <= 256 ? (threads - 32) * V * 32 : 0);
     return launch_pdl_smem(kern, dim3(static_cast<unsigned>(a.chunks)), dim3(threads), smem, s, a);
 }
 template <typename T, bool VEC> cudaError_t back_rows(BackArgs a, cudaStream_t s) {
     const int64_t groups = (a.N + 7) / 8;
     a.pitch = row_pitch(a.N, sizeof(T));
     const int per = (a.gs != nullptr ? 3 : 2) * a.pitch;
-    a.ahead = (kRingMost / kBackCtas - weight_bytes(a.N)) / per;
+    a.ahead = ((a.N > kNarrowRow ? kRingMost / kBackCtas : (kRingMost + 5 * 1024) / back_ctas(a.N) - 2048) - weight_bytes(a.N)) / per;   // (2048: a CTA's own)
     a.ahead = a.ahead < 2 ? 2 : a.ahead > 3 ? 3 : a.ahead;
+    if (a.N <= kNarrowRow) return back_launch<T, 1, 128, VEC>(a, s);
     if (groups <= 256) return back_launch<T, 1, 256, VEC>(a, s);
     if (groups <= 512) return back_launch<T, 2, 256, VEC>(a, s);
     if (groups <= 1024) return back_launch<T, 2, 512, VEC>(a, s);
@@ -858,17 +913,16 @@ template <typename T, bool VEC> cudaError_t back_warps(const BackArgs &a, cudaSt
     // one eight a lane: with two its registers hide less of memory's delay (524288 x 128 bf16: 142 us, 93 with one)
     return launch_pdl(groups <= 8    ? rms_back_warp_kernel<T, 1, VEC, 8>
                       : groups <= 16 ? rms_back_warp_kernel<T, 1, VEC, 16>
-                      : groups <= 32 ? rms_back_warp_kernel<T, 1, VEC, 32>
-                                     : rms_back_warp_kernel<T, 2, VEC, 32>, dim3(static_cast<unsigned>(a.chunks)), dim3(256), s, a);
+                                     : rms_back_warp_kernel<T, 1, VEC, 32>, dim3(static_cast<unsigned>(a.chunks)), dim3(256), s, a);
 }
 template <typename T> cudaError_t backward(BackArgs a, bool vec, cudaStream_t s) {
     a.chunks = back_chunks(a.T, a.N, sizeof(T));
-    if (warp_rows(a.T, a.N)) return vec ? back_warps<T, true>(a, s) : back_warps<T, false>(a, s);
+    if (back_warp_rows(a.T, a.N)) return vec ? back_warps<T, true>(a, s) : back_warps<T, false>(a, s);
     if (back_ring(a.N, sizeof(T))) return vec ? back_rows<T, true>(a, s) : back_rows<T, false>(a, s);
-    const cudaError_t e = launch_pdl(rms_back_rows_kernel<T>, dim3(static_cast<unsigned>(a.T)), dim3(512), s, a);
+    const cudaError_t e = launch_pdl(vec ? rms_back_rows_kernel<T, true> : rms_back_rows_kernel<T, false>, dim3(static_cast<unsigned>(a.T)), dim3(512), s, a);
     if (e != cudaSuccess) return e;
-    return launch_pdl(rms_back_strips_kernel<T>,
-                      dim3(static_cast<unsigned>((a.N + kStrip - 1) / kStrip), static_cast<unsigned>(a.chunks)), dim3(kStrip), s, a);
+    return launch_pdl(vec ? rms_back_strips_kernel<T, true> : rms_back_strips_kernel<T, false>,
+                      dim3(static_cast<unsigned>((a.N + kStripColumns - 1) / kStripColumns), static_cast<unsigned>(a.chunks)), dim3(kStrip), s, a);
 }
 
 }  // namespace
