@@ -311,6 +311,15 @@ template <typename K> cudaError_t allow_smem(K kern, int bytes, ContextOnce &onc
         once.run(current_context_id, [&] { return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes); }));
 }
 
+// As allow_smem, and the SM's whole shared memory for it: what the driver sets aside by itself may hold fewer CTAs of a small size.
+template <typename K> cudaError_t allow_all_smem(K kern, int bytes, ContextOnce &once) {
+    return static_cast<cudaError_t>(once.run(current_context_id, [&] {
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e != cudaSuccess) return e;
+        return cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+    }));
+}
+
 // Microscaled operands (mx_quant.cu): whether [R, K] is a size they have, and rows to one. x [R, K] of float type xt, rows
 // ldx elements apart; q and scales as bt_mx_quantize writes them. The kernel lets the one after it begin only when
 // everything before it has ended.

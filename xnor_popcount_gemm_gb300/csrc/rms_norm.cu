@@ -5,8 +5,8 @@
 //   n = h / sqrt(mean h^2 + eps)      gx = (g w - n mean(g w n)) / sqrt(..) + gs
 //   gw = sum over the rows of g n
 //
-// Streams: every row is read once, kept in registers by its CTA and written once. 8192 x 4096 bf16 with a residual 43 us (268 MB,
-// 92 % of the copy rate), with E4M3 codes as well 52 (302 MB, 85 %, the issue slots three quarters busy).
+// Streams: every row is read once, kept in registers by its CTA (short rows: by some lanes of a warp) and written once. 8192 x 4096
+// bf16 with a residual 42 us (268 MB, 95 % of the copy rate), with E4M3 codes as well 49 to 50 (302 MB, 91 %).
 //
 // What is rounded to 8 or 4 bits falls one way or the other, so y is the correctly rounded fp32 value (but for about one
 // in 2^24): the squares are summed with the rounding errors of the sums beside them, and 1 / sqrt(mean) is a pair of
@@ -245,7 +245,7 @@ __global__ void __launch_bounds__(KIND == kWarp ? 256 : 1024) rms_norm_kernel(co
     }
 }
 
-// Rows of any alignment and width: thread t has the columns t, t + threads, ..., a
+// fp32 rows of odd widths or alignments, and rows wider than the registers above hold: thread t has the columns t, t + threads, ..., a
 // warp's 32 columns being a block. The first E of a thread's values stay in
 // registers; what is beyond (wider rows than 1024 E) is read a second time.
 template <typename T, int E>
@@ -705,7 +705,8 @@ __global__ void __launch_bounds__(256, 3) rms_back_warp_kernel(const BackArgs a)
     }
 }
 
-// Wider rows than a ring holds: the rows' sums, then strips of columns, so that g and h are read twice.
+// Wider rows than a ring holds: the rows' sums, then strips of columns, eight a thread, so that g and h are read twice. 1024 x 32768
+// bf16 with gs 83 us (268 MB, 48 % of the copy rate where 67 can be had; 236 with a column a thread), fp32 142.
 template <typename T, bool VEC> __device__ __forceinline__ void weight8(const BackArgs &a, const Columns<VEC> &c, float (&v)[8]) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = 1.0f;
@@ -822,8 +823,8 @@ bool float_type(bt_dtype t) { return t == BT_F32 || t == BT_BF16 || t == BT_F16;
 bool wide_rows(const void *p, int64_t ld, bt_dtype t) { return p == nullptr || (aligned(p, 16) && (ld * dtype_bytes(t)) % 16 == 0); }
 unsigned whole_warps(int64_t n) { return static_cast<unsigned>((n + 31) / 32 * 32); }
 
-// Many short rows go one to a warp: 131072 rows of 256 bf16 53 us (131 with a CTA each), backward 60 (231); of 1024 values the other
-// kernels are faster (with codes 48.5 and 52.7, backward 90 and 93).
+// Many short rows go to the lanes of a warp: 131072 rows of 256 bf16 with a residual 43 us (131 with a CTA each), backward 61 (231). Of
+// 1024 values a CTA a row is faster forward (with codes 48 us, 53 by a warp), and backward of 512 already (59 and 69).
 bool warp_rows(int64_t T, int64_t N) { return N <= kWarpRow && T >= 16 * device_sm_count(); }
 
 // Two eights a lane on no more lanes than that takes: a row's exchange and its root then serve as many rows as a warp holds
@@ -867,31 +868,33 @@ template <typename T> cudaError_t norm(const NormArgs &a, bool vec, cudaStream_t
 // Rows that rms_back_kernel takes: two of them (g, h and gs) fit in its ring.
 constexpr int kRingMost = 208 * 1024;
 int row_pitch(int64_t N, int elem) { return static_cast<int>((N * elem + 15) / 16 * 16 + 16); }
-int weight_bytes(int64_t N) { return N <= kNarrowRow ? static_cast<int>(whole_warps((N + 7) / 8) * 32) : N <= 4096 ? static_cast<int>((N + 2047) / 2048 * 2048 * 4) : 0; }
+int weight_bytes(int64_t N) {
+    if (N <= kNarrowRow) return static_cast<int>(whole_warps((N + 7) / 8) * 32);
+    return N <= 4096 ? static_cast<int>((N + 2047) / 2048 * 2048 * 4) : 0;
+}
 bool back_ring(int64_t N, int elem) { return N <= 16384 && 6 * row_pitch(N, elem) + weight_bytes(N) <= kRingMost; }
 
-// CTAs an SM. A short row leaves its CTA waiting for its exchange, so there are as many as an SM holds at 64 registers a thread: fewer
-// than that are not spread evenly, and more than two leave more parts of gw than fewer than eight rows each are worth (32768 x 1024 bf16: 51 us with six, 61 with seven, 57 with five, 68 with four, 90 with two).
+// CTAs an SM. A short row leaves its CTA waiting for its exchange, so there are as many as an SM holds at 64 registers a thread
+// (32768 x 1024 bf16: 51 us with six, 57 with five, 68 with four, 90 with two; 61 with seven, of which one waits for the others).
+// Below eight rows each, the parts of gw cost more than that gives (3000 x 1024: 12 us with two, 14 with six).
 int back_ctas(int64_t N) { return N > kNarrowRow ? kBackCtas : 32 / static_cast<int>(whole_warps((N + 7) / 8) / 32 + 1); }
 // (backward: the longest row that goes to a warp is shorter)
 bool back_warp_rows(int64_t T, int64_t N) { return N <= kBackWarpRow && warp_rows(T, N); }
 
 int back_chunks(int64_t T, int64_t N, int elem) {
     const int64_t sms = device_sm_count(), strips = (N + kStripColumns - 1) / kStripColumns;
-    int64_t n = back_warp_rows(T, N) ? 3 * sms : back_ring(N, elem) ? (T < 8 * back_ctas(N) * sms ? kBackCtas : back_ctas(N)) * sms : (kStripCtas * sms + strips - 1) / strips;
+    int64_t n;
+    if (back_warp_rows(T, N)) n = 3 * sms;
+    else if (back_ring(N, elem)) n = (T < 8 * back_ctas(N) * sms ? kBackCtas : back_ctas(N)) * sms;
+    else n = (kStripCtas * sms + strips - 1) / strips;
     if (n > T) n = T;
     return static_cast<int>(n < 1 ? 1 : n);
 }
 
 template <typename T, int V, int MOST, bool VEC> cudaError_t back_launch(const BackArgs &a, cudaStream_t s) {
     auto kern = rms_back_kernel<T, V, MOST, VEC>;
-    static ContextOnce once, carve;
-    if (const cudaError_t e = allow_smem(kern, kRingMost, once); e != cudaSuccess) return e;
-    // (what the driver sets aside by itself may hold fewer CTAs of small rings than there are)
-    if (const cudaError_t e = static_cast<cudaError_t>(carve.run(
-            current_context_id, [&] { return cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared); }));
-        e != cudaSuccess)
-        return e;
+    static ContextOnce once;
+    if (const cudaError_t e = allow_all_smem(kern, kRingMost, once); e != cudaSuccess) return e;
     const unsigned threads = whole_warps(((a.N + 7) / 8 + V - 1) / V) + 32;
     const size_t smem = static_cast<size_t>(a.ahead) * (a.gs != nullptr ? 3 : 2) * static_cast<size_t>(a.pitch) + (MOST <= 256 ? (threads - 32) * V * 32 : 0);
     return launch_pdl_smem(kern, dim3(static_cast<unsigned>(a.chunks)), dim3(threads), smem, s, a);
@@ -900,7 +903,9 @@ template <typename T, bool VEC> cudaError_t back_rows(BackArgs a, cudaStream_t s
     const int64_t groups = (a.N + 7) / 8;
     a.pitch = row_pitch(a.N, sizeof(T));
     const int per = (a.gs != nullptr ? 3 : 2) * a.pitch;
-    a.ahead = ((a.N > kNarrowRow ? kRingMost / kBackCtas : (kRingMost + 5 * 1024) / back_ctas(a.N) - 2048) - weight_bytes(a.N)) / per;   // (2048: a CTA's own)
+    // (a short row's CTAs are many: 2 KB each for what a CTA has besides, of 213)
+    const int share = a.N > kNarrowRow ? kRingMost / kBackCtas : 213 * 1024 / back_ctas(a.N) - 2048;
+    a.ahead = (share - weight_bytes(a.N)) / per;
     a.ahead = a.ahead < 2 ? 2 : a.ahead > 3 ? 3 : a.ahead;
     if (a.N <= kNarrowRow) return back_launch<T, 1, 128, VEC>(a, s);
     if (groups <= 256) return back_launch<T, 1, 256, VEC>(a, s);
