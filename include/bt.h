@@ -1023,7 +1023,8 @@ size_t bt_clip_grads_workspace(int64_t count);
  * The arrays are read before the call returns and the addresses go with the launches:
  * a captured graph keeps them. A norm that is infinite makes the factor 0, a NaN norm
  * makes every gradient NaN, as the formula says. Where the factor is not below one
- * the tensors are not written. Squares are summed in fp32 over at most 33 values, then
+ * the tensors are not written, and neither are gradients that are all zero, whatever
+ * max_norm and eps are. Squares are summed in fp32 over at most 33 values, then
  * in fp64, in an order that the sizes decide: equal calls give equal results. workspace:
  * bt_clip_grads_workspace(count) bytes, 256-byte aligned. count = 0 gives the norm 0.
  * Errors: INVALID_ARG (overlaps among them), ALIGNMENT, WORKSPACE, UNSUPPORTED, CUDA.

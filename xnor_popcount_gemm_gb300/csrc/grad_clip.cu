@@ -176,9 +176,10 @@ template <int MOST> __global__ void __launch_bounds__(kThreads, kCtasPerSm) clip
     const double total = block_total(sum, red);
     const float norm = static_cast<float>(sqrt(total));
     if (a.first == 0 && blockIdx.x == 0 && threadIdx.x == 0) *a.norm = norm;
-    // not below one: nothing to do; a NaN norm makes every gradient NaN, unless none was to be clipped
+    // not below one, or nothing but zeros (whose factor would be 0 / 0 without max_norm and eps): nothing to do; a NaN norm
+    // makes every gradient NaN, unless none was to be clipped
     const float f = a.max_norm / (norm + a.eps);
-    if (f >= 1.0f || isinf(a.max_norm)) return;
+    if (f >= 1.0f || total == 0.0 || isinf(a.max_norm)) return;
     const uint32_t n = t.before[t.count];
     for (uint32_t i = blockIdx.x; i < n; i += gridDim.x) {
         const Piece p = piece_of(t, n - 1 - i);
