@@ -25,12 +25,30 @@ using namespace mx;
 
 constexpr int kNoCode = -1;
 
+// Values of tiny rows are taken times kUp, of huge ones times kDown. eps as a pair of floats, and as it counts beside the squares of
+// values times kUp, where it may be too small for a float by itself.
+constexpr float kUp = 0x1p100f, kDown = 0x1p-80f;
+struct Eps {
+    float hi, lo, up_hi, up_lo;
+};
+Eps eps_of(double eps) {
+    // (beyond 1e38 no row is taken times kUp; a positive one stays a normal number, so that its root's inverse is finite)
+    const double up = eps > 0.0 ? std::fmin(std::fmax(std::ldexp(eps, 200), 0x1p-126), 1e38) : 0.0;
+    Eps e;
+    e.hi = static_cast<float>(eps);
+    e.lo = static_cast<float>(eps - e.hi);
+    e.up_hi = static_cast<float>(up);
+    e.up_lo = static_cast<float>(up - e.up_hi);
+    return e;
+}
+
 struct NormArgs {
     const void *x, *r, *w;                  // r, w: NULL where there is none
     int64_t ldx, ldr;
     int w_f32;
     int T, N;
-    float n_inv, n_inv_lo, eps, eps_lo;     // 1 / N and eps as pairs
+    float n_inv, n_inv_lo;                  // 1 / N as a pair
+    Eps eps;
     void *sum, *out;                        // NULL: not wanted
     int64_t lds, ldo;
     int code;                               // kNoCode, or a bt_code
@@ -96,9 +114,9 @@ __device__ __forceinline__ Sum2 block_sum(Sum2 v, float2 (&red)[32]) {
 }
 
 // Rows whose squares leave fp32 are summed again, their values times this power of two.
-__device__ __forceinline__ float power_for(float s, const float eps, int N) {
-    if (!(s <= 3.4e38f)) return 0x1p-80f;
-    if (fmaf(eps, static_cast<float>(N), s) < 0x1p-80f) return 0x1p100f;
+__device__ __forceinline__ float power_for(float s, const Eps &eps, int N) {
+    if (!(s <= 3.4e38f)) return kDown;
+    if (fmaf(eps.hi, static_cast<float>(N), s) < 0x1p-80f) return kUp;
     return 1.0f;
 }
 
@@ -110,7 +128,7 @@ __device__ __forceinline__ Inverse inverse_rms(const Sum2 &v, const NormArgs &a,
     if (!(v.s <= 3.4e38f)) return Inverse{rsqrtf(v.s), 0.0f};       // infinity: 0, NaN: NaN
     const float p = v.s * a.n_inv;
     float lo = fmaf(v.s, a.n_inv, -p) + fmaf(v.s, a.n_inv_lo, v.c * a.n_inv);
-    const float eh = (a.eps * k) * k, el = (a.eps_lo * k) * k;
+    const float eh = k == kUp ? a.eps.up_hi : (a.eps.hi * k) * k, el = k == kUp ? a.eps.up_lo : (a.eps.lo * k) * k;
     const float t = p + eh, b = t - p;
     lo += (p - (t - b)) + (eh - b) + el;
     const float m = t + lo, ml = lo - (m - t);
@@ -345,7 +363,8 @@ struct BackArgs {
     int64_t ldg, ldh, ldgs, ldgx;
     int w_f32;
     int T, N;
-    float n_inv, eps;
+    float n_inv;
+    Eps eps;
     void *gx;
     float *parts;                           // [chunks, N], NULL: gw not wanted
     float4 *rows;                           // (any) 1 / rms of the values times k, mean(g w n), k of every row
@@ -377,7 +396,7 @@ __device__ __forceinline__ float2 block_pair(float2 v, float2 (&red)[32]) {
     return warp_pair(lane < warps ? red[lane] : make_float2(0.0f, 0.0f));
 }
 __device__ __forceinline__ float inverse_plain(float s, const BackArgs &a, float k) {
-    return 1.0f / sqrtf(fmaf(s, a.n_inv, (a.eps * k) * k));
+    return 1.0f / sqrtf(fmaf(s, a.n_inv, k == kUp ? a.eps.up_hi : (a.eps.hi * k) * k));
 }
 
 // Eight of a row's values: eight neighbours (VEC: rows 16-byte aligned, N a multiple of 8), thread t's i-th eight at
@@ -972,8 +991,7 @@ bt_status bt_rms_norm(const void *x, bt_dtype dtype, int64_t ldx, const void *re
     const double inv = 1.0 / static_cast<double>(N);
     a.n_inv = static_cast<float>(inv);
     a.n_inv_lo = static_cast<float>(inv - a.n_inv);
-    a.eps = static_cast<float>(eps);
-    a.eps_lo = static_cast<float>(eps - a.eps);
+    a.eps = eps_of(eps);
     a.sum = sum; a.out = out;
     a.lds = lds; a.ldo = ldo;
     a.code = q == nullptr ? kNoCode : static_cast<int>(code);
@@ -1038,7 +1056,7 @@ bt_status bt_rms_norm_backward(const void *g, bt_dtype dtype, int64_t ldg, const
     a.w_f32 = weight_dtype == BT_F32;
     a.T = static_cast<int>(T); a.N = static_cast<int>(N);
     a.n_inv = static_cast<float>(1.0 / static_cast<double>(N));
-    a.eps = static_cast<float>(eps);
+    a.eps = eps_of(eps);
     a.gx = grad_x;
     a.rows = static_cast<float4 *>(workspace);
     const int elem = dtype_bytes(dtype);
