@@ -113,12 +113,9 @@ __device__ __forceinline__ Sum2 block_sum(Sum2 v, float2 (&red)[32]) {
     return warp_sum(Sum2{p.x, p.y});
 }
 
-// Rows whose squares leave fp32 are summed again, their values times this power of two.
-__device__ __forceinline__ float power_for(float s, const Eps &eps, int N) {
-    if (!(s <= 3.4e38f)) return kDown;
-    if (fmaf(eps.hi, static_cast<float>(N), s) < 0x1p-80f) return kUp;
-    return 1.0f;
-}
+// Rows whose squares leave fp32 are summed again, their values times a power of two.
+__device__ __forceinline__ bool leaves_fp32(float s, const Eps &eps, int N) { return !(s <= 3.4e38f && fmaf(eps.hi, static_cast<float>(N), s) >= 0x1p-80f); }
+__device__ __forceinline__ float power_for(float s) { return s < 1.0f ? kUp : kDown; }
 
 // 1 / sqrt(mean + eps) for values times k, as hi + lo.
 struct Inverse {
@@ -208,8 +205,11 @@ __global__ void __launch_bounds__(KIND == kWarp ? 256 : 1024) rms_norm_kernel(co
         };
         auto together = [&](Sum2 v, float2 (&x2)[32]) { return KIND == kWarp ? warp_sum<LANES>(v) : block_sum(v, x2); };
         Sum2 total = together(squares(1.0f), red[0]);
-        const float k = power_for(total.s, a.eps, a.N);
-        if (k != 1.0f) total = together(squares(k), red[1]);
+        float k = 1.0f;
+        if (leaves_fp32(total.s, a.eps, a.N)) {
+            k = power_for(total.s);
+            total = together(squares(k), red[1]);
+        }
         const Inverse inv = inverse_rms(total, a, k);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
@@ -320,8 +320,11 @@ __global__ void __launch_bounds__(1024) rms_norm_any_kernel(const NormArgs a) {
         return p.joined();
     };
     Sum2 total = block_sum(squares(1.0f, true), red[0]);
-    const float k = power_for(total.s, a.eps, a.N);
-    if (k != 1.0f) total = block_sum(squares(k, false), red[1]);
+    float k = 1.0f;
+    if (leaves_fp32(total.s, a.eps, a.N)) {
+        k = power_for(total.s);
+        total = block_sum(squares(k, false), red[1]);
+    }
     const Inverse inv = inverse_rms(total, a, k);
     auto finish = [&](int c, float v) {
         float y = 0.0f;
@@ -395,9 +398,8 @@ __device__ __forceinline__ float2 block_pair(float2 v, float2 (&red)[32]) {
     const int lane = threadIdx.x & 31;
     return warp_pair(lane < warps ? red[lane] : make_float2(0.0f, 0.0f));
 }
-__device__ __forceinline__ float inverse_plain(float s, const BackArgs &a, float k) {
-    return 1.0f / sqrtf(fmaf(s, a.n_inv, k == kUp ? a.eps.up_hi : (a.eps.hi * k) * k));
-}
+__device__ __forceinline__ float eps_times(const Eps &eps, float k) { return k == kUp ? eps.up_hi : (eps.hi * k) * k; }
+__device__ __forceinline__ float inverse_plain(float s, float n_inv, float eps) { return 1.0f / sqrtf(fmaf(s, n_inv, eps)); }
 
 // Eight of a row's values: eight neighbours (VEC: rows 16-byte aligned, N a multiple of 8), thread t's i-th eight at
 // (t + i threads) 8, or, at any alignment, every `threads`-th from t + 8 i threads on, so that neighbours take neighbours.
@@ -589,9 +591,13 @@ __global__ void __launch_bounds__(MOST + 32, MOST == 128 ? kNarrowCtas : MOST ==
             return make_float2(s.x + s.y, d.x + d.y);
         };
         float2 p = together(sums(1.0f), red[0][n & 1]);
-        const float k = power_for(p.x, a.eps, a.N);
-        if (k != 1.0f) p = together(sums(k), red[1][n & 1]);
-        const float inv = inverse_plain(p.x, a, k), mean = p.y * inv * a.n_inv, n1 = k * inv;
+        float k = 1.0f, eps = a.eps.hi;
+        if (leaves_fp32(p.x, a.eps, a.N)) {
+            k = power_for(p.x);
+            eps = eps_times(a.eps, k);
+            p = together(sums(k), red[1][n & 1]);
+        }
+        const float inv = inverse_plain(p.x, a.n_inv, eps), mean = p.y * inv * a.n_inv, n1 = k * inv;
         T *gx = static_cast<T *>(a.gx) + (blockIdx.x + static_cast<int64_t>(n) * gridDim.x) * a.ldgx;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
@@ -685,9 +691,13 @@ __global__ void __launch_bounds__(256, 3) rms_back_warp_kernel(const BackArgs a)
             return warp_pair<LANES>(make_float2(s.x + s.y, d.x + d.y));
         };
         float2 p = sums(1.0f);
-        const float k = power_for(p.x, a.eps, a.N);
-        if (k != 1.0f) p = sums(k);
-        const float inv = real ? inverse_plain(p.x, a, k) : 0.0f, mean = p.y * inv * a.n_inv, n1 = k * inv;
+        float k = 1.0f, eps = a.eps.hi;
+        if (leaves_fp32(p.x, a.eps, a.N)) {
+            k = power_for(p.x);
+            eps = eps_times(a.eps, k);
+            p = sums(k);
+        }
+        const float inv = real ? inverse_plain(p.x, a.n_inv, eps) : 0.0f, mean = p.y * inv * a.n_inv, n1 = k * inv;
         T *gx = static_cast<T *>(a.gx) + row * a.ldgx;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
@@ -758,9 +768,13 @@ template <typename T, bool VEC> __global__ void __launch_bounds__(512) rms_back_
         return make_float2(s.x + s.y, d.x + d.y);
     };
     float2 p = block_pair(sums(1.0f), red[0]);
-    const float k = power_for(p.x, a.eps, a.N);
-    if (k != 1.0f) p = block_pair(sums(k), red[1]);
-    const float inv = inverse_plain(p.x, a, k);
+    float k = 1.0f, eps = a.eps.hi;
+    if (leaves_fp32(p.x, a.eps, a.N)) {
+        k = power_for(p.x);
+        eps = eps_times(a.eps, k);
+        p = block_pair(sums(k), red[1]);
+    }
+    const float inv = inverse_plain(p.x, a.n_inv, eps);
     if (threadIdx.x == 0) a.rows[row] = make_float4(inv, p.y * inv * a.n_inv, k, 0.0f);
 }
 constexpr int kStrip = 128, kStripColumns = kStrip * 8, kStripCtas = 5;     // threads, columns, CTAs an SM
