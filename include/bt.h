@@ -1044,7 +1044,8 @@ bt_status bt_device_status(bt_stream stream);
 
 /*
  * bt_set_wait_timeout -- how long each bounded wait in the main loops of the
- * tensor-core contraction kernels (producer, MMA issuer, epilogue) waits
+ * tensor-core contraction kernels (producer, MMA issuer, epilogue) and of the
+ * kernels that bring rows by bulk copies (distillation, the norm's backward) waits
  * before giving up, in nanoseconds, for launches made after the call; 0
  * restores the default of 2 s. Process-wide. The pages have no counterpart:
  * it exists so that the timeout path can be exercised without breaking
