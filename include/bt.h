@@ -972,10 +972,11 @@ bt_status bt_mx_linear_backward(const void *g, int64_t ldg, const void *wt, int6
  *             codes at least. out may be x or, without sum there, residual.
  *   ldx, ldr, lds, ldo  elements from one row to the next, >= N.
  * The fp32 value under the last cast is the correctly rounded one but for about one
- * in 2^24, so that the codes do not depend on how the sum of squares was taken. Rows
- * whose squares leave fp32's range are scaled first. eps >= 0, at most 1e30; it
+ * in 2^24 (magnitudes below 2^-100 aside), wherever a row's values lie: rows whose
+ * sums come near the ends of fp32's range are scaled first. So the codes do not
+ * depend on how the sum of squares was taken. eps >= 0, at most 1e30; it
  * counts with all its digits, also where it is too small for fp32 (between 0 and
- * 1e-98 as 1e-98). A row with a NaN is NaN, one with an infinity NaN there and 0
+ * 2^-306 as 2^-306). A row with a NaN is NaN, one with an infinity NaN there and 0
  * elsewhere; with eps = 0 a row of zeros is NaN. The weight is finite. Any element
  * alignment; 16-byte rows with N a multiple of 8 are faster. T = 0 does nothing.
  * T, N < 2^24. Errors: INVALID_ARG, ALIGNMENT, UNSUPPORTED, CUDA.

@@ -25,15 +25,17 @@ using namespace mx;
 
 constexpr int kNoCode = -1;
 
-// Values of tiny rows are taken times kUp, of huge ones times kDown. eps as a pair of floats, and as it counts beside the squares of
-// values times kUp, where it may be too small for a float by itself.
-constexpr float kUp = 0x1p100f, kDown = 0x1p-80f;
+// Rows whose squares' sum lies beyond kMost (below kLeast) are taken times kDown (kUp): their sum, their mean's inverse and the last
+// digits of both, which a pair of floats has, are normal fp32 numbers then. (A sum of 2^124, in fp32's range, has an inverse whose
+// second half is not: of 4 million values of rows of 64 around 2^60, 1036 were rounded the other way.) eps as a pair, and as it counts
+// beside the squares of values times kUp, where it may be too small for a float by itself.
+constexpr float kUp = 0x1p90f, kDown = 0x1p-80f, kMost = 0x1p100f, kLeast = 0x1p-80f;
 struct Eps {
     float hi, lo, up_hi, up_lo;
 };
 Eps eps_of(double eps) {
     // (beyond 1e38 no row is taken times kUp; a positive one stays a normal number, so that its root's inverse is finite)
-    const double up = eps > 0.0 ? std::fmin(std::fmax(std::ldexp(eps, 200), 0x1p-126), 1e38) : 0.0;
+    const double up = eps > 0.0 ? std::fmin(std::fmax(std::ldexp(eps, 180), 0x1p-126), 1e38) : 0.0;
     Eps e;
     e.hi = static_cast<float>(eps);
     e.lo = static_cast<float>(eps - e.hi);
@@ -113,8 +115,8 @@ __device__ __forceinline__ Sum2 block_sum(Sum2 v, float2 (&red)[32]) {
     return warp_sum(Sum2{p.x, p.y});
 }
 
-// Rows whose squares leave fp32 are summed again, their values times a power of two.
-__device__ __forceinline__ bool leaves_fp32(float s, const Eps &eps, int N) { return !(s <= 3.4e38f && fmaf(eps.hi, static_cast<float>(N), s) >= 0x1p-80f); }
+// Rows that are summed again, their values times a power of two.
+__device__ __forceinline__ bool leaves_fp32(float s, const Eps &eps, int N) { return !(s <= kMost && fmaf(eps.hi, static_cast<float>(N), s) >= kLeast); }
 __device__ __forceinline__ float power_for(float s) { return s < 1.0f ? kUp : kDown; }
 
 // 1 / sqrt(mean + eps) for values times k, as hi + lo.
