@@ -136,10 +136,15 @@ template <typename T> struct Raw8;
 template <> struct Raw8<float> { uint4 a, b; };
 template <> struct Raw8<__nv_bfloat16> { uint4 a; };
 template <> struct Raw8<__half> { uint4 a; };
-template <typename T> __device__ __forceinline__ Raw8<T> raw_load(const T *p) {
+// FIXED: nothing writes there while the kernel runs (a load through the read-only path, which in-place operands may not take).
+template <bool FIXED, typename V> __device__ __forceinline__ V load_as(const V *p) {
+    if constexpr (FIXED) return __ldg(p);
+    else return *p;
+}
+template <typename T, bool FIXED = true> __device__ __forceinline__ Raw8<T> raw_load(const T *p) {
     Raw8<T> r;
-    r.a = __ldg(reinterpret_cast<const uint4 *>(p));
-    if constexpr (sizeof(T) == 4) r.b = __ldg(reinterpret_cast<const uint4 *>(p) + 1);
+    r.a = load_as<FIXED>(reinterpret_cast<const uint4 *>(p));
+    if constexpr (sizeof(T) == 4) r.b = load_as<FIXED>(reinterpret_cast<const uint4 *>(p) + 1);
     return r;
 }
 template <typename T> __device__ __forceinline__ void raw_unpack(const Raw8<T> &r, float (&v)[8]) {
@@ -173,28 +178,28 @@ template <typename T> __device__ __forceinline__ void raw_store(T *p, const Raw8
 }
 // The same at any element address: `valid` of them are there (<= 0: none), the rest zeros. al: what p is a multiple of
 // (16, 8, 4 or 2; smaller than 16 goes by the widest loads that it allows).
-template <typename T> __device__ __forceinline__ Raw8<T> raw_load_any(const T *p, int valid, int al) {
+template <typename T, bool FIXED = true> __device__ __forceinline__ Raw8<T> raw_load_any(const T *p, int valid, int al) {
     if (valid <= 0) return Raw8<T>{};       // (p may lie anywhere then)
-    if (al == 16 && valid >= 8) return raw_load<T>(p);
+    if (al == 16 && valid >= 8) return raw_load<T, FIXED>(p);
     uint32_t w[sizeof(T) * 2] = {};
     if (valid >= 8 && al == 8) {
 #pragma unroll
         for (int i = 0; i < static_cast<int>(sizeof(T)); ++i) {
-            const uint2 v = __ldg(reinterpret_cast<const uint2 *>(p) + i);
+            const uint2 v = load_as<FIXED>(reinterpret_cast<const uint2 *>(p) + i);
             w[2 * i] = v.x;
             w[2 * i + 1] = v.y;
         }
     } else if constexpr (sizeof(T) == 4) {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            if (i < valid) w[i] = __float_as_uint(__ldg(p + i));
+            if (i < valid) w[i] = __float_as_uint(load_as<FIXED>(p + i));
     } else {
         // from the aligned words that hold a valid one
         const int odd = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 2) >> 1;
         const uint32_t *q = reinterpret_cast<const uint32_t *>(reinterpret_cast<const uint16_t *>(p) - odd);
         uint32_t r[5];
 #pragma unroll
-        for (int i = 0; i < 5; ++i) r[i] = 2 * i - odd < valid && (i < 4 || odd) ? __ldg(q + i) : 0u;
+        for (int i = 0; i < 5; ++i) r[i] = 2 * i - odd < valid && (i < 4 || odd) ? load_as<FIXED>(q + i) : 0u;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const uint32_t v = odd ? __funnelshift_r(r[i], r[i + 1], 16) : r[i];

@@ -165,7 +165,8 @@ __global__ void __launch_bounds__(KIND == kWarp ? 256 : 1024) rms_norm_kernel(co
         const int N = LANES < 32 && row >= a.T ? 0 : a.N, cols = LANES < 32 && row >= a.T ? 0 : a.cols;     // (behind the last: no columns)
         const T *x = static_cast<const T *>(a.x) + row * a.ldx;
         const T *r = static_cast<const T *>(a.r) + row * a.ldr;
-        auto load = [&](const T *p, int c, int al) { return kWhole ? raw_load<T>(p + c) : raw_load_any<T>(p + c, a.N - c, al); };
+        // (x and r may be written in place; another row's elements that a word holds beside this one's are not used)
+        auto load = [&](const T *p, int c, int al) { return kWhole ? raw_load<T, false>(p + c) : raw_load_any<T, false>(p + c, a.N - c, al); };
         auto store = [&](void *p, int64_t ld, int c, int al, const Raw8<T> &v) {
             T *q = static_cast<T *>(p) + row * ld + c;
             if (kWhole) raw_store<T>(q, v);
@@ -233,7 +234,8 @@ __global__ void __launch_bounds__(KIND == kWarp ? 256 : 1024) rms_norm_kernel(co
                     const float *p = static_cast<const float *>(a.w) + c;
                     raw_unpack<float>(kWhole ? raw_load<float>(p) : raw_load_any<float>(p, a.N - c, a.al_w), w);
                 } else {
-                    raw_unpack<T>(load(static_cast<const T *>(a.w), c, a.al_w), w);
+                    const T *p = static_cast<const T *>(a.w) + c;
+                    raw_unpack<T>(kWhole ? raw_load<T>(p) : raw_load_any<T>(p, a.N - c, a.al_w), w);
                 }
                 const bool exact = sizeof(T) == 2 && !f32;
 #pragma unroll
