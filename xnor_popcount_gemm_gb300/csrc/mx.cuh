@@ -136,7 +136,8 @@ template <typename T> struct Raw8;
 template <> struct Raw8<float> { uint4 a, b; };
 template <> struct Raw8<__nv_bfloat16> { uint4 a; };
 template <> struct Raw8<__half> { uint4 a; };
-// FIXED: nothing writes there while the kernel runs (a load through the read-only path, which in-place operands may not take).
+// FIXED: nothing writes there from before the kernel's start to its end (a load through the read-only path). Operands that are
+// written in place, or by the kernel before, which may still be running when this one starts, may not take it.
 template <bool FIXED, typename V> __device__ __forceinline__ V load_as(const V *p) {
     if constexpr (FIXED) return __ldg(p);
     else return *p;

@@ -51,8 +51,8 @@ template <typename T, int CODE, bool WIDE> __global__ void __launch_bounds__(kTh
         const int k = static_cast<int>(g[i]) * 8;
         const T *p = x + static_cast<int64_t>(row[i]) * a.ldx + k;
         const int valid = first + i * kThreads < a.total ? a.K - k : 0;
-        if (!WIDE) raw[i] = raw_load_any<T>(p, valid, a.al);
-        else raw[i] = valid > 0 ? raw_load<T>(p) : Raw8<T>{};
+        if (!WIDE) raw[i] = raw_load_any<T, false>(p, valid, a.al);
+        else raw[i] = valid > 0 ? raw_load<T, false>(p) : Raw8<T>{};
     }
 #pragma unroll
     for (int i = 0; i < kGroups; ++i) {

@@ -806,7 +806,7 @@ template <typename T, bool VEC> __global__ void __launch_bounds__(kStrip, kStrip
         for (int r = 0; r < 2; ++r) {
             const int64_t row = first + r * static_cast<int64_t>(a.chunks);
             if (row >= a.T) continue;
-            s[r] = __ldg(a.rows + row);
+            s[r] = a.rows[row];
             g[r] = c.template load<T>(static_cast<const T *>(a.g) + row * a.ldg);
             h[r] = c.template load<T>(static_cast<const T *>(a.h) + row * a.ldh);
             if (a.gs != nullptr) gs[r] = c.template load<T>(static_cast<const T *>(a.gs) + row * a.ldgs);
