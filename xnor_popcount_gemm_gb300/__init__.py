@@ -12,8 +12,10 @@ from __future__ import annotations
 import array
 import ctypes
 import functools
+import math
 import operator
 import os
+import struct
 
 import torch
 
@@ -625,6 +627,14 @@ def _empty(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+def _written(*given) -> None:
+    """Tells autograd which tensors of the caller's a call has written (in place or not; None: not the caller's): a graph
+    that holds one for its backward refuses to go on with other values."""
+    given = [t for t in given if t is not None]
+    if given:
+        torch.autograd.graph.increment_version(given)
+
+
 def _dense(t, name: str, shape: tuple, dtype) -> None:
     if t.shape != shape or t.dtype != dtype or not t.is_cuda:
         raise ValueError(f"{name} must be a {dtype} CUDA tensor of shape {list(shape)}")
@@ -668,6 +678,7 @@ def bt_distill_topk(logits: torch.Tensor, ids: torch.Tensor, top: torch.Tensor, 
     remaining probability as one more outcome; without it the teacher is
     normalized over its slots."""
     T, V, ld = _distill_args(logits, ids, top, teacher_lse, stream, loss, stats)
+    given = loss, stats
     if loss is None:
         loss = _empty((T,), torch.float32, logits.device, stream)
     else:
@@ -679,6 +690,7 @@ def bt_distill_topk(logits: torch.Tensor, ids: torch.Tensor, top: torch.Tensor, 
     _check(_c_distill(_ptr(logits), _DT[logits.dtype], T, V, ld, _ptr(ids), _ID_BYTES[ids.dtype], _ptr(top),
                       _DT[top.dtype], ids.shape[1], _ptr(teacher_lse), temperature, _ptr(loss), _ptr(stats),
                       _on_stream(stream, logits.device)))
+    _written(*given)
     return loss, stats
 
 
@@ -691,12 +703,14 @@ def bt_distill_topk_backward(grad_loss: torch.Tensor, logits: torch.Tensor, ids:
     sum to one: with top in 16 bits, a teacher_lse below logsumexp(top /
     temperature) is to be raised to it. grad may be the logits."""
     T, V, ld = _distill_args(logits, ids, top, teacher_lse, stream, grad_loss, stats, grad)
+    given = grad
     _dense(grad_loss, "grad_loss", (T,), torch.float32)
     _dense(stats, "stats", (T, 2), torch.float32)
     grad, ldg = _distill_grad(logits, grad, T, V, stream)
     _check(_c_distill_bwd(_ptr(grad_loss), _ptr(logits), _DT[logits.dtype], T, V, ld, _ptr(ids), _ID_BYTES[ids.dtype],
                           _ptr(top), _DT[top.dtype], ids.shape[1], _ptr(stats), _ptr(teacher_lse), temperature,
                           _ptr(grad), ldg, _on_stream(stream, logits.device)))
+    _written(given)
     return grad
 
 
@@ -709,6 +723,7 @@ def bt_distill_topk_step(grad_loss: torch.Tensor, logits: torch.Tensor, ids: tor
     twice, the second time out of L2), for an upstream
     gradient grad_loss [T] known beforehand. grad may be the logits."""
     T, V, ld = _distill_args(logits, ids, top, teacher_lse, stream, grad_loss, loss, grad, stats)
+    given = loss, grad, stats
     _dense(grad_loss, "grad_loss", (T,), torch.float32)
     if loss is None:
         loss = _empty((T,), torch.float32, logits.device, stream)
@@ -720,6 +735,7 @@ def bt_distill_topk_step(grad_loss: torch.Tensor, logits: torch.Tensor, ids: tor
     _check(_c_distill_step(_ptr(grad_loss), _ptr(logits), _DT[logits.dtype], T, V, ld, _ptr(ids),
                            _ID_BYTES[ids.dtype], _ptr(top), _DT[top.dtype], ids.shape[1], _ptr(teacher_lse),
                            temperature, _ptr(loss), _ptr(stats), _ptr(grad), ldg, _on_stream(stream, logits.device)))
+    _written(*given)
     return loss, grad
 
 
@@ -817,6 +833,7 @@ def bt_adapter_linear(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, scale: 
     out_dtype (base's type, else x's). out may be base. u [T, R] (float), if
     given, receives a[i] x_t for the backward."""
     T, K, N, R = _adapter_args(x, a, b, scale, plan, stream, base, u, out, workspace)
+    given = u, out
     dt = x.dtype
     ldx = _rows(x, "x", T, K, (dt,))
     if base is None:
@@ -835,6 +852,7 @@ def bt_adapter_linear(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, scale: 
                    plan._ref, T, K, N, R, pbase, base_type, ldb, out.data_ptr(), _DT[out.dtype], ldo,
                    None if u is None else u.data_ptr(), None if workspace is None else workspace.data_ptr(), need,
                    _on_stream(stream, x.device)))
+    _written(*given)
     return out
 
 
@@ -853,6 +871,7 @@ def bt_adapter_linear_backward(x: torch.Tensor, g: torch.Tensor, u: torch.Tensor
     grad_b [L, N, R], both float). grad_base [T, K], the projection's own
     input gradient, is added to grad_x, which may be grad_base itself."""
     T, K, N, R = _adapter_args(x, a, b, scale, plan, stream, g, u, grad_base, grad_x, grad_a, grad_b, workspace)
+    given = grad_x, grad_a, grad_b
     ldx, ldg = _rows(x, "x", T, K, _BF16), _rows(g, "g", T, N, _BF16)
     _dense(u, "u", (T, R), torch.float32)
     ldgb = 0 if grad_base is None else _rows(grad_base, "grad_base", T, K, _BF16)
@@ -872,6 +891,7 @@ def bt_adapter_linear_backward(x: torch.Tensor, g: torch.Tensor, u: torch.Tensor
     _check(_c_abwd(_ptr(x), ldx, _ptr(g), ldg, _ptr(u), _ptr(a), _ptr(b), _ptr(scale), _ptr(plan.buffer), plan._ref, T,
                    K, N, R, _ptr(grad_base), ldgb, _ptr(grad_x), ldgx, _ptr(grad_a), _ptr(grad_b), _ptr(workspace), need,
                    _on_stream(stream, x.device)))
+    _written(*given)
     return grad_x, grad_a, grad_b
 
 
@@ -971,6 +991,7 @@ def _mx(q, name: str):
 def bt_mx_quantize(x: torch.Tensor, code: int, out: MxRows | None = None, stream=None) -> MxRows:
     """x [R, K] in blocks of 32 along K that share a power of two, as E4M3 or E2M1 values."""
     ld, R, K = _float_rows(x, "x")
+    given = out
     if out is not None:
         if _mx(out, "out").shape != (R, K) or out.code != code:
             raise ValueError("out must be MxRows of x's shape and the code")
@@ -979,6 +1000,8 @@ def bt_mx_quantize(x: torch.Tensor, code: int, out: MxRows | None = None, stream
         _same_device(x, stream)
         out = MxRows._new(R, K, code, x.device, stream)
     _check(_c_mx_q(x.data_ptr(), _DT[x.dtype], ld, R, K, code, *out._pointers(), _on_stream(stream, x.device)))
+    if given is not None:
+        _written(*given._tensors())
     return out
 
 
@@ -988,10 +1011,12 @@ def bt_mx_dequantize(q: MxRows, out_dtype=torch.float32, out: torch.Tensor | Non
     R, K = _mx(q, "q").shape
     first, *others = q._tensors()
     _same_device(first, stream, *others, out)
+    given = out
     if out is None:
         out = _empty((R, K), out_dtype, first.device, stream)
     ldo = _rows(out, "out", R, K, _FLOATS)
     _check(_c_mx_dq(*q._pointers(), R, K, q.code, out.data_ptr(), _DT[out.dtype], ldo, _on_stream(stream, first.device)))
+    _written(given)
     return out
 
 
@@ -1019,7 +1044,7 @@ def bt_mx_linear(x, w: MxRows, out_dtype=None, out: torch.Tensor | None = None, 
         dt, first, others, xp, xs = x.dtype, x, (), x.data_ptr(), None
         xt = _DT[dt]
     _same_device(first, stream, *others, *w._tensors(), out, workspace)
-    device = first.device
+    device, given = first.device, out
     if out is None:
         out = _empty((M, N), dt if out_dtype is None else out_dtype, device, stream)
     ldo = _rows(out, "out", M, N, _FLOATS if out_dtype is None else (out_dtype,))
@@ -1030,10 +1055,12 @@ def bt_mx_linear(x, w: MxRows, out_dtype=None, out: torch.Tensor | None = None, 
         status = _c_mx_lin(*call, None, 0, raw)
         if status != BT_ERR_WORKSPACE:
             _check(status)
+            _written(given)
             return out
     need = _c_mx_lin_ws(M, N, K, xt, code)
     workspace = _scratch(workspace, need, device, stream)
     _check(_c_mx_lin(*call, None if workspace is None else workspace.data_ptr(), need, raw))
+    _written(given)
     return out
 
 
@@ -1045,11 +1072,13 @@ def bt_mx_transpose(w: MxRows, ld: int | None = None, out: torch.Tensor | None =
     ld = bt_backward_weight_ld(N) if ld is None else ld
     first, *others = w._tensors()
     _same_device(first, stream, *others, out)
+    given = out
     if out is None:
         out = _empty((K, ld), torch.bfloat16, first.device, stream)
     else:
         _dense(out, "out", (K, ld), torch.bfloat16)
     _check(_c_mx_t(*w._pointers(), N, K, w.code, ld, out.data_ptr(), _on_stream(stream, first.device)))
+    _written(given)
     return out
 
 
@@ -1067,6 +1096,7 @@ def bt_mx_linear_backward(g: torch.Tensor, wt: torch.Tensor, out_dtype=torch.bfl
     _contig(wt, "wt")
     K, ldw = wt.shape
     _same_device(g, stream, wt, grad_x, workspace)
+    given = grad_x
     if grad_x is None:
         grad_x = _empty((M, K), out_dtype, g.device, stream)
     elif grad_x.dtype not in (torch.bfloat16, torch.float32):
@@ -1076,6 +1106,7 @@ def bt_mx_linear_backward(g: torch.Tensor, wt: torch.Tensor, out_dtype=torch.bfl
     workspace = _scratch(workspace, need, g.device, stream)
     _check(_c_mx_bwd(g.data_ptr(), ldg, wt.data_ptr(), ldw, M, N, K, grad_x.data_ptr(), _DT[grad_x.dtype],
                      None if workspace is None else workspace.data_ptr(), need, _on_stream(stream, g.device)))
+    _written(given)
     return grad_x
 
 
@@ -1105,7 +1136,8 @@ def bt_rms_norm(x: torch.Tensor, weight: torch.Tensor | None = None, eps: float 
         raise ValueError("out is given and not wanted")
     if sum is not None and residual is None:
         raise ValueError("sum needs a residual")
-    _same_device(x, stream, weight, residual, sum, out, *(() if q is None else q._tensors()))
+    given = sum, out, *(() if q is None else q._tensors())
+    _same_device(x, stream, weight, residual, *given)
     wt = _norm_weight(weight, N, x.dtype)
     ldr = lds = ldo = 0
     if residual is not None:
@@ -1122,6 +1154,7 @@ def bt_rms_norm(x: torch.Tensor, weight: torch.Tensor | None = None, eps: float 
     codes, scales = (None, None) if q is None else q._pointers()
     _check(_c_rms(x.data_ptr(), _DT[x.dtype], ldx, _ptr(residual), ldr, _ptr(weight), wt, T, N, eps, _ptr(sum), lds, _ptr(out),
                   ldo, 0 if q is None else code, codes, scales, _on_stream(stream, x.device)))
+    _written(*given)
     return out, sum, q
 
 
@@ -1141,6 +1174,7 @@ def bt_rms_norm_backward(g: torch.Tensor, h: torch.Tensor, weight: torch.Tensor 
     dt = (g.dtype,)
     ldh = _rows(h, "h", T, N, dt)
     _same_device(g, stream, h, weight, grad_sum, grad_x, grad_weight, workspace)
+    given = grad_x, grad_weight
     wt = _norm_weight(weight, N, g.dtype)
     ldgs = 0 if grad_sum is None else _rows(grad_sum, "grad_sum", T, N, dt)
     if grad_x is None:
@@ -1156,6 +1190,7 @@ def bt_rms_norm_backward(g: torch.Tensor, h: torch.Tensor, weight: torch.Tensor 
     workspace = _scratch(workspace, need, g.device, stream)
     _check(_c_rms_bwd(g.data_ptr(), _DT[g.dtype], ldg, h.data_ptr(), ldh, _ptr(weight), wt, T, N, eps, _ptr(grad_sum), ldgs,
                       grad_x.data_ptr(), ldgx, _ptr(grad_weight), _ptr(workspace), need, _on_stream(stream, g.device)))
+    _written(*given)
     return grad_x, grad_weight
 
 
@@ -1189,17 +1224,22 @@ def _clip_grads(first, grads, max_norm, eps, norm, workspace, stream):
         raise ValueError(f"grads must be on one device, {first.device} by the first")
     if not all(map(torch.Tensor.is_contiguous, grads)):
         raise ValueError("grads must be contiguous")
+    given = norm
     if norm is None:
         norm = _empty((), torch.float32, first.device, stream)
     else:
         _dense(norm, "norm", (), torch.float32)
     need = _c_clip_ws(n)
     workspace = _scratch(workspace, need, first.device, stream)
-    pointers = array.array("Q", map(torch.Tensor.data_ptr, grads))
-    numels = array.array("q", map(torch.Tensor.numel, grads))
+    pointers = struct.pack(f"{n}Q", *map(torch.Tensor.data_ptr, grads))
+    numels = struct.pack(f"{n}q", *map(torch.Tensor.numel, grads))
     types = array.array("i", map(_DT.__getitem__, dtypes)) if len(kinds) > 1 else array.array("i", (_DT[first.dtype],)) * n
-    _check(_c_clip(pointers.buffer_info()[0], numels.buffer_info()[0], types.buffer_info()[0], n, max_norm, eps, norm.data_ptr(),
-                   _ptr(workspace), need, _on_stream(stream, first.device)))
+    _check(_c_clip(pointers, numels, types.buffer_info()[0], n, max_norm, eps, norm.data_ptr(), _ptr(workspace), need,
+                   _on_stream(stream, first.device)))
+    # (while the GPU is at work)
+    _written(given)
+    if max_norm < math.inf:
+        torch.autograd.graph.increment_version(grads)
     return norm
 
 
