@@ -57,8 +57,8 @@ struct Product {
     unsigned int *err;
 };
 
-// Up to kSmallRows rows of x; of float type: quantised by the kernel itself, which pays up to kOwnRows. split: CTAs along K
-// (1, 2, 4, 8; 0: chosen).
+// Up to kSmallRows rows of x; of float type up to kOwnRows, which the kernel quantises itself. split: CTAs along K (1, 2, 4, 8;
+// 0: chosen).
 constexpr int kSmallRows = 32, kOwnRows = 16;
 cudaError_t launch_small(const Product &p, int split, cudaStream_t s);
 

@@ -4,8 +4,9 @@
 // and a cluster of up to 8 CTAs shares a tile's K, joining its parts through distributed shared memory in the CTAs'
 // order. Up to 16 rows of x are quantised where they are used: two warps take a slice of all rows (8 KB of bf16 at 16 rows
 // and 256 values), which costs less than a launch for it, and the codes never leave shared memory. One row by 4096 x 4096,
-// E2M1, weights out of DRAM: 4.3 us (5.7 with x quantised first), 16 rows 6.5 (6.9), 32 rows 9.2 (8.1); by 11008 x 4096 7.6 (8.6),
-// 11.9 (11.0) and 18.7 (13.0; tiles of 128 rows 11.3).
+// E2M1, weights out of DRAM: 4.3 us (5.7 with x quantised first), 16 rows 6.5 (6.9); by 11008 x 4096 7.6 (8.6) and 11.9 (11.0).
+// More rows, up to 32, come as an operand: 8.1 us and 13.0 with x quantised first (9.2 and 18.7 where each CTA did it, not kept;
+// by 11008 x 4096 tiles of 128 rows, which take those, 11.3).
 //   warp 0 lane 0   TMA: weights and their scales, a slice a stage
 //   warp 1          scales to TMEM, the slice's four MMAs
 //   warps 2..9      x to codes and scales, two warps a stage, half of the rows each; then (four of them) the epilogue
@@ -358,15 +359,17 @@ template <int CODE, int NB, int XB> cudaError_t launch(const Product &p, int spl
     cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, kern, mw, ms, static_cast<const SmallArgs>(a));
 }
-template <int CODE, int NB> cudaError_t launch_x(const Product &p, int split, cudaStream_t s) {
-    return p.x_t == BT_PACKED ? launch<CODE, NB, 0>(p, split, s) : p.x_t == BT_F32 ? launch<CODE, NB, 4>(p, split, s) : launch<CODE, NB, 2>(p, split, s);
+template <int CODE> cudaError_t launch_rows(const Product &p, int split, cudaStream_t s) {
+    if (p.M > kOwnRows) return p.x_t == BT_PACKED ? launch<CODE, kSmallRows, 0>(p, split, s) : cudaErrorInvalidValue;   // (quantised before)
+    return p.x_t == BT_PACKED ? launch<CODE, kOwnRows, 0>(p, split, s)
+           : p.x_t == BT_F32  ? launch<CODE, kOwnRows, 4>(p, split, s)
+                              : launch<CODE, kOwnRows, 2>(p, split, s);
 }
 
 }  // namespace
 
 cudaError_t mx::launch_small(const Product &p, int split, cudaStream_t s) {
-    if (p.code == BT_CODE_E2M1) return p.M <= 16 ? launch_x<BT_CODE_E2M1, 16>(p, split, s) : launch_x<BT_CODE_E2M1, 32>(p, split, s);
-    return p.M <= 16 ? launch_x<BT_CODE_E4M3, 16>(p, split, s) : launch_x<BT_CODE_E4M3, 32>(p, split, s);
+    return p.code == BT_CODE_E2M1 ? launch_rows<BT_CODE_E2M1>(p, split, s) : launch_rows<BT_CODE_E4M3>(p, split, s);
 }
 
 }  // namespace bt

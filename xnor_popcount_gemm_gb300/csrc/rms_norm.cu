@@ -650,19 +650,18 @@ __global__ void __launch_bounds__(MOST + 32, MOST == 128 ? kNarrowCtas : MOST ==
     }
 }
 
-// Many short rows: one to LANES lanes, V eights a lane, no exchange but theirs; the CTA's rows join their parts of gw
+// Many short rows: one to LANES lanes, eight columns a lane, no exchange but theirs; the CTA's rows join their parts of gw
 // at the end.
-template <typename T, int V, bool VEC, int LANES>
+template <typename T, bool VEC, int LANES>
 __global__ void __launch_bounds__(256, 3) rms_back_warp_kernel(const BackArgs a) {
-    constexpr int kRow = LANES * 8 * V, kRows = 256 / LANES;
+    constexpr int kRow = LANES * 8, kRows = 256 / LANES;
     __shared__ __align__(16) float join[kRows][kRow];
     if (threadIdx.x == 0) pdl_launch_dependents();
     pdl_wait();
     const int part = threadIdx.x / LANES, lane = threadIdx.x & (LANES - 1);
-    float2 acc[V][4], w[V][4];
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const Columns<VEC> c(lane, i, a.N, LANES);
+    float2 acc[4], w[4];
+    {
+        const Columns<VEC> c(lane, 0, a.N, LANES);
         float v[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] = 1.0f;
@@ -670,36 +669,29 @@ __global__ void __launch_bounds__(256, 3) rms_back_warp_kernel(const BackArgs a)
         else if (a.w != nullptr) raw_unpack<T>(c.template load<T>(static_cast<const T *>(a.w)), v);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            w[i][e] = make_float2(v[2 * e], v[2 * e + 1]);
-            acc[i][e] = make_float2(0.0f, 0.0f);
+            w[e] = make_float2(v[2 * e], v[2 * e + 1]);
+            acc[e] = make_float2(0.0f, 0.0f);
         }
     }
     // (a warp's lanes stay together: first is its first row)
     for (int64_t first = blockIdx.x * kRows + (threadIdx.x >> 5) * (32 / LANES); first < a.T; first += gridDim.x * kRows) {
         const int64_t row = LANES == 32 ? first : first + (threadIdx.x & 31) / LANES;
         const bool real = LANES == 32 || row < a.T;
-        const int N = real ? a.N : 0;                                   // (behind the last: no columns)
-        Raw8<T> g[V], h[V], gs[V];
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const Columns<VEC> c(lane, i, N, LANES);
-            g[i] = c.template load<T>(static_cast<const T *>(a.g) + row * a.ldg);
-            h[i] = c.template load<T>(static_cast<const T *>(a.h) + row * a.ldh);
-            if (a.gs != nullptr) gs[i] = c.template load<T>(static_cast<const T *>(a.gs) + row * a.ldgs);
-        }
+        const Columns<VEC> c(lane, 0, real ? a.N : 0, LANES);           // (behind the last: no columns)
+        const Raw8<T> g = c.template load<T>(static_cast<const T *>(a.g) + row * a.ldg);
+        const Raw8<T> h = c.template load<T>(static_cast<const T *>(a.h) + row * a.ldh);
+        Raw8<T> gs;
+        if (a.gs != nullptr) gs = c.template load<T>(static_cast<const T *>(a.gs) + row * a.ldgs);
         auto sums = [&](float k) {
             float2 s = make_float2(0.0f, 0.0f), d = s;
+            float vg[8], vh[8];
+            raw_unpack<T>(g, vg);
+            raw_unpack<T>(h, vh);
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                float vg[8], vh[8];
-                raw_unpack<T>(g[i], vg);
-                raw_unpack<T>(h[i], vh);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float2 u = mul2(make_float2(vh[2 * e], vh[2 * e + 1]), make_float2(k, k));
-                    s = fma2(u, u, s);
-                    d = fma2(mul2(make_float2(vg[2 * e], vg[2 * e + 1]), w[i][e]), u, d);
-                }
+            for (int e = 0; e < 4; ++e) {
+                const float2 u = mul2(make_float2(vh[2 * e], vh[2 * e + 1]), make_float2(k, k));
+                s = fma2(u, u, s);
+                d = fma2(mul2(make_float2(vg[2 * e], vg[2 * e + 1]), w[e]), u, d);
             }
             return warp_pair<LANES>(make_float2(s.x + s.y, d.x + d.y));
         };
@@ -711,39 +703,32 @@ __global__ void __launch_bounds__(256, 3) rms_back_warp_kernel(const BackArgs a)
             p = sums(k);
         }
         const float inv = real ? inverse_plain(p.x, a.n_inv, eps) : 0.0f, mean = p.y * inv * a.n_inv, n1 = k * inv;
-        T *gx = static_cast<T *>(a.gx) + row * a.ldgx;
+        float vg[8], vh[8], o[8];
+        raw_unpack<T>(g, vg);
+        raw_unpack<T>(h, vh);
+        if (a.gs != nullptr) raw_unpack<T>(gs, o);
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            float vg[8], vh[8], o[8];
-            raw_unpack<T>(g[i], vg);
-            raw_unpack<T>(h[i], vh);
-            if (a.gs != nullptr) raw_unpack<T>(gs[i], o);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                // (h k first: k brings it into range)
-                const float2 u = mul2(mul2(make_float2(vh[2 * e], vh[2 * e + 1]), make_float2(k, k)), make_float2(inv, inv));
-                const float2 gg = make_float2(vg[2 * e], vg[2 * e + 1]);
-                acc[i][e] = fma2(gg, u, acc[i][e]);
-                float2 d = mul2(fma2(u, make_float2(-mean, -mean), mul2(gg, w[i][e])), make_float2(n1, n1));
-                if (a.gs != nullptr) d = add2(d, make_float2(o[2 * e], o[2 * e + 1]));
-                o[2 * e] = d.x;
-                o[2 * e + 1] = d.y;
-            }
-            Columns<VEC>(lane, i, N, LANES).template store<T>(gx, o);
+        for (int e = 0; e < 4; ++e) {
+            // (h k first: k brings it into range)
+            const float2 u = mul2(mul2(make_float2(vh[2 * e], vh[2 * e + 1]), make_float2(k, k)), make_float2(inv, inv));
+            const float2 gg = make_float2(vg[2 * e], vg[2 * e + 1]);
+            acc[e] = fma2(gg, u, acc[e]);
+            float2 d = mul2(fma2(u, make_float2(-mean, -mean), mul2(gg, w[e])), make_float2(n1, n1));
+            if (a.gs != nullptr) d = add2(d, make_float2(o[2 * e], o[2 * e + 1]));
+            o[2 * e] = d.x;
+            o[2 * e + 1] = d.y;
         }
+        c.template store<T>(static_cast<T *>(a.gx) + row * a.ldgx, o);
     }
     if (a.parts == nullptr) return;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const float v[8] = {acc[i][0].x, acc[i][0].y, acc[i][1].x, acc[i][1].y, acc[i][2].x, acc[i][2].y, acc[i][3].x, acc[i][3].y};
-        Columns<VEC>(lane, i, a.N, LANES).template store<float>(join[part], v);
-    }
+    const float v[8] = {acc[0].x, acc[0].y, acc[1].x, acc[1].y, acc[2].x, acc[2].y, acc[3].x, acc[3].y};
+    Columns<VEC>(lane, 0, a.N, LANES).template store<float>(join[part], v);
     __syncthreads();
-    for (int c = threadIdx.x; c < a.N; c += 256) {
-        float v = 0.0f;
+    for (int col = threadIdx.x; col < a.N; col += 256) {
+        float sum = 0.0f;
 #pragma unroll
-        for (int k = 0; k < kRows; ++k) v += join[k][c];
-        a.parts[static_cast<int64_t>(blockIdx.x) * a.N + c] = v;
+        for (int r = 0; r < kRows; ++r) sum += join[r][col];
+        a.parts[static_cast<int64_t>(blockIdx.x) * a.N + col] = sum;
     }
 }
 
@@ -962,9 +947,9 @@ template <typename T, bool VEC> cudaError_t back_rows(BackArgs a, cudaStream_t s
 template <typename T, bool VEC> cudaError_t back_warps(const BackArgs &a, cudaStream_t s) {
     const int64_t groups = (a.N + 7) / 8;
     // one eight a lane: with two its registers hide less of memory's delay (524288 x 128 bf16: 142 us, 93 with one)
-    return launch_pdl(groups <= 8    ? rms_back_warp_kernel<T, 1, VEC, 8>
-                      : groups <= 16 ? rms_back_warp_kernel<T, 1, VEC, 16>
-                                     : rms_back_warp_kernel<T, 1, VEC, 32>, dim3(static_cast<unsigned>(a.chunks)), dim3(256), s, a);
+    return launch_pdl(groups <= 8    ? rms_back_warp_kernel<T, VEC, 8>
+                      : groups <= 16 ? rms_back_warp_kernel<T, VEC, 16>
+                                     : rms_back_warp_kernel<T, VEC, 32>, dim3(static_cast<unsigned>(a.chunks)), dim3(256), s, a);
 }
 template <typename T> cudaError_t backward(BackArgs a, bool vec, cudaStream_t s) {
     a.chunks = back_chunks(a.T, a.N, sizeof(T));
