@@ -921,7 +921,8 @@ size_t bt_mx_linear_workspace(int64_t M, int64_t N, int64_t K, bt_dtype x_dtype,
  *            `code` by the call; BT_PACKED: an operand's codes (ldx ignored), with
  *            x_scales.
  *   w        device, the operand [N, K] in `code`, with w_scales.
- *   out      rows ldo >= N elements apart; 16-byte rows are faster.
+ *   out      rows ldo >= N elements apart; 16-byte rows are faster. It shares no memory
+ *            with x, w or their scales.
  * A NaN block makes its row of out (its column, in W) NaN. M = 0 or N = 0 does
  * nothing. workspace: bt_mx_linear_workspace(M, N, K, x_dtype, code) bytes, 256-byte
  * aligned. Equal calls give equal results. Errors: INVALID_ARG, ALIGNMENT,

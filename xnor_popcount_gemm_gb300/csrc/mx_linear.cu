@@ -417,7 +417,9 @@ Shape choose(const Product &p) {
             best = Shape{t.pair, t.bn, t.d, 8};
         }
     }
-    // four epilogue warps make room for a sixth stage (8192 x 4096 x 11008 E2M1 102.6 -> 99.4 us) where a tile is long enough to hide them
+    // four epilogue warps make room for a sixth stage where a tile is long enough to hide them (E2M1, eight and four: 8192 x 4096 x 11008
+    // 103.4 and 100.0 us, 8192 x 8192 x 6144 122.7 and 119.5, 2048 x 11008 x 11008 80.7 and 75.0, 8192 x 2048 x 8192 48.2 and 47.3,
+    // 16384 x 4096 x 6400 130.5 and 124.2)
     if (best.pair && best.bn == 256 && p.code == BT_CODE_E2M1 && k >= 24 && wide && elem == 2) best.epi = 4;
     return best;
 }

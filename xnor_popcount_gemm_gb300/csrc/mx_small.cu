@@ -10,7 +10,7 @@
 //   warp 0 lane 0   TMA: weights and their scales, a slice a stage
 //   warp 1          scales to TMEM, the slice's four MMAs
 //   warps 2..9      x to codes and scales, two warps a stage, half of the rows each; then (four of them) the epilogue
-// Two CTAs an SM with 80 KB each on their way. One row by 11008 x 4096: 172 CTAs, 3.2 TB/s; what is left is the launch, a trip to memory
+// Two CTAs an SM with 80 KB each on their way. One row by 11008 x 4096, weights out of DRAM: 172 CTAs, 3.2 TB/s; what is left is the launch, a trip to memory
 // and the join. The weights' boxes asked into L2 before the grid before has ended: 8.0 us instead of 7.6.
 #include "mx_linear.cuh"
 

@@ -6,7 +6,7 @@
 //   gw = sum over the rows of g n
 //
 // Streams: every row is read once, kept in registers by its CTA (short rows: by some lanes of a warp) and written once. 8192 x 4096
-// bf16 with a residual 42 us (268 MB, 95 % of the copy rate), with E4M3 codes as well 49 to 50 (302 MB, 91 %).
+// bf16 with a residual 42 us (268 MB, 95 % of the copy rate), with E4M3 codes as well 48.6 (302 MB, 92 %).
 //
 // What is rounded to 8 or 4 bits falls one way or the other, so y is the correctly rounded fp32 value (but for about one
 // in 2^24): the squares are summed with the rounding errors of the sums beside them, and 1 / sqrt(mean) is a pair of
@@ -452,7 +452,7 @@ __device__ __noinline__ void await_row(uint32_t bar, uint32_t parity, uint32_t f
 
 // A CTA takes rows blockIdx.x, + gridDim.x, ..., keeps its threads' columns of gw in registers, and has the next two rows on
 // their way into a ring in shared memory: bulk copies of the 16-byte pieces that hold a row, asked for by a warp of its
-// own. Memory: 4096 x 4096 bf16 with gs 26.7 us (134 MB, 74 % of the copy rate), and 4 for the parts of gw and their sum;
+// own. Memory: 4096 x 4096 bf16 with gs 27 us (134 MB, 73 % of the copy rate), and 4 for the parts of gw and their sum;
 // with rows loaded when they are due 41.
 template <typename T, int V, int MOST, bool VEC>
 __global__ void __launch_bounds__(MOST + 32, MOST == 128 ? kNarrowCtas : MOST == 256 ? kBackCtas : 1) rms_back_kernel(const BackArgs a) {
@@ -733,7 +733,7 @@ __global__ void __launch_bounds__(256, 3) rms_back_warp_kernel(const BackArgs a)
 }
 
 // Wider rows than a ring holds: the rows' sums, then strips of columns, eight a thread, so that g and h are read twice. 1024 x 32768
-// bf16 with gs 83 us (268 MB, 48 % of the copy rate where 67 can be had; 236 with a column a thread), fp32 142.
+// bf16 with gs 77 us (268 MB, 51 % of the copy rate where 67 can be had; 236 with a column a thread).
 template <typename T, bool VEC> __device__ __forceinline__ void weight8(const BackArgs &a, const Columns<VEC> &c, float (&v)[8]) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = 1.0f;
