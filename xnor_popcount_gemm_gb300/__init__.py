@@ -1012,6 +1012,8 @@ def bt_mx_dequantize(q: MxRows, out_dtype=torch.float32, out: torch.Tensor | Non
     first, *others = q._tensors()
     _same_device(first, stream, *others, out)
     given = out
+    if out is None and out_dtype not in _FLOATS:
+        raise ValueError(f"out_dtype must be {' or '.join(map(str, _FLOATS))}")
     if out is None:
         out = _empty((R, K), out_dtype, first.device, stream)
     ldo = _rows(out, "out", R, K, _FLOATS)
@@ -1031,6 +1033,8 @@ def bt_mx_linear(x, w: MxRows, out_dtype=None, out: torch.Tensor | None = None, 
     call) or MxRows in w's code. out_dtype: x's type, bfloat16 for MxRows."""
     N, K = _mx(w, "w").shape
     code = w.code
+    if out_dtype is not None and out_dtype not in _FLOATS:
+        raise ValueError(f"out_dtype must be {' or '.join(map(str, _FLOATS))}")
     if type(x) is MxRows:
         if x.code != code or x.K != K:
             raise ValueError("x and w must agree on K and the code")
@@ -1097,10 +1101,10 @@ def bt_mx_linear_backward(g: torch.Tensor, wt: torch.Tensor, out_dtype=torch.bfl
     K, ldw = wt.shape
     _same_device(g, stream, wt, grad_x, workspace)
     given = grad_x
+    if (out_dtype if grad_x is None else grad_x.dtype) not in (torch.bfloat16, torch.float32):
+        raise ValueError("grad_x must be bfloat16 or float32")
     if grad_x is None:
         grad_x = _empty((M, K), out_dtype, g.device, stream)
-    elif grad_x.dtype not in (torch.bfloat16, torch.float32):
-        raise ValueError("grad_x must be bfloat16 or float32")
     _dense(grad_x, "grad_x", (M, K), grad_x.dtype)
     need = 0 if ldg % 8 == 0 and N % 8 == 0 and g.data_ptr() % 16 == 0 else _c_mx_bwd_ws(M, N)
     workspace = _scratch(workspace, need, g.device, stream)
