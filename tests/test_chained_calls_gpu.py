@@ -87,3 +87,54 @@ def test_product_then_clipping(M):
         b.copy_(n)
     for i, (a, b) in enumerate(got):
         assert torch.equal(a, want[i % 4][0]) and torch.equal(b, want[i % 4][1])
+
+
+# adapters beside a projection take what the norm has just written; the distillation's gradient takes its loss's statistics
+@pytest.mark.parametrize("T", [1, 8, 100, 1500])
+def test_norm_then_adapters(T):
+    K, N, R, L = 512, 384, 16, 3
+    gen = torch.Generator(device="cuda").manual_seed(T)
+    a, b = (torch.randn(*s, generator=gen, device="cuda").to(BF16) for s in ((L, R, K), (L, N, R)))
+    scale = torch.ones(L, device="cuda")
+    plan = bt.bt_adapter_plan(torch.randint(-1, L, (T,), generator=torch.Generator().manual_seed(T)), L)
+    xs = _sources(T, K)
+    want = []
+    for x in xs:
+        y = bt.bt_rms_norm(x, None, 1.0)[0]
+        torch.cuda.synchronize()
+        u = torch.empty(T, R, device="cuda")
+        o = bt.bt_adapter_linear(y, a, b, scale, plan, u=u)
+        torch.cuda.synchronize()
+        want.append((o, bt.bt_adapter_linear_backward(y, o, u, a, b, scale, plan)[0]))
+        torch.cuda.synchronize()
+    y, u, o, gx = torch.empty(T, K, dtype=BF16, device="cuda"), torch.empty(T, R, device="cuda"), torch.empty(T, N, dtype=BF16, device="cuda"), torch.empty(T, K, dtype=BF16, device="cuda")
+    got = [(torch.empty_like(o), torch.empty_like(gx)) for _ in range(24)]
+    torch.cuda.synchronize()
+    for i, (p, q) in enumerate(got):
+        bt.bt_rms_norm(xs[i % 4], None, 1.0, out=y)
+        bt.bt_adapter_linear(y, a, b, scale, plan, out=o, u=u)
+        bt.bt_adapter_linear_backward(y, o, u, a, b, scale, plan, grad_x=gx)
+        p.copy_(o)
+        q.copy_(gx)
+    for i, (p, q) in enumerate(got):
+        assert torch.equal(p, want[i % 4][0]) and torch.equal(q, want[i % 4][1])
+
+
+@pytest.mark.parametrize("T,V", [(1, 5000), (16, 32000), (700, 2000)])
+def test_distillation_and_its_gradient(T, V):
+    S = 8
+    zs = _sources(T, V)
+    ids = torch.arange(S, device="cuda").repeat(T, 1)
+    top, gl = torch.randn(T, S, generator=torch.Generator(device="cuda").manual_seed(1), device="cuda"), torch.ones(T, device="cuda")
+    want = []
+    for z in zs:
+        _, stats = bt.bt_distill_topk(z, ids, top)
+        torch.cuda.synchronize()
+        want.append(bt.bt_distill_topk_backward(gl, z, ids, top, stats))
+        torch.cuda.synchronize()
+    stats, loss, got = torch.empty(T, 2, device="cuda"), torch.empty(T, device="cuda"), [torch.empty_like(zs[0]) for _ in range(24)]
+    torch.cuda.synchronize()
+    for i, g in enumerate(got):
+        bt.bt_distill_topk(zs[i % 4], ids, top, loss=loss, stats=stats)
+        bt.bt_distill_topk_backward(gl, zs[i % 4], ids, top, stats, grad=g)
+    assert all(torch.equal(g, want[i % 4]) for i, g in enumerate(got))
